@@ -13,6 +13,9 @@ import torch
 
 from . import _lib
 from ._lib import GdnError, GDN_BF16, GDN_F32  # noqa: F401
+from .layer import (  # noqa: F401
+    gdn_conv_fwd, gdn_conv_step, gdn_group_norm, gdn_ssm_fwd, gdn_ssm_fwd_workspace_size,
+    gdn_ssm_step)
 
 _DTYPES = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
 
@@ -276,8 +279,9 @@ def gdn_get_device_status(stream=None):
 
 def gdn_last_launch_count():
     """(kernels enqueued by the last gdn_chunk_fwd / gdn_chunk_fwd_scan /
-    gdn_decode_step on this thread, path id: 0 fp32 chunk kernel, 1 tcgen05
-    chunk kernel, 2 decode, 3 chunk-level scan)."""
+    gdn_decode_step or layer operator on this thread, path id: 0 fp32 chunk
+    kernel, 1 tcgen05 chunk kernel, 2 decode, 3 chunk-level scan, 6 short
+    convolution, 7 state space scan or step, 8 group norm)."""
     path = ctypes.c_int(-1)
     n = _lib.load().gdn_last_launch_count(ctypes.byref(path))
     return n, path.value

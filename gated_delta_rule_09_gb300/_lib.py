@@ -22,10 +22,14 @@ GDN_DEV_BAD_SEQLENS = 0x1
 GDN_DEV_WAIT_TIMEOUT = 0x2
 GDN_DEV_F16_RANGE = 0x4
 GDN_DEV_F16_PRECISION = 0x8
+GDN_DEV_BAD_SLOT = 0x10
+GDN_ACT_NONE = 0
+GDN_ACT_SILU = 1
 
 # (name, restype, argtypes) for every entry point of include/gdn.h
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_l = ctypes.c_int64
 SIGNATURES = {
     "gdn_chunk_fwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                      _i, _i, _i, _i, _i, _i, _vp, _i, _vp]),
@@ -40,6 +44,14 @@ SIGNATURES = {
     "gdn_ut_inverse": (ctypes.c_int, [_vp, _vp, _i, _i, _i, _vp]),
     "gdn_decode_step": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                        _i, _i, _i, _i, _i, _i, _vp]),
+    "gdn_conv_fwd": (ctypes.c_int, [_vp] * 7 + [_i] * 4 + [_l] * 2 + [_i, _vp, _i, _i, _vp]),
+    "gdn_conv_step": (ctypes.c_int, [_vp] * 7 + [_i] * 3 + [_l] * 2 + [_i, _i, _i, _vp]),
+    "gdn_ssm_fwd_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i, _vp, _i]),
+    "gdn_ssm_fwd": (ctypes.c_int, [_vp] * 12 + [_i] * 5 + [_l] * 6
+                    + [_i, _vp, _i, _i, _i, _vp, ctypes.c_size_t, _vp]),
+    "gdn_ssm_step": (ctypes.c_int, [_vp] * 12 + [_i] * 4 + [_l] * 6 + [_i, _i, _i, _vp]),
+    "gdn_group_norm": (ctypes.c_int, [_vp] * 5 + [_l, _i, _i, _l, _l, _l, ctypes.c_float,
+                                                  _i, _i, _i, _vp]),
     "gdn_get_device_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint)]),
     "gdn_get_last_error": (ctypes.c_char_p, []),
     "gdn_version": (ctypes.c_int, []),

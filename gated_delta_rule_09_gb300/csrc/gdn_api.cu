@@ -6,6 +6,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_layer.h"
 
 namespace {
 
@@ -251,6 +252,28 @@ gdn_status_t chunk_fwd(const void *q, const void *k, const void *v, const float 
 }
 
 }  // namespace
+
+gdn_status_t gdn_fail(gdn_status_t st, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(t_msg, sizeof(t_msg), fmt, ap);
+    va_end(ap);
+    return st;
+}
+
+gdn_status_t gdn_device_status_word(unsigned int **out) { return status_word(out); }
+
+void gdn_begin_call()
+{
+    t_msg[0] = '\0';
+}
+
+void gdn_record_launch(int launches, int path)
+{
+    t_launches = launches;
+    t_path = path;
+}
 
 extern "C" {
 

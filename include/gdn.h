@@ -53,12 +53,16 @@ typedef enum {
 
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype_t;
 
+/* Activation of the layer operators (gdn_conv_*, gdn_group_norm). */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 /* v / (1 + e^-v) */ } gdn_act_t;
+
 /* Device-side status bits returned by gdn_get_device_status(). */
 #define GDN_DEV_BAD_SEQLENS 0x1u /* a cu_seqlens span was negative or past T */
 #define GDN_DEV_WAIT_TIMEOUT 0x2u /* a bounded pipeline wait gave up          */
 #define GDN_DEV_F16_RANGE 0x4u    /* a tensor-core operand left the fp16 range  */
 #define GDN_DEV_F16_PRECISION 0x8u /* a unit's state-chain operands all stayed
                                       below 2^-10: fp16 kept few bits of them   */
+#define GDN_DEV_BAD_SLOT 0x10u   /* a state slot was past the end of its pool  */
 
 /*
  * gdn_chunk_fwd — forward pass of the gated delta rule, chunkwise.
@@ -275,6 +279,136 @@ gdn_status_t gdn_decode_step(const void *q, const void *k, const void *v,
 gdn_status_t gdn_ut_inverse(const float *A, float *T, int count, int C, int method, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The layer around the recurrence: short causal convolution, selective state
+ * space scan, group norm.  Rules these entry points share, beside the
+ * conventions at the top of this file:
+ *
+ *  - Rows.  x, y, z and the like are matrices of token rows with unit stride
+ *    along the channels and a row stride ld_* (in elements, at least the row's
+ *    own width), so that each may be a slice of a projection's wider output.
+ *    Prompts [B, T, *] are B * T rows one ld apart.  Outputs must not overlap
+ *    inputs; two slices of the same rows (equal ld, separate columns) do not
+ *    overlap.
+ *  - Types.  x, y and what is drawn from the same projection share `dtype`;
+ *    parameters (weight, bias, A, D, delta_bias) are fp32, arithmetic is fp32,
+ *    the output is rounded once.  Alignment: that of the element type; 16
+ *    bytes with row strides that are a multiple of 16 bytes selects the
+ *    vectorised kernels.
+ *  - Packed prompts (cu_seqlens, device int32 [B + 1]) follow gdn_chunk_fwd:
+ *    B sequences along one token axis of T rows.  A span that is negative or
+ *    leaves [0, T] is skipped and raises GDN_DEV_BAD_SEQLENS.
+ *  - States live in a pool of `pool` entries: sequence n owns entry n, or
+ *    entry slots[n] when `slots` (device int32, one per sequence) is given,
+ *    so a serving loop keeps one pool for prompts and steps.  state_in may be
+ *    NULL (zeros); state_out NULL (prompts only) drops the final state.
+ *    state_out may be exactly state_in (in place).  A negative slot marks a
+ *    sequence that keeps no state: it starts from zeros and writes none (the
+ *    padding rows of a fixed-size batch).  A slot >= pool is treated the same
+ *    way and raises GDN_DEV_BAD_SLOT.  Two sequences must not share a slot.
+ *    A sequence without tokens hands its state on unchanged.
+ */
+
+/*
+ * gdn_conv_fwd — short causal depthwise convolution over prompts:
+ *
+ *     y[t, c] = act(bias[c] + sum_j weight[c, j] x[t - (width - 1) + j, c])
+ *
+ * with the inputs before a sequence's first token taken from its state (the
+ * last width - 1 inputs, oldest first) or zero.
+ *   x, y        [B, T, channels] dtype, row strides ld_x, ld_y
+ *   weight      [channels, width] fp32; bias [channels] fp32 or NULL
+ *   state_in, state_out  [pool, width - 1, channels] dtype; NULL allowed
+ *   width       1 to 8
+ * One kernel; gdn_last_launch_count reports path 6.
+ */
+gdn_status_t gdn_conv_fwd(const void *x, const float *weight, const float *bias,
+                          const void *state_in, const int32_t *slots, void *y, void *state_out,
+                          int B, int T, int channels, int width, int64_t ld_x, int64_t ld_y,
+                          int pool, const int32_t *cu_seqlens, gdn_act_t act, gdn_dtype_t dtype,
+                          void *stream);
+
+/*
+ * gdn_conv_step — the same for one new token of each of N sequences:
+ * x, y [N, channels]; the state (required in state_out, NULL state_in =
+ * zeros) moves on by one input.  One kernel, path 6.
+ */
+gdn_status_t gdn_conv_step(const void *x, const float *weight, const float *bias,
+                           const void *state_in, const int32_t *slots, void *y, void *state_out,
+                           int N, int channels, int width, int64_t ld_x, int64_t ld_y, int pool,
+                           gdn_act_t act, gdn_dtype_t dtype, void *stream);
+
+/*
+ * gdn_ssm_fwd — selective state space scan over prompts.  Channel c of group
+ * g = c / (channels / groups) carries d_state fp32 states; per token t
+ *
+ *     d      = delta[t, c] + delta_bias[c]       (softplus of it if asked)
+ *     h[s]   = exp(d A[c, s]) h[s] + d B[t, g, s] x[t, c]
+ *     y[t,c] = (sum_s C[t, g, s] h[s] + D[c] x[t, c]) * silu(z[t, c])
+ *
+ * softplus(v) = log(1 + e^v); without z the last factor is one, without D
+ * the skip term is zero.
+ *   x, delta, z, y  [B, T, channels] dtype, row strides ld_x, ld_delta, ld_z,
+ *                   ld_y; z NULL allowed
+ *   A               [channels, d_state] fp32 (negative for a decaying state)
+ *   Bm, Cm          [B, T, groups, d_state] dtype, row strides ld_b, ld_c
+ *   D, delta_bias   [channels] fp32 or NULL
+ *   state_in, state_out  [pool, channels, d_state] fp32; NULL allowed
+ *   d_state 1 to 128; channels a multiple of groups
+ *   segment         tokens per piece: long sequences are cut into pieces that
+ *                   run in parallel (each piece's decay is exp(A sum d), so
+ *                   the pieces chain exactly up to rounding); <= 0 lets the
+ *                   library choose (possibly one piece), else rounded up to a
+ *                   multiple of 64
+ *   workspace       gdn_ssm_fwd_workspace_size(...) bytes, 16-byte aligned,
+ *                   not overlapping any argument, not shared by calls that
+ *                   overlap in time; NULL allowed when that size is 0
+ * One kernel, or two when sequences are cut; path 7.
+ */
+size_t gdn_ssm_fwd_workspace_size(int B, int T, int channels, int d_state,
+                                  const int32_t *cu_seqlens, int segment);
+
+gdn_status_t gdn_ssm_fwd(const void *x, const void *delta, const float *A, const void *Bm,
+                         const void *Cm, const float *D, const void *z, const float *delta_bias,
+                         const float *state_in, const int32_t *slots, void *y, float *state_out,
+                         int B, int T, int channels, int d_state, int groups, int64_t ld_x,
+                         int64_t ld_delta, int64_t ld_b, int64_t ld_c, int64_t ld_z, int64_t ld_y,
+                         int pool, const int32_t *cu_seqlens, int delta_softplus,
+                         gdn_dtype_t dtype, int segment, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * gdn_ssm_step — the same recurrence for one new token of each of N
+ * sequences: x, delta, z, y [N, channels], Bm, Cm [N, groups, d_state].
+ * state_out is required; state_in NULL = zeros.  One kernel, path 7.
+ */
+gdn_status_t gdn_ssm_step(const void *x, const void *delta, const float *A, const void *Bm,
+                          const void *Cm, const float *D, const void *z, const float *delta_bias,
+                          const float *state_in, const int32_t *slots, void *y, float *state_out,
+                          int N, int channels, int d_state, int groups, int64_t ld_x,
+                          int64_t ld_delta, int64_t ld_b, int64_t ld_c, int64_t ld_z, int64_t ld_y,
+                          int pool, int delta_softplus, gdn_dtype_t dtype, void *stream);
+
+/*
+ * gdn_group_norm — group norm of token rows, channels last, the norm of the
+ * heads' outputs (a group is a head): the channels of a row are cut into
+ * `groups` equal runs, each normalised by its own statistics,
+ *
+ *     u = (x - mean) / sqrt(var + eps)     (rms != 0: x / sqrt(mean x^2 + eps))
+ *     y = act(u * weight[c] + bias[c]) * silu(gate)
+ *
+ *   x, gate, y  [rows, channels] dtype, row strides ld_x, ld_gate, ld_y; gate
+ *               NULL allowed (factor one); y may be exactly x or gate with
+ *               the same stride (in place)
+ *   weight, bias  [channels] fp32 or NULL; eps >= 0
+ * Statistics are per token: tokens do not see one another.  One kernel, path 8.
+ */
+gdn_status_t gdn_group_norm(const void *x, const void *gate, const float *weight,
+                            const float *bias, void *y, int64_t rows, int channels, int groups,
+                            int64_t ld_x, int64_t ld_gate, int64_t ld_y, float eps, int rms,
+                            gdn_act_t act, gdn_dtype_t dtype, void *stream);
+
+/*
  * gdn_get_device_status — synchronise `stream`, then read and clear the
  * device-side status bits (GDN_DEV_*) raised by kernels of this library on the
  * current device since the last read.  *flags receives the bits (0 = clean).
@@ -285,7 +419,8 @@ gdn_status_t gdn_ut_inverse(const float *A, float *T, int count, int C, int meth
  * Else GDN_ERR_RANGE when GDN_DEV_F16_RANGE is among them: an operand
  * overflowed fp16, so the outputs it fed are wrong.  The other bits (a bad
  * packed span: that sequence was skipped; fp16 precision: results are valid
- * but carry fewer bits) come back with GDN_OK.
+ * but carry fewer bits; a bad slot: that sequence ran without a state) come
+ * back with GDN_OK.
  * Returns GDN_ERR_CUDA if synchronising or reading fails.
  */
 gdn_status_t gdn_get_device_status(void *stream, unsigned int *flags);
@@ -298,11 +433,13 @@ int gdn_version(void);
 
 /*
  * gdn_last_launch_count — number of kernels the last successful gdn_chunk_fwd
- * gdn_chunk_fwd_scan or gdn_decode_step on the calling thread enqueued, and
+ * gdn_chunk_fwd_scan, gdn_decode_step or layer operator on the calling thread
+ * enqueued, and
  * in *path which kernel family ran (0 = fp32 CUDA-core chunk kernel,
  * 1 = tcgen05 tensor-core chunk kernel, 2 = recurrent decode kernel,
  * 3 = chunk-level scan over segments, 4 / 5 = UT inverse by forward
- * substitution / on the tensor cores).  For
+ * substitution / on the tensor cores, 6 = short convolution, 7 = state space
+ * scan or step, 8 = group norm).  For
  * accounting in benchmarks; no device work.
  */
 int gdn_last_launch_count(int *path);
