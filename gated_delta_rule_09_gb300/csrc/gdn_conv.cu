@@ -18,22 +18,87 @@ using namespace gdn_layer;
 constexpr int kThreads = 128;
 constexpr int kUnroll = 8;  // tokens loaded ahead of their use
 
-template <int VEC, int W>
-__device__ __forceinline__ void ld_params(const GdnConvArgs &a, int c0, float (&w)[W][VEC],
-                                          float (&b)[VEC])
+// Arithmetic on VEC channels, in pairs where there are pairs.
+template <int VEC> struct Lanes {
+    static constexpr int N = VEC > 1 ? VEC / 2 : 1;
+    f32x2 v[N];
+};
+
+template <typename E, int VEC> __device__ __forceinline__ Lanes<VEC> widen_lanes(const typename Word<VEC * sizeof(E)>::type &u)
 {
+    float x[VEC];
+    widen(u, x);
+    Lanes<VEC> l;
+    if constexpr (VEC == 1) {
+        l.v[0] = pack2(x[0], 0.f);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+        for (int i = 0; i < VEC; i += 2) l.v[i / 2] = pack2(x[i], x[i + 1]);
+    }
+    return l;
+}
+
+template <int VEC> __device__ __forceinline__ void unpack_lanes(const Lanes<VEC> &l, float (&x)[VEC])
+{
+    if constexpr (VEC == 1) {
+        float unused;
+        unpack2(l.v[0], x[0], unused);
+    } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = a.weight[(size_t)(c0 + i) * W + j];
-        b[i] = a.bias ? a.bias[c0 + i] : 0.f;
+        for (int i = 0; i < VEC; i += 2) unpack2(l.v[i / 2], x[i], x[i + 1]);
     }
 }
+
+// Taps and bias of the thread's channels.
+template <int VEC, int W> struct Taps {
+    Lanes<VEC> w[W], b;
+
+    __device__ __forceinline__ Taps(const GdnConvArgs &a, int c0)
+    {
+        float f[VEC * W], bias[VEC];
+        if constexpr (VEC == 1) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) f[j] = a.weight[(size_t)c0 * W + j];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC * W; i += 4) {  // VEC W is a multiple of 4, and so is c0
+                const float4 t = *reinterpret_cast<const float4 *>(a.weight + (size_t)c0 * W + i);
+                f[i] = t.x;
+                f[i + 1] = t.y;
+                f[i + 2] = t.z;
+                f[i + 3] = t.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c0 + i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < Lanes<VEC>::N; ++i) {
+            const int lo = VEC > 1 ? 2 * i : 0, hi = VEC > 1 ? 2 * i + 1 : 0;
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j].v[i] = pack2(f[lo * W + j], f[hi * W + j]);
+            b.v[i] = pack2(bias[lo], bias[hi]);
+        }
+    }
+
+    // y of the token whose input is win[W - 1]
+    __device__ __forceinline__ void apply(const Lanes<VEC> (&win)[W], int act, float (&y)[VEC]) const
+    {
+        Lanes<VEC> r = b;
+#pragma unroll
+        for (int i = 0; i < Lanes<VEC>::N; ++i) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) r.v[i] = fma2(w[j].v[i], win[j].v[i], r.v[i]);
+            if (act == GDN_ACT_SILU) r.v[i] = silu2(r.v[i]);
+        }
+        unpack_lanes<VEC>(r, y);
+    }
+};
 
 template <typename E, int VEC, int W>
 __global__ void __launch_bounds__(kThreads)
     gdn_conv_fwd_kernel(const GdnConvArgs a, int tl, int tiles)
 {
+    typedef typename Word<VEC * sizeof(E)>::type Vec;
     Span s;
     if (!find_span(a.cu_seqlens, a.N, a.T, tl, blockIdx.x, tiles, a.status, s)) return;
     const int c0 = (blockIdx.y * kThreads + threadIdx.x) * VEC;
@@ -41,111 +106,94 @@ __global__ void __launch_bounds__(kThreads)
     const E *x = static_cast<const E *>(a.x) + s.row * a.ld_x + c0;
     E *y = static_cast<E *>(a.y) + s.row * a.ld_y + c0;
     const int t0 = s.tile * tl, t1 = min(s.len, t0 + tl);
+    auto input = [&](int64_t t) { return *reinterpret_cast<const Vec *>(x + t * a.ld_x); };
 
-    float win[W][VEC];  // win[j]: the input j - (W - 1) tokens from the current one; win[W-1] is current
+    Lanes<VEC> win[W];  // win[j]: the input j - (W - 1) tokens from the current one
     if (s.tile == 0) {
         // The state is read and written by this thread alone (whichever tile
         // the sequence ends in), so it may be updated in place.
         const int entry = state_entry(a.slots, s.n, a.pool, a.status);
         const E *in = static_cast<const E *>(a.state_in);
         const size_t at = entry < 0 ? 0 : (size_t)entry * (W - 1) * a.channels + c0;
+        Vec kept[W];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            if (in && entry >= 0) {
-                ld_vec<E, VEC>(in + at + (size_t)j * a.channels, win[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
-            }
+            kept[j] = Vec();
+            if (in && entry >= 0) kept[j] = *reinterpret_cast<const Vec *>(in + at + (size_t)j * a.channels);
+            win[j] = widen_lanes<E, VEC>(kept[j]);
         }
         if (a.state_out && entry >= 0) {
             E *out = static_cast<E *>(a.state_out);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
                 const int p = s.len - (W - 1) + j;
-                float v[VEC];
+                Vec v = Vec();
                 if (p >= 0) {
-                    ld_vec<E, VEC>(x + p * a.ld_x, v);
+                    v = input(p);
                 } else {  // fewer tokens than taps: the older state moves up
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k)
-                        if (k == p + W - 1)
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i) v[i] = win[k][i];
+                        if (k == p + W - 1) v = kept[k];
                 }
-                st_vec<E, VEC>(out + at + (size_t)j * a.channels, v);
+                *reinterpret_cast<Vec *>(out + at + (size_t)j * a.channels) = v;
             }
         }
     } else {  // a tile is longer than the taps, so these lie in the same sequence
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            ld_vec<E, VEC>(x + (int64_t)(t0 - (W - 1) + j) * a.ld_x, win[j]);
+        for (int j = 0; j < W - 1; ++j) win[j] = widen_lanes<E, VEC>(input(t0 - (W - 1) + j));
     }
     if (t0 >= t1) return;
 
-    float w[W][VEC], b[VEC];
-    ld_params<VEC, W>(a, c0, w, b);
-    for (int t = t0; t < t1; t += kUnroll) {
-        Pack<E, VEC> u[kUnroll];
+    const Taps<VEC, W> taps(a, c0);
+    auto token = [&](int t, const Vec &u) {
+        float r[VEC];
+        win[W - 1] = widen_lanes<E, VEC>(u);
+        taps.apply(win, a.act, r);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            if (t + k < t1)
-                u[k] = *reinterpret_cast<const Pack<E, VEC> *>(x + (int64_t)(t + k) * a.ld_x);
+        for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
+        st_vec<E, VEC>(y + (int64_t)t * a.ld_y, r);
+    };
+    int t = t0;
+    for (; t + kUnroll <= t1; t += kUnroll) {
+        Vec u[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            if (t + k >= t1) break;
-            float r[VEC];
+        for (int k = 0; k < kUnroll; ++k) u[k] = input(t + k);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                win[W - 1][i] = to_f(u[k].v[i]);
-                r[i] = b[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j) r[i] = fmaf(w[j][i], win[j][i], r[i]);
-                if (a.act == GDN_ACT_SILU) r[i] = silu(r[i]);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
-            }
-            st_vec<E, VEC>(y + (int64_t)(t + k) * a.ld_y, r);
-        }
+        for (int k = 0; k < kUnroll; ++k) token(t + k, u[k]);
     }
+    for (; t < t1; ++t) token(t, input(t));
 }
 
-// One token per sequence: the state row group moves on by one input.
+// One token per sequence: the state moves on by one input.
 template <typename E, int VEC, int W>
 __global__ void __launch_bounds__(kThreads) gdn_conv_step_kernel(const GdnConvArgs a)
 {
+    typedef typename Word<VEC * sizeof(E)>::type Vec;
     const int c0 = (blockIdx.y * kThreads + threadIdx.x) * VEC;
     if (c0 >= a.channels) return;
     const int n = blockIdx.x;
-    float w[W][VEC], b[VEC], win[W][VEC];
-    ld_params<VEC, W>(a, c0, w, b);
     const int entry = state_entry(a.slots, n, a.pool, a.status);
     const E *in = static_cast<const E *>(a.state_in);
     const size_t at = entry < 0 ? 0 : (size_t)entry * (W - 1) * a.channels + c0;
+    Vec u[W];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-        if (in && entry >= 0) {
-            ld_vec<E, VEC>(in + at + (size_t)j * a.channels, win[j]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
-        }
+        u[j] = Vec();
+        if (in && entry >= 0) u[j] = *reinterpret_cast<const Vec *>(in + at + (size_t)j * a.channels);
     }
-    ld_vec<E, VEC>(static_cast<const E *>(a.x) + n * a.ld_x + c0, win[W - 1]);
+    u[W - 1] = *reinterpret_cast<const Vec *>(static_cast<const E *>(a.x) + n * a.ld_x + c0);
+    const Taps<VEC, W> taps(a, c0);
+    Lanes<VEC> win[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) win[j] = widen_lanes<E, VEC>(u[j]);
     float r[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        r[i] = b[i];
-#pragma unroll
-        for (int j = 0; j < W; ++j) r[i] = fmaf(w[j][i], win[j][i], r[i]);
-        if (a.act == GDN_ACT_SILU) r[i] = silu(r[i]);
-    }
+    taps.apply(win, a.act, r);
     st_vec<E, VEC>(static_cast<E *>(a.y) + n * a.ld_y + c0, r);
     if (entry >= 0) {
         E *out = static_cast<E *>(a.state_out);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            st_vec<E, VEC>(out + at + (size_t)j * a.channels, win[j + 1]);
+            *reinterpret_cast<Vec *>(out + at + (size_t)j * a.channels) = u[j + 1];
     }
 }
 
@@ -154,14 +202,18 @@ bool vector_rows(const GdnConvArgs &a)
 {
     constexpr int V = 16 / sizeof(E);
     return a.channels % V == 0 && a.ld_x % V == 0 && a.ld_y % V == 0 && aligned16(a.x) &&
-           aligned16(a.y) && aligned16(a.state_in) && aligned16(a.state_out);
+           aligned16(a.y) && aligned16(a.state_in) && aligned16(a.state_out) && aligned16(a.weight);
 }
 
 template <typename E, int VEC, int W>
 cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
 {
     const int blocks = (a.channels / VEC + (a.channels % VEC != 0) + kThreads - 1) / kThreads;
-    const int tl = 32;
+    // Tiles of 64 tokens re-read 5% of the rows (width 4); shorter ones when that
+    // would leave SMs without work.
+    const int64_t rows = a.cu_seqlens ? a.T : (int64_t)a.N * a.T;
+    int tl = 64;
+    while (tl > 16 && rows / tl * blocks < 1200) tl /= 2;
     const int tiles = a.T > tl ? (a.T + tl - 1) / tl : 1;
     const int64_t slots = a.cu_seqlens ? (int64_t)a.T / tl + a.N : (int64_t)a.N * tiles;
     gdn_conv_fwd_kernel<E, VEC, W><<<dim3((unsigned)slots, blocks), kThreads, 0, s>>>(a, tl, tiles);

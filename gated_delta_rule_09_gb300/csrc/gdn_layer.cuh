@@ -18,57 +18,213 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
     return __float2bfloat16_rn(x);
 }
 
-// VEC consecutive elements as floats: one 16-byte access for the widths the
-// vectorised kernels use (8 bf16 or 4 fp32), element by element otherwise.
-template <typename E, int VEC> struct alignas(VEC * sizeof(E)) Pack {
-    E v[VEC];
-};
+// N consecutive elements as one word, and its fp32 values.  N sizeof(E) is 2 to
+// 16 bytes, aligned to its size.
+template <int BYTES> struct Word;
+template <> struct Word<2> { typedef unsigned short type; };
+template <> struct Word<4> { typedef uint32_t type; };
+template <> struct Word<8> { typedef uint2 type; };
+template <> struct Word<16> { typedef uint4 type; };
 
-template <typename E, int VEC>
-__device__ __forceinline__ void ld_vec(const E *p, float (&x)[VEC])
+__device__ __forceinline__ void widen(unsigned short u, float (&x)[1])
 {
-    const Pack<E, VEC> u = *reinterpret_cast<const Pack<E, VEC> *>(p);
+    x[0] = __uint_as_float((uint32_t)u << 16);
+}
+__device__ __forceinline__ void widen_pair(uint32_t u, float &lo, float &hi)
+{
+    lo = __uint_as_float(u << 16);
+    hi = __uint_as_float(u & 0xffff0000u);
+}
+__device__ __forceinline__ void widen(uint32_t u, float (&x)[2]) { widen_pair(u, x[0], x[1]); }
+__device__ __forceinline__ void widen(uint2 u, float (&x)[4])
+{
+    widen_pair(u.x, x[0], x[1]);
+    widen_pair(u.y, x[2], x[3]);
+}
+__device__ __forceinline__ void widen(uint4 u, float (&x)[8])
+{
+    widen_pair(u.x, x[0], x[1]);
+    widen_pair(u.y, x[2], x[3]);
+    widen_pair(u.z, x[4], x[5]);
+    widen_pair(u.w, x[6], x[7]);
+}
+__device__ __forceinline__ void widen(uint32_t u, float (&x)[1]) { x[0] = __uint_as_float(u); }
+__device__ __forceinline__ void widen(uint2 u, float (&x)[2])
+{
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+}
+__device__ __forceinline__ void widen(uint4 u, float (&x)[4])
+{
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z);
+    x[3] = __uint_as_float(u.w);
+}
+
+__device__ __forceinline__ uint32_t narrow_pair(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void narrow(unsigned short &u, const float (&x)[1])
+{
+    u = (unsigned short)narrow_pair(x[0], 0.f);
+}
+__device__ __forceinline__ void narrow(uint2 &u, const float (&x)[4])
+{
+    u = make_uint2(narrow_pair(x[0], x[1]), narrow_pair(x[2], x[3]));
+}
+__device__ __forceinline__ void narrow(uint4 &u, const float (&x)[8])
+{
+    u = make_uint4(narrow_pair(x[0], x[1]), narrow_pair(x[2], x[3]), narrow_pair(x[4], x[5]),
+                   narrow_pair(x[6], x[7]));
+}
+__device__ __forceinline__ void narrow(uint32_t &u, const float (&x)[1]) { u = __float_as_uint(x[0]); }
+__device__ __forceinline__ void narrow(uint4 &u, const float (&x)[4])
+{
+    u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                   __float_as_uint(x[3]));
+}
+
+// N elements from memory as fp32 and back, in words of at most 16 bytes.
+template <typename E, int N> __device__ __forceinline__ void ld_vec(const E *p, float (&x)[N])
+{
+    if constexpr (N * sizeof(E) > 16) {
+        constexpr int H = N / 2;
+        float a[H], b[H];
+        ld_vec<E, H>(p, a);
+        ld_vec<E, H>(p + H, b);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = to_f(u.v[i]);
+        for (int i = 0; i < H; ++i) {
+            x[i] = a[i];
+            x[H + i] = b[i];
+        }
+    } else {
+        widen(*reinterpret_cast<const typename Word<N * sizeof(E)>::type *>(p), x);
+    }
 }
 
-template <typename E, int VEC>
-__device__ __forceinline__ void st_vec(E *p, const float (&x)[VEC])
+template <typename E, int N> __device__ __forceinline__ void st_vec(E *p, const float (&x)[N])
 {
-    Pack<E, VEC> u;
+    if constexpr (N * sizeof(E) > 16) {
+        constexpr int H = N / 2;
+        float a[H], b[H];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) u.v[i] = from_f<E>(x[i]);
-    *reinterpret_cast<Pack<E, VEC> *>(p) = u;
+        for (int i = 0; i < H; ++i) {
+            a[i] = x[i];
+            b[i] = x[H + i];
+        }
+        st_vec<E, H>(p, a);
+        st_vec<E, H>(p + H, b);
+    } else {
+        typename Word<N * sizeof(E)>::type u;
+        narrow(u, x);
+        *reinterpret_cast<typename Word<N * sizeof(E)>::type *>(p) = u;
+    }
 }
 
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
-
-// log(1 + e^v) = max(v, 0) + log1p(w) with w = e^-|v| in (0, 1].  log1p by the
-// series of 2 artanh(r), r = w / (2 + w) <= 1/3: nine odd terms leave less than
-// 2^-31 of the value, and small w keeps its relative precision, which
-// log(1 + w) would round away (a step size of 1e-3 would be off by 6e-5).
-__device__ __forceinline__ float softplus(float v)
-{
-    const float w = __expf(-fabsf(v));
-    const float r = __fdividef(w, 2.f + w), q = r * r;
-    float p = 1.f / 17.f;
-    p = fmaf(p, q, 1.f / 15.f);
-    p = fmaf(p, q, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    return fmaxf(v, 0.f) + 2.f * r * p;
-}
-
-// 2^v, flushing to zero like the rest of the library's fp32 arithmetic.
+// 2^v and 1 / v to 2 and 1 ulp, flushing subnormals like the rest of the
+// library's fp32 arithmetic.
 __device__ __forceinline__ float ex2(float v)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
     return y;
+}
+
+__device__ __forceinline__ float rcp(float v)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+    return y;
+}
+
+// Two fp32 operations in one instruction.
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pack2(float lo, float hi)
+{
+    f32x2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+
+__device__ __forceinline__ void unpack2(f32x2 v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ f32x2 dup2(float v) { return pack2(v, v); }
+
+__device__ __forceinline__ f32x2 ex2x2(f32x2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(ex2(a), ex2(b));
+}
+
+__device__ __forceinline__ f32x2 rcp2(f32x2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(rcp(a), rcp(b));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// v / (1 + e^-v).
+__device__ __forceinline__ float silu(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
+
+__device__ __forceinline__ f32x2 silu2(f32x2 v)
+{
+    return mul2(v, rcp2(add2(dup2(1.f), ex2x2(mul2(v, dup2(-kLog2e))))));
+}
+
+// log(1 + e^v) = max(v, 0) + log1p(w) with w = e^-|v| in (0, 1], and
+// log1p(w) = 2 artanh(r), r = w / (2 + w) <= 1/3.  2 artanh(r) / r as a
+// polynomial in r^2, interpolated at the Chebyshev nodes of [0, 1/9] (relative
+// error below 2^-26).  Small w keeps its relative precision, which
+// log(1 + w) would round away (a step size of 1e-3 would be off by 6e-5).
+__device__ __forceinline__ f32x2 softplus2(f32x2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    const f32x2 w = pack2(ex2(-kLog2e * fabsf(a)), ex2(-kLog2e * fabsf(b)));
+    const f32x2 r = mul2(w, rcp2(add2(dup2(2.f), w))), q = mul2(r, r);
+    f32x2 p = fma2(dup2(0.281746566f), q, dup2(0.27961418f));
+    p = fma2(p, q, dup2(0.400248528f));
+    p = fma2(p, q, dup2(0.66666317f));
+    p = fma2(p, q, dup2(2.f));
+    return fma2(r, p, pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+
+__device__ __forceinline__ float softplus(float v)
+{
+    float a, b;
+    unpack2(softplus2(dup2(v)), a, b);
+    return a;
 }
 
 // A sequence's tile of tokens, found from the block's tile slot.
@@ -139,6 +295,52 @@ __device__ __forceinline__ int state_entry(const int32_t *slots, int n, int pool
     return e < 0 ? -1 : e;
 }
 
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// Asynchronous copies to shared memory.
+__device__ __forceinline__ uint32_t smem_addr(const void *p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src)
+{
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(BYTES)
+                     : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Wait until at most PENDING of this thread's copy groups are in flight.
+template <int PENDING> __device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// A tensor copy of the box at column x (on a 16-byte boundary), row y of a
+// matrix, completing on `bar`.
+__device__ __forceinline__ void copy_box(void *dst, const void *map, int x, int y, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+
+// Barrier `id` between parts of a block: arrivals that do not wait, and waits.
+__device__ __forceinline__ void part_arrive(int id, int threads)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void part_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+inline bool aligned_to(const void *p, size_t al) { return reinterpret_cast<uintptr_t>(p) % al == 0; }
+inline bool aligned16(const void *p) { return aligned_to(p, 16); }
 
 }  // namespace gdn_layer

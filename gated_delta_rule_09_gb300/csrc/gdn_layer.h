@@ -59,6 +59,9 @@ struct GdnSsmArgs {
 // of piece slots the workspace holds.
 void gdn_ssm_plan(int N, int T, int channels, int d_state, bool packed, int asked, int *segment,
                   int64_t *piece_slots);
+constexpr int kScanChannels = 64;  // of one group, per block of the scan
+cudaError_t gdn_ssm_scan_bf16(const GdnSsmArgs &a, cudaStream_t s);
+cudaError_t gdn_ssm_scan_f32(const GdnSsmArgs &a, cudaStream_t s);
 cudaError_t gdn_launch_ssm_fwd(const GdnSsmArgs &a, cudaStream_t s, int *launches);
 cudaError_t gdn_launch_ssm_step(const GdnSsmArgs &a, cudaStream_t s);
 

@@ -1,0 +1,687 @@
+// Selective state space scan over prompts: the kernel and its launch, for one
+// element type (gdn_ssm_bf16.cu, gdn_ssm_f32.cu).
+//
+// Per channel c with d_state fp32 states, token by token:
+//
+//     h[s] = exp(d A[c, s]) h[s] + d B[t, s] x        y = sum_s C[t, s] h[s] + D x
+//
+// with d = softplus(delta + bias); exp is 2^(d A log2 e).
+//
+// What bounds the prompt kernel is arithmetic: per token, channel and state an
+// exponential (32 per clock and SM) and four fp32 operations (128 lanes per
+// clock), beside the shared-memory bytes that bring each lane its operands (128
+// per clock).  The work is split so that no pipe does what another can:
+//
+//  - Recurrence warps (4 per block, 16 channels each; 8 with half the states
+//    each when d_state > 64) do nothing but the recurrence.  A lane holds NS
+//    states of a pair of neighbouring channels, the operations on the pair in
+//    packed instructions.  y = C h is left to the tensor cores: the lanes' states
+//    are the A operand of an m16n8k8 product as they stand (rows = the warp's 16
+//    channels), its eight columns are the C of eight consecutive tokens, loaded
+//    once per eight tokens; of each token's product the one column of that token
+//    is kept.  That takes the place of the fourth fp32 operation, of a butterfly
+//    over the lanes of a channel and of most loads of C.
+//  - What is done once per token and channel is done by other warps.  Four
+//    prepare: they fetch tiles of kTile tokens into a ring, compute the softplus
+//    and hand over (d, d x) of a channel pair as one 16-byte word, beside B
+//    widened and doubled (packed operands as it stands) and C widened.  Four
+//    finish: D x, the gate and the store of y.  Two hand-over buffers alternate.
+//    The recurrence warps need most registers, so they take over what the others
+//    leave of the block's.
+//  - Where the rows allow it the tiles are fetched by tensor copies, five per
+//    tile and one thread.  Copies of 16 bytes per thread (the other rows) kept
+//    the preparing warps busy for a third of their time; a bulk copy per row,
+//    80 per tile, took 38 clocks each.
+//
+// The tensor product takes tf32 operands (11 bits).  bf16 calls pass h as it is
+// (cut to 11 bits; C is exact): the sum over states is fp32 and y is stored in 8
+// bits.  fp32 calls split h and C into two such parts each and add the four
+// products, which leaves less than 2^-21.  The states themselves stay fp32.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "gdn_layer.h"
+#include "gdn_layer.cuh"
+#include "sm100_ptx.cuh"
+
+namespace {
+
+using namespace gdn_layer;
+
+constexpr uint64_t kWaitLimit = 2000000000;     // ns a wait for a copy may take,
+constexpr uint64_t kWaitAfterTimeout = 50000;   // and every later one once that ran out
+constexpr int kTile = 16;            // tokens handed over at a time
+constexpr int kPairs = 32;           // channel pairs per block: 4 warps of 8 pairs
+constexpr int kCols = kPairs / 4;    // 8-channel columns of a token row
+constexpr int kPrep = 128;           // preparing threads, and finishing ones: a column of a row each
+constexpr int kYPitch = kPairs / 2 + 1;  // 16-byte words between rows of y: rows 2 q fall on separate banks
+static_assert(kCols * kTile == kPrep && 2 * kPairs == kScanChannels, "a column of a row per thread");
+
+// Consecutive states (zeros past the end).
+template <int W> __device__ __forceinline__ void ld_state(const float *p, int s0, int ds, float (&h)[W])
+{
+#pragma unroll
+    for (int j = 0; j < W; ++j) h[j] = s0 + j < ds ? p[s0 + j] : 0.f;
+}
+
+template <int W> __device__ __forceinline__ void st_state(float *p, int s0, int ds, const float (&h)[W])
+{
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        if (s0 + j < ds) p[s0 + j] = h[j];
+}
+
+// What a launch over tiles of tokens does.  A call whose sequences are one
+// tile each is kWhole.  Cut into pieces, kPieces finds every piece's end state
+// (the first from the sequence's own state, the others from zero) and the sum
+// of its d, and kOutputs starts each piece from the states chained up to it:
+// a run of tokens takes h to exp(A sum d) h + (its end state from zero).  The
+// last piece's end state is not needed, and its place keeps the sequence's
+// start state instead: kOutputs writes the final state while the first piece
+// may still be starting, so in place that piece cannot read it from the pool.
+enum Mode { kWhole, kPieces, kOutputs };
+
+// How wide the copies into the ring can be.
+enum Width { kWide, kWord, kSingle };  // whole; 4 bytes; element by element
+
+// Threads and shared memory of one block of 64 channels.  The states are in H
+// parts, a lane has NS of a part: d_state is padded to 4 NS H.
+template <typename E, int NS, int H> struct Layout {
+    static constexpr int kRecur = 4 * kPairs * H;         // recurrence threads
+    static constexpr int kStates = 4 * NS * H;
+    static constexpr int kBC = kTile * kStates / 2;       // pairs of B (and of C) per tile
+    static constexpr int kRowElems = kTile * 2 * kPairs;
+    static constexpr int kRing = sizeof(E) * H > 4 ? 5 : 6;  // tiles of inputs held or on their way
+    static constexpr size_t kSlot = sizeof(E) * (3 * kRowElems + 4 * kBC);  // x, delta, z, B, C
+    static constexpr size_t kHandD = 16 * (size_t)kTile * kPairs;           // (d, d, d x, d x) per pair
+    static constexpr size_t kHandB = 16 * (size_t)kBC;                      // (b, b, b', b') per pair of B
+    static constexpr size_t kHandC = 8 * (size_t)kBC;                       // C
+    static constexpr size_t kPartY = 16 * (size_t)kTile * kYPitch;          // y per pair, from one part
+    static constexpr size_t kHand = kHandD + kHandB + kHandC + H * kPartY;
+    static constexpr size_t kBytes = kRing * kSlot + 2 * kHand + 8 * kRing;
+    static_assert(kBC % kPrep == 0 && kBytes <= 227 * 1024, "");
+};
+
+// The inputs as matrices of rows, for tensor copies of a tile's 64 channels (or
+// padded states) by kTile rows.
+struct Maps {
+    CUtensorMap x, delta, z, b, c;
+};
+
+// Place of a channel pair's word in a token row of a hand-over buffer, and of
+// its 8 bytes in a row of y: a preparing thread writes four neighbouring words
+// and a finishing one reads 2 x 16 bytes, which this spreads over the banks.
+__device__ __forceinline__ int place(int pair) { return pair ^ ((pair >> 3) & 3); }
+__device__ __forceinline__ int y_place(int pair) { return pair ^ ((pair >> 3) & 2); }
+
+// State i of lane quarter q in part `part`: runs of four, 16 apart.
+template <int NS> __device__ __forceinline__ int state_of(int part, int q, int i)
+{
+    return part * 4 * NS + 16 * (i / 4) + 4 * q + i % 4;
+}
+
+// N elements of a row, the first `valid` of them from memory, zeros after.
+template <typename E, int N>
+__device__ __forceinline__ void ring_copy(E *dst, const E *src, int valid, int width)
+{
+    constexpr int step = N * sizeof(E) < 16 ? N : 16 / sizeof(E), word = 4 / sizeof(E);
+    if (width == kWide && valid) {
+#pragma unroll
+        for (int i = 0; i < N; i += step) copy_async<step * sizeof(E)>(dst + i, src + i);
+    } else if (width == kWord && valid == N) {
+#pragma unroll
+        for (int i = 0; i < N; i += word) copy_async<4>(dst + i, src + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) dst[i] = i < valid ? src[i] : from_f<E>(0.f);
+    }
+}
+
+// d = a b + c on the tensor cores, tf32 operands (their upper 19 bits count),
+// fp32 accumulation.  Lane (g, q) = (lane / 4, lane % 4) gives a = rows g, g + 8
+// of columns q and q + 4 and b = rows q, q + 4 of column g, and holds d = rows
+// g, g + 8 of columns 2q, 2q + 1.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0,
+                                         float b1, const float (&c)[4])
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)),
+          "r"(__float_as_uint(a3)), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
+}
+
+// The part of v that a tf32 operand keeps.
+__device__ __forceinline__ float tf32_part(float v)
+{
+    return __uint_as_float(__float_as_uint(v) & 0xffffe000u);
+}
+
+template <typename E, int NS, int H, int MODE, bool BULK>
+__global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 && BULK ? 2 : 1)
+    gdn_ssm_fwd_kernel(const GdnSsmArgs a, const __grid_constant__ Maps maps, int tl, int tiles,
+                       unsigned slots, int row_width, int bc_width)
+{
+    using L = Layout<E, NS, H>;
+    constexpr int kRing = L::kRing, kRecur = L::kRecur;
+    extern __shared__ __align__(128) unsigned char smem[];
+    Span s;
+    const int64_t slot = blockIdx.x % slots;
+    if (!find_span(a.cu_seqlens, a.N, a.T, tl, slot, tiles, a.status, s)) return;
+    const int pieces = s.len > tl ? (s.len + tl - 1) / tl : 1;
+    if (MODE == kPieces && s.tile == pieces - 1) return;
+    const int t0 = s.tile * tl, t1 = min(s.len, t0 + tl);
+    const int ntiles = (t1 - t0 + kTile - 1) / kTile;
+    // the block's channels: [cbase, cend), all of one group
+    const int per_group = a.channels / a.groups;
+    const int blocks = (per_group + 2 * kPairs - 1) / (2 * kPairs);
+    const int chunk = blockIdx.x / slots, g = chunk / blocks;
+    const int cbase = g * per_group + (chunk % blocks) * 2 * kPairs;
+    const int cend = min(cbase + 2 * kPairs, (g + 1) * per_group);
+
+    auto hand = [&](int k) { return smem + kRing * L::kSlot + (k & 1) * L::kHand; };
+    auto hand_b = [&](int k) { return hand(k) + L::kHandD; };
+    auto hand_c = [&](int k) { return hand(k) + L::kHandD + L::kHandB; };
+    auto part_y = [&](int k, int part) { return hand(k) + L::kHandD + L::kHandB + L::kHandC + part * L::kPartY; };
+    auto next = [](int at) { return at + 1 == kRing ? 0 : at + 1; };
+    uint64_t *landed = reinterpret_cast<uint64_t *>(smem + kRing * L::kSlot + 2 * L::kHand);  // per ring slot
+    uint64_t limit = kWaitLimit;
+    auto wait_for = [&](int at, int round) {  // the bulk copies of ring slot `at`, its `round`th use
+        if (!sm100::mbar_wait(&landed[at], round & 1, limit)) {
+            atomicOr(a.status, GDN_DEV_WAIT_TIMEOUT);
+            limit = kWaitAfterTimeout;
+        }
+    };
+    if (BULK) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < kRing; ++i) sm100::mbar_init(&landed[i], 1);
+            sm100::fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    // Barriers.  Of hand-over buffer i: kFull + i, prepared (prepare -> recurrence); kDone + i,
+    // read, and y written (recurrence -> prepare, finish).  kFree: y read and the ring slot with
+    // it (finish -> prepare).  kPieces has no finishing warps.
+    enum { kFull = 1, kDone = 3, kFree = 5 };
+    constexpr int kFullN = kRecur + kPrep, kDoneN = MODE == kPieces ? kRecur + kPrep : kRecur + 2 * kPrep;
+
+    // Two blocks of 384 threads leave 80 registers each: 112 for the recurrence warps, 64 for
+    // the other eight (112 + 2 x 64 = 3 x 80).
+    constexpr bool kSplit = NS == 4 && BULK && MODE != kPieces;
+
+    if (threadIdx.x < kRecur) {  // ---- recurrence
+        if (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+        const int part = H == 1 ? 0 : threadIdx.x / (4 * kPairs);
+        const int q = threadIdx.x & 3, pair = (threadIdx.x >> 2) & (kPairs - 1);
+        const int tok = pair & 7, c = cbase + 2 * pair, ds = a.d_state;
+        const int entry = state_entry(a.slots, s.n, a.pool, a.status);
+        const int64_t slot0 = slot - s.tile;  // the sequence's first piece
+        f32x2 h[NS], A[NS], dsum = 0;
+#pragma unroll
+        for (int i = 0; i < NS; i += 4) {
+            const int s0 = state_of<NS>(part, q, i);
+            float hv[2][4], Av[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) hv[j][u] = Av[j][u] = 0.f;
+                if (c + j >= cend) continue;
+                auto piece = [&](int64_t k) { return a.piece_state + ((size_t)k * a.channels + c + j) * ds; };
+                ld_state(a.A + (size_t)(c + j) * ds, s0, ds, Av[j]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) Av[j][u] *= kLog2e;
+                if (MODE == kOutputs && pieces > 1) {
+                    ld_state(piece(s.tile == 0 ? slot0 + pieces - 1 : slot0), s0, ds, hv[j]);
+                    for (int k = 1; k < s.tile; ++k) {
+                        const float sum = a.piece_delta[(size_t)(slot0 + k) * a.channels + c + j];
+                        float e[4];
+                        ld_state(piece(slot0 + k), s0, ds, e);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) hv[j][u] = fmaf(ex2(sum * Av[j][u]), hv[j][u], e[u]);
+                    }
+                } else if (s.tile == 0 && a.state_in && entry >= 0) {
+                    ld_state(a.state_in + ((size_t)entry * a.channels + c + j) * ds, s0, ds, hv[j]);
+                }
+                if (MODE == kPieces && s.tile == 0) st_state(piece(slot0 + pieces - 1), s0, ds, hv[j]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                h[i + u] = pack2(hv[0][u], hv[1][u]);
+                A[i + u] = pack2(Av[0][u], Av[1][u]);
+            }
+        }
+        constexpr int kRuns = L::kStates / 16;  // runs of B words per token: [run][2][q]
+        // A warp has its scheduler nearly to itself, so it covers its own latencies: a token's
+        // words are loaded and its decays computed (kAhead) while the token before goes through
+        // the states, and its y is picked up one token later.  With more states per lane there is
+        // as much to overlap within a token, and no registers for this.
+        constexpr int kAhead = NS == 4 ? 1 : 0;
+        for (int k = 0; k < ntiles; ++k) {
+            const ulonglong2 *dx = reinterpret_cast<const ulonglong2 *>(hand(k)) + place(pair);
+            const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(hand_b(k)) + part * 2 * NS + q;
+            const float4 *C = reinterpret_cast<const float4 *>(hand_c(k)) +
+                              (tok * L::kStates + state_of<NS>(part, q, 0)) / 4;
+            unsigned char *yout = part_y(k, part) + 8 * y_place(pair) + 32 * q * kYPitch;
+            ulonglong2 dv[2 + kAhead], bv[2 + kAhead][NS == 4 ? 2 : 1];
+            f32x2 e[1 + kAhead][NS], w[1 + kAhead][NS], tile_sum = 0;
+            float C1[NS], C2[sizeof(E) == 4 ? NS : 1], acc[2][2][4], keep[4];
+            auto word = [&](int t, int i) { return B[((t * kRuns + i / 4) * 2 + i % 4 / 2) * 4]; };
+            auto load = [&](int t) {
+                dv[t % (2 + kAhead)] = dx[t * kPairs];  // d, d x
+#pragma unroll
+                for (int i = 0; i < (NS == 4 ? 4 : 0); i += 2) bv[t % (2 + kAhead)][i / 2] = word(t, i);
+            };
+            auto decay = [&](int t) {
+                const ulonglong2 v = dv[t % (2 + kAhead)];
+                const int p = t % (1 + kAhead);
+                if (MODE == kPieces) tile_sum = add2(tile_sum, v.x);
+#pragma unroll
+                for (int i = 0; i < NS; i += 2) {
+                    const ulonglong2 bb = NS == 4 ? bv[t % (2 + kAhead)][NS == 4 ? i / 2 : 0] : word(t, i);
+                    e[p][i] = ex2x2(mul2(v.x, A[i]));
+                    e[p][i + 1] = ex2x2(mul2(v.x, A[i + 1]));
+                    w[p][i] = mul2(v.y, bb.x);
+                    w[p][i + 1] = mul2(v.y, bb.y);
+                }
+            };
+            auto pick = [&](int t) {  // of token t's product, column t % 8: lanes q = t % 8 / 2
+                const float(*d)[4] = acc[t & 1];
+                if (q == t % 8 / 2) {
+                    keep[t & 1] = d[0][t & 1] + d[1][t & 1];
+                    keep[2 + (t & 1)] = d[0][2 + (t & 1)] + d[1][2 + (t & 1)];
+                }
+                if (t % 8 == 7)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)  // a lane has tokens 2 q and 2 q + 1 of the eight
+                        *reinterpret_cast<f32x2 *>(yout + (t - 7 + j) * 16 * kYPitch) = pack2(keep[j], keep[2 + j]);
+            };
+            part_sync(kFull + (k & 1), kFullN);
+            load(0);
+            if (kAhead) {
+                load(1);
+                decay(0);
+            }
+#pragma unroll
+            for (int t = 0; t < kTile; ++t) {
+                if (MODE != kPieces && t % 8 == 0) {
+                    // C of token t + tok; for fp32 calls, also what 11 bits leave over of it
+#pragma unroll
+                    for (int i = 0; i < NS; i += 4) {
+                        const float4 c4 = C[(t * L::kStates + 4 * i) / 4];
+                        const float v[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            C1[i + u] = v[u];
+                            if (sizeof(E) == 4) {
+                                C1[i + u] = tf32_part(v[u]);
+                                C2[i + u] = v[u] - C1[i + u];
+                            }
+                        }
+                    }
+                }
+                if (t + 1 + kAhead < kTile) load(t + 1 + kAhead);
+                if (t + kAhead < kTile) decay(t + kAhead);
+#pragma unroll
+                for (int i = 0; i < NS; ++i) h[i] = fma2(e[t % (1 + kAhead)][i], h[i], w[t % (1 + kAhead)][i]);
+                if (MODE == kPieces) continue;
+                // two sums, so that the products do not wait for one another
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[t & 1][i][u] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NS; i += 2) {  // columns q and q + 4: states i, i + 1
+                    float(&d)[4] = acc[t & 1][i / 2 % 2];
+                    float h0, h1, h2, h3;
+                    unpack2(h[i], h0, h1);
+                    unpack2(h[i + 1], h2, h3);
+                    if (sizeof(E) == 4) {
+                        const float p0 = tf32_part(h0), p1 = tf32_part(h1), p2 = tf32_part(h2), p3 = tf32_part(h3);
+                        mma_tf32(d, h0 - p0, h1 - p1, h2 - p2, h3 - p3, C2[i], C2[i + 1], d);
+                        mma_tf32(d, h0 - p0, h1 - p1, h2 - p2, h3 - p3, C1[i], C1[i + 1], d);
+                        mma_tf32(d, p0, p1, p2, p3, C2[i], C2[i + 1], d);
+                        mma_tf32(d, p0, p1, p2, p3, C1[i], C1[i + 1], d);
+                    } else {
+                        mma_tf32(d, h0, h1, h2, h3, C1[i], C1[i + 1], d);
+                    }
+                }
+                if (t > 0) pick(t - 1);
+            }
+            if (MODE == kPieces)
+                dsum = add2(dsum, tile_sum);
+            else
+                pick(kTile - 1);
+            part_arrive(kDone + (k & 1), kDoneN);
+        }
+        float d1[2];
+        unpack2(dsum, d1[0], d1[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (c + j >= cend) continue;
+            float *out = nullptr;
+            if (MODE == kPieces) {
+                out = a.piece_state + ((size_t)slot * a.channels + c + j) * ds;
+                if (q == 0 && part == 0) a.piece_delta[(size_t)slot * a.channels + c + j] = d1[j];
+            } else if (s.tile == pieces - 1 && a.state_out && entry >= 0) {
+                out = a.state_out + ((size_t)entry * a.channels + c + j) * ds;
+            }
+            if (!out) continue;
+#pragma unroll
+            for (int i = 0; i < NS; i += 4) {
+                float v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float lo, hi;
+                    unpack2(h[i + u], lo, hi);
+                    v[u] = j ? hi : lo;
+                }
+                st_state(out, state_of<NS>(part, q, i), ds, v);
+            }
+        }
+        return;
+    }
+
+    if (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // ---- prepare and finish: a thread has one 8-channel column of one row of every tile
+    const int id = threadIdx.x & (kPrep - 1), col = id % kCols, row = id / kCols;
+    const int c = cbase + 8 * col, nc = max(0, min(8, cend - c)), off = id * 8;
+    const int rows = nc > 0 ? t1 - t0 - row : 0;  // this thread's rows are those of tiles k with 16 k < rows
+    const int64_t first = s.row + t0, mine = first + (rows > 0 ? row : 0);
+    const int cc = nc > 0 ? c : cbase;
+    auto column = [&](const float *p, f32x2 (&v)[4]) {  // of a vector over channels
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = pack2(p && 2 * i < nc ? p[c + 2 * i] : 0.f, p && 2 * i + 1 < nc ? p[c + 2 * i + 1] : 0.f);
+    };
+
+    if (MODE != kPieces && threadIdx.x >= kRecur + kPrep) {  // ---- finish
+        f32x2 D[4];
+        column(a.D, D);
+        E *out = static_cast<E *>(a.y) + mine * a.ld_y + cc;
+        for (int k = 0, at = 0, round = 0; k < ntiles; ++k, at = next(at), round += at == 0) {
+            const E *r = reinterpret_cast<const E *>(smem + at * L::kSlot);
+            float x[8], z[8];
+            ulonglong2 sum[2];
+            if (BULK) wait_for(at, round);
+            part_sync(kDone + (k & 1), kDoneN);
+            ld_vec<E, 8>(r + off, x);
+            if (a.z) ld_vec<E, 8>(r + 2 * L::kRowElems + off, z);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int w = row * kYPitch + y_place(4 * col + 2 * j) / 2;
+                sum[j] = reinterpret_cast<const ulonglong2 *>(part_y(k, 0))[w];
+                if (H == 2) {
+                    const ulonglong2 more = reinterpret_cast<const ulonglong2 *>(part_y(k, 1))[w];
+                    sum[j] = make_ulonglong2(add2(sum[j].x, more.x), add2(sum[j].y, more.y));
+                }
+            }
+            part_arrive(kFree, 2 * kPrep);
+            if (k * kTile < rows) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x2 v = fma2(D[i], pack2(x[2 * i], x[2 * i + 1]), i % 2 ? sum[i / 2].y : sum[i / 2].x);
+                    if (a.z) v = mul2(v, silu2(pack2(z[2 * i], z[2 * i + 1])));
+                    unpack2(v, y[2 * i], y[2 * i + 1]);
+                }
+                if (BULK || row_width == kWide) {
+                    st_vec<E, 8>(out, y);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < nc) out[i] = from_f<E>(y[i]);
+                }
+                out += kTile * a.ld_y;
+            }
+        }
+        return;
+    }
+
+    // ---- prepare
+    f32x2 bias[4];
+    column(a.delta_bias, bias);
+    // pair p = id + i kPrep of B and C of a tile: a token's states 2 (p % kHalf) and the next, and
+    // where the recurrence wants B (state_of, [run][2][q])
+    constexpr int kHalf = L::kStates / 2, kPer = L::kBC / kPrep, kTokStep = kPrep / kHalf;
+    const int st = 2 * (id % kHalf), tok0 = id / kHalf;
+    const int b_word = (st / 16 * 2 + st % 4 / 2) * 4 + st % 16 / 4;
+    const int ns = max(0, min(2, a.d_state - st));
+    const int64_t channel = (int64_t)g * a.d_state;
+
+    // Copies per thread: what it copies next; rows past the end are never read
+    // (their address stays on the piece's first row).
+    const E *x_in = nullptr, *d_in = nullptr, *z_in = nullptr, *b_in = nullptr, *c_in = nullptr;
+    if (!BULK) {
+        x_in = static_cast<const E *>(a.x) + mine * a.ld_x + cc;
+        d_in = static_cast<const E *>(a.delta) + mine * a.ld_delta + cc;
+        z_in = a.z ? static_cast<const E *>(a.z) + mine * a.ld_z + cc : nullptr;
+        b_in = static_cast<const E *>(a.Bm) + first * a.ld_b + channel + (ns > 0 ? st : 0);
+        c_in = static_cast<const E *>(a.Cm) + first * a.ld_c + channel + (ns > 0 ? st : 0);
+    }
+
+    auto issue = [&](int k, int at) {  // tile k into ring slot `at`
+        if (BULK) {
+            if (id != 0 || k >= ntiles) return;
+            // whole boxes: rows past the piece's end are another's or zeros, and masked later
+            constexpr int kX = L::kRowElems * sizeof(E), kB = 2 * L::kBC * sizeof(E);
+            unsigned char *r = smem + at * L::kSlot;
+            const int y = (int)(first + k * kTile), sc = g * a.d_state;
+            sm100::mbar_arrive_expect_tx(&landed[at],
+                                         MODE == kPieces ? 2 * kX + kB : (a.z ? 3 : 2) * kX + 2 * kB);
+            copy_box(r, &maps.x, cbase, y, &landed[at]);
+            copy_box(r + kX, &maps.delta, cbase, y, &landed[at]);
+            copy_box(r + 3 * kX, &maps.b, sc, y, &landed[at]);
+            if (MODE == kPieces) return;
+            copy_box(r + 3 * kX + kB, &maps.c, sc, y, &landed[at]);
+            if (a.z) copy_box(r + 2 * kX, &maps.z, cbase, y, &landed[at]);
+            return;
+        }
+        if (k < ntiles) {
+            E *r = reinterpret_cast<E *>(smem + at * L::kSlot);
+            const int valid = k * kTile < rows ? nc : 0;
+            ring_copy<E, 8>(r + off, x_in, valid, row_width);
+            ring_copy<E, 8>(r + L::kRowElems + off, d_in, valid, row_width);
+            if (MODE != kPieces && a.z) ring_copy<E, 8>(r + 2 * L::kRowElems + off, z_in, valid, row_width);
+            E *rb = r + 3 * L::kRowElems + 2 * id, *rc = rb + 2 * L::kBC;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int t = tok0 + i * kTokStep, n = k * kTile + t < t1 - t0 ? ns : 0;
+                ring_copy<E, 2>(rb + 2 * i * kPrep, b_in + t * a.ld_b, n, bc_width);
+                if (MODE != kPieces) ring_copy<E, 2>(rc + 2 * i * kPrep, c_in + t * a.ld_c, n, bc_width);
+            }
+            if ((k + 1) * kTile < rows) {
+                x_in += kTile * a.ld_x;
+                d_in += kTile * a.ld_delta;
+                z_in += kTile * a.ld_z;
+            }
+            b_in += kTile * a.ld_b;
+            c_in += kTile * a.ld_c;
+        }
+        copy_commit();  // one group per tile, so that a group's number is its tile's
+    };
+
+    // Tile k from ring slot `at` into its hand-over buffer.  `edge`: rows past the end or padded
+    // states, where the ring may hold anything, are set to zero.
+    auto prepare_as = [&](int k, int at, auto edge) {
+        constexpr bool kEdge = decltype(edge)::value;
+        const E *r = reinterpret_cast<const E *>(smem + at * L::kSlot);
+        float x[8], d[8];
+        ld_vec<E, 8>(r + L::kRowElems + off, d);
+        ld_vec<E, 8>(r + off, x);
+        ulonglong2 *dx = reinterpret_cast<ulonglong2 *>(hand(k)) + row * kPairs;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x2 v = add2(pack2(d[2 * i], d[2 * i + 1]), bias[i]);
+            if (a.softplus) v = softplus2(v);
+            ulonglong2 word = make_ulonglong2(v, mul2(v, pack2(x[2 * i], x[2 * i + 1])));
+            if (kEdge && k * kTile >= rows) word = make_ulonglong2(0, 0);  // exp(0) h + 0
+            dx[place(4 * col + i)] = word;
+        }
+        const E *rb = r + 3 * L::kRowElems + 2 * id, *rc = rb + 2 * L::kBC;
+        float4 *B = reinterpret_cast<float4 *>(hand_b(k)) + tok0 * kHalf + b_word;
+        float2 *C = reinterpret_cast<float2 *>(hand_c(k)) + id;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int n = !kEdge || k * kTile + tok0 + i * kTokStep < t1 - t0 ? ns : 0;
+            float v[2];
+            ld_vec<E, 2>(rb + 2 * i * kPrep, v);
+            if (kEdge && n < 1) v[0] = 0.f;
+            if (kEdge && n < 2) v[1] = 0.f;
+            B[i * kPrep] = make_float4(v[0], v[0], v[1], v[1]);
+            if (MODE == kPieces) continue;
+            ld_vec<E, 2>(rc + 2 * i * kPrep, v);
+            if (kEdge && n < 1) v[0] = 0.f;
+            if (kEdge && n < 2) v[1] = 0.f;
+            C[i * kPrep] = make_float2(v[0], v[1]);
+        }
+    };
+    auto prepare = [&](int k, int at) {
+        if ((k + 1) * kTile <= t1 - t0 && a.d_state == L::kStates && cend - cbase == 2 * kPairs)
+            prepare_as(k, at, std::false_type());
+        else
+            prepare_as(k, at, std::true_type());
+    };
+
+#pragma unroll 1
+    for (int k = 0; k < kRing; ++k) issue(k, k);
+    if (ntiles > 0) {
+        if (BULK) wait_for(0, 0); else copy_wait<kRing - 1>();
+        prepare(0, 0);
+        part_arrive(kFull, kFullN);
+    }
+    if (ntiles > 1) {
+        if (BULK) wait_for(1, 0); else copy_wait<kRing - 2>();
+        prepare(1, 1);
+        part_arrive(kFull + 1, kFullN);
+    }
+#pragma unroll 1
+    for (int k = 0, done = 0, ahead = 2, round = 0; k < ntiles; ++k, done = next(done), ahead = next(ahead)) {
+        round += ahead == 0;
+        if (k + 2 < ntiles) {
+            if (BULK) wait_for(ahead, round); else copy_wait<kRing - 3>();
+        }
+        part_sync(kDone + (k & 1), kDoneN);
+        if (k + 2 < ntiles) prepare(k + 2, ahead);
+        if (MODE != kPieces) part_sync(kFree, 2 * kPrep);
+        if (k + 2 < ntiles) part_arrive(kFull + (k & 1), kFullN);
+        issue(k + kRing, done);
+    }
+}
+
+// Copy widths into the ring: 16 bytes when whole 8-channel columns start on
+// 16-byte boundaries in every matrix, 4 bytes when bf16 pairs are aligned (fp32
+// elements always are).
+template <typename E> int row_width(const GdnSsmArgs &a)
+{
+    const int per_group = a.channels / a.groups;
+    const void *p[] = {a.x, a.delta, a.y, a.z};
+    const int64_t ld[] = {a.ld_x, a.ld_delta, a.ld_y, a.z ? a.ld_z : 0};
+    bool wide = per_group % 8 == 0, word = per_group % (4 / sizeof(E)) == 0;
+    for (int i = 0; i < 4; ++i) {
+        wide = wide && aligned16(p[i]) && ld[i] * sizeof(E) % 16 == 0;
+        word = word && aligned_to(p[i], 4) && ld[i] * sizeof(E) % 4 == 0;
+    }
+    return wide ? kWide : word ? kWord : kSingle;
+}
+
+template <typename E> int bc_width(const GdnSsmArgs &a)
+{
+    return a.d_state % 2 == 0 && a.ld_b % 2 == 0 && a.ld_c % 2 == 0 && aligned_to(a.Bm, 2 * sizeof(E)) &&
+                   aligned_to(a.Cm, 2 * sizeof(E))
+               ? kWide
+               : kSingle;
+}
+
+// Tensor copies want a matrix and its rows on 16-byte boundaries, boxes that
+// start on them, and row numbers of 31 bits.
+template <typename E> bool box_rows(const GdnSsmArgs &a)
+{
+    const int64_t rows = a.cu_seqlens ? a.T : (int64_t)a.N * a.T;
+    return row_width<E>(a) == kWide && a.d_state * sizeof(E) % 16 == 0 && a.ld_b * sizeof(E) % 16 == 0 &&
+           a.ld_c * sizeof(E) % 16 == 0 && aligned16(a.Bm) && aligned16(a.Cm) && rows > 0 &&
+           rows <= 0x7fffffff - kTile;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;  // the same for every thread
+    if (!fn) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+template <typename E> bool make_maps(const GdnSsmArgs &a, int states, Maps *m)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
+    if (!encode) return false;
+    const cuuint64_t rows = a.cu_seqlens ? a.T : (cuuint64_t)a.N * a.T;
+    auto map = [&](CUtensorMap *to, const void *p, int64_t ld, int columns, int box_columns) {
+        const cuuint64_t dims[2] = {(cuuint64_t)columns, rows}, strides[1] = {(cuuint64_t)ld * sizeof(E)};
+        const cuuint32_t box[2] = {(cuuint32_t)box_columns, kTile}, steps[2] = {1, 1};
+        return encode(to, sizeof(E) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                      2, const_cast<void *>(p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return map(&m->x, a.x, a.ld_x, a.channels, 2 * kPairs) &&
+           map(&m->delta, a.delta, a.ld_delta, a.channels, 2 * kPairs) &&
+           (!a.z || map(&m->z, a.z, a.ld_z, a.channels, 2 * kPairs)) &&
+           map(&m->b, a.Bm, a.ld_b, a.groups * a.d_state, states) &&
+           map(&m->c, a.Cm, a.ld_c, a.groups * a.d_state, states);
+}
+
+template <typename E, int NS, int H, int MODE, bool BULK>
+cudaError_t launch_mode(const GdnSsmArgs &a, const Maps &maps, int tl, int tiles, int64_t slots, cudaStream_t s)
+{
+    using L = Layout<E, NS, H>;
+    const int per_group = a.channels / a.groups;
+    const int64_t grid = slots * a.groups * ((per_group + 2 * kPairs - 1) / (2 * kPairs));
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(gdn_ssm_fwd_kernel<E, NS, H, MODE, BULK>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
+    if (e != cudaSuccess) return e;
+    gdn_ssm_fwd_kernel<E, NS, H, MODE, BULK><<<(unsigned)grid, L::kRecur + (MODE == kPieces ? 1 : 2) * kPrep, L::kBytes, s>>>(
+        a, maps, tl, tiles, (unsigned)slots, row_width<E>(a), bc_width<E>(a));
+    return cudaGetLastError();
+}
+
+template <typename E, int NS, int H, bool BULK> cudaError_t launch_modes(const GdnSsmArgs &a, cudaStream_t s)
+{
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (BULK && !make_maps<E>(a, Layout<E, NS, H>::kStates, &maps)) return cudaErrorInvalidValue;
+    if (a.segment) {
+        const int tiles = (a.T + a.segment - 1) / a.segment;
+        const cudaError_t e = launch_mode<E, NS, H, kPieces, BULK>(a, maps, a.segment, tiles, a.pieces, s);
+        return e != cudaSuccess ? e : launch_mode<E, NS, H, kOutputs, BULK>(a, maps, a.segment, tiles, a.pieces, s);
+    }
+    const int tl = a.T > 0 ? a.T : 1;
+    return launch_mode<E, NS, H, kWhole, BULK>(a, maps, tl, 1, a.cu_seqlens ? a.T / tl + a.N : a.N, s);
+}
+
+template <typename E, int NS, int H> cudaError_t launch_fwd(const GdnSsmArgs &a, cudaStream_t s)
+{
+    return box_rows<E>(a) ? launch_modes<E, NS, H, true>(a, s) : launch_modes<E, NS, H, false>(a, s);
+}
+
+template <typename E> cudaError_t scan(const GdnSsmArgs &a, cudaStream_t s)
+{
+    if (a.d_state <= 16) return launch_fwd<E, 4, 1>(a, s);
+    if (a.d_state <= 32) return launch_fwd<E, 8, 1>(a, s);
+    if (a.d_state <= 64) return launch_fwd<E, 16, 1>(a, s);
+    return launch_fwd<E, 16, 2>(a, s);
+}
+
+}  // namespace

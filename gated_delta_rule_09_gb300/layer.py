@@ -8,9 +8,6 @@ parameters are contiguous fp32.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
-
 import torch
 
 from . import _lib
@@ -28,32 +25,34 @@ def _cuda(name, t):
         raise TypeError("%s must be a CUDA tensor" % name)
 
 
-def _on(name, t, dtype, device):
-    _cuda(name, t)
-    if t.dtype != dtype:
+def _on(name, t, dtype, index):
+    """Type and device (by number) of an argument; x's are those of the call."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, x on %s" % (name, t.device, device))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, x on device %d" % (name, t.device, index))
 
 
-def _param(name, t, dtype, device, shape):
-    """A contiguous parameter or state of the given shape (None allowed)."""
-    if t is None:
-        return
-    _on(name, t, dtype, device)
+def _param(name, t, dtype, index, shape):
+    """A contiguous parameter or state of the given shape."""
+    _on(name, t, dtype, index)
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
 
 
-def _rows(name, t, dtype, device, shape, inner=1):
+def _rows(name, t, dtype, index, shape, inner=1):
     """Row stride in elements of a matrix argument whose last ``inner``
     dimensions are a row and whose others count rows one stride apart."""
-    _on(name, t, dtype, device)
+    _on(name, t, dtype, index)
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    size, stride = t.shape, t.stride()
+    if t.is_contiguous():
+        return shape[-1] if inner == 1 else shape[-1] * shape[-2]
+    size, stride = shape, t.stride()
     width = 1
     for k in range(len(size) - 1, len(size) - 1 - inner, -1):
         if size[k] > 1 and stride[k] != width:
@@ -61,8 +60,6 @@ def _rows(name, t, dtype, device, shape, inner=1):
         width *= size[k]
     ld, rows = width, 1
     for k in range(len(size) - 1 - inner, -1, -1):
-        if size[k] == 0:
-            return width
         if size[k] > 1:
             if rows == 1:
                 ld = stride[k]
@@ -74,20 +71,33 @@ def _rows(name, t, dtype, device, shape, inner=1):
     return ld
 
 
-def _stream(stream, device):
-    """(raw handle, context in which to allocate for it): what a call allocates
-    belongs to the stream that its kernels run on."""
+def _empty(stream, like, shape=None, dtype=None):
+    """A new tensor that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream, contextlib.nullcontext()
+        if shape is None:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return _empty(None, like, shape, dtype)
 
 
-def _device(device):
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _handle(stream, index):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _call(fn, index, *args):
+    """One library call on the device of its tensors."""
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args)
+    if status:
+        _lib.check(status)
 
 
 def _act(act):
@@ -97,20 +107,22 @@ def _act(act):
 
 
 def _first(x, dims, layout):
-    """Checks of the argument that fixes type, device and sizes."""
+    """The argument that fixes sizes, type and device: (shape, dtype, device number)."""
     _cuda("x", x)
-    if x.dtype not in _DTYPES:
-        raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
+    dtype = x.dtype
+    if dtype not in _DTYPES:
+        raise TypeError("x must be float32 or bfloat16, got %s" % dtype)
     if x.dim() != dims:
         raise ValueError("x must be %s" % layout)
+    return x.shape, dtype, x.get_device()
 
 
-def _sequences(x, cu_seqlens):
+def _sequences(shape, cu_seqlens, index):
     """Number of sequences of a prompt call and tokens per sequence (or of the pack)."""
-    B, T = x.shape[:2]
+    B, T = shape[:2]
     if cu_seqlens is None:
         return B, T
-    _on("cu_seqlens", cu_seqlens, torch.int32, x.device)
+    _on("cu_seqlens", cu_seqlens, torch.int32, index)
     if B != 1:
         raise ValueError("packed (cu_seqlens) inputs must have B == 1")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or not cu_seqlens.is_contiguous():
@@ -118,12 +130,12 @@ def _sequences(x, cu_seqlens):
     return cu_seqlens.numel() - 1, T
 
 
-def _states(state_in, state_out, slots, N, entry, dtype, device, want, alloc):
+def _states(state_in, state_out, slots, N, entry, dtype, index, want, x, stream):
     """Checked pools and the number of their entries; ``state_out`` is filled
     in: the pool itself in place when slots address it, else a new tensor."""
     pool = N
     if slots is not None:
-        _param("slots", slots, torch.int32, device, (N,))
+        _param("slots", slots, torch.int32, index, (N,))
         given = state_in if state_in is not None else state_out
         if given is None:
             if want:
@@ -133,22 +145,23 @@ def _states(state_in, state_out, slots, N, entry, dtype, device, want, alloc):
             raise ValueError("a pool of states must be [pool, %s]" % ", ".join(map(str, entry)))
         pool = given.shape[0]
     shape = (pool,) + entry
-    _param("state_in", state_in, dtype, device, shape)
-    _param("state_out", state_out, dtype, device, shape)
-    if state_out is None and want:
-        if slots is not None:
-            state_out = state_in
-        else:
-            with alloc:
-                state_out = torch.empty(shape, dtype=dtype, device=device)
+    if state_in is not None:
+        _param("state_in", state_in, dtype, index, shape)
+    if state_out is not None:
+        _param("state_out", state_out, dtype, index, shape)
+    elif want:
+        state_out = state_in if slots is not None else _empty(stream, x, shape, dtype)
     return state_out, pool
 
 
-def _out(name, y, x, alloc):
-    if y is None:
-        with alloc:
-            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    return y
+def _taps(weight, bias, C, index):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [C,W]")
+    W = weight.shape[1]
+    _param("weight", weight, torch.float32, index, (C, W))
+    if bias is not None:
+        _param("bias", bias, torch.float32, index, (C,))
+    return W
 
 
 def gdn_conv_fwd(x, weight, bias=None, state_in=None, y=None, state_out=None, slots=None,
@@ -164,27 +177,22 @@ def gdn_conv_fwd(x, weight, bias=None, state_in=None, y=None, state_out=None, sl
     updated in place unless ``state_out`` is another pool.  ``cu_seqlens``
     (int32 [N+1]) packs N sequences into B == 1.  ``act`` is "silu" or "none".
     """
-    _first(x, 3, "[B,T,C]")
-    C, dev = x.shape[2], x.device
-    N, T = _sequences(x, cu_seqlens)
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
-        raise ValueError("weight must be [C,W]")
-    W = weight.shape[1]
-    _param("weight", weight, torch.float32, dev, (C, W))
-    _param("bias", bias, torch.float32, dev, (C,))
+    shape, dtype, index = _first(x, 3, "[B,T,C]")
+    C = shape[2]
+    N, T = _sequences(shape, cu_seqlens, index)
+    W = _taps(weight, bias, C, index)
+    ld_x = _rows("x", x, dtype, index, shape)
     code = _act(act)
-    handle, alloc = _stream(stream, dev)
-    ld_x = _rows("x", x, x.dtype, dev, x.shape)
-    lib = _lib.load()
-    with _device(dev):
-        state_out, pool = _states(state_in, state_out, slots, N, (W - 1, C), x.dtype, dev,
-                                  want_final_state, alloc)
-        y = _out("y", y, x, alloc)
-        ld_y = _rows("y", y, x.dtype, dev, x.shape)
-        _lib.check(lib.gdn_conv_fwd(
-            _ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(slots), _ptr(y),
-            _ptr(state_out), N, T, C, W, ld_x, ld_y, pool, _ptr(cu_seqlens), code,
-            _DTYPES[x.dtype], handle))
+    fn = _lib.load().gdn_conv_fwd
+    state_out, pool = _states(state_in, state_out, slots, N, (W - 1, C), dtype, index,
+                              want_final_state, x, stream)
+    if y is None:
+        y, ld_y = _empty(stream, x), C
+    else:
+        ld_y = _rows("y", y, dtype, index, shape)
+    _call(fn, index, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(slots), _ptr(y),
+          _ptr(state_out), N, T, C, W, ld_x, ld_y, pool, _ptr(cu_seqlens), code, _DTYPES[dtype],
+          _handle(stream, index))
     return y, state_out
 
 
@@ -192,43 +200,39 @@ def gdn_conv_step(x, weight, bias=None, state_in=None, y=None, state_out=None, s
                   act="silu", stream=None):
     """``gdn_conv_fwd`` for one new token per sequence: x, y [N,C]; returns
     ``(y, state_out)``.  States as there; ``state_out`` may be ``state_in``."""
-    _first(x, 2, "[N,C]")
-    (N, C), dev = x.shape, x.device
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
-        raise ValueError("weight must be [C,W]")
-    W = weight.shape[1]
-    _param("weight", weight, torch.float32, dev, (C, W))
-    _param("bias", bias, torch.float32, dev, (C,))
+    shape, dtype, index = _first(x, 2, "[N,C]")
+    N, C = shape
+    W = _taps(weight, bias, C, index)
+    ld_x = _rows("x", x, dtype, index, shape)
     code = _act(act)
-    handle, alloc = _stream(stream, dev)
-    ld_x = _rows("x", x, x.dtype, dev, x.shape)
-    lib = _lib.load()
-    with _device(dev):
-        state_out, pool = _states(state_in, state_out, slots, N, (W - 1, C), x.dtype, dev, True, alloc)
-        y = _out("y", y, x, alloc)
-        ld_y = _rows("y", y, x.dtype, dev, x.shape)
-        _lib.check(lib.gdn_conv_step(
-            _ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(slots), _ptr(y),
-            _ptr(state_out), N, C, W, ld_x, ld_y, pool, code, _DTYPES[x.dtype], handle))
+    fn = _lib.load().gdn_conv_step
+    state_out, pool = _states(state_in, state_out, slots, N, (W - 1, C), dtype, index, True, x, stream)
+    if y is None:
+        y, ld_y = _empty(stream, x), C
+    else:
+        ld_y = _rows("y", y, dtype, index, shape)
+    _call(fn, index, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(slots), _ptr(y),
+          _ptr(state_out), N, C, W, ld_x, ld_y, pool, code, _DTYPES[dtype], _handle(stream, index))
     return y, state_out
 
 
-def _ssm_params(x, delta, A, B, C, D, z, delta_bias):
-    """Checks shared by scan and step; returns (d_state, groups, row strides)."""
-    ch, dt, dev = x.shape[-1], x.dtype, x.device
+def _ssm_params(x, shape, dtype, index, delta, A, B, C, D, z, delta_bias):
+    """Checks shared by scan and step: (d_state, groups, row strides of x, delta, B, C, z)."""
+    ch = shape[-1]
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be [C,d_state]")
-    if not isinstance(B, torch.Tensor) or B.dim() != x.dim() + 1:
+    if not isinstance(B, torch.Tensor) or B.dim() != len(shape) + 1:
         raise ValueError("B and C must be [..., groups, d_state]")
     S, G = A.shape[1], B.shape[-2]
-    _param("A", A, torch.float32, dev, (ch, S))
-    _param("D", D, torch.float32, dev, (ch,))
-    _param("delta_bias", delta_bias, torch.float32, dev, (ch,))
-    bc = tuple(x.shape[:-1]) + (G, S)
-    lds = [_rows("x", x, dt, dev, x.shape), _rows("delta", delta, dt, dev, x.shape),
-           _rows("B", B, dt, dev, bc, 2), _rows("C", C, dt, dev, bc, 2),
-           0 if z is None else _rows("z", z, dt, dev, x.shape)]
-    return S, G, lds
+    _param("A", A, torch.float32, index, (ch, S))
+    if D is not None:
+        _param("D", D, torch.float32, index, (ch,))
+    if delta_bias is not None:
+        _param("delta_bias", delta_bias, torch.float32, index, (ch,))
+    bc = shape[:-1] + (G, S)
+    return (S, G, _rows("x", x, dtype, index, shape), _rows("delta", delta, dtype, index, shape),
+            _rows("B", B, dtype, index, bc, 2), _rows("C", C, dtype, index, bc, 2),
+            0 if z is None else _rows("z", z, dtype, index, shape))
 
 
 def gdn_ssm_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, state_in=None, y=None,
@@ -245,28 +249,29 @@ def gdn_ssm_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, state_in=Non
     cut into (0: chosen by the library); ``workspace`` a uint8 CUDA tensor of
     ``gdn_ssm_fwd_workspace_size(...)`` bytes, allocated here if None.
     """
-    _first(x, 3, "[b,T,ch]")
-    ch, dev = x.shape[2], x.device
-    N, T = _sequences(x, cu_seqlens)
-    S, G, lds = _ssm_params(x, delta, A, B, C, D, z, delta_bias)
-    handle, alloc = _stream(stream, dev)
+    shape, dtype, index = _first(x, 3, "[b,T,ch]")
+    ch = shape[2]
+    N, T = _sequences(shape, cu_seqlens, index)
+    S, G, ld_x, ld_d, ld_b, ld_c, ld_z = _ssm_params(x, shape, dtype, index, delta, A, B, C, D, z, delta_bias)
     lib = _lib.load()
-    with _device(dev):
-        state_out, pool = _states(state_in, state_out, slots, N, (ch, S), torch.float32, dev,
-                                  want_final_state, alloc)
-        y = _out("y", y, x, alloc)
-        lds.append(_rows("y", y, x.dtype, dev, x.shape))
-        need = lib.gdn_ssm_fwd_workspace_size(N, T, ch, S, _ptr(cu_seqlens), int(segment))
-        if workspace is None and need:
-            with alloc:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            _on("workspace", workspace, torch.uint8, dev)
-        _lib.check(lib.gdn_ssm_fwd(
-            _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias),
-            _ptr(state_in), _ptr(slots), _ptr(y), _ptr(state_out), N, T, ch, S, G, *lds, pool,
-            _ptr(cu_seqlens), bool(delta_softplus), _DTYPES[x.dtype], int(segment),
-            _ptr(workspace), 0 if workspace is None else workspace.numel(), handle))
+    state_out, pool = _states(state_in, state_out, slots, N, (ch, S), torch.float32, index,
+                              want_final_state, x, stream)
+    if y is None:
+        y, ld_y = _empty(stream, x), ch
+    else:
+        ld_y = _rows("y", y, dtype, index, shape)
+    segment = int(segment)
+    if workspace is None:
+        need = lib.gdn_ssm_fwd_workspace_size(N, T, ch, S, _ptr(cu_seqlens), segment)
+        if need:
+            workspace = _empty(stream, x, (need,), torch.uint8)
+    else:
+        _on("workspace", workspace, torch.uint8, index)
+    _call(lib.gdn_ssm_fwd, index, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+          _ptr(delta_bias), _ptr(state_in), _ptr(slots), _ptr(y), _ptr(state_out), N, T, ch, S, G,
+          ld_x, ld_d, ld_b, ld_c, ld_z, ld_y, pool, _ptr(cu_seqlens), bool(delta_softplus),
+          _DTYPES[dtype], segment, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+          _handle(stream, index))
     return y, state_out
 
 
@@ -282,19 +287,19 @@ def gdn_ssm_step(x, delta, A, B, C, D=None, z=None, delta_bias=None, state_in=No
     """``gdn_ssm_fwd`` for one new token per sequence: x, delta, z, y [N,ch],
     B, C [N,groups,S]; returns ``(y, state_out)``; ``state_out`` may be
     ``state_in``."""
-    _first(x, 2, "[N,ch]")
-    (N, ch), dev = x.shape, x.device
-    S, G, lds = _ssm_params(x, delta, A, B, C, D, z, delta_bias)
-    handle, alloc = _stream(stream, dev)
-    lib = _lib.load()
-    with _device(dev):
-        state_out, pool = _states(state_in, state_out, slots, N, (ch, S), torch.float32, dev, True, alloc)
-        y = _out("y", y, x, alloc)
-        lds.append(_rows("y", y, x.dtype, dev, x.shape))
-        _lib.check(lib.gdn_ssm_step(
-            _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias),
-            _ptr(state_in), _ptr(slots), _ptr(y), _ptr(state_out), N, ch, S, G, *lds, pool,
-            bool(delta_softplus), _DTYPES[x.dtype], handle))
+    shape, dtype, index = _first(x, 2, "[N,ch]")
+    N, ch = shape
+    S, G, ld_x, ld_d, ld_b, ld_c, ld_z = _ssm_params(x, shape, dtype, index, delta, A, B, C, D, z, delta_bias)
+    fn = _lib.load().gdn_ssm_step
+    state_out, pool = _states(state_in, state_out, slots, N, (ch, S), torch.float32, index, True, x, stream)
+    if y is None:
+        y, ld_y = _empty(stream, x), ch
+    else:
+        ld_y = _rows("y", y, dtype, index, shape)
+    _call(fn, index, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+          _ptr(delta_bias), _ptr(state_in), _ptr(slots), _ptr(y), _ptr(state_out), N, ch, S, G, ld_x,
+          ld_d, ld_b, ld_c, ld_z, ld_y, pool, bool(delta_softplus), _DTYPES[dtype],
+          _handle(stream, index))
     return y, state_out
 
 
@@ -309,23 +314,25 @@ def gdn_group_norm(x, groups, weight=None, bias=None, gate=None, y=None, eps=1e-
     ``x`` or ``gate``.
     """
     _cuda("x", x)
-    if x.dtype not in _DTYPES:
-        raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
-    if x.dim() < 1:
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    if dtype not in _DTYPES:
+        raise TypeError("x must be float32 or bfloat16, got %s" % dtype)
+    if len(shape) < 1:
         raise ValueError("x must be [..., C]")
-    C, dev = x.shape[-1], x.device
-    rows = x.numel() // C if C else 0
-    _param("weight", weight, torch.float32, dev, (C,))
-    _param("bias", bias, torch.float32, dev, (C,))
+    C = shape[-1]
+    if weight is not None:
+        _param("weight", weight, torch.float32, index, (C,))
+    if bias is not None:
+        _param("bias", bias, torch.float32, index, (C,))
     code = _act(act)
-    handle, alloc = _stream(stream, dev)
-    ld_x = _rows("x", x, x.dtype, dev, x.shape)
-    ld_g = 0 if gate is None else _rows("gate", gate, x.dtype, dev, x.shape)
-    lib = _lib.load()
-    with _device(dev):
-        y = _out("y", y, x, alloc)
-        ld_y = _rows("y", y, x.dtype, dev, x.shape)
-        _lib.check(lib.gdn_group_norm(
-            _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y), rows, C, int(groups), ld_x,
-            ld_g, ld_y, float(eps), bool(rms), code, _DTYPES[x.dtype], handle))
+    ld_x = _rows("x", x, dtype, index, shape)
+    ld_g = 0 if gate is None else _rows("gate", gate, dtype, index, shape)
+    fn = _lib.load().gdn_group_norm
+    if y is None:
+        y, ld_y = _empty(stream, x), C
+    else:
+        ld_y = _rows("y", y, dtype, index, shape)
+    _call(fn, index, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y), x.numel() // C if C else 0,
+          C, int(groups), ld_x, ld_g, ld_y, float(eps), bool(rms), code, _DTYPES[dtype],
+          _handle(stream, index))
     return y

@@ -86,6 +86,9 @@ def ssm(x, delta, A, B, C, D, z, delta_bias, softplus, state_in, slots, cu, piec
     ed = (8 * U + EX + 4 * U * np.abs(raw)) if softplus else np.full_like(raw, 2 * U)   # relative, of d
     skip = np.zeros(ch) if D is None else f64(D)
     rep = lambda m: np.repeat(m, ch // G, axis=0)  # noqa: E731
+    # h enters C h with 11 significant bits in bf16 calls; in fp32 calls h and C in two such
+    # parts each, which leaves less than 2^-22 of either
+    cut = 2.0 ** -10 if x.dtype == torch.bfloat16 else 2.0 ** -21
     y, bound, new, eb = np.zeros_like(X), np.zeros_like(X), [], []
     P = f64(state_in)
     for i, e in enumerate(entries(slots, len(cu) - 1)):
@@ -103,7 +106,10 @@ def ssm(x, delta, A, B, C, D, z, delta_bias, softplus, state_in, slots, cu, piec
             # to 64 + 64 terms, times |v| e^-|v| <= 0.37, for each earlier piece
             extra = (0.37 * 128 + 8) * U * m * (pieces - 1)
             v = (c * h).sum(1) + skip * X[t]
-            ev = (np.abs(c) * (err + extra + (S + 2) * U * m)).sum(1) + 2 * U * np.abs(skip * X[t])
+            # C h on the tensor cores: operands cut to what tf32 keeps, sums in fp32 that need
+            # not round to nearest
+            ev = (np.abs(c) * (err + extra + cut * np.abs(h) + (S + 8) * 2 * U * m)).sum(1)
+            ev = ev + 2 * U * np.abs(skip * X[t])
             if Z is not None:
                 g = silu(Z[t])
                 ev = (ev + 2 * U * np.abs(v)) * np.abs(g) + np.abs(v) * silu_error(Z[t])

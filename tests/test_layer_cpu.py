@@ -143,15 +143,16 @@ def test_workspace_size(lib):
 def host_only(monkeypatch):
     """CPU tensors let through, no library and no streams."""
     monkeypatch.setattr(layer, "_cuda", lambda *a: None)
-    import contextlib
-    monkeypatch.setattr(layer, "_stream", lambda *a: (0, contextlib.nullcontext()))
-    monkeypatch.setattr(layer, "_device", lambda *a: contextlib.nullcontext())
+    monkeypatch.setattr(layer, "_handle", lambda *a: 0)
+    monkeypatch.setattr(layer, "_call", lambda fn, index, *a: fn(*a))
 
     class Lib:
         def __getattr__(self, name):
-            if name.endswith("workspace_size"):
-                return lambda *a: 0
-            raise RuntimeError("reached the library")
+            def call(*a):
+                if name.endswith("workspace_size"):
+                    return 0
+                raise RuntimeError("reached the library")
+            return call
 
     monkeypatch.setattr(layer._lib, "load", lambda: Lib())
 
