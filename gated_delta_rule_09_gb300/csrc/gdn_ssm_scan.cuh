@@ -87,7 +87,7 @@ template <int W> __device__ __forceinline__ void st_state(float *p, int s0, int 
 enum Mode { kWhole, kPieces, kOutputs };
 
 // How wide the copies into the ring can be.
-enum Width { kWide, kWord, kSingle };  // whole; 4 bytes; element by element
+enum Width { kWide, kWord, kSingle };  // 16 bytes (pairs whole); 4 bytes; through registers
 
 // Threads and shared memory of one block of 64 channels.  The states are in H
 // parts, a lane has NS of a part: d_state is padded to 4 NS H.
@@ -130,17 +130,35 @@ template <typename E, int N>
 __device__ __forceinline__ void ring_copy(E *dst, const E *src, int valid, int width)
 {
     constexpr int step = N * sizeof(E) < 16 ? N : 16 / sizeof(E), word = 4 / sizeof(E);
-    if (width == kWide && valid) {
+    if (width == kWide && valid == N) {
 #pragma unroll
         for (int i = 0; i < N; i += step) copy_async<step * sizeof(E)>(dst + i, src + i);
-    } else if (width == kWord && valid == N) {
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < N; i += word) copy_async<4>(dst + i, src + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) dst[i] = i < valid ? src[i] : from_f<E>(0.f);
+    for (int i = 0; i < N; i += word) {  // `valid` is a multiple of a word here
+        if (i < valid)
+            copy_async<4>(dst + i, src + i);
+        else
+            *reinterpret_cast<uint32_t *>(dst + i) = 0;
     }
 }
+
+// The same for rows that no copy fits (bf16 off 4 bytes): through registers,
+// loaded well before they are stored.
+template <typename E, int N> struct Held {
+    E v[N];
+    __device__ __forceinline__ void load(const E *src, int valid)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < valid ? src[i] : from_f<E>(0.f);
+    }
+    __device__ __forceinline__ void store(E *dst) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) dst[i] = v[i];
+    }
+};
 
 // d = a b + c on the tensor cores, tf32 operands (their upper 19 bits count),
 // fp32 accumulation.  Lane (g, q) = (lane / 4, lane % 4) gives a = rows g, g + 8
@@ -465,6 +483,25 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
         c_in = static_cast<const E *>(a.Cm) + first * a.ld_c + channel + (ns > 0 ? st : 0);
     }
 
+    constexpr bool kHold = !BULK && sizeof(E) == 2;
+    Held<E, kHold ? 8 : 1> held_x, held_d, held_z;
+    Held<E, kHold ? 2 : 1> held_b[kHold ? kPer : 1], held_c[kHold ? kPer : 1];
+    auto hold = [&](int k) {  // the next issue's rows that have to go through registers
+        if (!kHold || k >= ntiles) return;
+        if (row_width == kSingle) {
+            const int valid = k * kTile < rows ? nc : 0;
+            held_x.load(x_in, valid);
+            held_d.load(d_in, valid);
+            held_z.load(z_in, MODE != kPieces && a.z ? valid : 0);
+        }
+        if (bc_width == kSingle)
+#pragma unroll
+            for (int i = 0; i < (kHold ? kPer : 1); ++i) {
+                const int t = tok0 + i * kTokStep, n = k * kTile + t < t1 - t0 ? ns : 0;
+                held_b[i].load(b_in + t * a.ld_b, n);
+                held_c[i].load(c_in + t * a.ld_c, MODE != kPieces ? n : 0);
+            }
+    };
     auto issue = [&](int k, int at) {  // tile k into ring slot `at`
         if (BULK) {
             if (id != 0 || k >= ntiles) return;
@@ -485,15 +522,26 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
         if (k < ntiles) {
             E *r = reinterpret_cast<E *>(smem + at * L::kSlot);
             const int valid = k * kTile < rows ? nc : 0;
-            ring_copy<E, 8>(r + off, x_in, valid, row_width);
-            ring_copy<E, 8>(r + L::kRowElems + off, d_in, valid, row_width);
-            if (MODE != kPieces && a.z) ring_copy<E, 8>(r + 2 * L::kRowElems + off, z_in, valid, row_width);
+            if (kHold && row_width == kSingle) {
+                held_x.store(r + off);
+                held_d.store(r + L::kRowElems + off);
+                held_z.store(r + 2 * L::kRowElems + off);
+            } else {
+                ring_copy<E, 8>(r + off, x_in, valid, row_width);
+                ring_copy<E, 8>(r + L::kRowElems + off, d_in, valid, row_width);
+                if (MODE != kPieces && a.z) ring_copy<E, 8>(r + 2 * L::kRowElems + off, z_in, valid, row_width);
+            }
             E *rb = r + 3 * L::kRowElems + 2 * id, *rc = rb + 2 * L::kBC;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int t = tok0 + i * kTokStep, n = k * kTile + t < t1 - t0 ? ns : 0;
-                ring_copy<E, 2>(rb + 2 * i * kPrep, b_in + t * a.ld_b, n, bc_width);
-                if (MODE != kPieces) ring_copy<E, 2>(rc + 2 * i * kPrep, c_in + t * a.ld_c, n, bc_width);
+                if (kHold && bc_width == kSingle) {
+                    held_b[i].store(rb + 2 * i * kPrep);
+                    held_c[i].store(rc + 2 * i * kPrep);
+                } else {
+                    ring_copy<E, 2>(rb + 2 * i * kPrep, b_in + t * a.ld_b, n, bc_width);
+                    if (MODE != kPieces) ring_copy<E, 2>(rc + 2 * i * kPrep, c_in + t * a.ld_c, n, bc_width);
+                }
             }
             if ((k + 1) * kTile < rows) {
                 x_in += kTile * a.ld_x;
@@ -549,7 +597,10 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     };
 
 #pragma unroll 1
-    for (int k = 0; k < kRing; ++k) issue(k, k);
+    for (int k = 0; k < kRing; ++k) {
+        hold(k);
+        issue(k, k);
+    }
     if (ntiles > 0) {
         if (BULK) wait_for(0, 0); else copy_wait<kRing - 1>();
         prepare(0, 0);
@@ -563,6 +614,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
 #pragma unroll 1
     for (int k = 0, done = 0, ahead = 2, round = 0; k < ntiles; ++k, done = next(done), ahead = next(ahead)) {
         round += ahead == 0;
+        hold(k + kRing);
         if (k + 2 < ntiles) {
             if (BULK) wait_for(ahead, round); else copy_wait<kRing - 3>();
         }
@@ -592,10 +644,9 @@ template <typename E> int row_width(const GdnSsmArgs &a)
 
 template <typename E> int bc_width(const GdnSsmArgs &a)
 {
-    return a.d_state % 2 == 0 && a.ld_b % 2 == 0 && a.ld_c % 2 == 0 && aligned_to(a.Bm, 2 * sizeof(E)) &&
-                   aligned_to(a.Cm, 2 * sizeof(E))
-               ? kWide
-               : kSingle;
+    const bool pairs = a.d_state % 2 == 0 && a.ld_b % 2 == 0 && a.ld_c % 2 == 0 &&
+                       aligned_to(a.Bm, 2 * sizeof(E)) && aligned_to(a.Cm, 2 * sizeof(E));
+    return pairs ? kWide : sizeof(E) == 4 ? kWord : kSingle;
 }
 
 // Tensor copies want a matrix and its rows on 16-byte boundaries, boxes that
