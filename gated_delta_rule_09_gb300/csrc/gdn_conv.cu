@@ -16,7 +16,7 @@ namespace {
 using namespace gdn_layer;
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 8;  // tokens loaded ahead of their use
+constexpr int kUnroll = 4;  // tokens per load batch; the next batch is in flight while one is used
 
 // Arithmetic on VEC channels, in pairs where there are pairs.
 template <int VEC> struct Lanes {
@@ -153,47 +153,73 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
         st_vec<E, VEC>(y + (int64_t)t * a.ld_y, r);
     };
-    int t = t0;
-    for (; t + kUnroll <= t1; t += kUnroll) {
-        Vec u[kUnroll];
+    auto load = [&](Vec (&u)[kUnroll], int t) {  // past the end: the last token again, not used
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) u[k] = input(t + k);
+        for (int k = 0; k < kUnroll; ++k) u[k] = input(min(t + k, t1 - 1));
+    };
+    auto use = [&](const Vec (&u)[kUnroll], int t) {
+        if (t + kUnroll <= t1) {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) token(t + k, u[k]);
+            for (int k = 0; k < kUnroll; ++k) token(t + k, u[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (t + k < t1) token(t + k, u[k]);
+        }
+    };
+    Vec u[2][kUnroll];
+    load(u[0], t0);
+    for (int t = t0; t < t1; t += 2 * kUnroll) {
+        load(u[1], t + kUnroll);
+        use(u[0], t);
+        if (t + 2 * kUnroll < t1) load(u[0], t + 2 * kUnroll);
+        use(u[1], t + kUnroll);
     }
-    for (; t < t1; ++t) token(t, input(t));
 }
 
-// One token per sequence: the state moves on by one input.
-template <typename E, int VEC, int W>
+// One token per sequence: the state moves on by one input.  A thread takes its
+// channels of kRows sequences, whose loads are in flight together and share the
+// taps (64 bytes per tap and thread, more than a sequence's own).
+template <typename E, int VEC, int W, int kRows>
 __global__ void __launch_bounds__(kThreads) gdn_conv_step_kernel(const GdnConvArgs a)
 {
     typedef typename Word<VEC * sizeof(E)>::type Vec;
     const int c0 = (blockIdx.y * kThreads + threadIdx.x) * VEC;
     if (c0 >= a.channels) return;
-    const int n = blockIdx.x;
-    const int entry = state_entry(a.slots, n, a.pool, a.status);
-    const E *in = static_cast<const E *>(a.state_in);
-    const size_t at = entry < 0 ? 0 : (size_t)entry * (W - 1) * a.channels + c0;
-    Vec u[W];
+    const int n0 = blockIdx.x * kRows;
+    const E *in = static_cast<const E *>(a.state_in), *x = static_cast<const E *>(a.x) + n0 * a.ld_x + c0;
+    int entry[kRows];
+    Vec u[kRows][W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        u[j] = Vec();
-        if (in && entry >= 0) u[j] = *reinterpret_cast<const Vec *>(in + at + (size_t)j * a.channels);
+    for (int r = 0; r < kRows; ++r) {
+        const int n = n0 + r;
+        entry[r] = n < a.N ? state_entry(a.slots, n, a.pool, a.status) : -1;
+        u[r][W - 1] = Vec();
+        if (n < a.N) u[r][W - 1] = *reinterpret_cast<const Vec *>(x + r * a.ld_x);
     }
-    u[W - 1] = *reinterpret_cast<const Vec *>(static_cast<const E *>(a.x) + n * a.ld_x + c0);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            u[r][j] = Vec();
+            if (in && entry[r] >= 0)
+                u[r][j] = *reinterpret_cast<const Vec *>(in + ((size_t)entry[r] * (W - 1) + j) * a.channels + c0);
+        }
     const Taps<VEC, W> taps(a, c0);
-    Lanes<VEC> win[W];
+    E *y = static_cast<E *>(a.y) + n0 * a.ld_y + c0;
 #pragma unroll
-    for (int j = 0; j < W; ++j) win[j] = widen_lanes<E, VEC>(u[j]);
-    float r[VEC];
-    taps.apply(win, a.act, r);
-    st_vec<E, VEC>(static_cast<E *>(a.y) + n * a.ld_y + c0, r);
-    if (entry >= 0) {
-        E *out = static_cast<E *>(a.state_out);
+    for (int r = 0; r < kRows; ++r) {
+        if (n0 + r >= a.N) break;
+        Lanes<VEC> win[W];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            *reinterpret_cast<Vec *>(out + at + (size_t)j * a.channels) = u[j + 1];
+        for (int j = 0; j < W; ++j) win[j] = widen_lanes<E, VEC>(u[r][j]);
+        float v[VEC];
+        taps.apply(win, a.act, v);
+        st_vec<E, VEC>(y + r * a.ld_y, v);
+        if (entry[r] < 0) continue;
+        E *out = static_cast<E *>(a.state_out) + (size_t)entry[r] * (W - 1) * a.channels + c0;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Vec *>(out + (size_t)j * a.channels) = u[r][j + 1];
     }
 }
 
@@ -209,11 +235,28 @@ template <typename E, int VEC, int W>
 cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
 {
     const int blocks = (a.channels / VEC + (a.channels % VEC != 0) + kThreads - 1) / kThreads;
-    // Tiles of 64 tokens re-read 5% of the rows (width 4); shorter ones when that
-    // would leave SMs without work.
-    const int64_t rows = a.cu_seqlens ? a.T : (int64_t)a.N * a.T;
-    int tl = 64;
-    while (tl > 16 && rows / tl * blocks < 1200) tl /= 2;
+    // The tile length of at least 16 tokens that takes the fewest token times: blocks run in
+    // waves of what is resident at once, and a tile reads width - 1 rows ahead of its own.
+    static int resident = 0;  // blocks per device of this kind; the same for every caller
+    if (!resident) {
+        int dev = 0, sms = 0, n = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gdn_conv_fwd_kernel<E, VEC, W>, kThreads, 0);
+        if (e != cudaSuccess) return e;
+        resident = sms * (n > 0 ? n : 1);
+    }
+    int tl = 16;
+    int64_t best = INT64_MAX;
+    for (int t = 16; t <= 128; t += 8) {
+        const int64_t n = (a.cu_seqlens ? a.T / t + a.N : (int64_t)a.N * ((a.T + t - 1) / t)) * blocks;
+        const int64_t cost = (n + resident - 1) / resident * (t + W - 1);
+        if (cost <= best) {
+            best = cost;
+            tl = t;
+        }
+    }
     const int tiles = a.T > tl ? (a.T + tl - 1) / tl : 1;
     const int64_t slots = a.cu_seqlens ? (int64_t)a.T / tl + a.N : (int64_t)a.N * tiles;
     gdn_conv_fwd_kernel<E, VEC, W><<<dim3((unsigned)slots, blocks), kThreads, 0, s>>>(a, tl, tiles);
@@ -224,7 +267,11 @@ template <typename E, int VEC, int W>
 cudaError_t step(const GdnConvArgs &a, cudaStream_t s)
 {
     const int blocks = (a.channels / VEC + (a.channels % VEC != 0) + kThreads - 1) / kThreads;
-    gdn_conv_step_kernel<E, VEC, W><<<dim3(a.N, blocks), kThreads, 0, s>>>(a);
+    // Four sequences per thread once that leaves a block or two per SM.
+    if ((int64_t)a.N * blocks >= 1024)
+        gdn_conv_step_kernel<E, VEC, W, 4><<<dim3((a.N + 3) / 4, blocks), kThreads, 0, s>>>(a);
+    else
+        gdn_conv_step_kernel<E, VEC, W, 1><<<dim3(a.N, blocks), kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

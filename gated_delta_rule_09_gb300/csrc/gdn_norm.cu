@@ -4,10 +4,11 @@
 // own mean and variance (or mean square); y = act(u weight + bias) silu(gate).
 // A few operations per element moved: bound by HBM, so every element is read
 // once, in 16-byte words where rows allow it, and kept in registers between the
-// statistics and the output.  A team of T lanes of a warp (width up to 8 words
-// per lane), or a whole block, has one group of kRows rows: their loads are in
-// flight together and share the weights.  The variance is taken about the mean
-// in a second pass over the registers.
+// statistics and the output.  A team of T lanes of a warp, or a whole block,
+// keeps to one group, whose weights it holds, and
+// walks down the rows, kRows at a time; the next rows are in flight while these
+// are normalised.  The variance is taken about the mean in a second pass over
+// the registers.
 #include "gdn_layer.h"
 #include "gdn_layer.cuh"
 
@@ -20,109 +21,152 @@ constexpr int kThreads = 256;
 // Sum over the team: T lanes of a warp, or the block.
 template <bool BLOCK> __device__ __forceinline__ float team_sum(float v, int T, float *sh)
 {
-    if (!BLOCK) {
+    if constexpr (BLOCK) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        __syncthreads();  // sh may still be read from the previous sum
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
+    } else {
         for (int o = T >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();  // sh may still be read from the previous sum
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
     return v;
 }
 
-__device__ __forceinline__ float finish(const GdnNormArgs &a, float u, float w, float b, bool gated, float gate)
-{
-    u = fmaf(u, w, b);
-    if (a.act == GDN_ACT_SILU) u = silu(u);
-    return gated ? u * silu(gate) : u;
-}
-
-// K words of VEC elements per thread and row, kRows rows per team.
+// K words of VEC elements per thread and row, kRows rows at a time.  `walkers`
+// teams share the rows of a group.
 template <typename E, int VEC, int K, int kRows, bool BLOCK>
-__global__ void __launch_bounds__(kThreads) gdn_group_norm_kernel(const GdnNormArgs a, int T)
+__global__ void __launch_bounds__(kThreads) gdn_group_norm_kernel(const GdnNormArgs a, int T, int walkers)
 {
     __shared__ float sh[kThreads / 32];
     typedef typename Word<VEC * sizeof(E)>::type Vec;
+    constexpr int P = VEC > 1 ? VEC / 2 : 1;  // pairs, for packed arithmetic; a lone element is half a pair
     const int width = a.channels / a.groups;
-    const int64_t teams = ((a.rows + kRows - 1) / kRows) * a.groups;
     const int64_t mine = BLOCK ? blockIdx.x : (int64_t)blockIdx.x * (kThreads / T) + threadIdx.x / T;
-    const int64_t team = mine < teams ? mine : teams - 1;  // surplus teams repeat the last, and store nothing
+    const bool live = mine < (int64_t)walkers * a.groups;  // surplus teams walk with the first, and store nothing
+    const int64_t team = live ? mine : 0;
     const int lane = BLOCK ? threadIdx.x : threadIdx.x & (T - 1);
-    const int64_t row0 = team / a.groups * kRows;
     const int c0 = (int)(team % a.groups) * width;
     const bool gated = a.gate != nullptr;
-    Vec xv[kRows][K], gv[kRows][K];
-    int64_t at[kRows];  // rows past the end repeat the last, and store nothing
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) at[r] = row0 + r < a.rows ? row0 + r : a.rows - 1;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int i = (lane + k * T) * VEC;
-            if (i >= width) continue;
-            xv[r][k] = *reinterpret_cast<const Vec *>(static_cast<const E *>(a.x) + at[r] * a.ld_x + c0 + i);
-            if (gated)
-                gv[r][k] = *reinterpret_cast<const Vec *>(static_cast<const E *>(a.gate) + at[r] * a.ld_gate + c0 + i);
-        }
-    const float inv = 1.f / width;
-    float mean[kRows], rstd[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        mean[r] = 0.f;
-        if (!a.rms) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if ((lane + k * T) * VEC >= width) continue;
-                float x[VEC];
-                widen(xv[r][k], x);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) mean[r] += x[i];
-            }
-            mean[r] = team_sum<BLOCK>(mean[r], T, sh) * inv;
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        float q = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if ((lane + k * T) * VEC >= width) continue;
-            float x[VEC];
-            widen(xv[r][k], x);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) q = fmaf(x[i] - mean[r], x[i] - mean[r], q);
-        }
-        rstd[r] = rsqrtf(team_sum<BLOCK>(q, T, sh) * inv + a.eps);
-    }
-    if (mine >= teams) return;
+    const E *x = static_cast<const E *>(a.x) + c0 + lane * VEC, *gate = static_cast<const E *>(a.gate) + c0 + lane * VEC;
+    E *y = static_cast<E *>(a.y) + c0 + lane * VEC;
+    bool has[K];
+    f32x2 w[K][P], b[K][P];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int i0 = (lane + k * T) * VEC;
-        if (i0 >= width) continue;
-        float w[VEC], b[VEC];
+        const int at = (lane + k * T) * VEC;
+        float f[VEC], g[VEC];
+        has[k] = at < width;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            w[i] = 1.f;
-            b[i] = 0.f;
+            f[i] = 1.f;
+            g[i] = 0.f;
         }
-        if (a.weight) ld_vec<float, VEC>(a.weight + c0 + i0, w);
-        if (a.bias) ld_vec<float, VEC>(a.bias + c0 + i0, b);
+        if (a.weight && has[k]) ld_vec<float, VEC>(a.weight + c0 + at, f);
+        if (a.bias && has[k]) ld_vec<float, VEC>(a.bias + c0 + at, g);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int lo = VEC > 1 ? 2 * i : 0, hi = VEC > 1 ? 2 * i + 1 : 0;
+            w[k][i] = pack2(f[lo], f[hi]);
+            b[k][i] = pack2(g[lo], g[hi]);
+        }
+    }
+    auto pairs = [](const Vec &u, f32x2 (&v)[P]) {
+        float f[VEC];
+        widen(u, f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = pack2(f[VEC > 1 ? 2 * i : 0], VEC > 1 ? f[VEC > 1 ? 2 * i + 1 : 0] : 0.f);
+    };
+    auto both = [](f32x2 v) {
+        float lo, hi;
+        unpack2(v, lo, hi);
+        return VEC > 1 ? lo + hi : lo;
+    };
+    Vec xv[kRows][K], gv[kRows][K];
+    auto load = [&](int64_t row0) {  // rows past the end repeat the last
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            if (row0 + r >= a.rows) continue;
-            float x[VEC], g[VEC];
-            widen(xv[r][k], x);
-            if (gated) widen(gv[r][k], g);
+            const int64_t row = row0 + r < a.rows ? row0 + r : a.rows - 1;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                x[i] = finish(a, (x[i] - mean[r]) * rstd[r], w[i], b[i], gated, gated ? g[i] : 0.f);
-            st_vec<E, VEC>(static_cast<E *>(a.y) + at[r] * a.ld_y + c0 + i0, x);
+            for (int k = 0; k < K; ++k) {
+                xv[r][k] = Vec();
+                gv[r][k] = Vec();
+                if (!has[k]) continue;
+                xv[r][k] = *reinterpret_cast<const Vec *>(x + row * a.ld_x + k * T * VEC);
+                if (gated) gv[r][k] = *reinterpret_cast<const Vec *>(gate + row * a.ld_gate + k * T * VEC);
+            }
+        }
+    };
+    const float inv = 1.f / width;
+    const int64_t stride = (int64_t)walkers * kRows;
+    int64_t row0 = team / a.groups * kRows;
+    load(row0 < a.rows ? row0 : 0);
+    // the same number of turns for every team: teams of a warp shuffle together
+    for (int64_t turn = 0; turn * stride < a.rows; ++turn, row0 += stride) {
+        f32x2 c[kRows][K][P];  // about the mean
+        Vec gn[kRows][K];
+        float rstd[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                pairs(xv[r][k], c[r][k]);  // zeros past the width
+                gn[r][k] = gv[r][k];
+            }
+        if (row0 + stride < a.rows) load(row0 + stride);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            f32x2 sum = 0, sq = 0;
+            float mean = 0.f;
+            if (!a.rms) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < P; ++i) sum = add2(sum, c[r][k][i]);
+                mean = team_sum<BLOCK>(both(sum), T, sh) * inv;
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!has[k]) continue;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    c[r][k][i] = add2(c[r][k][i], dup2(-mean));
+                    sq = fma2(c[r][k][i], c[r][k][i], sq);
+                }
+            }
+            rstd[r] = rsqrtf(team_sum<BLOCK>(both(sq), T, sh) * inv + a.eps);
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (!live || row0 + r >= a.rows) break;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!has[k]) continue;
+                f32x2 u[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i) u[i] = fma2(mul2(c[r][k][i], dup2(rstd[r])), w[k][i], b[k][i]);
+                if (a.act == GDN_ACT_SILU)
+#pragma unroll
+                    for (int i = 0; i < P; ++i) u[i] = silu2(u[i]);
+                if (gated) {
+                    f32x2 g[P];
+                    pairs(gn[r][k], g);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) u[i] = mul2(u[i], silu2(g[i]));
+                }
+                float out[VEC];
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    float lo, hi;
+                    unpack2(u[i], lo, hi);
+                    out[VEC > 1 ? 2 * i : 0] = lo;
+                    if (VEC > 1) out[VEC > 1 ? 2 * i + 1 : 0] = hi;
+                }
+                st_vec<E, VEC>(y + (row0 + r) * a.ld_y + k * T * VEC, out);
+            }
         }
     }
 }
@@ -148,39 +192,55 @@ __global__ void __launch_bounds__(kThreads) gdn_group_norm_wide_kernel(const Gdn
         q = fmaf(v, v, q);
     }
     const float rstd = rsqrtf(team_sum<true>(q, 0, sh) / width + a.eps);
-    for (int i = threadIdx.x; i < width; i += kThreads)
-        y[i] = from_f<E>(finish(a, (to_f(x[i]) - mean) * rstd, a.weight ? a.weight[c0 + i] : 1.f,
-                                a.bias ? a.bias[c0 + i] : 0.f, gate != nullptr, gate ? to_f(gate[i]) : 0.f));
+    for (int i = threadIdx.x; i < width; i += kThreads) {
+        float u = fmaf((to_f(x[i]) - mean) * rstd, a.weight ? a.weight[c0 + i] : 1.f, a.bias ? a.bias[c0 + i] : 0.f);
+        if (a.act == GDN_ACT_SILU) u = silu(u);
+        y[i] = from_f<E>(gate ? u * silu(to_f(gate[i])) : u);
+    }
 }
 
 template <typename E, int VEC, int K, int kRows, bool BLOCK>
 cudaError_t launch(const GdnNormArgs &a, int T, cudaStream_t s)
 {
-    const int64_t teams = (a.rows + kRows - 1) / kRows * a.groups, per = BLOCK ? 1 : kThreads / T;
-    const int64_t blocks = (teams + per - 1) / per;
+    // As many teams as are resident at once, or as there are rows for.
+    static int resident = 0;  // threads' teams per device of this kind; the same for every caller
+    const int per = BLOCK ? 1 : kThreads / T;
+    if (!resident) {
+        int dev = 0, sms = 0, blocks = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                &blocks, gdn_group_norm_kernel<E, VEC, K, kRows, BLOCK>, kThreads, 0);
+        if (e != cudaSuccess) return e;
+        resident = sms * (blocks > 0 ? blocks : 1);
+    }
+    const int64_t turns = (a.rows + kRows - 1) / kRows;
+    int64_t walkers = ((int64_t)resident * per + a.groups - 1) / a.groups;
+    if (walkers > turns) walkers = turns;
+    // equal shares: the last turn is as full as the others
+    const int64_t each = (turns + walkers - 1) / walkers;
+    walkers = (turns + each - 1) / each;
+    const int64_t blocks = (walkers * a.groups + per - 1) / per;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    gdn_group_norm_kernel<E, VEC, K, kRows, BLOCK><<<(unsigned)blocks, kThreads, 0, s>>>(a, T);
+    gdn_group_norm_kernel<E, VEC, K, kRows, BLOCK><<<(unsigned)blocks, kThreads, 0, s>>>(a, T, (int)walkers);
     return cudaGetLastError();
 }
 
-// The team by the group's words: lanes of a warp up to 8 words each, then a
-// block.  Four loads per thread and matrix in flight, from as many rows as that
-// takes; few rows are spread one to a team.
+// The team by the group's words: lanes of a warp up to 2 words each, a block up
+// to 4.
 template <typename E, int VEC> cudaError_t by_width(const GdnNormArgs &a, cudaStream_t s)
 {
     const int words = (a.channels / a.groups + VEC - 1) / VEC;
-    const bool few = a.rows * a.groups < 16384;
     if (words <= 32) {
         int T = 1;
         while (T < words) T *= 2;
-        return few ? launch<E, VEC, 1, 1, false>(a, T, s) : launch<E, VEC, 1, 4, false>(a, T, s);
+        return launch<E, VEC, 1, 2, false>(a, T, s);
     }
-    if (words <= 64) return few ? launch<E, VEC, 2, 1, false>(a, 32, s) : launch<E, VEC, 2, 2, false>(a, 32, s);
-    if (words <= 128) return launch<E, VEC, 4, 1, false>(a, 32, s);
-    if (words <= 256) return launch<E, VEC, 8, 1, false>(a, 32, s);
-    if (words <= 512) return launch<E, VEC, 2, 1, true>(a, kThreads, s);
-    if (words <= 1024) return launch<E, VEC, 4, 1, true>(a, kThreads, s);
-    if (words <= 2048) return launch<E, VEC, 8, 1, true>(a, kThreads, s);
+    if (words <= 64) return launch<E, VEC, 2, 1, false>(a, 32, s);
+    if (words <= kThreads) return launch<E, VEC, 1, 1, true>(a, kThreads, s);
+    if (words <= 2 * kThreads) return launch<E, VEC, 2, 1, true>(a, kThreads, s);
+    if (words <= 4 * kThreads) return launch<E, VEC, 4, 1, true>(a, kThreads, s);
     const int64_t blocks = a.rows * a.groups;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     gdn_group_norm_wide_kernel<E><<<(unsigned)blocks, kThreads, 0, s>>>(a);

@@ -57,59 +57,69 @@ template <typename E> struct Four<false, E> {
     }
 };
 
+// kRows <= LPC sequences per thread.  What is needed once per channel (softplus,
+// gate, store) is done for sequence r by the channel's lanes q with q % kRows = r
+// and passed round; the butterfly leaves that lane with that sequence's y.
 template <typename E, int LPC, int kRows, bool VEC>
 __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kernel(const GdnSsmArgs a)
 {
-    const int per_block = kThreads / LPC;
-    const int c = blockIdx.y * per_block + threadIdx.x / LPC;
+    const int c = blockIdx.y * (kThreads / LPC) + threadIdx.x / LPC;
     const bool live = c < a.channels;
     const int cc = live ? c : a.channels - 1;
-    const int s0 = 4 * (threadIdx.x % LPC), ds = a.d_state;
+    const int q = threadIdx.x % LPC, s0 = 4 * q, ds = a.d_state;
     const int g = cc / (a.channels / a.groups);
-    const int n0 = blockIdx.x * kRows;
-    float h[kRows][4], d[kRows], x[kRows], z[kRows];
-    Four<VEC, E> B[kRows], C[kRows];
+    const int n0 = blockIdx.x * kRows, own = n0 + q % kRows;
+    // the lane's own sequence; rows past the end repeat the last and store nothing
+    const int64_t row = min(own, a.N - 1);
+    const int mine = own < a.N ? state_entry(a.slots, own, a.pool, a.status) : -1;
     int entry[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) entry[r] = n0 + r < a.N ? state_entry(a.slots, n0 + r, a.pool, a.status) : -1;
+    float h[kRows][4];
+    Four<VEC, E> B[kRows], C[kRows];
+    const E *b = static_cast<const E *>(a.Bm) + (int64_t)n0 * a.ld_b + (int64_t)g * ds;
+    const E *cm = static_cast<const E *>(a.Cm) + (int64_t)n0 * a.ld_c + (int64_t)g * ds;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        const int64_t n = min(n0 + r, a.N - 1);
+        entry[r] = kRows == 1 ? mine : __shfl_sync(0xffffffffu, mine, (threadIdx.x & 31) / LPC * LPC + r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[r][j] = 0.f;
         if (a.state_in && entry[r] >= 0)
             ld_state<VEC>(a.state_in + ((size_t)entry[r] * a.channels + cc) * ds, s0, ds, h[r]);
-        d[r] = to_f(static_cast<const E *>(a.delta)[n * a.ld_delta + cc]);
-        x[r] = to_f(static_cast<const E *>(a.x)[n * a.ld_x + cc]);
-        z[r] = a.z ? to_f(static_cast<const E *>(a.z)[n * a.ld_z + cc]) : 0.f;
-        B[r].load(static_cast<const E *>(a.Bm) + n * a.ld_b + (size_t)g * ds, s0, ds);
-        C[r].load(static_cast<const E *>(a.Cm) + n * a.ld_c + (size_t)g * ds, s0, ds);
     }
+    float d = to_f(static_cast<const E *>(a.delta)[row * a.ld_delta + cc]);
+    const float x = to_f(static_cast<const E *>(a.x)[row * a.ld_x + cc]);
+    const float z = a.z ? to_f(static_cast<const E *>(a.z)[row * a.ld_z + cc]) : 0.f;
     float A[4];
     ld_state<VEC>(a.A + (size_t)cc * ds, s0, ds, A);
-    const float bias = a.delta_bias ? a.delta_bias[cc] : 0.f, D = a.D ? a.D[cc] : 0.f;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        d[r] += bias;
-        if (a.softplus) d[r] = softplus(d[r]);
-        const float dx = d[r] * x[r];
-        float y = 0.f, b[4], cm[4];
-        B[r].get(b);
-        C[r].get(cm);
+        B[r].load(b, s0, ds);
+        C[r].load(cm, s0, ds);
+        if (n0 + r + 1 < a.N) {
+            b += a.ld_b;
+            cm += a.ld_c;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) A[j] *= kLog2e;
+    d += a.delta_bias ? a.delta_bias[cc] : 0.f;
+    if (a.softplus) d = softplus(d);
+    const float dx = d * x;
+    float y[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int from = (threadIdx.x & 31) / LPC * LPC + r;
+        const float dr = kRows == 1 ? d : __shfl_sync(0xffffffffu, d, from);
+        const float dxr = kRows == 1 ? dx : __shfl_sync(0xffffffffu, dx, from);
+        float bv[4], cv[4];
+        B[r].get(bv);
+        C[r].get(cv);
+        y[r] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            h[r][j] = fmaf(ex2(d[r] * (A[j] * kLog2e)), h[r][j], dx * b[j]);
-            y = fmaf(cm[j], h[r][j], y);
+            h[r][j] = fmaf(ex2(dr * A[j]), h[r][j], dxr * bv[j]);
+            y[r] = fmaf(cv[j], h[r][j], y[r]);
         }
-#pragma unroll
-        for (int o = 1; o < LPC; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (!live || n0 + r >= a.N) continue;
-        if (threadIdx.x % LPC == 0) {
-            y = fmaf(D, x[r], y);
-            if (a.z) y *= silu(z[r]);
-            static_cast<E *>(a.y)[(int64_t)(n0 + r) * a.ld_y + cc] = from_f<E>(y);
-        }
-        if (entry[r] < 0) continue;
+        if (!live || entry[r] < 0) continue;
         float *out = a.state_out + ((size_t)entry[r] * a.channels + cc) * ds;
         if (VEC) {
             if (s0 < ds) st_vec<float, 4>(out + s0, h[r]);
@@ -119,6 +129,20 @@ __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kern
                 if (s0 + j < ds) out[s0 + j] = h[r][j];
         }
     }
+    // each halving step sends the sums that the partner's sequences need; then the rest of the lanes
+#pragma unroll
+    for (int o = kRows / 2; o >= 1; o /= 2)
+#pragma unroll
+        for (int r = 0; r < o; ++r) {
+            const float send = q & o ? y[r] : y[r + o], keep = q & o ? y[r + o] : y[r];
+            y[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+#pragma unroll
+    for (int o = kRows; o < LPC; o <<= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
+    if (!live || q >= kRows || own >= a.N) return;
+    float v = fmaf(a.D ? a.D[cc] : 0.f, x, y[0]);
+    if (a.z) v *= silu(z);
+    static_cast<E *>(a.y)[row * a.ld_y + cc] = from_f<E>(v);
 }
 
 template <typename E, int LPC, int kRows> cudaError_t launch_step(const GdnSsmArgs &a, cudaStream_t s)
@@ -135,13 +159,14 @@ template <typename E, int LPC, int kRows> cudaError_t launch_step(const GdnSsmAr
     return cudaGetLastError();
 }
 
-// Four sequences per thread once that still leaves a few blocks per SM; a small
-// batch is spread as widely as it goes.
+// Up to four sequences per thread once that still leaves a few blocks per SM; a
+// small batch is spread as widely as it goes.
 template <typename E, int LPC> cudaError_t by_rows(const GdnSsmArgs &a, cudaStream_t s)
 {
+    constexpr int kRows = LPC < 4 ? LPC : 4;
     const int per = kThreads / LPC;
-    const int64_t blocks = (int64_t)((a.N + 3) / 4) * ((a.channels + per - 1) / per);
-    return blocks >= 1024 ? launch_step<E, LPC, 4>(a, s) : launch_step<E, LPC, 1>(a, s);
+    const int64_t blocks = (int64_t)((a.N + kRows - 1) / kRows) * ((a.channels + per - 1) / per);
+    return blocks >= 1024 ? launch_step<E, LPC, kRows>(a, s) : launch_step<E, LPC, 1>(a, s);
 }
 
 template <typename E> cudaError_t step(const GdnSsmArgs &a, cudaStream_t s)
