@@ -99,8 +99,8 @@ template <typename E, int NS, int H> struct Layout {
     static constexpr int kRing = sizeof(E) * H > 4 ? 5 : 6;  // tiles of inputs held or on their way
     static constexpr size_t kSlot = sizeof(E) * (3 * kRowElems + 4 * kBC);  // x, delta, z, B, C
     static constexpr size_t kHandD = 16 * (size_t)kTile * kPairs;           // (d, d, d x, d x) per pair
-    static constexpr size_t kHandB = 16 * (size_t)kBC;                      // (b, b, b', b') per pair of B
-    static constexpr size_t kHandC = 8 * (size_t)kBC;                       // C
+    static constexpr size_t kHandB = 8 * (size_t)kBC;                       // B, and C, widened
+    static constexpr size_t kHandC = kHandB;
     static constexpr size_t kPartY = 16 * (size_t)kTile * kYPitch;          // y per pair, from one part
     static constexpr size_t kHand = kHandD + kHandB + kHandC + H * kPartY;
     static constexpr size_t kBytes = kRing * kSlot + 2 * kHand + 8 * kRing;
@@ -274,7 +274,6 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
                 A[i + u] = pack2(Av[0][u], Av[1][u]);
             }
         }
-        constexpr int kRuns = L::kStates / 16;  // runs of B words per token: [run][2][q]
         // A warp has its scheduler nearly to itself, so it covers its own latencies: a token's
         // words are loaded and its decays computed (kAhead) while the token before goes through
         // the states, and its y is picked up one token later.  With more states per lane there is
@@ -282,30 +281,34 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
         constexpr int kAhead = NS == 4 ? 1 : 0;
         for (int k = 0; k < ntiles; ++k) {
             const ulonglong2 *dx = reinterpret_cast<const ulonglong2 *>(hand(k)) + place(pair);
-            const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(hand_b(k)) + part * 2 * NS + q;
+            const float4 *B = reinterpret_cast<const float4 *>(hand_b(k)) + state_of<NS>(part, q, 0) / 4;
             const float4 *C = reinterpret_cast<const float4 *>(hand_c(k)) +
                               (tok * L::kStates + state_of<NS>(part, q, 0)) / 4;
             unsigned char *yout = part_y(k, part) + 8 * y_place(pair) + 32 * q * kYPitch;
-            ulonglong2 dv[2 + kAhead], bv[2 + kAhead][NS == 4 ? 2 : 1];
+            ulonglong2 dv[2 + kAhead];
+            float4 bv[2 + kAhead];
             f32x2 e[1 + kAhead][NS], w[1 + kAhead][NS], tile_sum = 0;
             float C1[NS], C2[sizeof(E) == 4 ? NS : 1], acc[2][2][4], keep[4];
-            auto word = [&](int t, int i) { return B[((t * kRuns + i / 4) * 2 + i % 4 / 2) * 4]; };
+            auto word = [&](int t, int i) { return B[(t * L::kStates + 4 * i) / 4]; };
             auto load = [&](int t) {
                 dv[t % (2 + kAhead)] = dx[t * kPairs];  // d, d x
-#pragma unroll
-                for (int i = 0; i < (NS == 4 ? 4 : 0); i += 2) bv[t % (2 + kAhead)][i / 2] = word(t, i);
+                if (NS == 4) bv[t % (2 + kAhead)] = word(t, 0);
             };
             auto decay = [&](int t) {
                 const ulonglong2 v = dv[t % (2 + kAhead)];
                 const int p = t % (1 + kAhead);
                 if (MODE == kPieces) tile_sum = add2(tile_sum, v.x);
+                float x0, x1;
+                unpack2(v.y, x0, x1);
 #pragma unroll
-                for (int i = 0; i < NS; i += 2) {
-                    const ulonglong2 bb = NS == 4 ? bv[t % (2 + kAhead)][NS == 4 ? i / 2 : 0] : word(t, i);
-                    e[p][i] = ex2x2(mul2(v.x, A[i]));
-                    e[p][i + 1] = ex2x2(mul2(v.x, A[i + 1]));
-                    w[p][i] = mul2(v.y, bb.x);
-                    w[p][i + 1] = mul2(v.y, bb.y);
+                for (int i = 0; i < NS; i += 4) {
+                    const float4 b4 = NS == 4 ? bv[t % (2 + kAhead)] : word(t, i);
+                    const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        e[p][i + u] = ex2x2(mul2(v.x, A[i + u]));
+                        w[p][i + u] = pack2(x0 * bb[u], x1 * bb[u]);
+                    }
                 }
             };
             auto pick = [&](int t) {  // of token t's product, column t % 8: lanes q = t % 8 / 2
@@ -464,11 +467,9 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     // ---- prepare
     f32x2 bias[4];
     column(a.delta_bias, bias);
-    // pair p = id + i kPrep of B and C of a tile: a token's states 2 (p % kHalf) and the next, and
-    // where the recurrence wants B (state_of, [run][2][q])
+    // pair p = id + i kPrep of B and C of a tile: a token's states 2 (p % kHalf) and the next
     constexpr int kHalf = L::kStates / 2, kPer = L::kBC / kPrep, kTokStep = kPrep / kHalf;
     const int st = 2 * (id % kHalf), tok0 = id / kHalf;
-    const int b_word = (st / 16 * 2 + st % 4 / 2) * 4 + st % 16 / 4;
     const int ns = max(0, min(2, a.d_state - st));
     const int64_t channel = (int64_t)g * a.d_state;
 
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
             dx[place(4 * col + i)] = word;
         }
         const E *rb = r + 3 * L::kRowElems + 2 * id, *rc = rb + 2 * L::kBC;
-        float4 *B = reinterpret_cast<float4 *>(hand_b(k)) + tok0 * kHalf + b_word;
+        float2 *B = reinterpret_cast<float2 *>(hand_b(k)) + id;
         float2 *C = reinterpret_cast<float2 *>(hand_c(k)) + id;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
             ld_vec<E, 2>(rb + 2 * i * kPrep, v);
             if (kEdge && n < 1) v[0] = 0.f;
             if (kEdge && n < 2) v[1] = 0.f;
-            B[i * kPrep] = make_float4(v[0], v[0], v[1], v[1]);
+            B[i * kPrep] = make_float2(v[0], v[1]);
             if (MODE == kPieces) continue;
             ld_vec<E, 2>(rc + 2 * i * kPrep, v);
             if (kEdge && n < 1) v[0] = 0.f;
