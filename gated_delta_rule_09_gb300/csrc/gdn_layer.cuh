@@ -282,6 +282,43 @@ __device__ __forceinline__ bool find_span(const int32_t *cu, int N, int T, int t
     return found;
 }
 
+// The packed sequence of a given rank by length, longest first, of at most 64
+// (of more, the sequence of that number): blocks start about in the order of
+// their numbers, and a sequence that takes as long as the rest together must
+// not be the last to start.  Called by whole warps; false for a malformed span.
+__device__ __forceinline__ bool find_ranked(const int32_t *cu, int N, int T, int rank,
+                                            unsigned int *status, Span &s)
+{
+    const int lane = threadIdx.x & 31;
+    int n = rank;
+    if (N <= 64) {
+        int len[2], ahead[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int m = lane + 32 * i;
+            len[i] = m < N ? cu[m + 1] - cu[m] : INT32_MIN;
+        }
+        for (int m = 0; m < N; ++m) {
+            const int other = __shfl_sync(0xffffffffu, m < 32 ? len[0] : len[1], m & 31);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ahead[i] += other > len[i] || (other == len[i] && m < lane + 32 * i);
+        }
+        const unsigned lo = __ballot_sync(0xffffffffu, lane < N && ahead[0] == rank);
+        const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 < N && ahead[1] == rank);
+        n = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
+    }
+    const int first = cu[n], end = cu[n + 1];
+    if (first < 0 || end < first || end > T) {
+        atomicOr(status, GDN_DEV_BAD_SEQLENS);
+        return false;
+    }
+    s.n = n;
+    s.tile = 0;
+    s.len = end - first;
+    s.row = first;
+    return true;
+}
+
 // The pool entry of sequence n's state, or -1 when it keeps none.
 __device__ __forceinline__ int state_entry(const int32_t *slots, int n, int pool,
                                            unsigned int *status)

@@ -197,7 +197,7 @@ void gdn_ssm_plan(int N, int T, int channels, int d_state, bool packed, int aske
         if (!sms && (cudaGetDevice(&dev) != cudaSuccess ||
                      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess))
             sms = 152;
-        constexpr double kAlone = 58, kShared = 53, kCut = 85, kLaunch = 10000;
+        constexpr double kAlone = 58, kShared = 46, kCut = 81, kLaunch = 10000;
         const int64_t chunks = (channels + kScanChannels - 1) / (kScanChannels);
         const double tokens = (double)(packed ? T : (int64_t)N * T);
         // a packed sequence may be the longest by far; twice the mean is taken for it

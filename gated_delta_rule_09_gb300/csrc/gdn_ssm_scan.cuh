@@ -190,8 +190,15 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     constexpr int kRing = L::kRing, kRecur = L::kRecur;
     extern __shared__ __align__(128) unsigned char smem[];
     Span s;
-    const int64_t slot = blockIdx.x % slots;
-    if (!find_span(a.cu_seqlens, a.N, a.T, tl, slot, tiles, a.status, s)) return;
+    // Pieces of one chunk of channels side by side; whole packed sequences by length, each with
+    // its chunks side by side.
+    const bool ranked = MODE == kWhole && a.cu_seqlens;
+    const unsigned chunks = gridDim.x / slots;
+    const int64_t slot = ranked ? blockIdx.x / chunks : blockIdx.x % slots;
+    const int chunk = ranked ? blockIdx.x % chunks : blockIdx.x / slots;
+    if (ranked ? !find_ranked(a.cu_seqlens, a.N, a.T, (int)slot, a.status, s)
+               : !find_span(a.cu_seqlens, a.N, a.T, tl, slot, tiles, a.status, s))
+        return;
     const int pieces = s.len > tl ? (s.len + tl - 1) / tl : 1;
     if (MODE == kPieces && s.tile == pieces - 1) return;
     const int t0 = s.tile * tl, t1 = min(s.len, t0 + tl);
@@ -199,7 +206,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     // the block's channels: [cbase, cend), all of one group
     const int per_group = a.channels / a.groups;
     const int blocks = (per_group + 2 * kPairs - 1) / (2 * kPairs);
-    const int chunk = blockIdx.x / slots, g = chunk / blocks;
+    const int g = chunk / blocks;
     const int cbase = g * per_group + (chunk % blocks) * 2 * kPairs;
     const int cend = min(cbase + 2 * kPairs, (g + 1) * per_group);
 
@@ -720,7 +727,7 @@ template <typename E, int NS, int H, bool BULK> cudaError_t launch_modes(const G
         return e != cudaSuccess ? e : launch_mode<E, NS, H, kOutputs, BULK>(a, maps, a.segment, tiles, a.pieces, s);
     }
     const int tl = a.T > 0 ? a.T : 1;
-    return launch_mode<E, NS, H, kWhole, BULK>(a, maps, tl, 1, a.cu_seqlens ? a.T / tl + a.N : a.N, s);
+    return launch_mode<E, NS, H, kWhole, BULK>(a, maps, tl, 1, a.N, s);
 }
 
 template <typename E, int NS, int H> cudaError_t launch_fwd(const GdnSsmArgs &a, cudaStream_t s)
