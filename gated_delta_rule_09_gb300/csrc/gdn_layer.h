@@ -60,6 +60,7 @@ struct GdnSsmArgs {
 void gdn_ssm_plan(int N, int T, int channels, int d_state, bool packed, int asked, int *segment,
                   int64_t *piece_slots);
 constexpr int kScanChannels = 64;  // of one group, per block of the scan
+int gdn_ssm_sms();                 // multiprocessors of the current device
 cudaError_t gdn_ssm_scan_bf16(const GdnSsmArgs &a, cudaStream_t s);
 cudaError_t gdn_ssm_scan_f32(const GdnSsmArgs &a, cudaStream_t s);
 cudaError_t gdn_launch_ssm_fwd(const GdnSsmArgs &a, cudaStream_t s, int *launches);

@@ -181,6 +181,16 @@ template <typename E> cudaError_t step(const GdnSsmArgs &a, cudaStream_t s)
 
 }  // namespace
 
+int gdn_ssm_sms()
+{
+    static int sms = 0;  // the same for every caller
+    int dev = 0;
+    if (!sms && (cudaGetDevice(&dev) != cudaSuccess ||
+                 cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess))
+        sms = 152;
+    return sms;
+}
+
 // Whether sequences are cut, by the time either way.  A block (64 channels of a
 // sequence) takes kAlone ns per token when it has its SM to itself, an SM gets
 // through a token of a block every kShared ns when blocks share it, and cut
@@ -192,12 +202,8 @@ void gdn_ssm_plan(int N, int T, int channels, int d_state, bool packed, int aske
 {
     int64_t seg = ((int64_t)asked + 63) / 64 * 64;
     if (asked <= 0) {
-        static int sms = 0;
-        int dev = 0;
-        if (!sms && (cudaGetDevice(&dev) != cudaSuccess ||
-                     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess))
-            sms = 152;
-        constexpr double kAlone = 58, kShared = 46, kCut = 81, kLaunch = 10000;
+        const int sms = gdn_ssm_sms();
+        constexpr double kAlone = 51, kShared = 45, kCut = 79, kLaunch = 10000;
         const int64_t chunks = (channels + kScanChannels - 1) / (kScanChannels);
         const double tokens = (double)(packed ? T : (int64_t)N * T);
         // a packed sequence may be the longest by far; twice the mean is taken for it

@@ -7,10 +7,12 @@
 //
 // with d = softplus(delta + bias); exp is 2^(d A log2 e).
 //
-// What bounds the prompt kernel is arithmetic: per token, channel and state an
-// exponential (32 per clock and SM) and four fp32 operations (128 lanes per
-// clock), beside the shared-memory bytes that bring each lane its operands (128
-// per clock).  The work is split so that no pipe does what another can:
+// What bounds it is arithmetic: per token, channel and state an exponential (32
+// per clock and SM) and four fp32 operations (128 lanes per clock), so 32 states
+// per clock at best; a loop of this mix alone reaches 24.  HBM would allow 58
+// for bf16 and 16 states.  Shared memory (128 bytes per clock into registers)
+// comes next, at 16 to 80 bytes per lane and token by how operands are shared.
+// The work is split so that no pipe does what another can:
 //
 //  - Recurrence warps (4 per block, 16 channels each; 8 with half the states
 //    each when d_state > 64) do nothing but the recurrence.  A lane holds NS
@@ -22,16 +24,20 @@
 //    is kept.  That takes the place of the fourth fp32 operation, of a butterfly
 //    over the lanes of a channel and of most loads of C.
 //  - What is done once per token and channel is done by other warps.  Four
-//    prepare: they fetch tiles of kTile tokens into a ring, compute the softplus
-//    and hand over (d, d x) of a channel pair as one 16-byte word, beside B
-//    widened and doubled (packed operands as it stands) and C widened.  Four
-//    finish: D x, the gate and the store of y.  Two hand-over buffers alternate.
-//    The recurrence warps need most registers, so they take over what the others
-//    leave of the block's.
-//  - Where the rows allow it the tiles are fetched by tensor copies, five per
-//    tile and one thread.  Copies of 16 bytes per thread (the other rows) kept
-//    the preparing warps busy for a third of their time; a bulk copy per row,
-//    80 per tile, took 38 clocks each.
+//    prepare: the softplus, (d, d x) of a channel pair as one 16-byte word in a
+//    hand-over buffer, and B and C widened.  Four finish: D x, the gate and the
+//    store of y.  The recurrence warps need most registers and take over what the
+//    others leave of the block's.
+//  - Tiles of kTile tokens come into a ring by tensor copies where the rows allow
+//    it, five per tile from one finishing thread (from a preparing one they
+//    lengthened the whole block's turn: 236 against 210 us on the first shape
+//    below).  Other rows come by copies of 16 or 4 bytes per thread.  A bulk copy
+//    per row, 80 per tile, took 38 clocks each and twice the time.
+//
+// Measured, bf16, 16 states: 4 x 4096 tokens x 2048 channels 208 us (a block per
+// SM, 128 of 152 busy: 51 ns per token, of which the recurrence alone takes 43);
+// x 9728 channels 685 us (two blocks per SM: 12.2 states per clock and SM, issue
+// slots 60 % full, exponentials 47 %, shared memory under 68 %).
 //
 // The tensor product takes tf32 operands (11 bits).  bf16 calls pass h as it is
 // (cut to 11 bits; C is exact): the sum over states is fp32 and y is stored in 8
@@ -56,6 +62,7 @@ using namespace gdn_layer;
 constexpr uint64_t kWaitLimit = 2000000000;     // ns a wait for a copy may take,
 constexpr uint64_t kWaitAfterTimeout = 50000;   // and every later one once that ran out
 constexpr int kTile = 16;            // tokens handed over at a time
+constexpr int kHands = 2;            // hand-over buffers; a third: 213 against 208 us
 constexpr int kPairs = 32;           // channel pairs per block: 4 warps of 8 pairs
 constexpr int kCols = kPairs / 4;    // 8-channel columns of a token row
 constexpr int kPrep = 128;           // preparing threads, and finishing ones: a column of a row each
@@ -96,15 +103,17 @@ template <typename E, int NS, int H> struct Layout {
     static constexpr int kStates = 4 * NS * H;
     static constexpr int kBC = kTile * kStates / 2;       // pairs of B (and of C) per tile
     static constexpr int kRowElems = kTile * 2 * kPairs;
-    static constexpr int kRing = sizeof(E) * H > 4 ? 5 : 6;  // tiles of inputs held or on their way
+    // Tiles of inputs held or on their way.  A tile is fetched once the tile kRing before it is
+    // finished, and waited for before the tile kHands before it is through the recurrence.
+    static constexpr int kRing = sizeof(E) * H > 4 ? 5 : 6;
     static constexpr size_t kSlot = sizeof(E) * (3 * kRowElems + 4 * kBC);  // x, delta, z, B, C
     static constexpr size_t kHandD = 16 * (size_t)kTile * kPairs;           // (d, d, d x, d x) per pair
     static constexpr size_t kHandB = 8 * (size_t)kBC;                       // B, and C, widened
     static constexpr size_t kHandC = kHandB;
     static constexpr size_t kPartY = 16 * (size_t)kTile * kYPitch;          // y per pair, from one part
     static constexpr size_t kHand = kHandD + kHandB + kHandC + H * kPartY;
-    static constexpr size_t kBytes = kRing * kSlot + 2 * kHand + 8 * kRing;
-    static_assert(kBC % kPrep == 0 && kBytes <= 227 * 1024, "");
+    static constexpr size_t kBytes = kRing * kSlot + kHands * kHand + 8 * kRing;
+    static_assert(kBC % kPrep == 0 && kBytes <= 227 * 1024 && kRing >= kHands + 2, "");
 };
 
 // The inputs as matrices of rows, for tensor copies of a tile's 64 channels (or
@@ -210,12 +219,12 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     const int cbase = g * per_group + (chunk % blocks) * 2 * kPairs;
     const int cend = min(cbase + 2 * kPairs, (g + 1) * per_group);
 
-    auto hand = [&](int k) { return smem + kRing * L::kSlot + (k & 1) * L::kHand; };
+    auto hand = [&](int k) { return smem + kRing * L::kSlot + k % kHands * L::kHand; };
     auto hand_b = [&](int k) { return hand(k) + L::kHandD; };
     auto hand_c = [&](int k) { return hand(k) + L::kHandD + L::kHandB; };
     auto part_y = [&](int k, int part) { return hand(k) + L::kHandD + L::kHandB + L::kHandC + part * L::kPartY; };
     auto next = [](int at) { return at + 1 == kRing ? 0 : at + 1; };
-    uint64_t *landed = reinterpret_cast<uint64_t *>(smem + kRing * L::kSlot + 2 * L::kHand);  // per ring slot
+    uint64_t *landed = reinterpret_cast<uint64_t *>(smem + kRing * L::kSlot + kHands * L::kHand);  // per ring slot
     uint64_t limit = kWaitLimit;
     auto wait_for = [&](int at, int round) {  // the bulk copies of ring slot `at`, its `round`th use
         if (!sm100::mbar_wait(&landed[at], round & 1, limit)) {
@@ -233,7 +242,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     // Barriers.  Of hand-over buffer i: kFull + i, prepared (prepare -> recurrence); kDone + i,
     // read, and y written (recurrence -> prepare, finish).  kFree: y read and the ring slot with
     // it (finish -> prepare).  kPieces has no finishing warps.
-    enum { kFull = 1, kDone = 3, kFree = 5 };
+    enum { kFull = 1, kDone = kFull + kHands, kFree = kDone + kHands };
     constexpr int kFullN = kRecur + kPrep, kDoneN = MODE == kPieces ? kRecur + kPrep : kRecur + 2 * kPrep;
 
     // Two blocks of 384 threads leave 80 registers each: 112 for the recurrence warps, 64 for
@@ -329,7 +338,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
                     for (int j = 0; j < 2; ++j)  // a lane has tokens 2 q and 2 q + 1 of the eight
                         *reinterpret_cast<f32x2 *>(yout + (t - 7 + j) * 16 * kYPitch) = pack2(keep[j], keep[2 + j]);
             };
-            part_sync(kFull + (k & 1), kFullN);
+            part_sync(kFull + k % kHands, kFullN);
             load(0);
             if (kAhead) {
                 load(1);
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
                 dsum = add2(dsum, tile_sum);
             else
                 pick(kTile - 1);
-            part_arrive(kDone + (k & 1), kDoneN);
+            part_arrive(kDone + k % kHands, kDoneN);
         }
         float d1[2];
         unpack2(dsum, d1[0], d1[1]);
@@ -428,7 +437,26 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
             v[i] = pack2(p && 2 * i < nc ? p[c + 2 * i] : 0.f, p && 2 * i + 1 < nc ? p[c + 2 * i + 1] : 0.f);
     };
 
+    // One thread fetches a tile: whole boxes, where rows past the piece's end are another's or
+    // zeros, and masked later.  Five copies take a warp longer than its share of a tile's other
+    // work, so it is a finishing warp's, the ones with time to spare.
+    auto fetch = [&](int k, int at) {
+        if (k >= ntiles) return;
+        constexpr int kX = L::kRowElems * sizeof(E), kB = 2 * L::kBC * sizeof(E);
+        unsigned char *r = smem + at * L::kSlot;
+        const int y = (int)(first + k * kTile), sc = g * a.d_state;
+        sm100::mbar_arrive_expect_tx(&landed[at], MODE == kPieces ? 2 * kX + kB : (a.z ? 3 : 2) * kX + 2 * kB);
+        copy_box(r, &maps.x, cbase, y, &landed[at]);
+        copy_box(r + kX, &maps.delta, cbase, y, &landed[at]);
+        copy_box(r + 3 * kX, &maps.b, sc, y, &landed[at]);
+        if (MODE == kPieces) return;
+        copy_box(r + 3 * kX + kB, &maps.c, sc, y, &landed[at]);
+        if (a.z) copy_box(r + 2 * kX, &maps.z, cbase, y, &landed[at]);
+    };
+
     if (MODE != kPieces && threadIdx.x >= kRecur + kPrep) {  // ---- finish
+        if (BULK && id == 0)
+            for (int k = 0; k < kRing - 1; ++k) fetch(k, k);
         f32x2 D[4];
         column(a.D, D);
         E *out = static_cast<E *>(a.y) + mine * a.ld_y + cc;
@@ -437,7 +465,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
             float x[8], z[8];
             ulonglong2 sum[2];
             if (BULK) wait_for(at, round);
-            part_sync(kDone + (k & 1), kDoneN);
+            part_sync(kDone + k % kHands, kDoneN);
             ld_vec<E, 8>(r + off, x);
             if (a.z) ld_vec<E, 8>(r + 2 * L::kRowElems + off, z);
 #pragma unroll
@@ -467,6 +495,8 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
                 }
                 out += kTile * a.ld_y;
             }
+            // every finishing thread came to this tile's barrier, so the slot before is free
+            if (BULK && id == 0) fetch(k - 1 + kRing, at == 0 ? kRing - 1 : at - 1);
         }
         return;
     }
@@ -512,19 +542,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     };
     auto issue = [&](int k, int at) {  // tile k into ring slot `at`
         if (BULK) {
-            if (id != 0 || k >= ntiles) return;
-            // whole boxes: rows past the piece's end are another's or zeros, and masked later
-            constexpr int kX = L::kRowElems * sizeof(E), kB = 2 * L::kBC * sizeof(E);
-            unsigned char *r = smem + at * L::kSlot;
-            const int y = (int)(first + k * kTile), sc = g * a.d_state;
-            sm100::mbar_arrive_expect_tx(&landed[at],
-                                         MODE == kPieces ? 2 * kX + kB : (a.z ? 3 : 2) * kX + 2 * kB);
-            copy_box(r, &maps.x, cbase, y, &landed[at]);
-            copy_box(r + kX, &maps.delta, cbase, y, &landed[at]);
-            copy_box(r + 3 * kX, &maps.b, sc, y, &landed[at]);
-            if (MODE == kPieces) return;
-            copy_box(r + 3 * kX + kB, &maps.c, sc, y, &landed[at]);
-            if (a.z) copy_box(r + 2 * kX, &maps.z, cbase, y, &landed[at]);
+            if (MODE == kPieces && id == 0) fetch(k, at);
             return;
         }
         if (k < ntiles) {
@@ -609,27 +627,28 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
         hold(k);
         issue(k, k);
     }
-    if (ntiles > 0) {
-        if (BULK) wait_for(0, 0); else copy_wait<kRing - 1>();
-        prepare(0, 0);
-        part_arrive(kFull, kFullN);
-    }
-    if (ntiles > 1) {
-        if (BULK) wait_for(1, 0); else copy_wait<kRing - 2>();
-        prepare(1, 1);
-        part_arrive(kFull + 1, kFullN);
+    auto wait_tile = [&](int k, int at, int round) {  // copies of tile k, of at least k + 1 and at most
+        if (BULK)                                      // k + kRing - kHands + 1 issued by this thread
+            wait_for(at, round);
+        else
+            copy_wait<kRing - kHands - 1>();
+    };
+    if (!BULK) copy_wait<kRing - kHands>();
+    for (int k = 0; k < kHands && k < ntiles; ++k) {
+        if (BULK) wait_for(k, 0);
+        prepare(k, k);
+        part_arrive(kFull + k, kFullN);
     }
 #pragma unroll 1
-    for (int k = 0, done = 0, ahead = 2, round = 0; k < ntiles; ++k, done = next(done), ahead = next(ahead)) {
+    for (int k = 0, done = 0, ahead = kHands % kRing, round = 0; k < ntiles;
+         ++k, done = next(done), ahead = next(ahead)) {
         round += ahead == 0;
         hold(k + kRing);
-        if (k + 2 < ntiles) {
-            if (BULK) wait_for(ahead, round); else copy_wait<kRing - 3>();
-        }
-        part_sync(kDone + (k & 1), kDoneN);
-        if (k + 2 < ntiles) prepare(k + 2, ahead);
+        if (k + kHands < ntiles) wait_tile(k + kHands, ahead, round);
+        part_sync(kDone + k % kHands, kDoneN);
+        if (k + kHands < ntiles) prepare(k + kHands, ahead);
         if (MODE != kPieces) part_sync(kFree, 2 * kPrep);
-        if (k + 2 < ntiles) part_arrive(kFull + (k & 1), kFullN);
+        if (k + kHands < ntiles) part_arrive(kFull + k % kHands, kFullN);
         issue(k + kRing, done);
     }
 }
