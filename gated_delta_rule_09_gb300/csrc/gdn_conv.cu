@@ -7,7 +7,8 @@
 // 16 bytes of channels (one wide access per token, a block's threads side by
 // side along the row) and walks a tile of tokens with the last width - 1 inputs
 // in registers: every input is loaded once, plus the width - 1 rows ahead of
-// each tile.
+// each tile.  What keeps HBM busy is bytes on their way: a thread has 8 to 12
+// tokens in flight through shared memory.
 #include "gdn_layer.h"
 #include "gdn_layer.cuh"
 
@@ -16,7 +17,8 @@ namespace {
 using namespace gdn_layer;
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;  // tokens per load batch; the next batch is in flight while one is used
+constexpr int kGroup = 4;   // tokens loaded at a time
+constexpr int kStages = 3;  // groups held or on their way
 
 // Arithmetic on VEC channels, in pairs where there are pairs.
 template <int VEC> struct Lanes {
@@ -99,6 +101,7 @@ __global__ void __launch_bounds__(kThreads)
     gdn_conv_fwd_kernel(const GdnConvArgs a, int tl, int tiles)
 {
     typedef typename Word<VEC * sizeof(E)>::type Vec;
+    extern __shared__ __align__(16) unsigned char smem[];
     Span s;
     if (!find_span(a.cu_seqlens, a.N, a.T, tl, blockIdx.x, tiles, a.status, s)) return;
     const int c0 = (blockIdx.y * kThreads + threadIdx.x) * VEC;
@@ -153,27 +156,53 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
         st_vec<E, VEC>(y + (int64_t)t * a.ld_y, r);
     };
-    auto load = [&](Vec (&u)[kUnroll], int t) {  // past the end: the last token again, not used
+    auto use = [&](const Vec (&u)[kGroup], int t) {
+        if (t + kGroup <= t1) {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) u[k] = input(min(t + k, t1 - 1));
-    };
-    auto use = [&](const Vec (&u)[kUnroll], int t) {
-        if (t + kUnroll <= t1) {
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) token(t + k, u[k]);
+            for (int k = 0; k < kGroup; ++k) token(t + k, u[k]);
         } else {
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
+            for (int k = 0; k < kGroup; ++k)
                 if (t + k < t1) token(t + k, u[k]);
         }
     };
-    Vec u[2][kUnroll];
-    load(u[0], t0);
-    for (int t = t0; t < t1; t += 2 * kUnroll) {
-        load(u[1], t + kUnroll);
-        use(u[0], t);
-        if (t + 2 * kUnroll < t1) load(u[0], t + 2 * kUnroll);
-        use(u[1], t + kUnroll);
+    if constexpr (sizeof(Vec) == 16) {
+        // A column of shared memory per thread, filled and read by it alone.
+        Vec *ring = reinterpret_cast<Vec *>(smem) + threadIdx.x;
+        auto fetch = [&](int t, int stage) {
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k)
+                if (t + k < t1)
+                    copy_async<sizeof(Vec)>(ring + (stage * kGroup + k) * kThreads, x + (int64_t)(t + k) * a.ld_x);
+            copy_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(t0 + i * kGroup, i);
+        int at = 0, to = kStages - 1;
+#pragma unroll 1
+        for (int t = t0; t < t1; t += kGroup) {
+            fetch(t + (kStages - 1) * kGroup, to);
+            copy_wait<kStages - 1>();
+            Vec u[kGroup];
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) u[k] = ring[(at * kGroup + k) * kThreads];
+            use(u, t);
+            to = at;  // what was read is filled next
+            at = at + 1 == kStages ? 0 : at + 1;
+        }
+    } else {  // small words, and so few registers: more threads fit instead
+        Vec u[2][kGroup];
+        auto load = [&](Vec (&v)[kGroup], int t) {  // past the end: the last token again, not used
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) v[k] = input(min(t + k, t1 - 1));
+        };
+        load(u[0], t0);
+        for (int t = t0; t < t1; t += 2 * kGroup) {
+            load(u[1], t + kGroup);
+            use(u[0], t);
+            if (t + 2 * kGroup < t1) load(u[0], t + 2 * kGroup);
+            use(u[1], t + kGroup);
+        }
     }
 }
 
@@ -237,13 +266,16 @@ cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
     const int blocks = (a.channels / VEC + (a.channels % VEC != 0) + kThreads - 1) / kThreads;
     // The tile length of at least 16 tokens that takes the fewest token times: blocks run in
     // waves of what is resident at once, and a tile reads width - 1 rows ahead of its own.
+    constexpr size_t smem = VEC == 1 ? 0 : kStages * kGroup * kThreads * VEC * sizeof(E);
     static int resident = 0;  // blocks per device of this kind; the same for every caller
     if (!resident) {
         int dev = 0, sms = 0, n = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gdn_conv_fwd_kernel<E, VEC, W>, kThreads, 0);
+            e = cudaFuncSetAttribute(gdn_conv_fwd_kernel<E, VEC, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gdn_conv_fwd_kernel<E, VEC, W>, kThreads, smem);
         if (e != cudaSuccess) return e;
         resident = sms * (n > 0 ? n : 1);
     }
@@ -259,7 +291,7 @@ cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
     }
     const int tiles = a.T > tl ? (a.T + tl - 1) / tl : 1;
     const int64_t slots = a.cu_seqlens ? (int64_t)a.T / tl + a.N : (int64_t)a.N * tiles;
-    gdn_conv_fwd_kernel<E, VEC, W><<<dim3((unsigned)slots, blocks), kThreads, 0, s>>>(a, tl, tiles);
+    gdn_conv_fwd_kernel<E, VEC, W><<<dim3((unsigned)slots, blocks), kThreads, smem, s>>>(a, tl, tiles);
     return cudaGetLastError();
 }
 

@@ -366,29 +366,30 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
                 if (t + kAhead < kTile) decay(t + kAhead);
 #pragma unroll
                 for (int i = 0; i < NS; ++i) h[i] = fma2(e[t % (1 + kAhead)][i], h[i], w[t % (1 + kAhead)][i]);
-                if (MODE == kPieces) continue;
-                // two sums, so that the products do not wait for one another
+                if constexpr (MODE != kPieces) {
+                    // two sums, so that the products do not wait for one another
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[t & 1][i][u] = 0.f;
+                        for (int u = 0; u < 4; ++u) acc[t & 1][i][u] = 0.f;
 #pragma unroll
-                for (int i = 0; i < NS; i += 2) {  // columns q and q + 4: states i, i + 1
-                    float(&d)[4] = acc[t & 1][i / 2 % 2];
-                    float h0, h1, h2, h3;
-                    unpack2(h[i], h0, h1);
-                    unpack2(h[i + 1], h2, h3);
-                    if (sizeof(E) == 4) {
-                        const float p0 = tf32_part(h0), p1 = tf32_part(h1), p2 = tf32_part(h2), p3 = tf32_part(h3);
-                        mma_tf32(d, h0 - p0, h1 - p1, h2 - p2, h3 - p3, C2[i], C2[i + 1], d);
-                        mma_tf32(d, h0 - p0, h1 - p1, h2 - p2, h3 - p3, C1[i], C1[i + 1], d);
-                        mma_tf32(d, p0, p1, p2, p3, C2[i], C2[i + 1], d);
-                        mma_tf32(d, p0, p1, p2, p3, C1[i], C1[i + 1], d);
-                    } else {
-                        mma_tf32(d, h0, h1, h2, h3, C1[i], C1[i + 1], d);
+                    for (int i = 0; i < NS; i += 2) {  // columns q and q + 4: states i, i + 1
+                        float(&d)[4] = acc[t & 1][i / 2 % 2];
+                        float h0, h1, h2, h3;
+                        unpack2(h[i], h0, h1);
+                        unpack2(h[i + 1], h2, h3);
+                        if (sizeof(E) == 4) {
+                            const float p0 = tf32_part(h0), p1 = tf32_part(h1), p2 = tf32_part(h2), p3 = tf32_part(h3);
+                            mma_tf32(d, h0 - p0, h1 - p1, h2 - p2, h3 - p3, C2[i], C2[i + 1], d);
+                            mma_tf32(d, h0 - p0, h1 - p1, h2 - p2, h3 - p3, C1[i], C1[i + 1], d);
+                            mma_tf32(d, p0, p1, p2, p3, C2[i], C2[i + 1], d);
+                            mma_tf32(d, p0, p1, p2, p3, C1[i], C1[i + 1], d);
+                        } else {
+                            mma_tf32(d, h0, h1, h2, h3, C1[i], C1[i + 1], d);
+                        }
                     }
+                    if (t > 0) pick(t - 1);
                 }
-                if (t > 0) pick(t - 1);
             }
             if (MODE == kPieces)
                 dsum = add2(dsum, tile_sum);
