@@ -61,6 +61,13 @@ template <int VEC, int W> struct Taps {
         if constexpr (VEC == 1) {
 #pragma unroll
             for (int j = 0; j < W; ++j) f[j] = a.weight[(size_t)c0 * W + j];
+        } else if constexpr (VEC == 2) {
+#pragma unroll
+            for (int i = 0; i < VEC * W; i += 2) {
+                const float2 t = *reinterpret_cast<const float2 *>(a.weight + (size_t)c0 * W + i);
+                f[i] = t.x;
+                f[i + 1] = t.y;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < VEC * W; i += 4) {  // VEC W is a multiple of 4, and so is c0
@@ -252,21 +259,21 @@ __global__ void __launch_bounds__(kThreads) gdn_conv_step_kernel(const GdnConvAr
     }
 }
 
-template <typename E>
-bool vector_rows(const GdnConvArgs &a)
+// Whether rows, states and taps can be read in words of V elements.
+template <typename E> bool words_of(const GdnConvArgs &a, int V)
 {
-    constexpr int V = 16 / sizeof(E);
-    return a.channels % V == 0 && a.ld_x % V == 0 && a.ld_y % V == 0 && aligned16(a.x) &&
-           aligned16(a.y) && aligned16(a.state_in) && aligned16(a.state_out) && aligned16(a.weight);
+    const size_t al = V * sizeof(E);
+    return a.channels % V == 0 && a.ld_x % V == 0 && a.ld_y % V == 0 && aligned_to(a.x, al) && aligned_to(a.y, al) &&
+           aligned_to(a.state_in, al) && aligned_to(a.state_out, al) && aligned_to(a.weight, V == 2 ? 8 : 16);
 }
 
 template <typename E, int VEC, int W>
 cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
 {
-    const int blocks = (a.channels / VEC + (a.channels % VEC != 0) + kThreads - 1) / kThreads;
+    const int blocks = (a.channels / VEC + kThreads - 1) / kThreads;
     // The tile length of at least 16 tokens that takes the fewest token times: blocks run in
     // waves of what is resident at once, and a tile reads width - 1 rows ahead of its own.
-    constexpr size_t smem = VEC == 1 ? 0 : kStages * kGroup * kThreads * VEC * sizeof(E);
+    constexpr size_t smem = VEC <= 2 ? 0 : kStages * kGroup * kThreads * VEC * sizeof(E);
     static int resident = 0;  // blocks per device of this kind; the same for every caller
     if (!resident) {
         int dev = 0, sms = 0, n = 0;
@@ -298,9 +305,9 @@ cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
 template <typename E, int VEC, int W>
 cudaError_t step(const GdnConvArgs &a, cudaStream_t s)
 {
-    const int blocks = (a.channels / VEC + (a.channels % VEC != 0) + kThreads - 1) / kThreads;
+    const int blocks = (a.channels / VEC + kThreads - 1) / kThreads;
     // Four sequences per thread once that leaves a block or two per SM.
-    if ((int64_t)a.N * blocks >= 1024)
+    if ((int64_t)a.N * blocks >= 384)
         gdn_conv_step_kernel<E, VEC, W, 4><<<dim3((a.N + 3) / 4, blocks), kThreads, 0, s>>>(a);
     else
         gdn_conv_step_kernel<E, VEC, W, 1><<<dim3(a.N, blocks), kThreads, 0, s>>>(a);
@@ -311,7 +318,8 @@ template <bool STEP, typename E, int W>
 cudaError_t by_vector(const GdnConvArgs &a, cudaStream_t s)
 {
     constexpr int V = 16 / sizeof(E);
-    if (vector_rows<E>(a)) return STEP ? step<E, V, W>(a, s) : fwd<E, V, W>(a, s);
+    if (words_of<E>(a, V)) return STEP ? step<E, V, W>(a, s) : fwd<E, V, W>(a, s);
+    if (words_of<E>(a, 2)) return STEP ? step<E, 2, W>(a, s) : fwd<E, 2, W>(a, s);
     return STEP ? step<E, 1, W>(a, s) : fwd<E, 1, W>(a, s);
 }
 

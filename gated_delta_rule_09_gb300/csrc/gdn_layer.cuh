@@ -71,6 +71,7 @@ __device__ __forceinline__ void narrow(unsigned short &u, const float (&x)[1])
 {
     u = (unsigned short)narrow_pair(x[0], 0.f);
 }
+__device__ __forceinline__ void narrow(uint32_t &u, const float (&x)[2]) { u = narrow_pair(x[0], x[1]); }
 __device__ __forceinline__ void narrow(uint2 &u, const float (&x)[4])
 {
     u = make_uint2(narrow_pair(x[0], x[1]), narrow_pair(x[2], x[3]));
@@ -81,6 +82,10 @@ __device__ __forceinline__ void narrow(uint4 &u, const float (&x)[8])
                    narrow_pair(x[6], x[7]));
 }
 __device__ __forceinline__ void narrow(uint32_t &u, const float (&x)[1]) { u = __float_as_uint(x[0]); }
+__device__ __forceinline__ void narrow(uint2 &u, const float (&x)[2])
+{
+    u = make_uint2(__float_as_uint(x[0]), __float_as_uint(x[1]));
+}
 __device__ __forceinline__ void narrow(uint4 &u, const float (&x)[4])
 {
     u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),

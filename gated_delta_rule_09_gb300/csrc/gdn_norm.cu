@@ -18,30 +18,41 @@ using namespace gdn_layer;
 
 constexpr int kThreads = 256;
 
-// Sum over the team: T lanes of a warp, or the block.
-template <bool BLOCK> __device__ __forceinline__ float team_sum(float v, int T, float *sh)
-{
-    if constexpr (BLOCK) {
+// Sums over the team, T lanes of a warp or the block, of R values at a time.  A
+// block's warps meet in one of two buffers: by the time one is filled again, the
+// barrier of the sum between has seen everybody through reading it.
+template <int BLOCK, int R> struct TeamSum {
+    float (*sh)[R][kThreads / 32];
+    int turn;
+
+    __device__ __forceinline__ void operator()(float (&v)[R], int T)
+    {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        __syncthreads();  // sh may still be read from the previous sum
-        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = 0.f;
+        for (int r = 0; r < R; ++r)
+            for (int o = (BLOCK ? 32 : T) >> 1; o > 0; o >>= 1) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+        if constexpr (BLOCK != 0) {
+            if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
-    } else {
-        for (int o = T >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                for (int r = 0; r < R; ++r) sh[turn][r][threadIdx.x >> 5] = v[r];
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                v[r] = 0.f;
+#pragma unroll
+                for (int i = 0; i < BLOCK / 32; ++i) v[r] += sh[turn][r][i];
+            }
+            turn ^= 1;
+        }
     }
-    return v;
-}
+};
 
 // K words of VEC elements per thread and row, kRows rows at a time.  `walkers`
 // teams share the rows of a group.
-template <typename E, int VEC, int K, int kRows, bool BLOCK>
-__global__ void __launch_bounds__(kThreads) gdn_group_norm_kernel(const GdnNormArgs a, int T, int walkers)
+template <typename E, int VEC, int K, int kRows, int BLOCK>
+__global__ void __launch_bounds__(BLOCK ? BLOCK : kThreads) gdn_group_norm_kernel(const GdnNormArgs a, int T, int walkers)
 {
-    __shared__ float sh[kThreads / 32];
+    __shared__ __align__(16) float sh[BLOCK ? 2 : 1][kRows][kThreads / 32];
+    TeamSum<BLOCK, kRows> team_sum = {sh, 0};
     typedef typename Word<VEC * sizeof(E)>::type Vec;
     constexpr int P = VEC > 1 ? VEC / 2 : 1;  // pairs, for packed arithmetic; a lone element is half a pair
     const int width = a.channels / a.groups;
@@ -108,7 +119,6 @@ __global__ void __launch_bounds__(kThreads) gdn_group_norm_kernel(const GdnNormA
     for (int64_t turn = 0; turn * stride < a.rows; ++turn, row0 += stride) {
         f32x2 c[kRows][K][P];  // about the mean
         Vec gn[kRows][K];
-        float rstd[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
 #pragma unroll
@@ -117,28 +127,39 @@ __global__ void __launch_bounds__(kThreads) gdn_group_norm_kernel(const GdnNormA
                 gn[r][k] = gv[r][k];
             }
         if (row0 + stride < a.rows) load(row0 + stride);
+        float mean[kRows], rstd[kRows];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            f32x2 sum = 0, sq = 0;
-            float mean = 0.f;
-            if (!a.rms) {
+        for (int r = 0; r < kRows; ++r) mean[r] = 0.f;
+        if (!a.rms) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                f32x2 sum = 0;
 #pragma unroll
                 for (int k = 0; k < K; ++k)
 #pragma unroll
                     for (int i = 0; i < P; ++i) sum = add2(sum, c[r][k][i]);
-                mean = team_sum<BLOCK>(both(sum), T, sh) * inv;
+                mean[r] = both(sum);
             }
+            team_sum(mean, T);
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const f32x2 off = dup2(-mean[r] * inv);
+            f32x2 sq = 0;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!has[k]) continue;
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    c[r][k][i] = add2(c[r][k][i], dup2(-mean));
+                    c[r][k][i] = add2(c[r][k][i], off);
                     sq = fma2(c[r][k][i], c[r][k][i], sq);
                 }
             }
-            rstd[r] = rsqrtf(team_sum<BLOCK>(both(sq), T, sh) * inv + a.eps);
+            rstd[r] = both(sq);
         }
+        team_sum(rstd, T);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) rstd[r] = rsqrtf(rstd[r] * inv + a.eps);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             if (!live || row0 + r >= a.rows) break;
@@ -175,23 +196,26 @@ __global__ void __launch_bounds__(kThreads) gdn_group_norm_kernel(const GdnNormA
 template <typename E>
 __global__ void __launch_bounds__(kThreads) gdn_group_norm_wide_kernel(const GdnNormArgs a)
 {
-    __shared__ float sh[kThreads / 32];
+    __shared__ __align__(16) float sh[2][1][kThreads / 32];
+    TeamSum<kThreads, 1> team_sum = {sh, 0};
     const int width = a.channels / a.groups;
     const int64_t row = blockIdx.x / a.groups;
     const int c0 = (int)(blockIdx.x % a.groups) * width;
     const E *x = static_cast<const E *>(a.x) + row * a.ld_x + c0;
     const E *gate = a.gate ? static_cast<const E *>(a.gate) + row * a.ld_gate + c0 : nullptr;
     E *y = static_cast<E *>(a.y) + row * a.ld_y + c0;
-    float mean = 0.f, q = 0.f;
+    float sum[1] = {0.f}, q[1] = {0.f};
     if (!a.rms) {
-        for (int i = threadIdx.x; i < width; i += kThreads) mean += to_f(x[i]);
-        mean = team_sum<true>(mean, 0, sh) / width;
+        for (int i = threadIdx.x; i < width; i += kThreads) sum[0] += to_f(x[i]);
+        team_sum(sum, kThreads);
     }
+    const float mean = sum[0] / width;
     for (int i = threadIdx.x; i < width; i += kThreads) {
         const float v = to_f(x[i]) - mean;
-        q = fmaf(v, v, q);
+        q[0] = fmaf(v, v, q[0]);
     }
-    const float rstd = rsqrtf(team_sum<true>(q, 0, sh) / width + a.eps);
+    team_sum(q, kThreads);
+    const float rstd = rsqrtf(q[0] / width + a.eps);
     for (int i = threadIdx.x; i < width; i += kThreads) {
         float u = fmaf((to_f(x[i]) - mean) * rstd, a.weight ? a.weight[c0 + i] : 1.f, a.bias ? a.bias[c0 + i] : 0.f);
         if (a.act == GDN_ACT_SILU) u = silu(u);
@@ -199,61 +223,81 @@ __global__ void __launch_bounds__(kThreads) gdn_group_norm_wide_kernel(const Gdn
     }
 }
 
-template <typename E, int VEC, int K, int kRows, bool BLOCK>
+template <typename E, int VEC, int K, int kRows, int BLOCK>
 cudaError_t launch(const GdnNormArgs &a, int T, cudaStream_t s)
 {
     // As many teams as are resident at once, or as there are rows for.
-    static int resident = 0;  // threads' teams per device of this kind; the same for every caller
-    const int per = BLOCK ? 1 : kThreads / T;
-    if (!resident) {
+    static int fit = 0;  // blocks per device of this kind; the same for every caller
+    constexpr int threads = BLOCK ? BLOCK : kThreads;
+    const int per = threads / T;
+    if (!fit) {
         int dev = 0, sms = 0, blocks = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &blocks, gdn_group_norm_kernel<E, VEC, K, kRows, BLOCK>, kThreads, 0);
+                &blocks, gdn_group_norm_kernel<E, VEC, K, kRows, BLOCK>, threads, 0);
         if (e != cudaSuccess) return e;
-        resident = sms * (blocks > 0 ? blocks : 1);
+        fit = sms * (blocks > 0 ? blocks : 1);
     }
     const int64_t turns = (a.rows + kRows - 1) / kRows;
-    int64_t walkers = ((int64_t)resident * per + a.groups - 1) / a.groups;
+    int64_t walkers = ((int64_t)fit * per + a.groups - 1) / a.groups;
     if (walkers > turns) walkers = turns;
     // equal shares: the last turn is as full as the others
     const int64_t each = (turns + walkers - 1) / walkers;
     walkers = (turns + each - 1) / each;
     const int64_t blocks = (walkers * a.groups + per - 1) / per;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    gdn_group_norm_kernel<E, VEC, K, kRows, BLOCK><<<(unsigned)blocks, kThreads, 0, s>>>(a, T, (int)walkers);
+    gdn_group_norm_kernel<E, VEC, K, kRows, BLOCK><<<(unsigned)blocks, threads, 0, s>>>(a, T, (int)walkers);
     return cudaGetLastError();
 }
 
-// The team by the group's words: lanes of a warp up to 2 words each, a block up
-// to 4.
+// The team by the group's words: as many lanes of a warp as there are words, and
+// beyond that few words per lane and two rows at a time, whichever kept more
+// loads in flight.
 template <typename E, int VEC> cudaError_t by_width(const GdnNormArgs &a, cudaStream_t s)
 {
     const int words = (a.channels / a.groups + VEC - 1) / VEC;
     if (words <= 32) {
         int T = 1;
         while (T < words) T *= 2;
-        return launch<E, VEC, 1, 2, false>(a, T, s);
+        return launch<E, VEC, 1, 2, 0>(a, T, s);
     }
-    if (words <= 64) return launch<E, VEC, 2, 1, false>(a, 32, s);
-    if (words <= kThreads) return launch<E, VEC, 1, 1, true>(a, kThreads, s);
-    if (words <= 2 * kThreads) return launch<E, VEC, 2, 1, true>(a, kThreads, s);
-    if (words <= 4 * kThreads) return launch<E, VEC, 4, 1, true>(a, kThreads, s);
+    if constexpr (VEC <= 2) {
+        if (words <= 64) return launch<E, VEC, 2, 2, 0>(a, 32, s);
+        if (words <= 96) return launch<E, VEC, 3, 2, 0>(a, 32, s);
+        if (words <= 128) return launch<E, VEC, 4, 2, 0>(a, 32, s);
+        if (words <= 160) return launch<E, VEC, 5, 1, 0>(a, 32, s);
+        if (words <= 192) return launch<E, VEC, 6, 1, 0>(a, 32, s);
+        if (words <= 256) return launch<E, VEC, 2, 2, 128>(a, 128, s);
+        if (words <= 512) return launch<E, VEC, 4, 2, 128>(a, 128, s);
+        if (words <= 1024) return launch<E, VEC, 4, 2, 256>(a, 256, s);
+    } else {
+        if (words <= 64) return launch<E, VEC, 2, 1, 0>(a, 32, s);
+        if (words <= 128) return launch<E, VEC, 1, 2, 128>(a, 128, s);
+        if (words <= 256) return launch<E, VEC, 1, 2, 256>(a, 256, s);
+        if (words <= 512) return launch<E, VEC, 2, 1, 256>(a, 256, s);
+        if (words <= 1024) return launch<E, VEC, 4, 1, 256>(a, 256, s);
+    }
     const int64_t blocks = a.rows * a.groups;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     gdn_group_norm_wide_kernel<E><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
+// Whether all rows of all groups, and the weights, can be read in words of V elements.
+template <typename E> bool words_of(const GdnNormArgs &a, int V)
+{
+    const size_t al = V * sizeof(E);
+    return a.channels / a.groups % V == 0 && a.ld_x % V == 0 && a.ld_y % V == 0 && (!a.gate || a.ld_gate % V == 0) &&
+           aligned_to(a.x, al) && aligned_to(a.y, al) && aligned_to(a.gate, al) &&
+           aligned_to(a.weight, V == 2 ? 8 : 16) && aligned_to(a.bias, V == 2 ? 8 : 16);
+}
+
 template <typename E> cudaError_t by_rows(const GdnNormArgs &a, cudaStream_t s)
 {
     constexpr int V = 16 / sizeof(E);
-    const bool words = a.channels / a.groups % V == 0 && a.ld_x % V == 0 && a.ld_y % V == 0 &&
-                       (!a.gate || a.ld_gate % V == 0) && aligned16(a.x) && aligned16(a.y) && aligned16(a.gate) &&
-                       aligned16(a.weight) && aligned16(a.bias);
-    return words ? by_width<E, V>(a, s) : by_width<E, 1>(a, s);
+    return words_of<E>(a, V) ? by_width<E, V>(a, s) : words_of<E>(a, 2) ? by_width<E, 2>(a, s) : by_width<E, 1>(a, s);
 }
 
 }  // namespace

@@ -166,7 +166,7 @@ template <typename E, int LPC> cudaError_t by_rows(const GdnSsmArgs &a, cudaStre
     constexpr int kRows = LPC < 4 ? LPC : 4;
     const int per = kThreads / LPC;
     const int64_t blocks = (int64_t)((a.N + kRows - 1) / kRows) * ((a.channels + per - 1) / per);
-    return blocks >= 1024 ? launch_step<E, LPC, kRows>(a, s) : launch_step<E, LPC, 1>(a, s);
+    return blocks >= 512 ? launch_step<E, LPC, kRows>(a, s) : launch_step<E, LPC, 1>(a, s);
 }
 
 template <typename E> cudaError_t step(const GdnSsmArgs &a, cudaStream_t s)
