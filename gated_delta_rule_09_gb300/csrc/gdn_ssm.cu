@@ -9,6 +9,9 @@
 // lanes of a channel (d_state padded to 4 LPC) are neighbours, and their parts
 // of y meet in a butterfly.  A has the size of a sequence's states, so a thread
 // keeps its four of A for kRows sequences; their loads are in flight together.
+// 256 sequences x 4096 channels x 16 states, bf16: 31 us, 4.6 TB/s (1024
+// sequences 5.2); with one sequence per thread, and softplus, gate and store in
+// every lane of a channel, 46.
 #include "gdn_layer.h"
 #include "gdn_layer.cuh"
 
@@ -160,7 +163,9 @@ template <typename E, int LPC, int kRows> cudaError_t launch_step(const GdnSsmAr
 }
 
 // Up to four sequences per thread once that still leaves a few blocks per SM; a
-// small batch is spread as widely as it goes.
+// small batch is spread as widely as it goes.  bf16, 4096 channels x 16 states,
+// us with one against four: 8 sequences (256 blocks of four) 3.6 : 4.2, 16
+// 5.3 : 4.9, 32 7.7 : 6.0, 256 43.3 : 31.0.
 template <typename E, int LPC> cudaError_t by_rows(const GdnSsmArgs &a, cudaStream_t s)
 {
     constexpr int kRows = LPC < 4 ? LPC : 4;
@@ -196,7 +201,10 @@ int gdn_ssm_sms()
 // through a token of a block every kShared ns when blocks share it, and cut
 // sequences take kCut ns instead, the piece pass included, but not less than a
 // piece alone in each of the two launches and kLaunch.  A grid of a few blocks
-// per SM is long enough to even out.
+// per SM is long enough to even out.  One sequence of 131 072 tokens x 1024
+// channels: 1.09 ms cut, 6.26 ms whole (16 blocks); four of 4096 tokens x 2048
+// channels: 208 us whole, 261 to 316 cut into 512 to 2048 tokens; a pack of eight,
+// 27 610 tokens with a longest of 7671, x 4096 channels: 656 us whole, 857 cut.
 void gdn_ssm_plan(int N, int T, int channels, int d_state, bool packed, int asked, int *segment,
                   int64_t *piece_slots)
 {
