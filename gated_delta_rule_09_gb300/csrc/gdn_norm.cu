@@ -32,8 +32,11 @@ template <int BLOCK, int R> struct TeamSum {
     __device__ __forceinline__ void operator()(float (&v)[R], int T)
     {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            for (int o = (BLOCK ? 32 : T) >> 1; o > 0; o >>= 1) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+        for (int o = 16; o > 0; o >>= 1) {
+            if (!BLOCK && o >= T) continue;
+#pragma unroll
+            for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+        }
         if constexpr (BLOCK != 0) {
             if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -101,26 +104,33 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : kThreads) gdn_group_norm_kerne
         return VEC > 1 ? lo + hi : lo;
     };
     Vec xv[kRows][K], gv[kRows][K];
-    auto load = [&](int64_t row0) {  // rows past the end repeat the last
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int k = 0; k < K; ++k) xv[r][k] = gv[r][k] = Vec();
+    const float inv = 1.f / width;
+    const int64_t first = team / a.groups * kRows, stride = (int64_t)walkers * kRows;
+    x += first * a.ld_x;
+    gate += first * a.ld_gate;
+    y += first * a.ld_y;
+    auto load = [&](int64_t left) {  // the next rows; past the last the values stay, and are not stored
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            const int64_t row = row0 + r < a.rows ? row0 + r : a.rows - 1;
+            if (r >= left) break;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                xv[r][k] = Vec();
-                gv[r][k] = Vec();
                 if (!has[k]) continue;
-                xv[r][k] = *reinterpret_cast<const Vec *>(x + row * a.ld_x + k * T * VEC);
-                if (gated) gv[r][k] = *reinterpret_cast<const Vec *>(gate + row * a.ld_gate + k * T * VEC);
+                xv[r][k] = *reinterpret_cast<const Vec *>(x + r * a.ld_x + k * T * VEC);
+                if (gated) gv[r][k] = *reinterpret_cast<const Vec *>(gate + r * a.ld_gate + k * T * VEC);
             }
         }
+        x += stride * a.ld_x;
+        gate += stride * a.ld_gate;
     };
-    const float inv = 1.f / width;
-    const int64_t stride = (int64_t)walkers * kRows;
-    int64_t row0 = team / a.groups * kRows;
-    load(row0 < a.rows ? row0 : 0);
+    int64_t left = a.rows - first;
+    load(left);
     // the same number of turns for every team: teams of a warp shuffle together
-    for (int64_t turn = 0; turn * stride < a.rows; ++turn, row0 += stride) {
+    for (int64_t ahead = a.rows; ahead > 0; ahead -= stride, left -= stride, y += stride * a.ld_y) {
         f32x2 c[kRows][K][P];  // about the mean
         Vec gn[kRows][K];
 #pragma unroll
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : kThreads) gdn_group_norm_kerne
                 pairs(xv[r][k], c[r][k]);  // zeros past the width
                 gn[r][k] = gv[r][k];
             }
-        if (row0 + stride < a.rows) load(row0 + stride);
+        load(left - stride);
         float mean[kRows], rstd[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) mean[r] = 0.f;
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : kThreads) gdn_group_norm_kerne
         for (int r = 0; r < kRows; ++r) rstd[r] = rsqrtf(rstd[r] * inv + a.eps);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            if (!live || row0 + r >= a.rows) break;
+            if (!live || r >= left) break;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!has[k]) continue;
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : kThreads) gdn_group_norm_kerne
                     out[VEC > 1 ? 2 * i : 0] = lo;
                     if (VEC > 1) out[VEC > 1 ? 2 * i + 1 : 0] = hi;
                 }
-                st_vec<E, VEC>(y + (row0 + r) * a.ld_y + k * T * VEC, out);
+                st_vec<E, VEC>(y + r * a.ld_y + k * T * VEC, out);
             }
         }
     }
