@@ -10,9 +10,11 @@
 // normalised.  The variance is taken about the mean in a second pass over the
 // registers.
 //
-// Measured, bf16, gated, 16 384 rows of 2048 channels: 16 groups 37 us, 2 groups
-// 34 us, one group 37 us (5.4 to 5.9 TB/s).  Heads of 130 (words of two) 73 us,
-// 115 element by element; heads of 129 116 us, where issue slots bound it.
+// Measured, bf16, gated, 16 384 rows of 2048 channels: 16 groups 34 us, 2 groups
+// 34 us, one group 35 us (5.7 to 6.0 TB/s); fp32 62 us, 6.4 TB/s.  16 groups with
+// the butterflies in a loop over the team's size and row offsets multiplied out
+// for each access: 37 us, 72 % of the issue slots.  Heads of 130 (words of two)
+// 53 us; heads of 129, element by element, 81 us: issue slots.
 #include "gdn_layer.h"
 #include "gdn_layer.cuh"
 
@@ -270,13 +272,14 @@ cudaError_t launch(const GdnNormArgs &a, int T, cudaStream_t s)
 
 // The team by the group's words: as many lanes of a warp as there are words, then
 // what was fastest at each width.  us per 16 384 rows of about 2048 channels, bf16,
-// gated.  16-byte words: heads of 1024 (128 words) 34 with a block of 128 and two
-// rows at a time, 37 with one row, 43 with 4 words per lane of a warp, 55 with a
-// block of 256; heads of 2048 37 with a block of 256, 62 with 8 words per lane.
-// Single elements: heads of 125 95 with 4 per lane, 198 with a block; of 129 116
-// with 5 per lane, 182 with 8, 274 with a block; of 255 94 with a block of 128, 114
-// with 8 per lane; of 293 119 with a block of 128 and two rows, 155 with one row,
-// 236 with a block of 256.
+// gated (a team of T threads, K words each, R rows at a time as T x K x R).
+// 16-byte words: heads of 128 16 x 1 x 2 34, x 3 34, x 1 36; of 512 64 x 1 x 2 33,
+// 32 x 2 x 1 37, 32 x 2 x 2 48; of 1024 128 x 1 x 2 34, 32 x 4 x 1 43, 256 x 1 x 2
+// 55; of 2048 256 x 1 x 2 35, 32 x 8 x 1 62.
+// Single elements: heads of 129 32 x 5 x 2 81, 32 x 5 x 1 87, 64 x 3 x 2 100; of 189
+// 32 x 6 x 1 74, 64 x 3 x 2 82, 32 x 6 x 2 109; of 255 64 x 4 x 2 66, 128 x 2 x 3 78,
+// 128 x 2 x 2 83; of 293 128 x 3 x 2 87, 32 x 10 x 1 95, 128 x 4 x 2 140; of 405
+// 64 x 8 x 1 85, 256 x 2 x 2 102, 128 x 4 x 2 110; of 679 256 x 4 x 2 95, x 1 135.
 template <typename E, int VEC> cudaError_t by_width(const GdnNormArgs &a, cudaStream_t s)
 {
     const int words = (a.channels / a.groups + VEC - 1) / VEC;
@@ -289,13 +292,14 @@ template <typename E, int VEC> cudaError_t by_width(const GdnNormArgs &a, cudaSt
         if (words <= 64) return launch<E, VEC, 2, 2, 0>(a, 32, s);
         if (words <= 96) return launch<E, VEC, 3, 2, 0>(a, 32, s);
         if (words <= 128) return launch<E, VEC, 4, 2, 0>(a, 32, s);
-        if (words <= 160) return launch<E, VEC, 5, 1, 0>(a, 32, s);
+        if (words <= 160) return launch<E, VEC, 5, 2, 0>(a, 32, s);
         if (words <= 192) return launch<E, VEC, 6, 1, 0>(a, 32, s);
-        if (words <= 256) return launch<E, VEC, 2, 2, 128>(a, 128, s);
-        if (words <= 512) return launch<E, VEC, 4, 2, 128>(a, 128, s);
+        if (words <= 256) return launch<E, VEC, 4, 2, 64>(a, 64, s);
+        if (words <= 384) return launch<E, VEC, 3, 2, 128>(a, 128, s);
+        if (words <= 512) return launch<E, VEC, 8, 1, 64>(a, 64, s);
         if (words <= 1024) return launch<E, VEC, 4, 2, 256>(a, 256, s);
     } else {
-        if (words <= 64) return launch<E, VEC, 2, 1, 0>(a, 32, s);
+        if (words <= 64) return launch<E, VEC, 1, 2, 64>(a, 64, s);
         if (words <= 128) return launch<E, VEC, 1, 2, 128>(a, 128, s);
         if (words <= 256) return launch<E, VEC, 1, 2, 256>(a, 256, s);
         if (words <= 512) return launch<E, VEC, 2, 1, 256>(a, 256, s);
