@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kern
         y[r] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            h[r][j] = fmaf(ex2(dr * A[j]), h[r][j], dxr * bv[j]);
+            h[r][j] = fmaf(ex2(fmaf(dr, A[j], kDecayShift)), h[r][j], dxr * bv[j]);
             y[r] = fmaf(cv[j], h[r][j], y[r]);
         }
         if (!live || entry[r] < 0) continue;

@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
                     const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        e[p][i + u] = ex2x2(mul2(v.x, A[i + u]));
+                        e[p][i + u] = ex2x2(fma2(v.x, A[i + u], dup2(kDecayShift)));
                         w[p][i + u] = pack2(x0 * bb[u], x1 * bb[u]);
                     }
                 }
