@@ -368,6 +368,14 @@ template <int PENDING> __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
+__device__ __forceinline__ void prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// One arrival at `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // A tensor copy of the box at column x (on a 16-byte boundary), row y of a
 // matrix, completing on `bar`.
 __device__ __forceinline__ void copy_box(void *dst, const void *map, int x, int y, uint64_t *bar)

@@ -31,8 +31,9 @@
 //  - Tiles of kTile tokens come into a ring by tensor copies where the rows allow
 //    it, five per tile from one finishing thread (from a preparing one they
 //    lengthened the whole block's turn: 236 against 210 us on the first shape
-//    below).  Other rows come by copies of 16 or 4 bytes per thread.  A bulk copy
-//    per row, 80 per tile, took 38 clocks each and twice the time.
+//    below).  Other rows come by copies of 16 or 4 bytes or through registers,
+//    per thread (247 us with 2044 channels instead of 2048).  A bulk copy per row,
+//    80 per tile, took 38 clocks each and twice the time.
 //
 // Measured, bf16, 16 states: 4 x 4096 tokens x 2048 channels 208 us (a block per
 // SM, 128 of 152 busy: 51 ns per token, of which the recurrence alone takes 43);
@@ -162,10 +163,18 @@ template <typename E, int N> struct Held {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = i < valid ? src[i] : from_f<E>(0.f);
     }
-    __device__ __forceinline__ void store(E *dst) const
+    __device__ __forceinline__ void store(E *dst) const  // aligned to the N elements
     {
+        if constexpr (sizeof(E) == 2 && N % 2 == 0) {
+            uint32_t w[N / 2];
 #pragma unroll
-        for (int i = 0; i < N; ++i) dst[i] = v[i];
+            for (int i = 0; i < N / 2; ++i)
+                w[i] = __bfloat16_as_ushort(v[2 * i]) | (uint32_t)__bfloat16_as_ushort(v[2 * i + 1]) << 16;
+            if constexpr (N == 8)
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+                *reinterpret_cast<uint32_t *>(dst) = w[0];
+        }
     }
 };
 
@@ -190,8 +199,26 @@ __device__ __forceinline__ float tf32_part(float v)
     return __uint_as_float(__float_as_uint(v) & 0xffffe000u);
 }
 
+// Whether rows that need copies per thread have four warps of their own for them.
+// bf16, 4 x 4096 tokens, 16 states, us with the copies made by preparing, by
+// finishing and by fetching threads: 2044 channels (4-byte copies) 302, 359, 247;
+// 2043 channels (2-byte loads) 308, 393, 281; 2048 channels x 13 states (B and C
+// through registers) 243, 310, 209.  fp32 loses by them (203 channels 100 against
+// 110: its recurrence wants the registers), and with more states per lane there
+// are no registers for more warps.
+template <typename E, int NS, int MODE, bool BULK> struct Fetchers {
+    static constexpr bool on = !BULK && MODE != kPieces && NS == 4 && sizeof(E) == 2;
+};
+
+// Threads of a block: recurrence, then preparing, finishing, fetching ones.
+template <typename E, int NS, int H, int MODE, bool BULK> struct Threads {
+    static constexpr int n = Layout<E, NS, H>::kRecur +
+                             (MODE == kPieces ? 1 : Fetchers<E, NS, MODE, BULK>::on ? 3 : 2) * kPrep;
+};
+
 template <typename E, int NS, int H, int MODE, bool BULK>
-__global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 && BULK ? 2 : 1)
+__global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MODE, BULK>::on ? 3 : 2) * kPrep,
+                                  NS == 4 && BULK ? 2 : 1)
     gdn_ssm_fwd_kernel(const GdnSsmArgs a, const __grid_constant__ Maps maps, int tl, int tiles,
                        unsigned slots, int row_width, int bc_width)
 {
@@ -226,24 +253,27 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     auto next = [](int at) { return at + 1 == kRing ? 0 : at + 1; };
     uint64_t *landed = reinterpret_cast<uint64_t *>(smem + kRing * L::kSlot + kHands * L::kHand);  // per ring slot
     uint64_t limit = kWaitLimit;
-    auto wait_for = [&](int at, int round) {  // the bulk copies of ring slot `at`, its `round`th use
+    // Tiles that other threads than the preparing ones copy are waited for at these; else each
+    // preparing thread waits for its own copies, and the finishing ones learn of them at kDone.
+    constexpr bool kFetch = Fetchers<E, NS, MODE, BULK>::on, kLanded = BULK || kFetch;
+    auto wait_for = [&](int at, int round) {  // the copies of ring slot `at`, its `round`th use
         if (!sm100::mbar_wait(&landed[at], round & 1, limit)) {
             atomicOr(a.status, GDN_DEV_WAIT_TIMEOUT);
             limit = kWaitAfterTimeout;
         }
     };
-    if (BULK) {
+    if (kLanded) {
         if (threadIdx.x == 0) {
-            for (int i = 0; i < kRing; ++i) sm100::mbar_init(&landed[i], 1);
+            for (int i = 0; i < kRing; ++i) sm100::mbar_init(&landed[i], BULK ? 1 : 2 * kPrep);
             sm100::fence_mbar_init();
         }
         __syncthreads();
     }
     // Barriers.  Of hand-over buffer i: kFull + i, prepared (prepare -> recurrence); kDone + i,
-    // read, and y written (recurrence -> prepare, finish).  kFree: y read and the ring slot with
-    // it (finish -> prepare).  kPieces has no finishing warps.
+    // read, and y written (recurrence -> prepare, finish, fetch).  kFree: y read and the ring slot
+    // with it (finish -> prepare).  kPieces has no finishing warps.
     enum { kFull = 1, kDone = kFull + kHands, kFree = kDone + kHands };
-    constexpr int kFullN = kRecur + kPrep, kDoneN = MODE == kPieces ? kRecur + kPrep : kRecur + 2 * kPrep;
+    constexpr int kFullN = kRecur + kPrep, kDoneN = Threads<E, NS, H, MODE, BULK>::n;
 
     // Two blocks of 384 threads leave 80 registers each: 112 for the recurrence warps, 64 for
     // the other eight (112 + 2 x 64 = 3 x 80).
@@ -455,56 +485,6 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
         if (a.z) copy_box(r + 2 * kX, &maps.z, cbase, y, &landed[at]);
     };
 
-    if (MODE != kPieces && threadIdx.x >= kRecur + kPrep) {  // ---- finish
-        if (BULK && id == 0)
-            for (int k = 0; k < kRing - 1; ++k) fetch(k, k);
-        f32x2 D[4];
-        column(a.D, D);
-        E *out = static_cast<E *>(a.y) + mine * a.ld_y + cc;
-        for (int k = 0, at = 0, round = 0; k < ntiles; ++k, at = next(at), round += at == 0) {
-            const E *r = reinterpret_cast<const E *>(smem + at * L::kSlot);
-            float x[8], z[8];
-            ulonglong2 sum[2];
-            if (BULK) wait_for(at, round);
-            part_sync(kDone + k % kHands, kDoneN);
-            ld_vec<E, 8>(r + off, x);
-            if (a.z) ld_vec<E, 8>(r + 2 * L::kRowElems + off, z);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int w = row * kYPitch + y_place(4 * col + 2 * j) / 2;
-                sum[j] = reinterpret_cast<const ulonglong2 *>(part_y(k, 0))[w];
-                if (H == 2) {
-                    const ulonglong2 more = reinterpret_cast<const ulonglong2 *>(part_y(k, 1))[w];
-                    sum[j] = make_ulonglong2(add2(sum[j].x, more.x), add2(sum[j].y, more.y));
-                }
-            }
-            part_arrive(kFree, 2 * kPrep);
-            if (k * kTile < rows) {
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f32x2 v = fma2(D[i], pack2(x[2 * i], x[2 * i + 1]), i % 2 ? sum[i / 2].y : sum[i / 2].x);
-                    if (a.z) v = mul2(v, silu2(pack2(z[2 * i], z[2 * i + 1])));
-                    unpack2(v, y[2 * i], y[2 * i + 1]);
-                }
-                if (BULK || row_width == kWide) {
-                    st_vec<E, 8>(out, y);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < nc) out[i] = from_f<E>(y[i]);
-                }
-                out += kTile * a.ld_y;
-            }
-            // every finishing thread came to this tile's barrier, so the slot before is free
-            if (BULK && id == 0) fetch(k - 1 + kRing, at == 0 ? kRing - 1 : at - 1);
-        }
-        return;
-    }
-
-    // ---- prepare
-    f32x2 bias[4];
-    column(a.delta_bias, bias);
     // pair p = id + i kPrep of B and C of a tile: a token's states 2 (p % kHalf) and the next
     constexpr int kHalf = L::kStates / 2, kPer = L::kBC / kPrep, kTokStep = kPrep / kHalf;
     const int st = 2 * (id % kHalf), tok0 = id / kHalf;
@@ -532,6 +512,11 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
             held_x.load(x_in, valid);
             held_d.load(d_in, valid);
             held_z.load(z_in, MODE != kPieces && a.z ? valid : 0);
+            if (kFetch && (k + 1) * kTile < rows) {  // the next turn's loads then wait for L2 alone
+                prefetch(x_in + kTile * a.ld_x);
+                prefetch(d_in + kTile * a.ld_delta);
+                if (a.z) prefetch(z_in + kTile * a.ld_z);
+            }
         }
         if (bc_width == kSingle)
 #pragma unroll
@@ -577,10 +562,79 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
             }
             b_in += kTile * a.ld_b;
             c_in += kTile * a.ld_c;
+            if (kLanded) {  // once for the copies, once for what was stored
+                copy_arrive(&landed[at]);
+                sm100::mbar_arrive(&landed[at]);
+            }
         }
-        copy_commit();  // one group per tile, so that a group's number is its tile's
+        if (!kLanded) copy_commit();  // one group per tile, so that a group's number is its tile's
     };
 
+    if (kFetch && threadIdx.x >= kRecur + 2 * kPrep) {  // ---- fetch
+#pragma unroll 1
+        for (int k = 0; k < kRing - 1; ++k) {
+            hold(k);
+            issue(k, k);
+        }
+#pragma unroll 1
+        for (int k = 0, at = kRing - 1; k < ntiles; ++k, at = next(at)) {
+            hold(k - 1 + kRing);
+            part_sync(kDone + k % kHands, kDoneN);  // as at the end of a finishing thread's turn
+            issue(k - 1 + kRing, at);
+        }
+        return;
+    }
+
+    if (MODE != kPieces && threadIdx.x >= kRecur + kPrep) {  // ---- finish
+        if (BULK && id == 0)
+            for (int k = 0; k < kRing - 1; ++k) fetch(k, k);
+        f32x2 D[4];
+        column(a.D, D);
+        E *out = static_cast<E *>(a.y) + mine * a.ld_y + cc;
+        for (int k = 0, at = 0, round = 0; k < ntiles; ++k, at = next(at), round += at == 0) {
+            const E *r = reinterpret_cast<const E *>(smem + at * L::kSlot);
+            float x[8], z[8];
+            ulonglong2 sum[2];
+            if (kLanded) wait_for(at, round);
+            part_sync(kDone + k % kHands, kDoneN);
+            ld_vec<E, 8>(r + off, x);
+            if (a.z) ld_vec<E, 8>(r + 2 * L::kRowElems + off, z);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int w = row * kYPitch + y_place(4 * col + 2 * j) / 2;
+                sum[j] = reinterpret_cast<const ulonglong2 *>(part_y(k, 0))[w];
+                if (H == 2) {
+                    const ulonglong2 more = reinterpret_cast<const ulonglong2 *>(part_y(k, 1))[w];
+                    sum[j] = make_ulonglong2(add2(sum[j].x, more.x), add2(sum[j].y, more.y));
+                }
+            }
+            part_arrive(kFree, 2 * kPrep);
+            if (k * kTile < rows) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x2 v = fma2(D[i], pack2(x[2 * i], x[2 * i + 1]), i % 2 ? sum[i / 2].y : sum[i / 2].x);
+                    if (a.z) v = mul2(v, silu2(pack2(z[2 * i], z[2 * i + 1])));
+                    unpack2(v, y[2 * i], y[2 * i + 1]);
+                }
+                if (BULK || row_width == kWide) {
+                    st_vec<E, 8>(out, y);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < nc) out[i] = from_f<E>(y[i]);
+                }
+                out += kTile * a.ld_y;
+            }
+            // every finishing thread came to this tile's barrier, so the slot before is free
+            if (BULK && id == 0) fetch(k - 1 + kRing, at == 0 ? kRing - 1 : at - 1);
+        }
+        return;
+    }
+
+    // ---- prepare
+    f32x2 bias[4];
+    column(a.delta_bias, bias);
     // Tile k from ring slot `at` into its hand-over buffer.  `edge`: rows past the end or padded
     // states, where the ring may hold anything, are set to zero.
     auto prepare_as = [&](int k, int at, auto edge) {
@@ -623,20 +677,22 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
             prepare_as(k, at, std::true_type());
     };
 
+    if (!kFetch) {
 #pragma unroll 1
-    for (int k = 0; k < kRing; ++k) {
-        hold(k);
-        issue(k, k);
+        for (int k = 0; k < kRing; ++k) {
+            hold(k);
+            issue(k, k);
+        }
     }
     auto wait_tile = [&](int k, int at, int round) {  // copies of tile k, of at least k + 1 and at most
-        if (BULK)                                      // k + kRing - kHands + 1 issued by this thread
+        if (kLanded)                                   // k + kRing - kHands + 1 issued by this thread
             wait_for(at, round);
         else
             copy_wait<kRing - kHands - 1>();
     };
-    if (!BULK) copy_wait<kRing - kHands>();
+    if (!kLanded) copy_wait<kRing - kHands>();
     for (int k = 0; k < kHands && k < ntiles; ++k) {
-        if (BULK) wait_for(k, 0);
+        if (kLanded) wait_for(k, 0);
         prepare(k, k);
         part_arrive(kFull + k, kFullN);
     }
@@ -644,13 +700,13 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + 2 * kPrep, NS == 4 
     for (int k = 0, done = 0, ahead = kHands % kRing, round = 0; k < ntiles;
          ++k, done = next(done), ahead = next(ahead)) {
         round += ahead == 0;
-        hold(k + kRing);
+        if (!kFetch) hold(k + kRing);
         if (k + kHands < ntiles) wait_tile(k + kHands, ahead, round);
         part_sync(kDone + k % kHands, kDoneN);
         if (k + kHands < ntiles) prepare(k + kHands, ahead);
         if (MODE != kPieces) part_sync(kFree, 2 * kPrep);
         if (k + kHands < ntiles) part_arrive(kFull + k % kHands, kFullN);
-        issue(k + kRing, done);
+        if (!kFetch) issue(k + kRing, done);
     }
 }
 
@@ -731,7 +787,7 @@ cudaError_t launch_mode(const GdnSsmArgs &a, const Maps &maps, int tl, int tiles
     cudaError_t e = cudaFuncSetAttribute(gdn_ssm_fwd_kernel<E, NS, H, MODE, BULK>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
     if (e != cudaSuccess) return e;
-    gdn_ssm_fwd_kernel<E, NS, H, MODE, BULK><<<(unsigned)grid, L::kRecur + (MODE == kPieces ? 1 : 2) * kPrep, L::kBytes, s>>>(
+    gdn_ssm_fwd_kernel<E, NS, H, MODE, BULK><<<(unsigned)grid, Threads<E, NS, H, MODE, BULK>::n, L::kBytes, s>>>(
         a, maps, tl, tiles, (unsigned)slots, row_width<E>(a), bc_width<E>(a));
     return cudaGetLastError();
 }
