@@ -15,14 +15,11 @@
 // The work is split so that no pipe does what another can:
 //
 //  - Recurrence warps (4 per block, 16 channels each; 8 with half the states
-//    each when d_state > 64) do nothing but the recurrence.  A lane holds NS
-//    states of a pair of neighbouring channels, the operations on the pair in
-//    packed instructions.  y = C h is left to the tensor cores: the lanes' states
-//    are the A operand of an m16n8k8 product as they stand (rows = the warp's 16
-//    channels), its eight columns are the C of eight consecutive tokens, loaded
-//    once per eight tokens; of each token's product the one column of that token
-//    is kept.  That takes the place of the fourth fp32 operation, of a butterfly
-//    over the lanes of a channel and of most loads of C.
+//    each when d_state > 64) do nothing but the recurrence and y = C h.  A lane
+//    holds NS states of a pair of neighbouring channels, the operations on the
+//    pair in packed instructions.  The four lanes of a pair add their parts of y
+//    over four tokens at a time: each exchange halves the tokens that a lane goes
+//    on with, which is 6 shuffles per four tokens and pair.
 //  - What is done once per token and channel is done by other warps.  Four
 //    prepare: the softplus, (d, d x) of a channel pair as one 16-byte word in a
 //    hand-over buffer, and B and C widened.  Four finish: D x, the gate and the
@@ -35,15 +32,15 @@
 //    per thread (247 us with 2044 channels instead of 2048).  A bulk copy per row,
 //    80 per tile, took 38 clocks each and twice the time.
 //
-// Measured, bf16, 16 states: 4 x 4096 tokens x 2048 channels 208 us (a block per
-// SM, 128 of 152 busy: 51 ns per token, of which the recurrence alone takes 43);
-// x 9728 channels 685 us (two blocks per SM: 12.2 states per clock and SM, issue
-// slots 60 % full, exponentials 47 %, shared memory under 68 %).
+// Measured, bf16, 16 states: 4 x 4096 tokens x 2048 channels 218 us (a block per
+// SM, 128 of 152 busy: 53 ns per token).
 //
-// The tensor product takes tf32 operands (11 bits).  bf16 calls pass h as it is
-// (cut to 11 bits; C is exact): the sum over states is fp32 and y is stored in 8
-// bits.  fp32 calls split h and C into two such parts each and add the four
-// products, which leaves less than 2^-21.  The states themselves stay fp32.
+// Everything is fp32 until y is stored, as in the step for single tokens.  The
+// sum over states on the tensor cores (m16n8k8, tf32: the states as operand as
+// they stand, of each product the one column of its token) takes 202 us when h is
+// cut to that operand's 11 bits, which leaves y 3.5e-4 of sum |C h| short on
+// average; with h in two such parts 270, with the lanes' fp32 parts of y added
+// there in two parts 228.
 #pragma once
 
 #include <cuda.h>
@@ -67,7 +64,7 @@ constexpr int kHands = 2;            // hand-over buffers; a third: 213 against 
 constexpr int kPairs = 32;           // channel pairs per block: 4 warps of 8 pairs
 constexpr int kCols = kPairs / 4;    // 8-channel columns of a token row
 constexpr int kPrep = 128;           // preparing threads, and finishing ones: a column of a row each
-constexpr int kYPitch = kPairs / 2 + 1;  // 16-byte words between rows of y: rows 2 q fall on separate banks
+constexpr int kYPitch = kPairs / 2 + 2;  // 16-byte words between rows of y: rows q fall on separate banks
 static_assert(kCols * kTile == kPrep && 2 * kPairs == kScanChannels, "a column of a row per thread");
 
 // Consecutive states (zeros past the end).
@@ -178,27 +175,6 @@ template <typename E, int N> struct Held {
     }
 };
 
-// d = a b + c on the tensor cores, tf32 operands (their upper 19 bits count),
-// fp32 accumulation.  Lane (g, q) = (lane / 4, lane % 4) gives a = rows g, g + 8
-// of columns q and q + 4 and b = rows q, q + 4 of column g, and holds d = rows
-// g, g + 8 of columns 2q, 2q + 1.
-__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0,
-                                         float b1, const float (&c)[4])
-{
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %11, %12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)),
-          "r"(__float_as_uint(a3)), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(c[0]), "f"(c[1]),
-          "f"(c[2]), "f"(c[3]));
-}
-
-// The part of v that a tf32 operand keeps.
-__device__ __forceinline__ float tf32_part(float v)
-{
-    return __uint_as_float(__float_as_uint(v) & 0xffffe000u);
-}
-
 // Whether rows that need copies per thread have four warps of their own for them.
 // bf16, 4 x 4096 tokens, 16 states, us with the copies made by preparing, by
 // finishing and by fetching threads: 2044 channels (4-byte copies) 302, 359, 247;
@@ -283,7 +259,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
         if (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         const int part = H == 1 ? 0 : threadIdx.x / (4 * kPairs);
         const int q = threadIdx.x & 3, pair = (threadIdx.x >> 2) & (kPairs - 1);
-        const int tok = pair & 7, c = cbase + 2 * pair, ds = a.d_state;
+        const int c = cbase + 2 * pair, ds = a.d_state;
         const int entry = state_entry(a.slots, s.n, a.pool, a.status);
         const int64_t slot0 = slot - s.tile;  // the sequence's first piece
         f32x2 h[NS], A[NS], dsum = 0;
@@ -328,17 +304,17 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
         for (int k = 0; k < ntiles; ++k) {
             const ulonglong2 *dx = reinterpret_cast<const ulonglong2 *>(hand(k)) + place(pair);
             const float4 *B = reinterpret_cast<const float4 *>(hand_b(k)) + state_of<NS>(part, q, 0) / 4;
-            const float4 *C = reinterpret_cast<const float4 *>(hand_c(k)) +
-                              (tok * L::kStates + state_of<NS>(part, q, 0)) / 4;
-            unsigned char *yout = part_y(k, part) + 8 * y_place(pair) + 32 * q * kYPitch;
+            const float4 *C = reinterpret_cast<const float4 *>(hand_c(k)) + state_of<NS>(part, q, 0) / 4;
+            unsigned char *yout = part_y(k, part) + 8 * y_place(pair) + 16 * q * kYPitch;
             ulonglong2 dv[2 + kAhead];
-            float4 bv[2 + kAhead];
-            f32x2 e[1 + kAhead][NS], w[1 + kAhead][NS], tile_sum = 0;
-            float C1[NS], C2[sizeof(E) == 4 ? NS : 1], acc[2][2][4], keep[4];
-            auto word = [&](int t, int i) { return B[(t * L::kStates + 4 * i) / 4]; };
+            float4 bv[2 + kAhead], cv[2 + kAhead];
+            f32x2 e[1 + kAhead][NS], w[1 + kAhead][NS], tile_sum = 0, y[4];
+            auto word = [&](const float4 *p, int t, int i) { return p[(t * L::kStates + 4 * i) / 4]; };
             auto load = [&](int t) {
                 dv[t % (2 + kAhead)] = dx[t * kPairs];  // d, d x
-                if (NS == 4) bv[t % (2 + kAhead)] = word(t, 0);
+                if (NS > 4) return;
+                bv[t % (2 + kAhead)] = word(B, t, 0);
+                if (MODE != kPieces) cv[t % (2 + kAhead)] = word(C, t, 0);
             };
             auto decay = [&](int t) {
                 const ulonglong2 v = dv[t % (2 + kAhead)];
@@ -348,7 +324,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                 unpack2(v.y, x0, x1);
 #pragma unroll
                 for (int i = 0; i < NS; i += 4) {
-                    const float4 b4 = NS == 4 ? bv[t % (2 + kAhead)] : word(t, i);
+                    const float4 b4 = NS == 4 ? bv[t % (2 + kAhead)] : word(B, t, i);
                     const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
@@ -357,16 +333,13 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                     }
                 }
             };
-            auto pick = [&](int t) {  // of token t's product, column t % 8: lanes q = t % 8 / 2
-                const float(*d)[4] = acc[t & 1];
-                if (q == t % 8 / 2) {
-                    keep[t & 1] = d[0][t & 1] + d[1][t & 1];
-                    keep[2 + (t & 1)] = d[0][2 + (t & 1)] + d[1][2 + (t & 1)];
-                }
-                if (t % 8 == 7)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)  // a lane has tokens 2 q and 2 q + 1 of the eight
-                        *reinterpret_cast<f32x2 *>(yout + (t - 7 + j) * 16 * kYPitch) = pack2(keep[j], keep[2 + j]);
+            // Over the lanes q of the pair: of two tokens (or sums of two) each half of the lanes goes
+            // on with one, so that after four tokens lane q has the sum of token q.
+            auto halve = [&](f32x2 even, f32x2 odd, int bit) {
+                float a0, a1, b0, b1;
+                unpack2(q & bit ? even : odd, a0, a1);
+                unpack2(q & bit ? odd : even, b0, b1);
+                return add2(pack2(b0, b1), pack2(__shfl_xor_sync(0xffffffffu, a0, bit), __shfl_xor_sync(0xffffffffu, a1, bit)));
             };
             part_sync(kFull + k % kHands, kFullN);
             load(0);
@@ -376,55 +349,31 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
             }
 #pragma unroll
             for (int t = 0; t < kTile; ++t) {
-                if (MODE != kPieces && t % 8 == 0) {
-                    // C of token t + tok; for fp32 calls, also what 11 bits leave over of it
-#pragma unroll
-                    for (int i = 0; i < NS; i += 4) {
-                        const float4 c4 = C[(t * L::kStates + 4 * i) / 4];
-                        const float v[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            C1[i + u] = v[u];
-                            if (sizeof(E) == 4) {
-                                C1[i + u] = tf32_part(v[u]);
-                                C2[i + u] = v[u] - C1[i + u];
-                            }
-                        }
-                    }
-                }
                 if (t + 1 + kAhead < kTile) load(t + 1 + kAhead);
                 if (t + kAhead < kTile) decay(t + kAhead);
 #pragma unroll
                 for (int i = 0; i < NS; ++i) h[i] = fma2(e[t % (1 + kAhead)][i], h[i], w[t % (1 + kAhead)][i]);
                 if constexpr (MODE != kPieces) {
-                    // two sums, so that the products do not wait for one another
+                    float y0 = 0.f, y1 = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < NS; i += 4) {
+                        const float4 c4 = NS == 4 ? cv[t % (2 + kAhead)] : word(C, t, i);
+                        const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) acc[t & 1][i][u] = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NS; i += 2) {  // columns q and q + 4: states i, i + 1
-                        float(&d)[4] = acc[t & 1][i / 2 % 2];
-                        float h0, h1, h2, h3;
-                        unpack2(h[i], h0, h1);
-                        unpack2(h[i + 1], h2, h3);
-                        if (sizeof(E) == 4) {
-                            const float p0 = tf32_part(h0), p1 = tf32_part(h1), p2 = tf32_part(h2), p3 = tf32_part(h3);
-                            mma_tf32(d, h0 - p0, h1 - p1, h2 - p2, h3 - p3, C2[i], C2[i + 1], d);
-                            mma_tf32(d, h0 - p0, h1 - p1, h2 - p2, h3 - p3, C1[i], C1[i + 1], d);
-                            mma_tf32(d, p0, p1, p2, p3, C2[i], C2[i + 1], d);
-                            mma_tf32(d, p0, p1, p2, p3, C1[i], C1[i + 1], d);
-                        } else {
-                            mma_tf32(d, h0, h1, h2, h3, C1[i], C1[i + 1], d);
+                        for (int u = 0; u < 4; ++u) {
+                            float h0, h1;
+                            unpack2(h[i + u], h0, h1);
+                            y0 = fmaf(cc[u], h0, y0);
+                            y1 = fmaf(cc[u], h1, y1);
                         }
                     }
-                    if (t > 0) pick(t - 1);
+                    y[t % 4] = pack2(y0, y1);
+                    if (t % 2) y[t % 4] = halve(y[t % 4 - 1], y[t % 4], 1);
+                    if (t % 4 == 3)
+                        *reinterpret_cast<f32x2 *>(yout + (t - 3) * 16 * kYPitch) = halve(y[1], y[3], 2);
                 }
             }
-            if (MODE == kPieces)
-                dsum = add2(dsum, tile_sum);
-            else
-                pick(kTile - 1);
+            if (MODE == kPieces) dsum = add2(dsum, tile_sum);
             part_arrive(kDone + k % kHands, kDoneN);
         }
         float d1[2];
