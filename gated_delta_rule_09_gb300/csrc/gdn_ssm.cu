@@ -112,7 +112,9 @@ __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kern
     for (int r = 0; r < kRows; ++r) {
         const int from = (threadIdx.x & 31) / LPC * LPC + r;
         const float dr = kRows == 1 ? d : __shfl_sync(0xffffffffu, d, from);
-        const float dxr = kRows == 1 ? dx : __shfl_sync(0xffffffffu, dx, from);
+        float dxr = kRows == 1 ? dx : __shfl_sync(0xffffffffu, dx, from);
+        // places past the last state stay zero, or out of y: an infinite d x times zero is NaN
+        if (VEC && s0 >= ds) dxr = 0.f;
         float bv[4], cv[4];
         B[r].get(bv);
         C[r].get(cv);
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kern
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             h[r][j] = fmaf(ex2(fmaf(dr, A[j], kDecayShift)), h[r][j], dxr * bv[j]);
-            y[r] = fmaf(cv[j], h[r][j], y[r]);
+            if (VEC || s0 + j < ds) y[r] = fmaf(cv[j], h[r][j], y[r]);
         }
         if (!live || entry[r] < 0) continue;
         float *out = a.state_out + ((size_t)entry[r] * a.channels + cc) * ds;

@@ -67,11 +67,23 @@ constexpr int kPrep = 128;           // preparing threads, and finishing ones: a
 constexpr int kYPitch = kPairs / 2 + 2;  // 16-byte words between rows of y: rows q fall on separate banks
 static_assert(kCols * kTile == kPrep && 2 * kPairs == kScanChannels, "a column of a row per thread");
 
-// Consecutive states (zeros past the end).
-template <int W> __device__ __forceinline__ void ld_state(const float *p, int s0, int ds, float (&h)[W])
+// The state in place s.  Places past the last state begin again with the first: a
+// state of zeros there would become d x times zero, NaN for an infinite d x, and
+// C's zero does not take that out of y.  The places of one state share its C.
+__device__ __forceinline__ int wrapped(int s, int ds) { return s < ds ? s : s % ds; }
+
+// The share of its state's C that place s of `places` has: 1/2, 1/4 and so on,
+// the last one as much as the one before, so that products are exact and add up.
+__device__ __forceinline__ float share_of(int s, int ds, int places)
+{
+    const int copies = (places - 1 - wrapped(s, ds)) / ds;  // beside the first
+    return __uint_as_float((uint32_t)(127 - min(s / ds + 1, copies)) << 23);
+}
+
+template <int W> __device__ __forceinline__ void ld_state(const float *p, const int (&at)[W], float (&h)[W])
 {
 #pragma unroll
-    for (int j = 0; j < W; ++j) h[j] = s0 + j < ds ? p[s0 + j] : 0.f;
+    for (int j = 0; j < W; ++j) h[j] = p[at[j]];
 }
 
 template <int W> __device__ __forceinline__ void st_state(float *p, int s0, int ds, const float (&h)[W])
@@ -132,22 +144,37 @@ template <int NS> __device__ __forceinline__ int state_of(int part, int q, int i
     return part * 4 * NS + 16 * (i / 4) + 4 * q + i % 4;
 }
 
-// N elements of a row, the first `valid` of them from memory, zeros after.
-template <typename E, int N>
+// Eight elements of a row, the first `valid` of them from memory, zeros after.
+template <typename E>
 __device__ __forceinline__ void ring_copy(E *dst, const E *src, int valid, int width)
 {
-    constexpr int step = N * sizeof(E) < 16 ? N : 16 / sizeof(E), word = 4 / sizeof(E);
-    if (width == kWide && valid == N) {
+    constexpr int step = 16 / sizeof(E), word = 4 / sizeof(E);
+    if (width == kWide && valid == 8) {
 #pragma unroll
-        for (int i = 0; i < N; i += step) copy_async<step * sizeof(E)>(dst + i, src + i);
+        for (int i = 0; i < 8; i += step) copy_async<16>(dst + i, src + i);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < N; i += word) {  // `valid` is a multiple of a word here
+    for (int i = 0; i < 8; i += word) {  // `valid` is a multiple of a word here
         if (i < valid)
             copy_async<4>(dst + i, src + i);
         else
             *reinterpret_cast<uint32_t *>(dst + i) = 0;
+    }
+}
+
+// Elements from[0] and from[1] of a row of B or C, neighbours where they are
+// copied as one; zeros for a row past the end.
+template <typename E>
+__device__ __forceinline__ void ring_copy_pair(E *dst, const E *row, const int (&from)[2], bool live, int width)
+{
+    if (!live) {
+        dst[0] = dst[1] = from_f<E>(0.f);
+    } else if (width == kWide) {
+        copy_async<2 * sizeof(E)>(dst, row + from[0]);
+    } else if (sizeof(E) == 4) {
+        copy_async<4>(dst, row + from[0]);
+        copy_async<4>(dst + 1, row + from[1]);
     }
 }
 
@@ -159,6 +186,11 @@ template <typename E, int N> struct Held {
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = i < valid ? src[i] : from_f<E>(0.f);
+    }
+    __device__ __forceinline__ void load_pair(const E *row, const int (&from)[2], bool live)
+    {
+        v[0] = live ? row[from[0]] : from_f<E>(0.f);
+        v[N - 1] = live ? row[from[1]] : from_f<E>(0.f);
     }
     __device__ __forceinline__ void store(E *dst) const  // aligned to the N elements
     {
@@ -266,6 +298,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
 #pragma unroll
         for (int i = 0; i < NS; i += 4) {
             const int s0 = state_of<NS>(part, q, i);
+            const int at[4] = {wrapped(s0, ds), wrapped(s0 + 1, ds), wrapped(s0 + 2, ds), wrapped(s0 + 3, ds)};
             float hv[2][4], Av[2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -273,20 +306,20 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                 for (int u = 0; u < 4; ++u) hv[j][u] = Av[j][u] = 0.f;
                 if (c + j >= cend) continue;
                 auto piece = [&](int64_t k) { return a.piece_state + ((size_t)k * a.channels + c + j) * ds; };
-                ld_state(a.A + (size_t)(c + j) * ds, s0, ds, Av[j]);
+                ld_state(a.A + (size_t)(c + j) * ds, at, Av[j]);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) Av[j][u] *= kLog2e;
                 if (MODE == kOutputs && pieces > 1) {
-                    ld_state(piece(s.tile == 0 ? slot0 + pieces - 1 : slot0), s0, ds, hv[j]);
+                    ld_state(piece(s.tile == 0 ? slot0 + pieces - 1 : slot0), at, hv[j]);
                     for (int k = 1; k < s.tile; ++k) {
                         const float sum = a.piece_delta[(size_t)(slot0 + k) * a.channels + c + j];
                         float e[4];
-                        ld_state(piece(slot0 + k), s0, ds, e);
+                        ld_state(piece(slot0 + k), at, e);
 #pragma unroll
                         for (int u = 0; u < 4; ++u) hv[j][u] = fmaf(ex2(sum * Av[j][u]), hv[j][u], e[u]);
                     }
                 } else if (s.tile == 0 && a.state_in && entry >= 0) {
-                    ld_state(a.state_in + ((size_t)entry * a.channels + c + j) * ds, s0, ds, hv[j]);
+                    ld_state(a.state_in + ((size_t)entry * a.channels + c + j) * ds, at, hv[j]);
                 }
                 if (MODE == kPieces && s.tile == 0) st_state(piece(slot0 + pieces - 1), s0, ds, hv[j]);
             }
@@ -437,7 +470,8 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
     // pair p = id + i kPrep of B and C of a tile: a token's states 2 (p % kHalf) and the next
     constexpr int kHalf = L::kStates / 2, kPer = L::kBC / kPrep, kTokStep = kPrep / kHalf;
     const int st = 2 * (id % kHalf), tok0 = id / kHalf;
-    const int ns = max(0, min(2, a.d_state - st));
+    const int from[2] = {wrapped(st, a.d_state), wrapped(st + 1, a.d_state)};
+    const float share[2] = {share_of(st, a.d_state, L::kStates), share_of(st + 1, a.d_state, L::kStates)};
     const int64_t channel = (int64_t)g * a.d_state;
 
     // Copies per thread: what it copies next; rows past the end are never read
@@ -447,8 +481,8 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
         x_in = static_cast<const E *>(a.x) + mine * a.ld_x + cc;
         d_in = static_cast<const E *>(a.delta) + mine * a.ld_delta + cc;
         z_in = a.z ? static_cast<const E *>(a.z) + mine * a.ld_z + cc : nullptr;
-        b_in = static_cast<const E *>(a.Bm) + first * a.ld_b + channel + (ns > 0 ? st : 0);
-        c_in = static_cast<const E *>(a.Cm) + first * a.ld_c + channel + (ns > 0 ? st : 0);
+        b_in = static_cast<const E *>(a.Bm) + first * a.ld_b + channel;
+        c_in = static_cast<const E *>(a.Cm) + first * a.ld_c + channel;
     }
 
     constexpr bool kHold = !BULK && sizeof(E) == 2;
@@ -470,9 +504,10 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
         if (bc_width == kSingle)
 #pragma unroll
             for (int i = 0; i < (kHold ? kPer : 1); ++i) {
-                const int t = tok0 + i * kTokStep, n = k * kTile + t < t1 - t0 ? ns : 0;
-                held_b[i].load(b_in + t * a.ld_b, n);
-                held_c[i].load(c_in + t * a.ld_c, MODE != kPieces ? n : 0);
+                const int t = tok0 + i * kTokStep;
+                const bool live = k * kTile + t < t1 - t0;
+                held_b[i].load_pair(b_in + t * a.ld_b, from, live);
+                held_c[i].load_pair(c_in + t * a.ld_c, from, MODE != kPieces && live);
             }
     };
     auto issue = [&](int k, int at) {  // tile k into ring slot `at`
@@ -488,20 +523,21 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                 held_d.store(r + L::kRowElems + off);
                 held_z.store(r + 2 * L::kRowElems + off);
             } else {
-                ring_copy<E, 8>(r + off, x_in, valid, row_width);
-                ring_copy<E, 8>(r + L::kRowElems + off, d_in, valid, row_width);
-                if (MODE != kPieces && a.z) ring_copy<E, 8>(r + 2 * L::kRowElems + off, z_in, valid, row_width);
+                ring_copy<E>(r + off, x_in, valid, row_width);
+                ring_copy<E>(r + L::kRowElems + off, d_in, valid, row_width);
+                if (MODE != kPieces && a.z) ring_copy<E>(r + 2 * L::kRowElems + off, z_in, valid, row_width);
             }
             E *rb = r + 3 * L::kRowElems + 2 * id, *rc = rb + 2 * L::kBC;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int t = tok0 + i * kTokStep, n = k * kTile + t < t1 - t0 ? ns : 0;
+                const int t = tok0 + i * kTokStep;
+                const bool live = k * kTile + t < t1 - t0;
                 if (kHold && bc_width == kSingle) {
                     held_b[i].store(rb + 2 * i * kPrep);
                     held_c[i].store(rc + 2 * i * kPrep);
                 } else {
-                    ring_copy<E, 2>(rb + 2 * i * kPrep, b_in + t * a.ld_b, n, bc_width);
-                    if (MODE != kPieces) ring_copy<E, 2>(rc + 2 * i * kPrep, c_in + t * a.ld_c, n, bc_width);
+                    ring_copy_pair<E>(rb + 2 * i * kPrep, b_in + t * a.ld_b, from, live, bc_width);
+                    if (MODE != kPieces) ring_copy_pair<E>(rc + 2 * i * kPrep, c_in + t * a.ld_c, from, live, bc_width);
                 }
             }
             if ((k + 1) * kTile < rows) {
@@ -584,8 +620,8 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
     // ---- prepare
     f32x2 bias[4];
     column(a.delta_bias, bias);
-    // Tile k from ring slot `at` into its hand-over buffer.  `edge`: rows past the end or padded
-    // states, where the ring may hold anything, are set to zero.
+    // Tile k from ring slot `at` into its hand-over buffer.  `edge`: rows past the end, where
+    // the ring may hold anything, are set to zero, and padding repeats states.
     auto prepare_as = [&](int k, int at, auto edge) {
         constexpr bool kEdge = decltype(edge)::value;
         const E *r = reinterpret_cast<const E *>(smem + at * L::kSlot);
@@ -604,19 +640,27 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
         const E *rb = r + 3 * L::kRowElems + 2 * id, *rc = rb + 2 * L::kBC;
         float2 *B = reinterpret_cast<float2 *>(hand_b(k)) + id;
         float2 *C = reinterpret_cast<float2 *>(hand_c(k)) + id;
+        auto pair = [&](const E *p, float (&v)[2]) {
+            if (kEdge && BULK) {  // boxes hold other groups' states in padding; copied pairs are right
+                v[0] = to_f(p[from[0] - st]);
+                v[1] = to_f(p[from[1] - st]);
+            } else {
+                ld_vec<E, 2>(p, v);
+            }
+        };
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int n = !kEdge || k * kTile + tok0 + i * kTokStep < t1 - t0 ? ns : 0;
+            const bool live = !kEdge || k * kTile + tok0 + i * kTokStep < t1 - t0;
             float v[2];
-            ld_vec<E, 2>(rb + 2 * i * kPrep, v);
-            if (kEdge && n < 1) v[0] = 0.f;
-            if (kEdge && n < 2) v[1] = 0.f;
-            B[i * kPrep] = make_float2(v[0], v[1]);
+            pair(rb + 2 * i * kPrep, v);
+            B[i * kPrep] = live ? make_float2(v[0], v[1]) : make_float2(0.f, 0.f);
             if (MODE == kPieces) continue;
-            ld_vec<E, 2>(rc + 2 * i * kPrep, v);
-            if (kEdge && n < 1) v[0] = 0.f;
-            if (kEdge && n < 2) v[1] = 0.f;
-            C[i * kPrep] = make_float2(v[0], v[1]);
+            pair(rc + 2 * i * kPrep, v);
+            if (kEdge) {
+                v[0] *= share[0];
+                v[1] *= share[1];
+            }
+            C[i * kPrep] = live ? make_float2(v[0], v[1]) : make_float2(0.f, 0.f);
         }
     };
     auto prepare = [&](int k, int at) {

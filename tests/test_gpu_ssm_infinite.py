@@ -1,0 +1,95 @@
+"""Infinite inputs, states that overflow and decays of -inf: scan and step give
+what the recurrence gives, infinity where it has one and NaN only where it has NaN."""
+import numpy as np
+import pytest
+import torch
+
+import layer_reference as R
+from test_gpu_ssm import draw, gdn, reference  # noqa: F401
+
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
+ROWS = ("x", "delta", "B", "C", "z")
+SIZES = [1, 3, 13, 16, 20, 32, 50, 64, 100, 128]
+inf = float("inf")
+
+
+def same(got, ref, bound):
+    """Equal NaN and infinities; the rest within the bound."""
+    got = R.f64(got)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    wild = np.isinf(got) | np.isinf(ref)
+    assert np.array_equal(got[wild], ref[wild])
+    ok = ~(wild | np.isnan(ref))
+    assert (np.abs(got[ok] - ref[ok]) <= bound[ok]).all()
+
+
+def both(gdn, a, segment=0):  # noqa: F811
+    """The scan, then the same tokens one by one, against the definition."""
+    T = a["x"].shape[1]
+    y0, bound, new, eb = reference(a, pieces=1 if segment == 0 else -(-T // 64))
+    y, s = gdn.gdn_ssm_fwd(**a, segment=segment or T)
+    same(y, y0, bound)
+    same(s, np.stack(new), np.stack(eb))
+    y0, bound, new, eb = reference(a)
+    s, ys = a["state_in"], []
+    for t in range(T):
+        y, s = gdn.gdn_ssm_step(**dict({k: (v[:, t] if k in ROWS and v is not None else v) for k, v in a.items()}, state_in=s))
+        ys.append(y)
+    same(torch.stack(ys, 1), y0, bound)
+    same(s, np.stack(new), np.stack(eb))
+    assert gdn.gdn_get_device_status() == 0
+
+
+def positive(a):
+    """All terms of y positive, so that an infinite one makes y infinite."""
+    a.update({k: a[k].abs() + 0.5 for k in ("x", "B", "C")}, z=None)
+    if a["state_in"] is not None:
+        a["state_in"] = a["state_in"].abs()
+    return a
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S", SIZES)
+def test_infinite_state(gdn, S, dtype):  # noqa: F811
+    a = positive(draw(S, (2, 37), 40, S, dtype=dtype, pool=2))
+    a["state_in"][0, 3] = inf
+    a["state_in"][1, 7, S - 1] = inf
+    both(gdn, a)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S", SIZES)
+def test_infinite_input(gdn, S, dtype):  # noqa: F811
+    """x = inf; also one whose products with B are infinities of both signs."""
+    a = positive(draw(S, (2, 37), 40, S, dtype=dtype, pool=2))
+    a["x"][0, 5, 3] = inf
+    a["x"][1, 18, 7] = -inf
+    a["x"][1, 20, 8] = inf
+    both(gdn, a)
+    a["B"][1, 20] *= torch.where(torch.arange(S, device="cuda") % 2 == 0, 1, -1).to(a["B"].dtype)
+    both(gdn, a)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S", SIZES)
+def test_infinite_c(gdn, S, dtype):  # noqa: F811
+    a = positive(draw(S, (2, 37), 40, S, dtype=dtype, pool=2))
+    a["state_in"][0, 4] = 2                             # exact in few bits: nothing left of it after rounding
+    a["C"][0, 0, 0, 0] = inf
+    a["C"][0, 33, 0, S - 1] = inf
+    a["C"][1, 9, 0, S // 2] = -inf
+    both(gdn, a)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [16, 33])
+def test_overflowing_state(gdn, T, dtype):  # noqa: F811
+    """States that grow by e^10 a token pass the largest number and stay infinite."""
+    a = positive(draw(T, (1, T), 24, 16, dtype=dtype, pool=1))
+    a.update(A=torch.ones_like(a["A"]), delta=torch.full_like(a["delta"], 10), delta_bias=None, delta_softplus=False, D=None)
+    ref, _, new, _ = reference(a)
+    y, s = gdn.gdn_ssm_fwd(**a)
+    top = float(torch.finfo(torch.float32).max)
+    assert (ref > 10 * top).any() and (ref < top / 10).any()
+    assert (R.f64(y)[ref > 10 * top] == np.inf).all() and np.isfinite(R.f64(y)[ref < top / 10]).all()
+    assert (s == inf).all()
