@@ -15,7 +15,7 @@
 // The work is split so that no pipe does what another can:
 //
 //  - Recurrence warps (4 per block, 16 channels each; 8 with half the states
-//    each when d_state > 64) do nothing but the recurrence and y = C h.  A lane
+//    each when d_state > 16) do nothing but the recurrence and y = C h.  A lane
 //    holds NS states of a pair of neighbouring channels, the operations on the
 //    pair in packed instructions.  The four lanes of a pair add their parts of y
 //    over four tokens at a time: each exchange halves the tokens that a lane goes
@@ -226,7 +226,7 @@ template <typename E, int NS, int H, int MODE, bool BULK> struct Threads {
 
 template <typename E, int NS, int H, int MODE, bool BULK>
 __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MODE, BULK>::on ? 3 : 2) * kPrep,
-                                  NS == 4 && BULK ? 2 : 1)
+                                  NS == 4 && H == 1 && BULK ? 2 : 1)
     gdn_ssm_fwd_kernel(const GdnSsmArgs a, const __grid_constant__ Maps maps, int tl, int tiles,
                        unsigned slots, int row_width, int bc_width)
 {
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
 
     // Two blocks of 384 threads leave 80 registers each: 112 for the recurrence warps, 64 for
     // the other eight (112 + 2 x 64 = 3 x 80).
-    constexpr bool kSplit = NS == 4 && BULK && MODE != kPieces;
+    constexpr bool kSplit = NS == 4 && H == 1 && BULK && MODE != kPieces;
 
     if (threadIdx.x < kRecur) {  // ---- recurrence
         if (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
@@ -804,11 +804,14 @@ template <typename E, int NS, int H> cudaError_t launch_fwd(const GdnSsmArgs &a,
     return box_rows<E>(a) ? launch_modes<E, NS, H, true>(a, s) : launch_modes<E, NS, H, false>(a, s);
 }
 
+// Two warps per scheduler cover one another's latencies where a lane would have
+// more than four states.  4 x 4096 tokens x 2048 channels, bf16, us with the
+// states in one part against two: 32 states 344 : 317, 64 states 935 : 540.
 template <typename E> cudaError_t scan(const GdnSsmArgs &a, cudaStream_t s)
 {
     if (a.d_state <= 16) return launch_fwd<E, 4, 1>(a, s);
-    if (a.d_state <= 32) return launch_fwd<E, 8, 1>(a, s);
-    if (a.d_state <= 64) return launch_fwd<E, 16, 1>(a, s);
+    if (a.d_state <= 32) return launch_fwd<E, 4, 2>(a, s);
+    if (a.d_state <= 64) return launch_fwd<E, 8, 2>(a, s);
     return launch_fwd<E, 16, 2>(a, s);
 }
 
