@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <float.h>
 #include <stdint.h>
 
 #include "gdn.h"
@@ -206,6 +207,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 // mean is within 3e-9 above -2^-8 and never further off than without; 2^0 is
 // still 1.
 constexpr float kDecayShift = 1.15e-8f;
+
+// A log2 e, the factor of d in a decay's exponent.  Infinities become the largest
+// number, so that d = 0 (in the scan also the rows past a sequence's end) decays
+// nothing and does not make NaN; any d above 5e-37 still decays everything.
+__device__ __forceinline__ float decay_rate(float A)
+{
+    float v;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(A * kLog2e), "f"(-FLT_MAX));  // NaN stays
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(FLT_MAX));
+    return v;
+}
 
 // v / (1 + e^-v).
 __device__ __forceinline__ float silu(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }

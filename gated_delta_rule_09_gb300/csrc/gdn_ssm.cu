@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kern
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A[j] *= kLog2e;
+    for (int j = 0; j < 4; ++j) A[j] = decay_rate(A[j]);
     d += a.delta_bias ? a.delta_bias[cc] : 0.f;
     if (a.softplus) d = softplus(d);
     const float dx = d * x;

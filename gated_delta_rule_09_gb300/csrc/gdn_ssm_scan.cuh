@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                 auto piece = [&](int64_t k) { return a.piece_state + ((size_t)k * a.channels + c + j) * ds; };
                 ld_state(a.A + (size_t)(c + j) * ds, at, Av[j]);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) Av[j][u] *= kLog2e;
+                for (int u = 0; u < 4; ++u) Av[j][u] = decay_rate(Av[j][u]);
                 if (MODE == kOutputs && pieces > 1) {
                     ld_state(piece(s.tile == 0 ? slot0 + pieces - 1 : slot0), at, hv[j]);
                     for (int k = 1; k < s.tile; ++k) {

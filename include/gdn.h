@@ -350,7 +350,9 @@ gdn_status_t gdn_conv_step(const void *x, const float *weight, const float *bias
  * the skip term is zero.
  *   x, delta, z, y  [B, T, channels] dtype, row strides ld_x, ld_delta, ld_z,
  *                   ld_y; z NULL allowed
- *   A               [channels, d_state] fp32 (negative for a decaying state)
+ *   A               [channels, d_state] fp32 (negative for a decaying state;
+ *                   -inf for one that forgets at once, which d = 0 leaves as
+ *                   it is)
  *   Bm, Cm          [B, T, groups, d_state] dtype, row strides ld_b, ld_c
  *   D, delta_bias   [channels] fp32 or NULL
  *   state_in, state_out  [pool, channels, d_state] fp32; NULL allowed

@@ -93,3 +93,35 @@ def test_overflowing_state(gdn, T, dtype):  # noqa: F811
     assert (ref > 10 * top).any() and (ref < top / 10).any()
     assert (R.f64(y)[ref > 10 * top] == np.inf).all() and np.isfinite(R.f64(y)[ref < top / 10]).all()
     assert (s == inf).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 40, 250])
+@pytest.mark.parametrize("S,ch", [(1, 40), (13, 40), (16, 64), (16, 43), (32, 40), (100, 40), (128, 64)])
+def test_a_state_that_forgets_at_once(gdn, S, ch, T, dtype):  # noqa: F811
+    """A = -inf: the state is the last token's d B x, whatever the length.  A decay
+    below the smallest number is the same, which the reference can take."""
+    a = draw(S + T, (2, T), ch, S, dtype=dtype, pool=2)
+    a["A"][:, S // 2] = -1e30
+    a["A"][5] = -1e30
+    ref = reference(a)
+    a["A"] = torch.where(a["A"] == -1e30, -inf, a["A"])
+    for segment in (T, 64):
+        y, s = gdn.gdn_ssm_fwd(**a, segment=segment)
+        y0, bound, new, eb = ref if segment == T else reference(dict(a, A=a["A"].clamp(min=-1e30)), pieces=4)
+        same(y, y0, bound)
+        same(s, np.stack(new), np.stack(eb))
+    b = {k: (v[:, 0] if k in ROWS else v) for k, v in a.items()}
+    y, _ = gdn.gdn_ssm_step(**b)
+    same(y, ref[0][:, 0], ref[1][:, 0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_zero_step_with_infinite_rate(gdn, dtype):  # noqa: F811
+    """A = -inf and a step size of zero: the state stays as it is, in scan and step."""
+    a = draw(9, (1, 20), 40, 16, dtype=dtype, pool=1)
+    a.update(delta_softplus=False, delta_bias=None, delta=torch.zeros_like(a["delta"]), A=torch.full_like(a["A"], -inf))
+    _, s = gdn.gdn_ssm_fwd(**a)
+    assert torch.equal(s, a["state_in"])
+    _, s = gdn.gdn_ssm_step(**{k: (v[:, 0] if k in ROWS else v) for k, v in a.items()})
+    assert torch.equal(s, a["state_in"])
