@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kern
 #pragma unroll
     for (int o = kRows; o < LPC; o <<= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
     if (!live || q >= kRows || own >= a.N) return;
-    float v = fmaf(a.D ? a.D[cc] : 0.f, x, y[0]);
+    float v = a.D ? fmaf(a.D[cc], x, y[0]) : y[0];
     if (a.z) v *= silu(z);
     static_cast<E *>(a.y)[row * a.ld_y + cc] = from_f<E>(v);
 }

@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f32x2 v = fma2(D[i], pack2(x[2 * i], x[2 * i + 1]), i % 2 ? sum[i / 2].y : sum[i / 2].x);
+                    f32x2 v = i % 2 ? sum[i / 2].y : sum[i / 2].x;
+                    if (a.D) v = fma2(D[i], pack2(x[2 * i], x[2 * i + 1]), v);  // not 0 x: x may be infinite
                     if (a.z) v = mul2(v, silu2(pack2(z[2 * i], z[2 * i + 1])));
                     unpack2(v, y[2 * i], y[2 * i + 1]);
                 }

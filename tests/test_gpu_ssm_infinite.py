@@ -125,3 +125,18 @@ def test_zero_step_with_infinite_rate(gdn, dtype):  # noqa: F811
     assert torch.equal(s, a["state_in"])
     _, s = gdn.gdn_ssm_step(**{k: (v[:, 0] if k in ROWS else v) for k, v in a.items()})
     assert torch.equal(s, a["state_in"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_input_without_skip(gdn, dtype):  # noqa: F811
+    """Without D there is no skip term to make NaN of an infinite x."""
+    a = positive(draw(3, (1, 20), 40, 4, dtype=dtype, pool=1))
+    a.update(D=None)
+    clean, _ = gdn.gdn_ssm_fwd(**a)
+    a["x"][0, 5, 3] = inf
+    clean[0, 5:, 3] = inf
+    y, s = gdn.gdn_ssm_fwd(**a)
+    assert torch.equal(y, clean) and (s[0, 3] == inf).all()
+    one = {k: (v[:, 5] if k in ROWS and v is not None else v) for k, v in a.items()}
+    y, _ = gdn.gdn_ssm_step(**one)
+    assert y[0, 3] == inf and torch.isfinite(torch.cat([y[0, :3], y[0, 4:]])).all()
