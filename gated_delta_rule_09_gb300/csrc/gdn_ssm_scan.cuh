@@ -207,6 +207,18 @@ template <typename E, int N> struct Held {
     }
 };
 
+// 2^(v / 2), twice of which takes a state over a piece, where 2^v may pass the
+// largest number although what it multiplies to does not.  Kept from zero and
+// from infinity: a zero state stays zero and an infinite one infinite, as token
+// by token.
+__device__ __forceinline__ float half_decay(float v)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(ex2(0.5f * v)), "f"(FLT_MIN));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(FLT_MAX));
+    return r;
+}
+
 // Whether rows that need copies per thread have four warps of their own for them.
 // bf16, 4 x 4096 tokens, 16 states, us with the copies made by preparing, by
 // finishing and by fetching threads: 2044 channels (4-byte copies) 302, 359, 247;
@@ -316,7 +328,10 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                         float e[4];
                         ld_state(piece(slot0 + k), at, e);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) hv[j][u] = fmaf(ex2(sum * Av[j][u]), hv[j][u], e[u]);
+                        for (int u = 0; u < 4; ++u) {
+                            const float half = half_decay(sum * Av[j][u]);
+                            hv[j][u] = fmaf(half * hv[j][u], half, e[u]);
+                        }
                     }
                 } else if (s.tile == 0 && a.state_in && entry >= 0) {
                     ld_state(a.state_in + ((size_t)entry * a.channels + c + j) * ds, at, hv[j]);

@@ -140,3 +140,36 @@ def test_infinite_input_without_skip(gdn, dtype):  # noqa: F811
     one = {k: (v[:, 5] if k in ROWS and v is not None else v) for k, v in a.items()}
     y, _ = gdn.gdn_ssm_step(**one)
     assert y[0, 3] == inf and torch.isfinite(torch.cat([y[0, :3], y[0, 4:]])).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S", [1, 13, 16, 50, 128])
+def test_infinite_state_over_pieces(gdn, S, dtype):  # noqa: F811
+    """Infinite however far a piece's decay is below the smallest number."""
+    a = positive(draw(S, (1, 300), 40, S, dtype=dtype, pool=1))
+    a["delta_bias"] += 2                                # 64 tokens decay by e^-1000 and more
+    a["state_in"][0, 3] = inf
+    a["x"][0, 40, 5] = inf
+    both(gdn, a, segment=64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_growth_over_pieces(gdn, dtype):  # noqa: F811
+    """Pieces that multiply by more than the largest number: zero stays zero, and a
+    small state becomes what it becomes token by token."""
+    a = draw(6, (1, 300), 40, 16, dtype=dtype, pool=1)
+    a.update(A=torch.ones_like(a["A"]), delta=torch.zeros_like(a["delta"]), delta_bias=None, delta_softplus=False, D=None,
+             z=None, x=torch.zeros_like(a["x"]))
+    a["delta"][:, 64:128] = 1.5                         # e^96 over the second piece
+    a["delta"][:, 200:210] = -1
+    a["state_in"] *= 1e-30
+    a["state_in"][:, 7] = 0
+    y0, bound, new, eb = reference(a, pieces=5)
+    y, s = gdn.gdn_ssm_fwd(**a, segment=64)
+    same(y, y0, bound)
+    same(s, np.stack(new), np.stack(eb))
+    assert (s[0, 7] == 0).all() and torch.isfinite(s).all()
+    a["delta"][:, 64:128] = 10                          # and by e^640
+    a["state_in"].zero_()
+    y, s = gdn.gdn_ssm_fwd(**a, segment=64)
+    assert (y == 0).all() and (s == 0).all()
