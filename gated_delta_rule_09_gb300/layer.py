@@ -267,6 +267,8 @@ def gdn_ssm_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, state_in=Non
             workspace = _empty(stream, x, (need,), torch.uint8)
     else:
         _on("workspace", workspace, torch.uint8, index)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     _call(lib.gdn_ssm_fwd, index, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
           _ptr(delta_bias), _ptr(state_in), _ptr(slots), _ptr(y), _ptr(state_out), N, T, ch, S, G,
           ld_x, ld_d, ld_b, ld_c, ld_z, ld_y, pool, _ptr(cu_seqlens), bool(delta_softplus),
