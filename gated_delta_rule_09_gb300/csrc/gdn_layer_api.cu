@@ -127,6 +127,7 @@ gdn_status_t conv(bool step, GdnConvArgs &a, int act, int dtype, void *stream)
     GDN_TRY(check_overlap(v, 8, 2));
     gdn_record_launch(0, -1);
     if (a.N == 0 || (rows == 0 && !a.state_out)) return GDN_OK;
+    if (!a.state_in && !a.state_out) a.slots = nullptr;  // no pool that a slot could be past the end of
     a.act = act;
     a.dtype = dtype == GDN_BF16 ? 1 : 0;
     GDN_TRY(gdn_device_status_word(&a.status));
@@ -196,6 +197,7 @@ gdn_status_t check_ssm(bool step, GdnSsmArgs &a, int dtype, bool *nothing)
     GDN_TRY(check_overlap(v, kSsmViews, 2));
     gdn_record_launch(0, -1);
     *nothing = a.N == 0 || (rows == 0 && !a.state_out);
+    if (!a.state_in && !a.state_out) a.slots = nullptr;  // no pool that a slot could be past the end of
     return GDN_OK;
 }
 

@@ -306,7 +306,8 @@ gdn_status_t gdn_ut_inverse(const float *A, float *T, int count, int C, int meth
  *    sequence that keeps no state: it starts from zeros and writes none (the
  *    padding rows of a fixed-size batch).  A slot >= pool is treated the same
  *    way and raises GDN_DEV_BAD_SLOT.  Two sequences must not share a slot.
- *    A sequence without tokens hands its state on unchanged.
+ *    A sequence without tokens hands its state on unchanged.  Without states
+ *    (both pointers NULL) the slots are not looked at.
  */
 
 /*
