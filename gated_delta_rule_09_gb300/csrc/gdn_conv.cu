@@ -333,7 +333,7 @@ cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
     int tl = 16;
     int64_t best = INT64_MAX;
     for (int t = 16; t <= 128; t += 8) {
-        const int64_t n = (a.cu_seqlens ? a.T / t + a.N : (int64_t)a.N * ((a.T + t - 1) / t)) * blocks;
+        const int64_t n = (a.cu_seqlens ? (int64_t)a.T / t + a.N : (int64_t)a.N * ((a.T + t - 1) / t)) * blocks;
         const int64_t cost = (n + resident - 1) / resident * (t + W - 1);
         if (cost <= best) {
             best = cost;
@@ -342,6 +342,7 @@ cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
     }
     const int tiles = a.T > tl ? (a.T + tl - 1) / tl : 1;
     const int64_t slots = a.cu_seqlens ? (int64_t)a.T / tl + a.N : (int64_t)a.N * tiles;
+    if (slots > 0x7fffffff) return cudaErrorInvalidConfiguration;
     gdn_conv_fwd_kernel<E, VEC, SPLIT, W><<<dim3((unsigned)slots, blocks), kThreads, smem, s>>>(a, tl, tiles);
     return cudaGetLastError();
 }

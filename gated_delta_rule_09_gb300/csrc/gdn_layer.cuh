@@ -290,7 +290,7 @@ __device__ __forceinline__ bool find_span(const int32_t *cu, int N, int T, int t
                 if (slot == 0) atomicOr(status, GDN_DEV_BAD_SEQLENS);
             } else {
                 first = lo / tl + n;
-                const int count = hi > lo ? (hi - lo + tl - 1) / tl : 1;
+                const int count = hi > lo ? (hi - lo - 1) / tl + 1 : 1;
                 hit = slot >= first && slot < (int64_t)first + count;
             }
         }

@@ -57,6 +57,18 @@ gdn_status_t check_rows(const View *v, int n, size_t esz)
     return check_alignment(v, n, esz);
 }
 
+// Kernels count tokens and sequences in 32 bits, up to a few tiles past the last.
+constexpr int kMaxCount = 0x7fff0000;
+
+gdn_status_t check_counts(int N, int T)
+{
+    if (N < 0 || T < 0)
+        return gdn_fail(GDN_ERR_INVALID_ARG, "negative size: %d sequences, %d tokens", N, T);
+    if (N > kMaxCount || T > kMaxCount)
+        return gdn_fail(GDN_ERR_UNSUPPORTED, "%d sequences, %d tokens (supported: up to %d)", N, T, kMaxCount);
+    return GDN_OK;
+}
+
 gdn_status_t check_types(int dtype, int act)
 {
     if (dtype != GDN_F32 && dtype != GDN_BF16)
@@ -92,8 +104,7 @@ gdn_status_t launched(cudaError_t e, const char *what, int launches, int path)
 gdn_status_t conv(bool step, GdnConvArgs &a, int act, int dtype, void *stream)
 {
     gdn_begin_call();
-    if (a.N < 0 || a.T < 0)
-        return gdn_fail(GDN_ERR_INVALID_ARG, "negative size: %d sequences, %d tokens", a.N, a.T);
+    GDN_TRY(check_counts(a.N, a.T));
     if (a.channels < 1)
         return gdn_fail(GDN_ERR_INVALID_ARG, "channels must be >= 1: %d", a.channels);
     if (a.width < 1 || a.width > 8)
@@ -165,8 +176,7 @@ gdn_status_t check_ssm(bool step, GdnSsmArgs &a, int dtype, bool *nothing)
 {
     gdn_begin_call();
     *nothing = true;
-    if (a.N < 0 || a.T < 0)
-        return gdn_fail(GDN_ERR_INVALID_ARG, "negative size: %d sequences, %d tokens", a.N, a.T);
+    GDN_TRY(check_counts(a.N, a.T));
     if (a.channels < 1 || a.d_state < 1 || a.groups < 1)
         return gdn_fail(GDN_ERR_INVALID_ARG, "channels, d_state and groups must be >= 1: %d, %d, %d",
                         a.channels, a.d_state, a.groups);

@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
     if (ranked ? !find_ranked(a.cu_seqlens, a.N, a.T, (int)slot, a.status, s)
                : !find_span(a.cu_seqlens, a.N, a.T, tl, slot, tiles, a.status, s))
         return;
-    const int pieces = s.len > tl ? (s.len + tl - 1) / tl : 1;
+    const int pieces = s.len > tl ? (s.len - 1) / tl + 1 : 1;
     if (MODE == kPieces && s.tile == pieces - 1) return;
-    const int t0 = s.tile * tl, t1 = min(s.len, t0 + tl);
+    const int t0 = s.tile * tl, t1 = t0 + min(s.len - t0, tl);
     const int ntiles = (t1 - t0 + kTile - 1) / kTile;
     // the block's channels: [cbase, cend), all of one group
     const int per_group = a.channels / a.groups;
@@ -807,7 +807,7 @@ template <typename E, int NS, int H, bool BULK> cudaError_t launch_modes(const G
     memset(&maps, 0, sizeof(maps));
     if (BULK && !make_maps<E>(a, Layout<E, NS, H>::kStates, &maps)) return cudaErrorInvalidValue;
     if (a.segment) {
-        const int tiles = (a.T + a.segment - 1) / a.segment;
+        const int tiles = (a.T - 1) / a.segment + 1;
         const cudaError_t e = launch_mode<E, NS, H, kPieces, BULK>(a, maps, a.segment, tiles, a.pieces, s);
         return e != cudaSuccess ? e : launch_mode<E, NS, H, kOutputs, BULK>(a, maps, a.segment, tiles, a.pieces, s);
     }

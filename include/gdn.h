@@ -297,7 +297,10 @@ gdn_status_t gdn_ut_inverse(const float *A, float *T, int count, int C, int meth
  *    vectorised kernels.
  *  - Packed prompts (cu_seqlens, device int32 [B + 1]) follow gdn_chunk_fwd:
  *    B sequences along one token axis of T rows.  A span that is negative or
- *    leaves [0, T] is skipped and raises GDN_DEV_BAD_SEQLENS.
+ *    leaves [0, T] is skipped and raises GDN_DEV_BAD_SEQLENS.  Where offsets go
+ *    back so far that two other spans share rows, y of those sequences and
+ *    their states are undefined (the bit is raised).  B, N and T are at most
+ *    2^31 - 2^16.
  *  - States live in a pool of `pool` entries: sequence n owns entry n, or
  *    entry slots[n] when `slots` (device int32, one per sequence) is given,
  *    so a serving loop keeps one pool for prompts and steps.  state_in may be
