@@ -50,7 +50,7 @@ template <typename E, int VEC, bool SPLIT> struct Access {
 
     __device__ __forceinline__ explicit Access(int channels)
     {
-        c0 = blockIdx.y * kThreads * VEC + threadIdx.x * (SPLIT ? 1 : VEC);
+        c0 = block_of() * kThreads * VEC + threadIdx.x * (SPLIT ? 1 : VEC);
         hi = c0 + kThreads < channels ? kThreads : 0;
     }
     __device__ __forceinline__ Vec load(const E *p) const
@@ -343,7 +343,7 @@ cudaError_t fwd(const GdnConvArgs &a, cudaStream_t s)
     const int tiles = a.T > tl ? (a.T + tl - 1) / tl : 1;
     const int64_t slots = a.cu_seqlens ? (int64_t)a.T / tl + a.N : (int64_t)a.N * tiles;
     if (slots > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    gdn_conv_fwd_kernel<E, VEC, SPLIT, W><<<dim3((unsigned)slots, blocks), kThreads, smem, s>>>(a, tl, tiles);
+    gdn_conv_fwd_kernel<E, VEC, SPLIT, W><<<grid_of((unsigned)slots, blocks), kThreads, smem, s>>>(a, tl, tiles);
     return cudaGetLastError();
 }
 
@@ -355,9 +355,9 @@ cudaError_t step(const GdnConvArgs &a, cudaStream_t s)
     // one against four, 6 blocks per sequence (16-byte words): 32 sequences 3.3 : 3.6, 64 4.9 : 4.3,
     // 256 11.4 : 7.7.  24 blocks (single elements): 16 sequences 2.1 : 2.6, 256 9.1 : 8.3.
     if ((int64_t)a.N * blocks >= (SPLIT ? 1024 : 384))
-        gdn_conv_step_kernel<E, VEC, SPLIT, W, 4><<<dim3((a.N + 3) / 4, blocks), kThreads, 0, s>>>(a);
+        gdn_conv_step_kernel<E, VEC, SPLIT, W, 4><<<grid_of((a.N + 3) / 4, blocks), kThreads, 0, s>>>(a);
     else
-        gdn_conv_step_kernel<E, VEC, SPLIT, W, 1><<<dim3(a.N, blocks), kThreads, 0, s>>>(a);
+        gdn_conv_step_kernel<E, VEC, SPLIT, W, 1><<<grid_of(a.N, blocks), kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -410,6 +410,14 @@ __device__ __forceinline__ void part_sync(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Grids of x by any number of blocks: the second dimension holds 65 535 and goes on in the third.
+inline dim3 grid_of(unsigned x, int64_t blocks)
+{
+    const unsigned z = (unsigned)((blocks + 65534) / 65535);
+    return dim3(x, (unsigned)((blocks + z - 1) / z), z);
+}
+__device__ __forceinline__ unsigned block_of() { return blockIdx.z * gridDim.y + blockIdx.y; }
+
 inline bool aligned_to(const void *p, size_t al) { return reinterpret_cast<uintptr_t>(p) % al == 0; }
 inline bool aligned16(const void *p) { return aligned_to(p, 16); }
 

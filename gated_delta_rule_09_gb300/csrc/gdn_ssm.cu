@@ -66,7 +66,7 @@ template <typename E> struct Four<false, E> {
 template <typename E, int LPC, int kRows, bool VEC>
 __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kernel(const GdnSsmArgs a)
 {
-    const int c = blockIdx.y * (kThreads / LPC) + threadIdx.x / LPC;
+    const int c = block_of() * (kThreads / LPC) + threadIdx.x / LPC;
     const bool live = c < a.channels;
     const int cc = live ? c : a.channels - 1;
     const int q = threadIdx.x % LPC, s0 = 4 * q, ds = a.d_state;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 1) gdn_ssm_step_kern
 template <typename E, int LPC, int kRows> cudaError_t launch_step(const GdnSsmArgs &a, cudaStream_t s)
 {
     const int per = kThreads / LPC;
-    const dim3 grid((a.N + kRows - 1) / kRows, (a.channels + per - 1) / per);
+    const dim3 grid = grid_of((a.N + kRows - 1) / kRows, (a.channels + per - 1) / per);
     const bool vec = a.d_state % 4 == 0 && aligned16(a.state_in) && aligned16(a.state_out) && aligned16(a.A) &&
                      a.ld_b % 4 == 0 && a.ld_c % 4 == 0 && aligned_to(a.Bm, 4 * sizeof(E)) &&
                      aligned_to(a.Cm, 4 * sizeof(E));
