@@ -17,30 +17,31 @@
 //  - Recurrence warps (4 per block, 16 channels each; 8 with half the states
 //    each when d_state > 16) do nothing but the recurrence and y = C h.  A lane
 //    holds NS states of a pair of neighbouring channels, the operations on the
-//    pair in packed instructions.  The four lanes of a pair add their parts of y
-//    over four tokens at a time: each exchange halves the tokens that a lane goes
-//    on with, which is 6 shuffles per four tokens and pair.
+//    pair in packed instructions, and stores its part of the pair's y.
 //  - What is done once per token and channel is done by other warps.  Four
 //    prepare: the softplus, (d, d x) of a channel pair as one 16-byte word in a
-//    hand-over buffer, and B and C widened.  Four finish: D x, the gate and the
-//    store of y.  The recurrence warps need most registers and take over what the
-//    others leave of the block's.
+//    hand-over buffer, and B and C widened.  Four finish: the sum of the parts of
+//    y, D x, the gate and the store.  The recurrence warps need most registers and
+//    take over what the others leave of the block's.
 //  - Tiles of kTile tokens come into a ring by tensor copies where the rows allow
 //    it, five per tile from one finishing thread (from a preparing one they
 //    lengthened the whole block's turn: 236 against 210 us on the first shape
 //    below).  Other rows come by copies of 16 or 4 bytes or through registers,
-//    per thread (247 us with 2044 channels instead of 2048).  A bulk copy per row,
+//    per thread (243 us with 2044 channels instead of 2048).  A bulk copy per row,
 //    80 per tile, took 38 clocks each and twice the time.
 //
-// Measured, bf16, 16 states: 4 x 4096 tokens x 2048 channels 218 us (a block per
-// SM, 128 of 152 busy: 53 ns per token).
+// Measured, 16 states: 4 x 4096 tokens x 2048 channels 209 us in bf16 (a block per
+// SM, 128 of 152 busy: 51 ns per token), 225 in fp32; x 9728 channels 662 us (two
+// blocks per SM: 13 states per clock and SM).  More states, 2048 channels, bf16
+// (fp32): 32 303 us (303), 64 522 (539), 128 908 (918).
 //
 // Everything is fp32 until y is stored, as in the step for single tokens.  The
 // sum over states on the tensor cores (m16n8k8, tf32: the states as operand as
 // they stand, of each product the one column of its token) takes 202 us when h is
 // cut to that operand's 11 bits, which leaves y 3.5e-4 of sum |C h| short on
 // average; with h in two such parts 270, with the lanes' fp32 parts of y added
-// there in two parts 228.
+// there in two parts 228.  The four lanes' parts added by shuffles, over four
+// tokens at a time, took 219.
 #pragma once
 
 #include <cuda.h>
@@ -64,7 +65,6 @@ constexpr int kHands = 2;            // hand-over buffers; a third: 213 against 
 constexpr int kPairs = 32;           // channel pairs per block: 4 warps of 8 pairs
 constexpr int kCols = kPairs / 4;    // 8-channel columns of a token row
 constexpr int kPrep = 128;           // preparing threads, and finishing ones: a column of a row each
-constexpr int kYPitch = kPairs / 2 + 2;  // 16-byte words between rows of y: rows q fall on separate banks
 static_assert(kCols * kTile == kPrep && 2 * kPairs == kScanChannels, "a column of a row per thread");
 
 // The state in place s.  Places past the last state begin again with the first: a
@@ -107,21 +107,22 @@ enum Mode { kWhole, kPieces, kOutputs };
 enum Width { kWide, kWord, kSingle };  // 16 bytes (pairs whole); 4 bytes; through registers
 
 // Threads and shared memory of one block of 64 channels.  The states are in H
-// parts, a lane has NS of a part: d_state is padded to 4 NS H.
-template <typename E, int NS, int H> struct Layout {
+// parts, a lane has NS of a part: d_state is padded to 4 NS H.  PIECES: the pass
+// that has no C and no y.
+template <typename E, int NS, int H, bool PIECES = false> struct Layout {
     static constexpr int kRecur = 4 * kPairs * H;         // recurrence threads
     static constexpr int kStates = 4 * NS * H;
     static constexpr int kBC = kTile * kStates / 2;       // pairs of B (and of C) per tile
     static constexpr int kRowElems = kTile * 2 * kPairs;
     // Tiles of inputs held or on their way.  A tile is fetched once the tile kRing before it is
     // finished, and waited for before the tile kHands before it is through the recurrence.
-    static constexpr int kRing = sizeof(E) * H > 4 ? 5 : 6;
+    static constexpr int kRing = sizeof(E) * kStates > 256 ? 4 : sizeof(E) * H > 4 ? 5 : 6;
     static constexpr size_t kSlot = sizeof(E) * (3 * kRowElems + 4 * kBC);  // x, delta, z, B, C
     static constexpr size_t kHandD = 16 * (size_t)kTile * kPairs;           // (d, d, d x, d x) per pair
     static constexpr size_t kHandB = 8 * (size_t)kBC;                       // B, and C, widened
     static constexpr size_t kHandC = kHandB;
-    static constexpr size_t kPartY = 16 * (size_t)kTile * kYPitch;          // y per pair, from one part
-    static constexpr size_t kHand = kHandD + kHandB + kHandC + H * kPartY;
+    static constexpr size_t kPartY = 32 * (size_t)kTile * kPairs;           // y per pair, four lanes' parts of it
+    static constexpr size_t kHand = kHandD + kHandB + (PIECES ? 0 : kHandC + H * kPartY);
     static constexpr size_t kBytes = kRing * kSlot + kHands * kHand + 8 * kRing;
     static_assert(kBC % kPrep == 0 && kBytes <= 227 * 1024 && kRing >= kHands + 2, "");
 };
@@ -132,11 +133,15 @@ struct Maps {
     CUtensorMap x, delta, z, b, c;
 };
 
-// Place of a channel pair's word in a token row of a hand-over buffer, and of
-// its 8 bytes in a row of y: a preparing thread writes four neighbouring words
-// and a finishing one reads 2 x 16 bytes, which this spreads over the banks.
+// Place of a channel pair's word in a token row of a hand-over buffer: a
+// preparing thread writes four neighbouring words, which this spreads over the
+// banks.
 __device__ __forceinline__ int place(int pair) { return pair ^ ((pair >> 3) & 3); }
-__device__ __forceinline__ int y_place(int pair) { return pair ^ ((pair >> 3) & 2); }
+
+// Place, in 16-byte words, of word w (0 to 7) of y of an 8-channel column: words 2
+// i and 2 i + 1 are the parts of its pair i from lanes 0, 1 and 2, 3.  A half warp
+// writes all words of a column, a finishing thread reads word w of its own.
+__device__ __forceinline__ int y_place(int col, int w) { return 8 * col + (w ^ col); }
 
 // State i of lane quarter q in part `part`: runs of four, 16 apart.
 template <int NS> __device__ __forceinline__ int state_of(int part, int q, int i)
@@ -223,7 +228,8 @@ __device__ __forceinline__ float half_decay(float v)
 // bf16, 4 x 4096 tokens, 16 states, us with the copies made by preparing, by
 // finishing and by fetching threads: 2044 channels (4-byte copies) 302, 359, 247;
 // 2043 channels (2-byte loads) 308, 393, 281; 2048 channels x 13 states (B and C
-// through registers) 243, 310, 209.  fp32 loses by them (203 channels 100 against
+// through registers) 243, 310, 209 (the fetching ones with today's sum of y: 243,
+// 298, 218).  fp32 loses by them (203 channels 100 against
 // 110: its recurrence wants the registers), and with more states per lane there
 // are no registers for more warps.
 template <typename E, int NS, int MODE, bool BULK> struct Fetchers {
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
     gdn_ssm_fwd_kernel(const GdnSsmArgs a, const __grid_constant__ Maps maps, int tl, int tiles,
                        unsigned slots, int row_width, int bc_width)
 {
-    using L = Layout<E, NS, H>;
+    using L = Layout<E, NS, H, MODE == kPieces>;
     constexpr int kRing = L::kRing, kRecur = L::kRecur;
     extern __shared__ __align__(128) unsigned char smem[];
     Span s;
@@ -353,10 +359,10 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
             const ulonglong2 *dx = reinterpret_cast<const ulonglong2 *>(hand(k)) + place(pair);
             const float4 *B = reinterpret_cast<const float4 *>(hand_b(k)) + state_of<NS>(part, q, 0) / 4;
             const float4 *C = reinterpret_cast<const float4 *>(hand_c(k)) + state_of<NS>(part, q, 0) / 4;
-            unsigned char *yout = part_y(k, part) + 8 * y_place(pair) + 16 * q * kYPitch;
+            unsigned char *yout = part_y(k, part) + 16 * y_place(pair / 4, 2 * (pair & 3) + q / 2) + 8 * (q & 1);
             ulonglong2 dv[2 + kAhead];
             float4 bv[2 + kAhead], cv[2 + kAhead];
-            f32x2 e[1 + kAhead][NS], w[1 + kAhead][NS], tile_sum = 0, y[4];
+            f32x2 e[1 + kAhead][NS], w[1 + kAhead][NS], tile_sum = 0;
             auto word = [&](const float4 *p, int t, int i) { return p[(t * L::kStates + 4 * i) / 4]; };
             auto load = [&](int t) {
                 dv[t % (2 + kAhead)] = dx[t * kPairs];  // d, d x
@@ -380,14 +386,6 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                         w[p][i + u] = pack2(x0 * bb[u], x1 * bb[u]);
                     }
                 }
-            };
-            // Over the lanes q of the pair: of two tokens (or sums of two) each half of the lanes goes
-            // on with one, so that after four tokens lane q has the sum of token q.
-            auto halve = [&](f32x2 even, f32x2 odd, int bit) {
-                float a0, a1, b0, b1;
-                unpack2(q & bit ? even : odd, a0, a1);
-                unpack2(q & bit ? odd : even, b0, b1);
-                return add2(pack2(b0, b1), pack2(__shfl_xor_sync(0xffffffffu, a0, bit), __shfl_xor_sync(0xffffffffu, a1, bit)));
             };
             part_sync(kFull + k % kHands, kFullN);
             load(0);
@@ -415,10 +413,7 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                             y1 = fmaf(cc[u], h1, y1);
                         }
                     }
-                    y[t % 4] = pack2(y0, y1);
-                    if (t % 2) y[t % 4] = halve(y[t % 4 - 1], y[t % 4], 1);
-                    if (t % 4 == 3)
-                        *reinterpret_cast<f32x2 *>(yout + (t - 3) * 16 * kYPitch) = halve(y[1], y[3], 2);
+                    *reinterpret_cast<f32x2 *>(yout + 32 * kPairs * t) = pack2(y0, y1);
                 }
             }
             if (MODE == kPieces) dsum = add2(dsum, tile_sum);
@@ -594,18 +589,19 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
         for (int k = 0, at = 0, round = 0; k < ntiles; ++k, at = next(at), round += at == 0) {
             const E *r = reinterpret_cast<const E *>(smem + at * L::kSlot);
             float x[8], z[8];
-            ulonglong2 sum[2];
+            f32x2 sum[4];
             if (kLanded) wait_for(at, round);
             part_sync(kDone + k % kHands, kDoneN);
             ld_vec<E, 8>(r + off, x);
             if (a.z) ld_vec<E, 8>(r + 2 * L::kRowElems + off, z);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int w = row * kYPitch + y_place(4 * col + 2 * j) / 2;
-                sum[j] = reinterpret_cast<const ulonglong2 *>(part_y(k, 0))[w];
-                if (H == 2) {
-                    const ulonglong2 more = reinterpret_cast<const ulonglong2 *>(part_y(k, 1))[w];
-                    sum[j] = make_ulonglong2(add2(sum[j].x, more.x), add2(sum[j].y, more.y));
+            for (int part = 0; part < H; ++part) {
+                const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(part_y(k, part)) + row * 2 * kPairs;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const ulonglong2 u = p[y_place(col, 2 * i)], v = p[y_place(col, 2 * i + 1)];
+                    const f32x2 four = add2(add2(u.x, u.y), add2(v.x, v.y));
+                    sum[i] = part ? add2(sum[i], four) : four;
                 }
             }
             part_arrive(kFree, 2 * kPrep);
@@ -613,13 +609,17 @@ __global__ void __launch_bounds__(Layout<E, NS, H>::kRecur + (Fetchers<E, NS, MO
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f32x2 v = i % 2 ? sum[i / 2].y : sum[i / 2].x;
+                    f32x2 v = sum[i];
                     if (a.D) v = fma2(D[i], pack2(x[2 * i], x[2 * i + 1]), v);  // not 0 x: x may be infinite
                     if (a.z) v = mul2(v, silu2(pack2(z[2 * i], z[2 * i + 1])));
                     unpack2(v, y[2 * i], y[2 * i + 1]);
                 }
                 if (BULK || row_width == kWide) {
                     st_vec<E, 8>(out, y);
+                } else if (sizeof(E) == 2 && row_width == kWord) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2)
+                        if (i < nc) *reinterpret_cast<uint32_t *>(out + i) = narrow_pair(y[i], y[i + 1]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -789,7 +789,7 @@ template <typename E> bool make_maps(const GdnSsmArgs &a, int states, Maps *m)
 template <typename E, int NS, int H, int MODE, bool BULK>
 cudaError_t launch_mode(const GdnSsmArgs &a, const Maps &maps, int tl, int tiles, int64_t slots, cudaStream_t s)
 {
-    using L = Layout<E, NS, H>;
+    using L = Layout<E, NS, H, MODE == kPieces>;
     const int per_group = a.channels / a.groups;
     const int64_t grid = slots * a.groups * ((per_group + 2 * kPairs - 1) / (2 * kPairs));
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
