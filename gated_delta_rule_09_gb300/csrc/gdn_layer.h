@@ -56,8 +56,8 @@ struct GdnSsmArgs {
 };
 
 // Pieces a call is cut into: *segment tokens each (0: not cut), and the number
-// of piece slots the workspace holds.
-void gdn_ssm_plan(int N, int T, int channels, int d_state, bool packed, int asked, int *segment,
+// of piece slots the workspace holds.  Never more slots than with one group.
+void gdn_ssm_plan(int N, int T, int channels, int groups, bool packed, int asked, int *segment,
                   int64_t *piece_slots);
 constexpr int kScanChannels = 64;  // of one group, per block of the scan
 int gdn_ssm_sms();                 // multiprocessors of the current device

@@ -221,7 +221,7 @@ size_t ssm_workspace(int64_t slots, int channels, int d_state)
 // Cuts the call into pieces if it is to be, and lays out the workspace.
 gdn_status_t take_workspace(GdnSsmArgs &a, int asked, void *workspace, size_t bytes)
 {
-    gdn_ssm_plan(a.N, a.T, a.channels, a.d_state, a.cu_seqlens != nullptr, asked, &a.segment, &a.pieces);
+    gdn_ssm_plan(a.N, a.T, a.channels, a.groups, a.cu_seqlens != nullptr, asked, &a.segment, &a.pieces);
     if (!a.segment) return GDN_OK;
     const size_t need = ssm_workspace(a.pieces, a.channels, a.d_state);
     if (!workspace || bytes < need)
@@ -268,7 +268,7 @@ size_t gdn_ssm_fwd_workspace_size(int B, int T, int channels, int d_state,
     if (B < 1 || T < 1 || channels < 1 || d_state < 1 || d_state > 128) return 0;
     int seg = 0;
     int64_t slots = 0;
-    gdn_ssm_plan(B, T, channels, d_state, cu_seqlens != nullptr, segment, &seg, &slots);
+    gdn_ssm_plan(B, T, channels, 1, cu_seqlens != nullptr, segment, &seg, &slots);  // enough for any groups
     return seg ? ssm_workspace(slots, channels, d_state) : 0;
 }
 

@@ -207,14 +207,19 @@ int gdn_ssm_sms()
 // channels: 1.09 ms cut, 6.26 ms whole (16 blocks); four of 4096 tokens x 2048
 // channels: 208 us whole, 261 to 316 cut into 512 to 2048 tokens; a pack of eight,
 // 27 610 tokens with a longest of 7671, x 4096 channels: 656 us whole, 857 cut.
-void gdn_ssm_plan(int N, int T, int channels, int d_state, bool packed, int asked, int *segment,
+// The constants are those of bf16, 16 states and tensor copies.
+//
+// Blocks end with their group, so groups make more of them; the workspace is
+// sized for one group.  More blocks only make pieces longer or a call whole:
+// each way's time grows with them, a cut call's at least as fast.
+void gdn_ssm_plan(int N, int T, int channels, int groups, bool packed, int asked, int *segment,
                   int64_t *piece_slots)
 {
     int64_t seg = ((int64_t)asked + 63) / 64 * 64;
     if (asked <= 0) {
         const int sms = gdn_ssm_sms();
         constexpr double kAlone = 51, kShared = 45, kCut = 79, kLaunch = 10000;
-        const int64_t chunks = (channels + kScanChannels - 1) / (kScanChannels);
+        const int64_t chunks = (int64_t)groups * ((channels / groups + kScanChannels - 1) / kScanChannels);
         const double tokens = (double)(packed ? T : (int64_t)N * T);
         // a packed sequence may be the longest by far; twice the mean is taken for it
         const double longest = packed && N > 1 ? 2. * T / N : T, work = tokens * chunks / sms;
