@@ -185,6 +185,9 @@ gdn_status_t check_ssm(bool step, GdnSsmArgs &a, int dtype, bool *nothing)
                         a.groups);
     if (a.d_state > 128)
         return gdn_fail(GDN_ERR_UNSUPPORTED, "d_state %d (supported: 1 to 128)", a.d_state);
+    if ((int64_t)a.groups * a.d_state > 0x7fffffff)
+        return gdn_fail(GDN_ERR_UNSUPPORTED, "rows of B and C of %d groups x %d states (supported: up to 2^31 - 1)",
+                        a.groups, a.d_state);
     GDN_TRY(check_types(dtype, GDN_ACT_NONE));
     if (a.cu_seqlens && a.N < 1)
         return gdn_fail(GDN_ERR_INVALID_ARG, "cu_seqlens given with %d sequences", a.N);

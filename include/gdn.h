@@ -360,7 +360,7 @@ gdn_status_t gdn_conv_step(const void *x, const float *weight, const float *bias
  *   Bm, Cm          [B, T, groups, d_state] dtype, row strides ld_b, ld_c
  *   D, delta_bias   [channels] fp32 or NULL
  *   state_in, state_out  [pool, channels, d_state] fp32; NULL allowed
- *   d_state 1 to 128; channels a multiple of groups
+ *   d_state 1 to 128; channels a multiple of groups; groups x d_state below 2^31
  *   segment         tokens per piece: long sequences are cut into pieces that
  *                   run in parallel (each piece's decay is exp(A sum d), so
  *                   the pieces chain exactly up to rounding); <= 0 lets the

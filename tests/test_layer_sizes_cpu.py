@@ -22,3 +22,11 @@ def test_large_counts_are_taken(lib):  # noqa: F811
     """No sequences of the longest length, or the most sequences without tokens and states."""
     assert conv_fwd(lib, B=0, T=TOP) == 0 and ssm_fwd(lib, B=0, T=TOP) == 0
     assert conv_fwd(lib, B=TOP, T=0) == 0 and ssm_fwd(lib, B=TOP, T=0) == 0
+
+
+def test_rows_of_b_past_32_bits_are_refused(lib):  # noqa: F811
+    """Columns of B and C are numbered in 32 bits."""
+    G = 1 << 24
+    kw = dict(C=G, G=G, S=128, A=1 << 40, delta=1 << 54, Bm=1 << 55, Cm=1 << 56, **FAR)
+    ld = (G, G, G * 128, G * 128, G, G)
+    assert ssm_fwd(lib, B=1, T=1, ld=ld, **kw) == 2 and ssm_step(lib, N=1, ld=ld, so=1 << 57, pool=1, **kw) == 2
