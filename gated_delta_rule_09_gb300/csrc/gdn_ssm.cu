@@ -204,9 +204,12 @@ int gdn_ssm_sms()
 // sequences take kCut ns instead, the piece pass included, but not less than a
 // piece alone in each of the two launches and kLaunch.  A grid of a few blocks
 // per SM is long enough to even out.  One sequence of 131 072 tokens x 1024
-// channels: 1.09 ms cut, 6.26 ms whole (16 blocks); four of 4096 tokens x 2048
-// channels: 208 us whole, 261 to 316 cut into 512 to 2048 tokens; a pack of eight,
-// 27 610 tokens with a longest of 7671, x 4096 channels: 656 us whole, 857 cut.
+// channels: 1.08 ms cut, 6.42 ms whole (16 blocks); four of 4096 tokens x 2048
+// channels: 210 us whole, 264 to 313 cut into 512 to 2048 tokens; a pack of eight,
+// 27 610 tokens with a longest of 7671, x 4096 channels: 498 us whole, 854 cut.
+// More states take longer either way: one sequence of 16 384 tokens x 1024
+// channels 0.33 cut : 1.18 ms whole with 32, 0.55 : 2.06 with 64, 1.03 : 3.59 with
+// 128; fp32, 16 states 0.23 : 0.86.
 // The constants are those of bf16, 16 states and tensor copies.
 //
 // Blocks end with their group, so groups make more of them; the workspace is
@@ -218,7 +221,7 @@ void gdn_ssm_plan(int N, int T, int channels, int groups, bool packed, int asked
     int64_t seg = ((int64_t)asked + 63) / 64 * 64;
     if (asked <= 0) {
         const int sms = gdn_ssm_sms();
-        constexpr double kAlone = 51, kShared = 45, kCut = 79, kLaunch = 10000;
+        constexpr double kAlone = 51, kShared = 41, kCut = 79, kLaunch = 10000;
         const int64_t chunks = (int64_t)groups * ((channels / groups + kScanChannels - 1) / kScanChannels);
         const double tokens = (double)(packed ? T : (int64_t)N * T);
         // a packed sequence may be the longest by far; twice the mean is taken for it

@@ -27,13 +27,13 @@
 //    it, five per tile from one finishing thread (from a preparing one they
 //    lengthened the whole block's turn: 236 against 210 us on the first shape
 //    below).  Other rows come by copies of 16 or 4 bytes or through registers,
-//    per thread (243 us with 2044 channels instead of 2048).  A bulk copy per row,
+//    per thread (240 us with 2044 channels instead of 2048).  A bulk copy per row,
 //    80 per tile, took 38 clocks each and twice the time.
 //
 // Measured, 16 states: 4 x 4096 tokens x 2048 channels 209 us in bf16 (a block per
-// SM, 128 of 152 busy: 51 ns per token), 225 in fp32; x 9728 channels 662 us (two
+// SM, 128 of 152 busy: 51 ns per token), 221 in fp32; x 9728 channels 662 us (two
 // blocks per SM: 13 states per clock and SM).  More states, 2048 channels, bf16
-// (fp32): 32 303 us (303), 64 522 (539), 128 908 (918).
+// (fp32): 32 301 us (326), 64 522 (538), 128 908 (917).
 //
 // Everything is fp32 until y is stored, as in the step for single tokens.  The
 // sum over states on the tensor cores (m16n8k8, tf32: the states as operand as
@@ -228,7 +228,7 @@ __device__ __forceinline__ float half_decay(float v)
 // bf16, 4 x 4096 tokens, 16 states, us with the copies made by preparing, by
 // finishing and by fetching threads: 2044 channels (4-byte copies) 302, 359, 247;
 // 2043 channels (2-byte loads) 308, 393, 281; 2048 channels x 13 states (B and C
-// through registers) 243, 310, 209 (the fetching ones with today's sum of y: 243,
+// through registers) 243, 310, 209 (the fetching ones with today's sum of y: 240,
 // 298, 218).  fp32 loses by them (203 channels 100 against
 // 110: its recurrence wants the registers), and with more states per lane there
 // are no registers for more warps.
