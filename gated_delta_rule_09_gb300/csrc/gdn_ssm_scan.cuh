@@ -822,7 +822,8 @@ template <typename E, int NS, int H> cudaError_t launch_fwd(const GdnSsmArgs &a,
 
 // Two warps per scheduler cover one another's latencies where a lane would have
 // more than four states.  4 x 4096 tokens x 2048 channels, bf16, us with the
-// states in one part against two: 32 states 344 : 317, 64 states 935 : 540.
+// states in one part against two: 32 states 344 : 317, 64 states 935 : 530 (301
+// and 522 with today's sum of y).
 template <typename E> cudaError_t scan(const GdnSsmArgs &a, cudaStream_t s)
 {
     if (a.d_state <= 16) return launch_fwd<E, 4, 1>(a, s);

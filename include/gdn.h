@@ -368,7 +368,7 @@ gdn_status_t gdn_conv_step(const void *x, const float *weight, const float *bias
  *                   multiple of 64.  Packed lengths are on the device, so the
  *                   library reckons with a longest of twice the mean: a pack
  *                   with one far longer sequence should ask for pieces (one of
- *                   130 000 tokens and 31 of 20, 1024 channels: 6.7 ms whole,
+ *                   130 000 tokens and 31 of 20, 1024 channels: 6.4 ms whole,
  *                   1.1 ms in pieces of 2048)
  *   workspace       gdn_ssm_fwd_workspace_size(...) bytes, 16-byte aligned,
  *                   not overlapping any argument, not shared by calls that
