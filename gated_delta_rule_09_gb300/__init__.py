@@ -14,7 +14,8 @@ import torch
 from . import _lib
 from ._lib import GdnError, GDN_BF16, GDN_F32  # noqa: F401
 from .layer import (  # noqa: F401
-    gdn_conv_fwd, gdn_conv_step, gdn_group_norm, gdn_ssm_fwd, gdn_ssm_fwd_workspace_size,
+    gdn_block_norm, gdn_conv_fwd, gdn_conv_step, gdn_group_norm, gdn_linattn_fwd,
+    gdn_linattn_fwd_workspace_size, gdn_linattn_step, gdn_ssm_fwd, gdn_ssm_fwd_workspace_size,
     gdn_ssm_step)
 
 _DTYPES = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}

@@ -25,6 +25,7 @@ GDN_DEV_F16_PRECISION = 0x8
 GDN_DEV_BAD_SLOT = 0x10
 GDN_ACT_NONE = 0
 GDN_ACT_SILU = 1
+GDN_ACT_SIGMOID = 2
 
 # (name, restype, argtypes) for every entry point of include/gdn.h
 _vp = ctypes.c_void_p
@@ -52,6 +53,13 @@ SIGNATURES = {
     "gdn_ssm_step": (ctypes.c_int, [_vp] * 12 + [_i] * 4 + [_l] * 6 + [_i, _i, _i, _vp]),
     "gdn_group_norm": (ctypes.c_int, [_vp] * 5 + [_l, _i, _i, _l, _l, _l, ctypes.c_float,
                                                   _i, _i, _i, _vp]),
+    "gdn_linattn_fwd_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i, _i, _vp, _i]),
+    "gdn_linattn_fwd": (ctypes.c_int, [_vp] * 8 + [_i] * 6 + [_l] * 5
+                        + [_i, _vp, ctypes.c_float, _i, _i, _vp, ctypes.c_size_t, _vp]),
+    "gdn_linattn_step": (ctypes.c_int, [_vp] * 8 + [_i] * 5 + [_l] * 5
+                         + [_i, ctypes.c_float, _i, _vp]),
+    "gdn_block_norm": (ctypes.c_int, [_vp] * 10 + [_l, _i] + [_l] * 5 + [ctypes.c_float] * 2
+                       + [_i] * 5 + [_vp]),
     "gdn_get_device_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint)]),
     "gdn_get_last_error": (ctypes.c_char_p, []),
     "gdn_version": (ctypes.c_int, []),

@@ -78,3 +78,50 @@ struct GdnNormArgs {
 };
 
 cudaError_t gdn_launch_group_norm(const GdnNormArgs &a, cudaStream_t s);
+
+struct GdnLinattnArgs {
+    const void *q, *k, *v;       // rows of groups x dk, groups x dk, heads x dv, dtype
+    const float *log_decay;      // rows of `heads`, stride ld_decay (0: one row for every token)
+    const float *state_in;       // [pool, heads, dv, dk] or null (zeros)
+    const int32_t *slots;        // [N] or null
+    void *o;                     // rows of heads x dv, dtype
+    float *state_out;            // [pool, heads, dv, dk] or null; may equal state_in
+    int N, T, heads, groups, dk, dv;
+    int64_t ld_q, ld_k, ld_v, ld_decay, ld_o;
+    int pool;
+    const int32_t *cu_seqlens;
+    float scale;
+    int dtype;
+    unsigned int *status;
+    int segment;                 // tokens per piece; 0: one piece per sequence
+    int64_t pieces;              // piece slots of the whole call, segment > 0
+    float *piece_state;          // [piece slot, heads, dv, dk]: what a piece adds, then the state it starts from
+    float *piece_decay;          // [piece slot, heads] decay over the piece
+};
+
+// Pieces a call is cut into, as gdn_ssm_plan; no more slots for a larger dv or other strides.
+void gdn_linattn_plan(int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment,
+                      int64_t *piece_slots);
+cudaError_t gdn_launch_linattn_fwd(const GdnLinattnArgs &a, cudaStream_t s, int *launches);
+cudaError_t gdn_launch_linattn_step(const GdnLinattnArgs &a, cudaStream_t s);
+
+// The tensor-core kernel over whole sequences or pieces (gdn_linattn_tc.cu), for calls it accepts.
+bool gdn_linattn_tc_supported(const GdnLinattnArgs &a);
+cudaError_t gdn_linattn_tc(const GdnLinattnArgs &a, bool states_only, cudaStream_t s);
+
+struct GdnBlockNormArgs {
+    const void *y, *gate;        // rows, dtype; gate may be null
+    const void *residual;        // rows, dtype or fp32; may be null (zeros)
+    const float *post_weight, *post_bias, *pre_weight, *pre_bias, *scale;  // [channels] or null
+    void *residual_out, *h;      // rows; may equal residual (residual_out), y, gate (h); h null without a norm before
+    int64_t rows;
+    int channels;
+    int64_t ld_y, ld_gate, ld_residual, ld_residual_out, ld_h;
+    float residual_scale, eps;
+    int rms, post, gate_act, dtype, residual_dtype;
+};
+
+// By the types of the rows and of the residual stream.
+cudaError_t gdn_block_norm_bf16(const GdnBlockNormArgs &a, cudaStream_t s);
+cudaError_t gdn_block_norm_bf16_f32(const GdnBlockNormArgs &a, cudaStream_t s);
+cudaError_t gdn_block_norm_f32(const GdnBlockNormArgs &a, cudaStream_t s);

@@ -1,0 +1,427 @@
+// Linear attention with a decay for each head: S <- e^g S + v k^T, o = scale S q,
+// S in R^{d_v x d_k} per (sequence, head), g per head or per token and head, q and
+// k shared by the heads of a group.
+//
+// Prompts go chunk by chunk.  With b_i the sum of g up to and with token i of a
+// chunk of n tokens,
+//
+//     o_i = scale (e^{b_i} S q_i + sum_{j <= i} e^{b_i - b_j} (q_i k_j) v_j)
+//     S  <- e^{b_n} S + sum_j e^{b_n - b_j} v_j k_j^T
+//
+// bf16 calls whose rows tensor copies can take run on the tensor cores
+// (gdn_linattn_tc.cu); this file has the kernel for every other call, in fp32 on
+// CUDA cores, the step for single tokens, and what joins the pieces of a long
+// sequence: a first pass forms what each piece adds to the state and its decay, a
+// chain over a sequence's pieces turns these into the states they start from, and
+// the second pass is the ordinary one over all pieces at once.
+#include "gdn_linattn.cuh"
+
+namespace {
+
+using namespace gdn_linattn;
+
+constexpr int kC = 32;        // tokens per chunk: one warp's worth of decays
+constexpr int kDVT = 64;      // columns of v per block
+constexpr int kThreads = 256;
+constexpr int kLdS = kDVT + 4;
+
+template <int DK> struct Smem {
+    float q[kC][DK + 4], k[kC][DK + 4], v[kC][kLdS], P[kC][kC + 1];
+    float S[DK][kLdS];        // the state's slice, transposed
+    float in[kC], start[kC], add[kC];
+    int first[kC];
+    float all;
+};
+
+template <typename E, int DK>
+__global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinattnArgs a, int tiles, int states_only)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    Smem<DK> &m = *reinterpret_cast<Smem<DK> *>(raw);
+    const int t = threadIdx.x, lane = t & 31;
+    const int64_t unit = blockIdx.x;
+    const int v0 = (int)(unit % tiles) * kDVT, h = (int)(unit / tiles % a.heads);
+    Unit u;
+    if (!find_unit(a, unit / tiles / a.heads, h, states_only, u)) return;
+    const int dk = a.dk, nv = min(kDVT, a.dv - v0), g = h / (a.heads / a.groups);
+    const E *q = static_cast<const E *>(a.q) + u.row * a.ld_q + (int64_t)g * dk;
+    const E *k = static_cast<const E *>(a.k) + u.row * a.ld_k + (int64_t)g * dk;
+    const E *v = static_cast<const E *>(a.v) + u.row * a.ld_v + (int64_t)h * a.dv + v0;
+    const float *decay = a.log_decay + u.row * a.ld_decay + h;
+    E *o = static_cast<E *>(a.o) + u.row * a.ld_o + (int64_t)h * a.dv + v0;
+
+    for (int i = t; i < DK * kDVT; i += kThreads) {  // d_k along the lanes, as the state lies
+        const int kk = i % DK, d = i / DK;
+        m.S[kk][d] = u.in && kk < dk && d < nv ? u.in[(int64_t)(v0 + d) * dk + kk] : 0.f;
+    }
+    const int i0 = t / 16 * 2, j0 = t % 16 * 2, d0 = t % 16 * 4;  // 2 x 2 of P, 2 x 4 of o
+    constexpr int KP = DK / 32;
+    const int k0 = t / 8 * KP, e0 = t % 8 * 8;                    // KP x 8 of S
+    for (int c = 0; c < u.len; c += kC) {
+        const int n = min(kC, u.len - c);
+        __syncthreads();
+        for (int i = t; i < kC * DK; i += kThreads) {
+            const int r = i / DK, kk = i % DK;
+            const bool is = r < n && kk < dk;
+            if (!states_only) m.q[r][kk] = is ? to_f(q[(c + r) * a.ld_q + kk]) : 0.f;
+            m.k[r][kk] = is ? to_f(k[(c + r) * a.ld_k + kk]) : 0.f;
+        }
+        for (int i = t; i < kC * kDVT; i += kThreads) {
+            const int r = i / kDVT, d = i % kDVT;
+            m.v[r][d] = r < n && d < nv ? to_f(v[(c + r) * a.ld_v + d]) : 0.f;
+        }
+        if (t < 32) {
+            Decays d;
+            d.scan(lane < n ? decay[(c + lane) * a.ld_decay] : 0.f);
+            m.in[lane] = d.in;
+            m.first[lane] = first_seen(d.mask, lane);
+            m.start[lane] = d.cut_upto(lane) ? 0.f : decay_of(d.in);
+            m.add[lane] = d.cut_behind(lane) ? 0.f : decay_of(d.after);
+            if (lane == 0) m.all = d.mask ? 0.f : decay_of(d.total);
+        }
+        __syncthreads();
+        float acc[2][4] = {};
+        if (!states_only) {
+            if (j0 <= i0 + 1) {
+                float p[2][2] = {};
+#pragma unroll 8
+                for (int kk = 0; kk < DK; kk += 4) {
+                    const float4 q0 = *reinterpret_cast<const float4 *>(&m.q[i0][kk]);
+                    const float4 q1 = *reinterpret_cast<const float4 *>(&m.q[i0 + 1][kk]);
+                    const float4 k0 = *reinterpret_cast<const float4 *>(&m.k[j0][kk]);
+                    const float4 k1 = *reinterpret_cast<const float4 *>(&m.k[j0 + 1][kk]);
+                    p[0][0] += q0.x * k0.x + q0.y * k0.y + q0.z * k0.z + q0.w * k0.w;
+                    p[0][1] += q0.x * k1.x + q0.y * k1.y + q0.z * k1.z + q0.w * k1.w;
+                    p[1][0] += q1.x * k0.x + q1.y * k0.y + q1.z * k0.z + q1.w * k0.w;
+                    p[1][1] += q1.x * k1.x + q1.y * k1.y + q1.z * k1.z + q1.w * k1.w;
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int i = i0 + x, j = j0 + y;
+                        m.P[i][j] = j <= i && j >= m.first[i] ? p[x][y] * decay_of(m.in[i] - m.in[j]) : 0.f;
+                    }
+            }
+#pragma unroll 4
+            for (int kk = 0; kk < DK; kk += 4) {
+                float q0[4], q1[4], s[4][4];
+                ld_vec<float, 4>(&m.q[i0][kk], q0);
+                ld_vec<float, 4>(&m.q[i0 + 1][kk], q1);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    ld_vec<float, 4>(&m.S[kk + x][d0], s[x]);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        acc[0][y] = fmaf(q0[x], s[x][y], acc[0][y]);
+                        acc[1][y] = fmaf(q1[x], s[x][y], acc[1][y]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float w = m.start[i0 + x];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) acc[x][y] = w == 0.f ? 0.f : w * acc[x][y];
+            }
+        }
+        __syncthreads();
+        if (!states_only) {
+            for (int j = 0; j <= i0 + 1; ++j) {
+                float w[4];
+                ld_vec<float, 4>(&m.v[j][d0], w);
+                const float p0 = m.P[i0][j], p1 = m.P[i0 + 1][j];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {  // a token sees nothing of those behind it, infinite or not
+                    acc[0][y] = j <= i0 ? fmaf(p0, w[y], acc[0][y]) : acc[0][y];
+                    acc[1][y] = fmaf(p1, w[y], acc[1][y]);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (i0 + x < n && d0 + y < nv) o[(c + i0 + x) * a.ld_o + d0 + y] = from_f<E>(a.scale * acc[x][y]);
+        }
+        float s[KP][8] = {};
+        for (int j = 0; j < n; ++j) {
+            float kk[KP], w[8];
+            ld_vec<float, KP>(&m.k[j][k0], kk);
+            ld_vec<float, 8>(&m.v[j][e0], w);
+            const float f = m.add[j];
+#pragma unroll
+            for (int x = 0; x < KP; ++x) {
+                const float fk = f * kk[x];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) s[x][y] = fmaf(fk, w[y], s[x][y]);
+            }
+        }
+        const float all = m.all;
+#pragma unroll
+        for (int x = 0; x < KP; ++x)
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                float &S = m.S[k0 + x][e0 + y];
+                S = all == 0.f ? s[x][y] : fmaf(all, S, s[x][y]);
+            }
+    }
+    __syncthreads();
+    if (u.out)
+        for (int i = t; i < DK * kDVT; i += kThreads) {
+            const int kk = i % DK, d = i / DK;
+            if (kk < dk && d < nv) u.out[(int64_t)(v0 + d) * dk + kk] = m.S[kk][d];
+        }
+}
+
+// Decay of each piece but a sequence's last, one warp each.
+__global__ void __launch_bounds__(kThreads) gdn_linattn_decay_kernel(const GdnLinattnArgs a)
+{
+    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    if (item >= a.pieces * a.heads) return;
+    const int64_t slot = item / a.heads;
+    const int h = (int)(item % a.heads), lane = threadIdx.x & 31;
+    Unit u;
+    if (!find_unit(a, slot, h, true, u)) return;
+    double sum = 0.;
+    bool cut = false;
+    if (a.ld_decay == 0) {
+        sum = (double)a.log_decay[h] * u.len;
+    } else {
+        for (int i = lane; i < u.len; i += 32) {
+            const float g = a.log_decay[(u.row + i) * a.ld_decay + h];
+            cut |= g * kLog2e <= kForget;
+            sum += g;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        cut = __any_sync(0xffffffffu, cut);
+    }
+    if (lane == 0) a.piece_decay[item] = cut ? 0.f : (float)exp(sum);
+}
+
+// The states that the pieces of each sequence start from, in place of what the
+// pieces add.  A block walks 4 x kThreads elements of one head's state through
+// the pieces; the next piece's are in flight while this one's are added.
+__global__ void __launch_bounds__(kThreads) gdn_linattn_chain_kernel(const GdnLinattnArgs a, int blocks)
+{
+    const int64_t per = (int64_t)a.dv * a.dk;
+    const int64_t head = blockIdx.x / blocks;
+    const int h = (int)(head % a.heads), n = (int)(head / a.heads);
+    int64_t first;
+    int count;
+    if (a.cu_seqlens) {
+        const int lo = a.cu_seqlens[n], hi = a.cu_seqlens[n + 1];
+        if (lo < 0 || hi < lo || hi > a.T) return;
+        first = lo / a.segment + n;
+        count = hi > lo ? (hi - lo - 1) / a.segment + 1 : 1;
+    } else {
+        count = (int)(((int64_t)a.T + a.segment - 1) / a.segment);
+        first = (int64_t)n * count;
+    }
+    const int e = a.state_in ? state_entry(a.slots, n, a.pool, a.status) : -1;
+    const float *in = e >= 0 ? a.state_in + ((int64_t)e * a.heads + h) * per : nullptr;
+    const int64_t i0 = (int64_t)(blockIdx.x % blocks) * (4 * kThreads) + threadIdx.x;
+    float S[4], next[4];
+    float *at = a.piece_state + (first * a.heads + h) * per;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int64_t i = i0 + x * kThreads;
+        S[x] = in && i < per ? in[i] : 0.f;
+        next[x] = count > 1 && i < per ? at[i] : 0.f;
+    }
+    for (int p = 0; p < count; ++p, at += a.heads * per) {
+        float add[4];
+        const bool more = p + 2 < count;
+        const float f = p + 1 < count ? a.piece_decay[(first + p) * a.heads + h] : 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int64_t i = i0 + x * kThreads;
+            add[x] = next[x];
+            if (more && i < per) next[x] = at[a.heads * per + i];
+            if (i < per) at[i] = S[x];
+            S[x] = f == 0.f ? add[x] : fmaf(f, S[x], add[x]);
+        }
+    }
+}
+
+// One new token per sequence.  Row i of S needs only itself, k, q and v_i: a warp
+// takes kRows rows of one head at a time, a row over its lanes.  Bound by HBM:
+// the state is read and written once.
+constexpr int kRows = 8;
+
+template <typename T, int V> __device__ __forceinline__ void ld_part(const T *p, int dk, int lane, bool vec, float (&x)[V])
+{
+    if (vec) {
+        if (V * lane < dk) {
+            ld_vec<T, V>(p + V * lane, x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = lane + 32 * j < dk ? to_f(p[lane + 32 * j]) : 0.f;
+    }
+}
+
+// Sums over the warp of 8 values at a time; lane l holds that of value l / 4.
+__device__ __forceinline__ float sum_rows(const float (&x)[kRows], int lane)
+{
+    float y[4], z[2];
+    const bool b16 = lane & 16, b8 = lane & 8, b4 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = (b16 ? x[i + 4] : x[i]) + __shfl_xor_sync(0xffffffffu, b16 ? x[i] : x[i + 4], 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        z[i] = (b8 ? y[i + 2] : y[i]) + __shfl_xor_sync(0xffffffffu, b8 ? y[i] : y[i + 2], 8);
+    float w = (b4 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, b4 ? z[0] : z[1], 4);
+    w += __shfl_xor_sync(0xffffffffu, w, 2);
+    return w + __shfl_xor_sync(0xffffffffu, w, 1);
+}
+
+// VEC: rows in words of V elements (d_k a multiple of V, V lane of each lane);
+// else elements lane + 32 j.
+template <typename E, int V, bool VEC>
+__global__ void __launch_bounds__(kThreads) gdn_linattn_step_kernel(const GdnLinattnArgs a, int64_t items, int groups_of_rows)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+    const int dk = a.dk, dv = a.dv, share = a.heads / a.groups;
+    const int64_t per = (int64_t)dv * dk;
+    for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; it < items; it += warps) {
+        const int r0 = (int)(it % groups_of_rows) * kRows;
+        const int64_t nh = it / groups_of_rows;
+        const int n = (int)(nh / a.heads), h = (int)(nh % a.heads);
+        const int e = state_entry(a.slots, n, a.pool, a.status);
+        const int64_t at = ((int64_t)e * a.heads + h) * per + (int64_t)r0 * dk;
+        float s[kRows][V];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (a.state_in && e >= 0 && r0 + r < dv) {
+                ld_part<float, V>(a.state_in + at + r * dk, dk, lane, VEC, s[r]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[r][j] = 0.f;
+            }
+        }
+        const int row = lane / 4;
+        const float d = decay_of(a.log_decay[n * a.ld_decay + h] * kLog2e);
+        float kk[V], qq[V];
+        ld_part<E, V>(static_cast<const E *>(a.k) + n * a.ld_k + (int64_t)(h / share) * dk, dk, lane, VEC, kk);
+        ld_part<E, V>(static_cast<const E *>(a.q) + n * a.ld_q + (int64_t)(h / share) * dk, dk, lane, VEC, qq);
+        const float vr = r0 + row < dv ? to_f(static_cast<const E *>(a.v)[n * a.ld_v + (int64_t)h * dv + r0 + row]) : 0.f;
+        float dot[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const float w = __shfl_sync(0xffffffffu, vr, 4 * r);
+            dot[r] = 0.f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s[r][j] = d == 0.f ? w * kk[j] : fmaf(d, s[r][j], w * kk[j]);
+                dot[r] = fmaf(s[r][j], qq[j], dot[r]);
+            }
+        }
+        const float sum = sum_rows(dot, lane);
+        if (lane % 4 == 0 && r0 + row < dv)
+            static_cast<E *>(a.o)[n * a.ld_o + (int64_t)h * dv + r0 + row] = from_f<E>(a.scale * sum);
+        if (e < 0) continue;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (r0 + r >= dv) break;
+            float *p = a.state_out + at + r * dk;
+            if (VEC) {
+                if (V * lane < dk) st_vec<float, V>(p + V * lane, s[r]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (lane + 32 * j < dk) p[lane + 32 * j] = s[r][j];
+            }
+        }
+    }
+}
+
+template <typename E, int V, bool VEC> cudaError_t step(const GdnLinattnArgs &a, cudaStream_t s)
+{
+    static int fit = 0;  // blocks resident at once; the same for every caller
+    if (!fit) {
+        int blocks = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &blocks, gdn_linattn_step_kernel<E, V, VEC>, kThreads, 0);
+        if (e != cudaSuccess) return e;
+        fit = gdn_ssm_sms() * (blocks > 0 ? blocks : 1);
+    }
+    const int rows = (a.dv + kRows - 1) / kRows;
+    const int64_t items = (int64_t)a.N * a.heads * rows, need = (items + kThreads / 32 - 1) / (kThreads / 32);
+    gdn_linattn_step_kernel<E, V, VEC><<<(unsigned)(need < fit ? need : fit), kThreads, 0, s>>>(a, items, rows);
+    return cudaGetLastError();
+}
+
+template <typename E> cudaError_t step_by_width(const GdnLinattnArgs &a, cudaStream_t s)
+{
+    const int V = a.dk > 64 ? 4 : 2;
+    const size_t al = V * sizeof(E);
+    const bool vec = a.dk % V == 0 && a.ld_q % V == 0 && a.ld_k % V == 0 && aligned_to(a.q, al) && aligned_to(a.k, al) &&
+                     aligned_to(a.state_in, V * 4) && aligned_to(a.state_out, V * 4);
+    if (V == 4) return vec ? step<E, 4, true>(a, s) : step<E, 4, false>(a, s);
+    return vec ? step<E, 2, true>(a, s) : step<E, 2, false>(a, s);
+}
+
+int64_t spans(const GdnLinattnArgs &a) { return a.segment ? a.pieces : a.N; }
+
+template <typename E, int DK> cudaError_t simt(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
+{
+    const int tiles = (a.dv + kDVT - 1) / kDVT;
+    const int64_t blocks = spans(a) * a.heads * tiles;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncSetAttribute(gdn_linattn_kernel<E, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)sizeof(Smem<DK>));
+    if (e != cudaSuccess) return e;
+    gdn_linattn_kernel<E, DK><<<(unsigned)blocks, kThreads, sizeof(Smem<DK>), s>>>(a, tiles, states_only);
+    return cudaGetLastError();
+}
+
+cudaError_t pass(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
+{
+    if (gdn_linattn_tc_supported(a)) return gdn_linattn_tc(a, states_only, s);
+    if (a.dtype == 1) return a.dk > 64 ? simt<__nv_bfloat16, 128>(a, states_only, s) : simt<__nv_bfloat16, 64>(a, states_only, s);
+    return a.dk > 64 ? simt<float, 128>(a, states_only, s) : simt<float, 64>(a, states_only, s);
+}
+
+}  // namespace
+
+void gdn_linattn_plan(int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment, int64_t *piece_slots)
+{
+    *segment = 0;
+    *piece_slots = 0;
+    if (asked <= 0) return;
+    const int seg = (int)(((int64_t)asked + 127) / 128 * 128);
+    if (seg >= T) return;
+    *segment = seg;
+    *piece_slots = packed ? (int64_t)T / seg + N : (int64_t)N * (((int64_t)T + seg - 1) / seg);
+}
+
+cudaError_t gdn_launch_linattn_fwd(const GdnLinattnArgs &a, cudaStream_t s, int *launches)
+{
+    *launches = 0;
+    if (a.segment) {
+        cudaError_t e = pass(a, true, s);
+        if (e != cudaSuccess) return e;
+        const int64_t warps = a.pieces * a.heads, blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+        const int per_head = (int)(((int64_t)a.dv * a.dk + 4 * kThreads - 1) / (4 * kThreads));
+        const int64_t chains = (int64_t)a.N * a.heads * per_head;
+        if (blocks > 0x7fffffff || chains > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        gdn_linattn_decay_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a);
+        gdn_linattn_chain_kernel<<<(unsigned)chains, kThreads, 0, s>>>(a, per_head);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        *launches = 3;
+    }
+    *launches += 1;
+    return pass(a, false, s);
+}
+
+cudaError_t gdn_launch_linattn_step(const GdnLinattnArgs &a, cudaStream_t s)
+{
+    return a.dtype == 1 ? step_by_width<__nv_bfloat16>(a, s) : step_by_width<float>(a, s);
+}

@@ -17,6 +17,7 @@
 // 53 us; heads of 129, element by element, 81 us: issue slots.
 #include "gdn_layer.h"
 #include "gdn_layer.cuh"
+#include "gdn_team.cuh"
 
 namespace {
 
@@ -24,43 +25,12 @@ using namespace gdn_layer;
 
 constexpr int kThreads = 256;
 
-// Sums over the team, T lanes of a warp or the block, of R values at a time.  A
-// block's warps meet in one of two buffers: by the time one is filled again, the
-// barrier of the sum between has seen everybody through reading it.
-template <int BLOCK, int R> struct TeamSum {
-    float (*sh)[R][kThreads / 32];
-    int turn;
-
-    __device__ __forceinline__ void operator()(float (&v)[R], int T)
-    {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            if (!BLOCK && o >= T) continue;
-#pragma unroll
-            for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
-        }
-        if constexpr (BLOCK != 0) {
-            if ((threadIdx.x & 31) == 0)
-#pragma unroll
-                for (int r = 0; r < R; ++r) sh[turn][r][threadIdx.x >> 5] = v[r];
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                v[r] = 0.f;
-#pragma unroll
-                for (int i = 0; i < BLOCK / 32; ++i) v[r] += sh[turn][r][i];
-            }
-            turn ^= 1;
-        }
-    }
-};
-
 // K words of VEC elements per thread and row, kRows rows at a time.  `walkers`
 // teams share the rows of a group.
 template <typename E, int VEC, int K, int kRows, int BLOCK>
 __global__ void __launch_bounds__(BLOCK ? BLOCK : kThreads) gdn_group_norm_kernel(const GdnNormArgs a, int T, int walkers)
 {
-    __shared__ __align__(16) float sh[BLOCK ? 2 : 1][kRows][kThreads / 32];
+    __shared__ __align__(16) float sh[BLOCK ? 2 : 1][kRows][kTeamWarps];
     TeamSum<BLOCK, kRows> team_sum = {sh, 0};
     typedef typename Word<VEC * sizeof(E)>::type Vec;
     constexpr int P = VEC > 1 ? VEC / 2 : 1;  // pairs, for packed arithmetic; a lone element is half a pair
@@ -214,7 +184,7 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : kThreads) gdn_group_norm_kerne
 template <typename E>
 __global__ void __launch_bounds__(kThreads) gdn_group_norm_wide_kernel(const GdnNormArgs a)
 {
-    __shared__ __align__(16) float sh[2][1][kThreads / 32];
+    __shared__ __align__(16) float sh[2][1][kTeamWarps];
     TeamSum<kThreads, 1> team_sum = {sh, 0};
     const int width = a.channels / a.groups;
     const int64_t row = blockIdx.x / a.groups;

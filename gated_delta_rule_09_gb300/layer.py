@@ -1,5 +1,6 @@
 """The operators around the recurrence: short causal convolution, selective
-state space scan (prompts and single tokens) and group norm.
+state space scan, linear attention with a decay for each head (prompts and
+single tokens), group norm, and the norms around a block.
 
 Marshalling only, as in the package's main module: the compute is in libgdn.so
 (``include/gdn.h`` has the contract of each call).  Activations may be slices
@@ -338,3 +339,158 @@ def gdn_group_norm(x, groups, weight=None, bias=None, gate=None, y=None, eps=1e-
           C, int(groups), ld_x, ld_g, ld_y, float(eps), bool(rms), code, _DTYPES[dtype],
           _handle(stream, index))
     return y
+
+
+def _linattn_params(q, k, v, log_decay, index, dtype):
+    """Checks shared by prompts and steps: (heads, groups, d_k, d_v, row strides
+    of q, k, v and log_decay)."""
+    lead, (H, dv) = v.shape[:-2], v.shape[-2:]
+    if not isinstance(q, torch.Tensor) or q.dim() != v.dim():
+        raise ValueError("q and k must be [..., groups, d_k]")
+    G, dk = q.shape[-2:]
+    qk = lead + (G, dk)
+    if not isinstance(log_decay, torch.Tensor):
+        raise TypeError("log_decay must be a CUDA tensor")
+    if log_decay.dim() == 1:
+        _param("log_decay", log_decay, torch.float32, index, (H,))
+        ld_decay = 0
+    else:
+        ld_decay = _rows("log_decay", log_decay, torch.float32, index, lead + (H,))
+    return (H, G, dk, dv, _rows("q", q, dtype, index, qk, 2), _rows("k", k, dtype, index, qk, 2),
+            _rows("v", v, dtype, index, v.shape, 2), ld_decay)
+
+
+def _values(v, dims, layout):
+    """The argument that fixes sizes, type and device of a linear attention call."""
+    _cuda("v", v)
+    if v.dtype not in _DTYPES:
+        raise TypeError("v must be float32 or bfloat16, got %s" % v.dtype)
+    if v.dim() != dims:
+        raise ValueError("v must be %s" % layout)
+    return v.shape, v.dtype, v.get_device()
+
+
+def gdn_linattn_fwd(q, k, v, log_decay, scale=1.0, state_in=None, o=None, state_out=None, slots=None,
+                    cu_seqlens=None, segment=0, workspace=None, stream=None, want_final_state=True):
+    """Linear attention with a decay for each head over prompts; returns
+    ``(o, state_out)``.
+
+    q, k [B,T,groups,d_k], v, o [B,T,H,d_v] (fp32 or bf16, one dtype), H a
+    multiple of groups (head h uses the q and k of group h / (H / groups)),
+    1 <= d_k <= 128; ``log_decay`` fp32 [B,T,H], or [H] for one fixed decay per
+    head.  Per head S = e^g S + v k^T, o = scale S q.  States are fp32
+    [N,H,d_v,d_k], or pools addressed by ``slots``, as in ``gdn_conv_fwd``.
+    ``segment`` is the length in tokens of the pieces that long sequences are
+    cut into (0: chosen by the library); ``workspace`` a uint8 CUDA tensor of
+    ``gdn_linattn_fwd_workspace_size(...)`` bytes, allocated here if None.
+    """
+    shape, dtype, index = _values(v, 4, "[B,T,H,d_v]")
+    N, T = _sequences(shape, cu_seqlens, index)
+    H, G, dk, dv, ld_q, ld_k, ld_v, ld_d = _linattn_params(q, k, v, log_decay, index, dtype)
+    lib = _lib.load()
+    state_out, pool = _states(state_in, state_out, slots, N, (H, dv, dk), torch.float32, index,
+                              want_final_state, v, stream)
+    if o is None:
+        o, ld_o = _empty(stream, v), H * dv
+    else:
+        ld_o = _rows("o", o, dtype, index, shape, 2)
+    segment = int(segment)
+    if workspace is None:
+        need = lib.gdn_linattn_fwd_workspace_size(N, T, H, dk, dv, _ptr(cu_seqlens), segment)
+        if need:
+            workspace = _empty(stream, v, (need,), torch.uint8)
+    else:
+        _on("workspace", workspace, torch.uint8, index)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _call(lib.gdn_linattn_fwd, index, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_in),
+          _ptr(slots), _ptr(o), _ptr(state_out), N, T, H, G, dk, dv, ld_q, ld_k, ld_v, ld_d, ld_o, pool,
+          _ptr(cu_seqlens), float(scale), _DTYPES[dtype], segment, _ptr(workspace),
+          0 if workspace is None else workspace.numel(), _handle(stream, index))
+    return o, state_out
+
+
+def gdn_linattn_fwd_workspace_size(N, T, heads, d_k, d_v, packed=False, segment=0):
+    """Bytes of device workspace ``gdn_linattn_fwd`` needs for N sequences of T
+    tokens (``packed``: T rows in all); 0 when it needs none."""
+    marker = 1 if packed else None  # only NULL-ness reaches the library
+    return int(_lib.load().gdn_linattn_fwd_workspace_size(N, T, heads, d_k, d_v, marker, int(segment)))
+
+
+def gdn_linattn_step(q, k, v, log_decay, scale=1.0, state_in=None, o=None, state_out=None, slots=None,
+                     stream=None):
+    """``gdn_linattn_fwd`` for one new token per sequence: q, k [N,groups,d_k],
+    v, o [N,H,d_v], ``log_decay`` [N,H] or [H]; returns ``(o, state_out)``;
+    ``state_out`` may be ``state_in``."""
+    shape, dtype, index = _values(v, 3, "[N,H,d_v]")
+    N = shape[0]
+    H, G, dk, dv, ld_q, ld_k, ld_v, ld_d = _linattn_params(q, k, v, log_decay, index, dtype)
+    fn = _lib.load().gdn_linattn_step
+    state_out, pool = _states(state_in, state_out, slots, N, (H, dv, dk), torch.float32, index, True, v,
+                              stream)
+    if o is None:
+        o, ld_o = _empty(stream, v), H * dv
+    else:
+        ld_o = _rows("o", o, dtype, index, shape, 2)
+    _call(fn, index, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_in), _ptr(slots), _ptr(o),
+          _ptr(state_out), N, H, G, dk, dv, ld_q, ld_k, ld_v, ld_d, ld_o, pool, float(scale),
+          _DTYPES[dtype], _handle(stream, index))
+    return o, state_out
+
+
+_GATES = {"none": _lib.GDN_ACT_NONE, "silu": _lib.GDN_ACT_SILU, "sigmoid": _lib.GDN_ACT_SIGMOID}
+
+
+def gdn_block_norm(y, residual=None, post_weight=None, post_bias=None, pre_weight=None, pre_bias=None,
+                   gate=None, gate_act="sigmoid", scale=None, residual_scale=1.0, residual_out=None,
+                   h=None, eps=1e-5, rms=True, post=True, pre=True, stream=None):
+    """What stands between two blocks, in one pass; returns ``(residual_out, h)``.
+
+    u = norm(y) post_weight + post_bias (``post=False``: y itself),
+    r = residual_scale residual + scale u act(gate), h = norm(r) pre_weight +
+    pre_bias, norms over the last dimension (``rms``: by the root mean square).
+    y, gate, h [..., C] fp32 or bf16; residual and residual_out of y's dtype or
+    fp32 (None: zeros, of y's dtype); parameters and ``scale`` [C] fp32 or None;
+    ``gate_act`` "sigmoid", "silu" or "none" (the gate itself).  ``pre=False``:
+    h is None.  Outputs may be inputs of their own type (in place).
+    """
+    _cuda("y", y)
+    shape, dtype, index = y.shape, y.dtype, y.get_device()
+    if dtype not in _DTYPES:
+        raise TypeError("y must be float32 or bfloat16, got %s" % dtype)
+    if len(shape) < 1:
+        raise ValueError("y must be [..., C]")
+    C = shape[-1]
+    if gate_act not in _GATES:
+        raise ValueError("gate_act must be one of %s, got %r" % (sorted(_GATES), gate_act))
+    if not post and (post_weight is not None or post_bias is not None):
+        raise ValueError("post_weight and post_bias need post=True")
+    if not pre and (pre_weight is not None or pre_bias is not None or h is not None):
+        raise ValueError("pre_weight, pre_bias and h need pre=True")
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
+                    ("pre_bias", pre_bias), ("scale", scale)):
+        if t is not None:
+            _param(name, t, torch.float32, index, (C,))
+    given = residual if residual is not None else residual_out
+    rtype = dtype if given is None else getattr(given, "dtype", None)
+    if rtype is not dtype and rtype is not torch.float32:
+        raise TypeError("residual must be %s or torch.float32, got %s" % (dtype, rtype))
+    ld_y = _rows("y", y, dtype, index, shape)
+    ld_g = 0 if gate is None else _rows("gate", gate, dtype, index, shape)
+    ld_r = 0 if residual is None else _rows("residual", residual, rtype, index, shape)
+    fn = _lib.load().gdn_block_norm
+    if residual_out is None:
+        residual_out, ld_ro = _empty(stream, y, shape, rtype), C
+    else:
+        ld_ro = _rows("residual_out", residual_out, rtype, index, shape)
+    ld_h = 0
+    if pre:
+        if h is None:
+            h, ld_h = _empty(stream, y), C
+        else:
+            ld_h = _rows("h", h, dtype, index, shape)
+    _call(fn, index, _ptr(y), _ptr(residual), _ptr(gate), _ptr(post_weight), _ptr(post_bias), _ptr(scale),
+          _ptr(pre_weight), _ptr(pre_bias), _ptr(residual_out), _ptr(h), y.numel() // C if C else 0, C,
+          ld_y, ld_r, ld_g, ld_ro, ld_h, float(residual_scale), float(eps), bool(rms), bool(post),
+          _GATES[gate_act], _DTYPES[dtype], _DTYPES[rtype], _handle(stream, index))
+    return residual_out, h

@@ -54,7 +54,11 @@ typedef enum {
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype_t;
 
 /* Activation of the layer operators (gdn_conv_*, gdn_group_norm). */
-typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 /* v / (1 + e^-v) */ } gdn_act_t;
+typedef enum {
+    GDN_ACT_NONE = 0,
+    GDN_ACT_SILU = 1,    /* v / (1 + e^-v) */
+    GDN_ACT_SIGMOID = 2  /* 1 / (1 + e^-v); gates of gdn_block_norm only */
+} gdn_act_t;
 
 /* Device-side status bits returned by gdn_get_device_status(). */
 #define GDN_DEV_BAD_SEQLENS 0x1u /* a cu_seqlens span was negative or past T */
@@ -419,6 +423,85 @@ gdn_status_t gdn_group_norm(const void *x, const void *gate, const float *weight
                             gdn_act_t act, gdn_dtype_t dtype, void *stream);
 
 /*
+ * gdn_linattn_fwd — linear attention with a decay for each head, over prompts:
+ *
+ *     S_t = e^{g_t} S_{t-1} + v_t k_t^T        S in R^{d_v x d_k}, per head
+ *     o_t = scale S_t q_t
+ *
+ * with g fixed per head (ld_decay = 0) or per token and head.  Head h uses the
+ * q and k of group h / (heads / groups).
+ *   q, k        [B, T, groups, d_k] dtype, row strides ld_q, ld_k
+ *   v, o        [B, T, heads, d_v] dtype, row strides ld_v, ld_o
+ *   log_decay   [B, T, heads] fp32, row stride ld_decay, or [heads] with
+ *               ld_decay = 0; <= 0 is the usual range.  A token whose decay is
+ *               below 2^-126 (-inf included) forgets what was before it, an
+ *               infinite state too.  Sums over 128 tokens above 80 overflow.
+ *   state_in, state_out  [pool, heads, d_v, d_k] fp32, the layout of
+ *               gdn_chunk_fwd's states; NULL allowed
+ *   d_k 1 to 128; heads a multiple of groups
+ *   segment     tokens per piece: long sequences are cut into pieces that run in
+ *               parallel (what each adds to the state first, then a chain over
+ *               the pieces, then the outputs); <= 0 lets the library choose
+ *               (possibly one piece), else rounded up to a multiple of 128
+ *   workspace   gdn_linattn_fwd_workspace_size(...) bytes, 16-byte aligned, not
+ *               overlapping any argument, not shared by calls that overlap in
+ *               time; NULL allowed when that size is 0
+ * bf16 with d_k, d_v and row strides multiples of 8 and q, k, v, o aligned to 16
+ * bytes runs on the tensor cores; everything else in fp32 on CUDA cores.  One
+ * kernel, or four when sequences are cut; path 9.
+ */
+size_t gdn_linattn_fwd_workspace_size(int B, int T, int heads, int d_k, int d_v,
+                                      const int32_t *cu_seqlens, int segment);
+
+gdn_status_t gdn_linattn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                             const float *state_in, const int32_t *slots, void *o, float *state_out,
+                             int B, int T, int heads, int groups, int d_k, int d_v, int64_t ld_q,
+                             int64_t ld_k, int64_t ld_v, int64_t ld_decay, int64_t ld_o, int pool,
+                             const int32_t *cu_seqlens, float scale, gdn_dtype_t dtype, int segment,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_linattn_step — the same for one new token of each of N sequences: q, k
+ * [N, groups, d_k], v, o [N, heads, d_v], log_decay [N, heads] or [heads] with
+ * ld_decay = 0.  state_out is required; state_in NULL = zeros.  One kernel,
+ * path 9.
+ */
+gdn_status_t gdn_linattn_step(const void *q, const void *k, const void *v, const float *log_decay,
+                              const float *state_in, const int32_t *slots, void *o, float *state_out,
+                              int N, int heads, int groups, int d_k, int d_v, int64_t ld_q,
+                              int64_t ld_k, int64_t ld_v, int64_t ld_decay, int64_t ld_o, int pool,
+                              float scale, gdn_dtype_t dtype, void *stream);
+
+/*
+ * gdn_block_norm — what stands between two blocks, in one pass over the rows:
+ * the norm after a block, its gate and scale, the residual sum, and the norm
+ * before the next block,
+ *
+ *     u = post ? norm(y) * post_weight[c] + post_bias[c] : y
+ *     r = residual_scale * residual + scale[c] * u * act(gate)
+ *     h = norm(r) * pre_weight[c] + pre_bias[c]
+ *
+ * with norm over the whole row: (x - mean) / sqrt(var + eps), or x / sqrt(mean
+ * x^2 + eps) with rms != 0.  h is formed from r in fp32, before r is rounded.
+ *   y, gate, h             [rows, channels] dtype, row strides ld_y, ld_gate, ld_h
+ *   residual, residual_out [rows, channels] residual_dtype (dtype, or GDN_F32 for
+ *               a stream kept in fp32), row strides ld_residual, ld_residual_out
+ *   post_weight, post_bias, scale, pre_weight, pre_bias  [channels] fp32 or NULL
+ *   gate NULL: factor one; gate_act GDN_ACT_NONE (the gate itself), _SIGMOID or
+ *   _SILU.  residual NULL: zeros (the first block).  h NULL: no second norm.
+ * Without a norm its parameters must be NULL.  Each output may be exactly one of
+ * y, gate and residual with the same stride and type (in place).  One kernel,
+ * path 10.
+ */
+gdn_status_t gdn_block_norm(const void *y, const void *residual, const void *gate,
+                            const float *post_weight, const float *post_bias, const float *scale,
+                            const float *pre_weight, const float *pre_bias, void *residual_out, void *h,
+                            int64_t rows, int channels, int64_t ld_y, int64_t ld_residual, int64_t ld_gate,
+                            int64_t ld_residual_out, int64_t ld_h, float residual_scale, float eps, int rms,
+                            int post, gdn_act_t gate_act, gdn_dtype_t dtype, gdn_dtype_t residual_dtype,
+                            void *stream);
+
+/*
  * gdn_get_device_status — synchronise `stream`, then read and clear the
  * device-side status bits (GDN_DEV_*) raised by kernels of this library on the
  * current device since the last read.  *flags receives the bits (0 = clean).
@@ -449,7 +532,7 @@ int gdn_version(void);
  * 1 = tcgen05 tensor-core chunk kernel, 2 = recurrent decode kernel,
  * 3 = chunk-level scan over segments, 4 / 5 = UT inverse by forward
  * substitution / on the tensor cores, 6 = short convolution, 7 = state space
- * scan or step, 8 = group norm).  For
+ * scan or step, 8 = group norm, 9 = linear attention, 10 = block norm).  For
  * accounting in benchmarks; no device work.
  */
 int gdn_last_launch_count(int *path);
