@@ -39,6 +39,7 @@ using namespace sm100;
 constexpr int kC = 128;     // tokens per chunk
 constexpr int kDVT = 64;    // columns of v per block
 constexpr int kThreads = 18 * 32;
+constexpr float kPlain = 120.f;  // decays of a block of 32, log 2, that go as products of two factors
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 50000;  // a wait's bound once the block has given up on one
 
@@ -52,9 +53,9 @@ constexpr int kOffS = kOffW + 2 * kTile;  // S^T: high and low parts
 constexpr int kOffSmall = kOffS + 2 * kTile;
 
 struct Small {
-    // decays of two chunks: sums up to and with a token within its block of 32, factors
-    // from a token to the end of its block, and the blocks' sums
-    float in[2][kC], back[2][kC], total[2][4];
+    // decays of two chunks: sums up to and with a token within its block of 32, their
+    // inverse factors 2^-in, and the blocks' sums
+    float in[2][kC], inverse[2][kC], total[2][4];
     unsigned mask[2][4];
     int odd[2];             // V has infinities or NaN
     uint64_t full[2], kq_free[2], v_free[2], dec_ready[2], dec_free[2], w_ready[2];
@@ -90,6 +91,14 @@ __device__ __forceinline__ uint32_t lane_addr(uint32_t tbase, int quad, uint32_t
     return tbase + (static_cast<uint32_t>(quad * 32) << 16) + col;
 }
 
+// Waits for this thread's loads from tensor memory; v is not looked at before.
+template <int N> __device__ __forceinline__ void landed(float (&v)[N])
+{
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
 {
     uint32_t v;
@@ -97,38 +106,83 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
     return v;
 }
 
-// Two values as bf16 pairs: the upper 16 bits of each, and what they leave, rounded.
-// `sign` collects NaN where a value is infinite or NaN, whose low part is then NaN.
-__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo, float &sign)
+// Two values as two bf16 pairs, the first rounded, the second what that leaves.
+// `sign` becomes NaN where a value is infinite or NaN, whose second part then is NaN.
+__device__ __forceinline__ void split(f32x2 v, uint32_t &hi, uint32_t &lo, f32x2 &sign)
 {
-    hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-    const float a = x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-    const float b = y - __uint_as_float(__float_as_uint(y) & 0xffff0000u);
-    sign = fmaf(a, 0.f, fmaf(b, 0.f, sign));
-    lo = narrow_pair(a, b);
+    float x, y;
+    unpack2(v, x, y);
+    hi = narrow_pair(x, y);
+    const f32x2 d = fma2(pack2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), dup2(-1.f), v);
+    sign = fma2(d, dup2(0.f), sign);
+    unpack2(d, x, y);
+    lo = narrow_pair(x, y);
 }
 
-// The low parts where a high part is infinite or NaN: zero.
-__device__ __forceinline__ uint32_t mend(uint32_t hi, uint32_t lo)
+__device__ __forceinline__ bool is_odd(f32x2 sign)
 {
-    if ((hi & 0x7f80u) == 0x7f80u) lo &= 0xffff0000u;
-    if ((hi & 0x7f800000u) == 0x7f800000u) lo &= 0xffffu;
-    return lo;
+    float x, y;
+    unpack2(sign, x, y);
+    return x + y != 0.f;
+}
+
+// Second parts where the first is infinite or NaN: zero.
+template <int N> __device__ __forceinline__ void mend(const uint32_t (&hi)[N], uint32_t (&lo)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if ((hi[i] & 0x7f80u) == 0x7f80u) lo[i] &= 0xffff0000u;
+        if ((hi[i] & 0x7f800000u) == 0x7f800000u) lo[i] &= 0xffffu;
+    }
 }
 
 // 8 values into 16-byte column c of row r of two tiles.
-__device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const float *x)
+__device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4])
 {
     uint32_t hi[4], lo[4];
-    float sign = 0.f;
+    f32x2 sign = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split(x[2 * i], x[2 * i + 1], hi[i], lo[i], sign);
-    if (sign != 0.f)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lo[i] = mend(hi[i], lo[i]);
+    for (int i = 0; i < 4; ++i) split(x[i], hi[i], lo[i], sign);
+    if (is_odd(sign)) mend(hi, lo);
     const uint32_t at = sw128(r, c);
     *reinterpret_cast<uint4 *>(tiles + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4 *>(tiles + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
+// P of one row in the cases that the plain path leaves: tokens that forget, blocks
+// that decay by more than 2^120, and products that are infinite or NaN.
+__device__ __noinline__ void odd_decays(uint32_t tbase, int quad, int lane, const float *in, const float *total,
+                                        const unsigned *mask)
+{
+    const float mine = in[32 * quad + lane];
+    float sum = mine;
+    bool cut = mask[quad] & (0xffffffffu >> (31 - lane));
+    const int first = first_seen(mask[quad], lane);
+#pragma unroll 1
+    for (int J = quad; J >= 0; --J) {
+        float x[32];
+        tmem_ld32(lane_addr(tbase, quad, kColQK + 32 * J), x);
+        landed(x);
+        uint32_t hi[16], lo[16];
+        f32x2 sign = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float w = in[32 * J + j];
+            const bool seen = J == quad ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
+            const float f = decay_of(J == quad ? mine - w : sum + (total[J] - w));
+            x[j] = seen && f != 0.f ? x[j] * f : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) split(pack2(x[2 * j], x[2 * j + 1]), hi[j], lo[j], sign);
+        mend(hi, lo);
+        __syncwarp();
+        tmem_st16(lane_addr(tbase, quad, kColP + 16 * J), hi);
+        tmem_st16(lane_addr(tbase, quad, kColP + 64 + 16 * J), lo);
+        if (J < quad) {
+            sum += total[J];
+            cut = cut || mask[J];
+        }
+    }
 }
 
 // P V of one row and 32 columns for a chunk whose V is infinite or NaN somewhere: a
@@ -140,8 +194,9 @@ __device__ __noinline__ void odd_row(uint32_t tbase, int quad, int i, int first,
 #pragma unroll 1
     for (int w = 0; w < 16 * (quad + 1); ++w) {
         __syncwarp();
-        const uint32_t hi = tmem_ld1(lane_addr(tbase, quad, kColP + w)), lo = tmem_ld1(lane_addr(tbase, quad, kColP + 64 + w));
+        uint32_t hi = tmem_ld1(lane_addr(tbase, quad, kColP + w)), lo = tmem_ld1(lane_addr(tbase, quad, kColP + 64 + w));
         tmem_ld_wait();
+        asm volatile("" : "+r"(hi), "+r"(lo));
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
             const int j = 2 * w + e;
@@ -178,7 +233,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
             mbar_init(&s.kq_free[i], 1);
             mbar_init(&s.v_free[i], 1);
             mbar_init(&s.dec_ready[i], 128);
-            mbar_init(&s.dec_free[i], states_only ? 128 : 256);
+            mbar_init(&s.dec_free[i], states_only ? 128 : 384);
             mbar_init(&s.w_ready[i], 128);
         }
         mbar_init(&s.qk_full, 1);
@@ -219,79 +274,65 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
         for (int c = 0; c < chunks && !states_only; ++c) {
             const int st = c & 1;
             wait(&s.dec_ready[st], c >> 1);
+            // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where J, the block
+            // of j, decays by less than 2^120; within a block without the middle factor.
             const float in = s.in[st][t];
-            const unsigned mask = s.mask[st][quad];
-            const int first = first_seen(mask, lane);
-            float far[4];  // factor from the end of an earlier block
-            {
-                float sum = in;
-                bool cut = mask & (0xffffffffu >> (31 - lane));
-#pragma unroll
-                for (int J = 3; J >= 0; --J)
-                    if (J < quad) {
-                        far[J] = cut ? 0.f : decay_of(sum);
-                        sum += s.total[st][J];
-                        cut = cut || s.mask[st][J];
-                    } else {
-                        far[J] = 0.f;
-                    }
-            }
+            bool plain = true;
+            for (int J = 0; J <= quad; ++J) plain = plain && s.mask[st][J] == 0 && fabsf(s.total[st][J]) < kPlain;
             wait(&s.qk_full, c);
             if (c > 0) wait(&s.p_free, c - 1);
             __syncwarp();
             tc_fence_after();
-#pragma unroll
-            for (int J = 0; J < 4; ++J) {
-                if (J > quad) break;
+            float sum = in;
+            bool odd = false;
+#pragma unroll 1
+            for (int J = quad; J >= 0 && plain; --J) {
                 float x[32];
                 tmem_ld32(lane_addr(tbase, quad, kColQK + 32 * J), x);
-                tmem_ld_wait();
-                if (J < quad) {
+                if (J < quad) sum += s.total[st][J];
+                const f32x2 f = dup2(decay_of(sum));
+                const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J]);
+                landed(x);
+                if (J == quad) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&s.back[st][32 * J + j]);
-                        const float w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float m = far[J] * w[e];
-                            x[j + e] = m == 0.f ? 0.f : m * x[j + e];
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&s.in[st][32 * J + j]);
-                        const float w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[j + e] = j + e <= lane && j + e >= first ? x[j + e] * decay_of(in - w[e]) : 0.f;
-                    }
+                    for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
                 }
                 uint32_t hi[16], lo[16];
-                float sign = 0.f;
+                f32x2 sign = 0;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) split(x[2 * j], x[2 * j + 1], hi[j], lo[j], sign);
-                if (sign != 0.f)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) lo[j] = mend(hi[j], lo[j]);
-                __syncwarp();
+                for (int j = 0; j < 8; ++j) {
+                    const float4 w = inverse[j];
+                    split(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), hi[2 * j], lo[2 * j], sign);
+                    split(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), hi[2 * j + 1],
+                          lo[2 * j + 1], sign);
+                }
+                odd |= is_odd(sign);
                 tmem_st16(lane_addr(tbase, quad, kColP + 16 * J), hi);
                 tmem_st16(lane_addr(tbase, quad, kColP + 64 + 16 * J), lo);
             }
+            if (__any_sync(0xffffffffu, odd || !plain)) odd_decays(tbase, quad, lane, s.in[st], s.total[st], s.mask[st]);
+            mbar_arrive(&s.dec_free[st]);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&s.p_ready);
         }
     } else if (warp < 8) {
         // ---- the state: row t of S^T
-        float S[kDVT];
+        f32x2 S[kDVT / 2];
         const int64_t at = (int64_t)v0 * dk + t;
         const int nv = min(kDVT, a.dv - v0);
 #pragma unroll
-        for (int d = 0; d < kDVT; ++d) S[d] = u.in && t < dk && d < nv ? u.in[at + (int64_t)d * dk] : 0.f;
+        for (int d = 0; d < kDVT; d += 2) {
+            const bool is = u.in && t < dk;
+            S[d / 2] = pack2(is && d < nv ? u.in[at + (int64_t)d * dk] : 0.f,
+                             is && d + 1 < nv ? u.in[at + (int64_t)(d + 1) * dk] : 0.f);
+        }
         auto hand_over = [&] {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) st_parts(sm + kOffS, t, q, S + 8 * q);
+            for (int q = 0; q < 8; ++q) {
+                const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
+                st_parts(sm + kOffS, t, q, x);
+            }
             fence_async_smem();
             mbar_arrive(&s.s_ready);
         };
@@ -303,6 +344,9 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
             const uint4 mask = *reinterpret_cast<const uint4 *>(s.mask[st]);
             const float all = mask.x | mask.y | mask.z | mask.w ? 0.f : decay_of(total.x + total.y + total.z + total.w);
             mbar_arrive(&s.dec_free[st]);
+            if (all == 0.f)
+#pragma unroll
+                for (int d = 0; d < kDVT / 2; ++d) S[d] = 0;  // forgotten, infinite or not
             wait(&s.u_full, c);
             __syncwarp();
             tc_fence_after();
@@ -310,9 +354,9 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
             for (int half = 0; half < 2; ++half) {
                 float x[32];
                 tmem_ld32(lane_addr(tbase, quad, kColU + 32 * half), x);
-                tmem_ld_wait();
+                landed(x);
 #pragma unroll
-                for (int d = 0; d < 32; ++d) S[32 * half + d] = all == 0.f ? x[d] : fmaf(all, S[32 * half + d], x[d]);
+                for (int d = 0; d < 16; ++d) S[16 * half + d] = fma2(dup2(all), S[16 * half + d], pack2(x[2 * d], x[2 * d + 1]));
             }
             tc_fence_before();
             mbar_arrive(&s.u_free);
@@ -323,8 +367,12 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
         }
         if (u.out && !*abort_flag)
 #pragma unroll
-            for (int d = 0; d < kDVT; ++d)
-                if (t < dk && d < nv) u.out[at + (int64_t)d * dk] = S[d];
+            for (int d = 0; d < kDVT; d += 2) {
+                float x, y;
+                unpack2(S[d / 2], x, y);
+                if (t < dk && d < nv) u.out[at + (int64_t)d * dk] = x;
+                if (t < dk && d + 1 < nv) u.out[at + (int64_t)(d + 1) * dk] = y;
+            }
     } else if (warp < 12) {
         // ---- decays, and V times the decay to the chunk's end
         const float *decay = a.log_decay + (u.row + t) * a.ld_decay + h;
@@ -336,7 +384,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
             next = t + (int64_t)(c + 1) * kC < u.len ? decay[(int64_t)(c + 1) * kC * a.ld_decay] : 0.f;
             if (c > 1) wait(&s.dec_free[st], (c - 2) >> 1);
             s.in[st][t] = d.in;
-            s.back[st][t] = d.cut_behind(lane) ? 0.f : decay_of(d.after);
+            s.inverse[st][t] = ex2(-d.in);
             if (lane == 0) {
                 s.total[st][quad] = d.total;
                 s.mask[st][quad] = d.mask;
@@ -357,19 +405,21 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
             if (c > 0) wait(&s.u_full, c - 1);  // the product has read the last chunk's
             uint8_t *V = sm + kOffV + st * kTile, *W = sm + kOffW;
             if (t < n) {
-                float sign = 0.f;
+                f32x2 sign = 0;
 #pragma unroll 2
                 for (int q = 0; q < 8; ++q) {
-                    float x[8];
-                    widen(*reinterpret_cast<const uint4 *>(V + sw128(t, q)), x);
+                    float f[8];
+                    widen(*reinterpret_cast<const uint4 *>(V + sw128(t, q)), f);
+                    f32x2 x[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        sign = fmaf(x[e], 0.f, sign);
-                        x[e] = w == 0.f ? 0.f : x[e] * w;
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = pack2(f[2 * e], f[2 * e + 1]);
+                        sign = fma2(x[e], dup2(0.f), sign);
+                        x[e] = w == 0.f ? 0 : mul2(x[e], dup2(w));
                     }
                     st_parts(W, t, q, x);
                 }
-                if (sign != 0.f) s.odd[st] = 1;
+                if (is_odd(sign)) s.odd[st] = 1;
             } else {  // rows past the end may be another sequence's
                 const uint4 zero = make_uint4(0, 0, 0, 0);
                 uint8_t *K = sm + kOffK + st * 2 * kTile;
@@ -403,7 +453,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
                     cut = cut || s.mask[st][J];
                     sum += s.total[st][J];
                 }
-            const float start = cut ? 0.f : decay_of(sum);
+            const float start = cut ? 0.f : a.scale * decay_of(sum);
             wait(&s.w_ready[st], c >> 1);
             const bool odd = s.odd[st];
             mbar_arrive(&s.dec_free[st]);
@@ -422,18 +472,25 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
                     odd_row(tbase, quad, t, first, sm + kOffV + st * kTile, half, y);
                 else
                     tmem_ld32(lane_addr(tbase, quad, kColO + 32 * half), y);
-                tmem_ld_wait();
+                landed(x);
+                landed(y);
                 if (half == 1) {
                     tc_fence_before();
                     mbar_arrive(&s.o_free);
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    float f[8];
+                    uint32_t f[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f[e] = a.scale * (start == 0.f ? y[8 * q + e] : fmaf(start, x[8 * q + e], y[8 * q + e]));
-                    if (t < n && 32 * half + 8 * q < nv) st_vec<__nv_bfloat16, 8>(o + 32 * half + 8 * q, f);
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = 8 * q + 2 * e;
+                        const f32x2 w = mul2(pack2(y[i], y[i + 1]), dup2(a.scale));
+                        float lo, hi;
+                        unpack2(start == 0.f ? w : fma2(pack2(x[i], x[i + 1]), dup2(start), w), lo, hi);
+                        f[e] = narrow_pair(lo, hi);
+                    }
+                    if (t < n && 32 * half + 8 * q < nv) 
+                        *reinterpret_cast<uint4 *>(o + 32 * half + 8 * q) = make_uint4(f[0], f[1], f[2], f[3]);
                 }
             }
             if (odd) {
@@ -525,7 +582,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
                 }
             }
         }
-    } else if (lane == 0) {
+    } else if (warp == 17 && lane == 0) {
         // ---- tensor copies
         const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
         const uint32_t bytes = (uint32_t)(halves * (states_only ? 1 : 2) + 1) * kTile;
