@@ -19,8 +19,10 @@
 //
 // Roles: warps 0-3 form P (tensor memory to tensor memory, a row per thread),
 // warps 4-7 keep the state and write its parts for the next chunk, warps 8-11 sum
-// the decays and form the decayed V, warps 12-15 write the outputs, warp 16 issues
-// the products, warp 17 the tensor copies into a ring of two stages.
+// the decays and form the decayed V, warps 12-15 write the outputs, warps 16 and 17
+// issue the products with P and those with the state, warps 18 and 19 the tensor
+// copies into rings of two stages, with later chunks fetched to L2 ahead.  All loops over chunks are kept small: together they have to
+// stay in the instruction cache.
 //
 // Every wait is bounded: on timeout the block raises GDN_DEV_WAIT_TIMEOUT, issues
 // no more copies and winds down with waits of 50 us, enough for what is in flight.
@@ -38,7 +40,8 @@ using namespace sm100;
 
 constexpr int kC = 128;     // tokens per chunk
 constexpr int kDVT = 64;    // columns of v per block
-constexpr int kThreads = 18 * 32;
+constexpr int kThreads = 20 * 32;
+constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one that is copied
 constexpr float kPlain = 120.f;  // decays of a block of 32, log 2, that go as products of two factors
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 50000;  // a wait's bound once the block has given up on one
@@ -58,16 +61,17 @@ struct Small {
     float in[2][kC], inverse[2][kC], total[2][4];
     unsigned mask[2][4];
     int odd[2];             // V has infinities or NaN
-    uint64_t full[2], kq_free[2], v_free[2], dec_ready[2], dec_free[2], w_ready[2];
-    uint64_t qk_full, p_ready, p_free, u_full, u_free, s_ready, o_full, o_free;
+    uint64_t full[2], v_full[2], kq_free[2], v_free[2], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2];
+    uint64_t p_free, u_full, u_free, s_ready, o_full;
     uint32_t tmem;
     int abort_flag;
 };
 constexpr int kSmemBytes = kOffSmall + (int)sizeof(Small);
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
-// Tensor memory, 512 columns: Q K^T | parts of P | Q S^T x 2 | P V | U.
-constexpr uint32_t kColQK = 0, kColP = 128, kColI = 256, kColO = 384, kColU = 448;
+// Tensor memory, 512 columns: Q K^T, then P in its place, x 2 | Q S^T x 2 | P V | U.
+// The parts of P of 32 tokens take the columns of their 32 products: 16 and 16.
+constexpr uint32_t kColP = 0, kColI = 256, kColO = 384, kColU = 448;
 
 __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *status)
 {
@@ -91,18 +95,56 @@ __device__ __forceinline__ uint32_t lane_addr(uint32_t tbase, int quad, uint32_t
     return tbase + (static_cast<uint32_t>(quad * 32) << 16) + col;
 }
 
-// Waits for this thread's loads from tensor memory; v is not looked at before.
-template <int N> __device__ __forceinline__ void landed(float (&v)[N])
+// One thread of the warp, the same each time: products and tensor copies are issued by
+// one thread, and the compiler has to know that it is one.
+__device__ __forceinline__ bool elect_one()
 {
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
 }
 
-__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
+__device__ __forceinline__ void fetch_l2(const CUtensorMap *map, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// Columns of this thread's lane.  A load and its wait are one statement: nothing the
+// compiler does with the registers, a move or a spill, comes between them.
+__device__ __forceinline__ void ld_cols(uint32_t taddr, float (&v)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31},\n\t[%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void ld_cols(uint32_t taddr, float (&v)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void ld_cols(uint32_t ta, uint32_t tb, float (&v)[16], float (&w)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]), "=f"(w[6]), "=f"(w[7]),
+          "=f"(w[8]), "=f"(w[9]), "=f"(w[10]), "=f"(w[11]), "=f"(w[12]), "=f"(w[13]), "=f"(w[14]), "=f"(w[15])
+        : "r"(ta), "r"(tb));
+}
+
+__device__ __forceinline__ uint32_t ld_col(uint32_t taddr)
 {
     uint32_t v;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(v) : "r"(taddr));
     return v;
 }
 
@@ -127,31 +169,52 @@ __device__ __forceinline__ bool is_odd(f32x2 sign)
 }
 
 // Second parts where the first is infinite or NaN: zero.
-template <int N> __device__ __forceinline__ void mend(const uint32_t (&hi)[N], uint32_t (&lo)[N])
+__device__ __forceinline__ uint32_t mend(uint32_t hi, uint32_t lo)
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if ((hi[i] & 0x7f80u) == 0x7f80u) lo[i] &= 0xffff0000u;
-        if ((hi[i] & 0x7f800000u) == 0x7f800000u) lo[i] &= 0xffffu;
+    if ((hi & 0x7f80u) == 0x7f80u) lo &= 0xffff0000u;
+    if ((hi & 0x7f800000u) == 0x7f800000u) lo &= 0xffffu;
+    return lo;
+}
+
+__device__ __noinline__ void mend_row(uint8_t *tiles, int r)
+{
+#pragma unroll 1
+    for (int w = 0; w < 32; ++w) {
+        const uint32_t at = sw128(r, w / 4) + w % 4 * 4;
+        uint32_t *lo = reinterpret_cast<uint32_t *>(tiles + kTile + at);
+        *lo = mend(*reinterpret_cast<const uint32_t *>(tiles + at), *lo);
     }
 }
 
+__device__ __noinline__ void zero_row(uint8_t *tiles, int r)
+{
+#pragma unroll 1
+    for (int c = 0; c < 16; ++c)
+        *reinterpret_cast<uint4 *>(tiles + (c >> 3) * kTile + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
+}
+
 // 8 values into 16-byte column c of row r of two tiles.
-__device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4])
+__device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4], f32x2 &sign)
 {
     uint32_t hi[4], lo[4];
-    f32x2 sign = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) split(x[i], hi[i], lo[i], sign);
-    if (is_odd(sign)) mend(hi, lo);
     const uint32_t at = sw128(r, c);
     *reinterpret_cast<uint4 *>(tiles + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4 *>(tiles + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
+// The parts of P of a row and 32 tokens, buffer p.
+__device__ __forceinline__ void st_p(uint32_t p, int quad, int J, const uint32_t (&hi)[16], const uint32_t (&lo)[16])
+{
+    tmem_st16(lane_addr(p, quad, 32 * J), hi);
+    tmem_st16(lane_addr(p, quad, 32 * J + 16), lo);
+}
+
 // P of one row in the cases that the plain path leaves: tokens that forget, blocks
-// that decay by more than 2^120, and products that are infinite or NaN.
-__device__ __noinline__ void odd_decays(uint32_t tbase, int quad, int lane, const float *in, const float *total,
+// that decay by more than 2^120, and products that are infinite or NaN.  Blocks
+// from `last` down.
+__device__ __noinline__ void odd_decays(uint32_t p, int quad, int lane, int last, const float *in, const float *total,
                                         const unsigned *mask)
 {
     const float mine = in[32 * quad + lane];
@@ -160,9 +223,15 @@ __device__ __noinline__ void odd_decays(uint32_t tbase, int quad, int lane, cons
     const int first = first_seen(mask[quad], lane);
 #pragma unroll 1
     for (int J = quad; J >= 0; --J) {
+        if (J > last) {  // done
+            if (J < quad) {
+                sum += total[J];
+                cut = cut || mask[J];
+            }
+            continue;
+        }
         float x[32];
-        tmem_ld32(lane_addr(tbase, quad, kColQK + 32 * J), x);
-        landed(x);
+        ld_cols(lane_addr(p, quad, 32 * J), x);
         uint32_t hi[16], lo[16];
         f32x2 sign = 0;
 #pragma unroll
@@ -173,11 +242,12 @@ __device__ __noinline__ void odd_decays(uint32_t tbase, int quad, int lane, cons
             x[j] = seen && f != 0.f ? x[j] * f : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) split(pack2(x[2 * j], x[2 * j + 1]), hi[j], lo[j], sign);
-        mend(hi, lo);
+        for (int j = 0; j < 16; ++j) {
+            split(pack2(x[2 * j], x[2 * j + 1]), hi[j], lo[j], sign);
+            lo[j] = mend(hi[j], lo[j]);
+        }
         __syncwarp();
-        tmem_st16(lane_addr(tbase, quad, kColP + 16 * J), hi);
-        tmem_st16(lane_addr(tbase, quad, kColP + 64 + 16 * J), lo);
+        st_p(p, quad, J, hi, lo);
         if (J < quad) {
             sum += total[J];
             cut = cut || mask[J];
@@ -186,21 +256,23 @@ __device__ __noinline__ void odd_decays(uint32_t tbase, int quad, int lane, cons
 }
 
 // P V of one row and 32 columns for a chunk whose V is infinite or NaN somewhere: a
-// token must see nothing of those behind it, and zero times infinity is NaN.
-__device__ __noinline__ void odd_row(uint32_t tbase, int quad, int i, int first, const uint8_t *V, int half, float (&acc)[32])
+// token must see nothing of those behind it, and zero times infinity is NaN.  To the
+// columns at o, in place of what the product left there.
+__device__ __noinline__ void odd_row(uint32_t p, uint32_t o, int quad, int i, int first, const uint8_t *V)
 {
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+    float acc[32];
 #pragma unroll
     for (int d = 0; d < 32; ++d) acc[d] = 0.f;
 #pragma unroll 1
     for (int w = 0; w < 16 * (quad + 1); ++w) {
         __syncwarp();
-        uint32_t hi = tmem_ld1(lane_addr(tbase, quad, kColP + w)), lo = tmem_ld1(lane_addr(tbase, quad, kColP + 64 + w));
-        tmem_ld_wait();
-        asm volatile("" : "+r"(hi), "+r"(lo));
+        const uint32_t hi = ld_col(lane_addr(p, quad, w / 16 * 32 + w % 16)), lo = ld_col(lane_addr(p, quad, w / 16 * 32 + 16 + w % 16));
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
             const int j = 2 * w + e;
-            const float p = e ? __uint_as_float(hi & 0xffff0000u) + __uint_as_float(lo & 0xffff0000u)
+            const float f = e ? __uint_as_float(hi & 0xffff0000u) + __uint_as_float(lo & 0xffff0000u)
                               : __uint_as_float(hi << 16) + __uint_as_float(lo << 16);
             if (j > i || j < first) continue;
 #pragma unroll
@@ -208,14 +280,25 @@ __device__ __noinline__ void odd_row(uint32_t tbase, int quad, int i, int first,
                 float v[8];
                 widen(*reinterpret_cast<const uint4 *>(V + sw128(j, half * 4 + q)), v);
 #pragma unroll
-                for (int d = 0; d < 8; ++d) acc[q * 8 + d] = fmaf(p, v[d], acc[q * 8 + d]);
+                for (int d = 0; d < 8; ++d) acc[q * 8 + d] = fmaf(f, v[d], acc[q * 8 + d]);
             }
         }
     }
+    __syncwarp();
+    tmem_st32(lane_addr(o, quad, 32 * half), acc);
+    tmem_st_wait();
+    }
 }
 
+// Descriptor steps of 16 along K, K-major (64 to a row) and MN-major (rows).
+__device__ __forceinline__ constexpr uint32_t k_step(int k) { return ((k >> 2) * kTile + (k & 3) * 32) >> 4; }
+__device__ __forceinline__ constexpr uint32_t mn_step(int k) { return k * 2048 >> 4; }
+
+// kStates: what pieces add to the state, without outputs.  KS: steps of 16 over d_k
+// (up to there tiles are filled up with zeros).
+template <bool kStates, int KS>
 __global__ void __launch_bounds__(kThreads, 1)
-gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const __grid_constant__ CUtensorMap tm_q,
+gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v)
 {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -224,26 +307,27 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
     const int64_t unit = blockIdx.x;
     const int v0 = (int)(unit % tiles) * kDVT, h = (int)(unit / tiles % a.heads);
     Unit u;
-    if (!find_unit(a, unit / tiles / a.heads, h, states_only, u)) return;
+    if (!find_unit(a, unit / tiles / a.heads, h, kStates, u)) return;
     const int chunks = (int)(((int64_t)u.len + kC - 1) / kC), dk = a.dk;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.kq_free[i], 1);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.kq_free[i], kStates ? 1 : 2);
             mbar_init(&s.v_free[i], 1);
             mbar_init(&s.dec_ready[i], 128);
-            mbar_init(&s.dec_free[i], states_only ? 128 : 384);
+            mbar_init(&s.dec_free[i], kStates ? 128 : 384);
             mbar_init(&s.w_ready[i], 128);
+            mbar_init(&s.o_free[i], 128);
+            mbar_init(&s.qk_full[i], 1);
+            mbar_init(&s.p_ready[i], 128);
         }
-        mbar_init(&s.qk_full, 1);
-        mbar_init(&s.p_ready, 128);
         mbar_init(&s.p_free, 1);
         mbar_init(&s.u_full, 1);
         mbar_init(&s.u_free, 128);
         mbar_init(&s.s_ready, 128);
         mbar_init(&s.o_full, 1);
-        mbar_init(&s.o_free, 128);
         s.abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tm_q);
@@ -262,121 +346,129 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
     const Waiter wait = {abort_flag, a.status};
 
     if (warp < 4) {
-        // ---- P
-        if (!states_only && chunks > 0) {
-            const uint32_t zero[16] = {};
-            for (int J = quad + 1; J < 4; ++J) {  // blocks above the diagonal stay zero
-                tmem_st16(lane_addr(tbase, quad, kColP + 16 * J), zero);
-                tmem_st16(lane_addr(tbase, quad, kColP + 64 + 16 * J), zero);
-            }
-            tmem_st_wait();
-        }
-        for (int c = 0; c < chunks && !states_only; ++c) {
-            const int st = c & 1;
-            wait(&s.dec_ready[st], c >> 1);
-            // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where J, the block
-            // of j, decays by less than 2^120; within a block without the middle factor.
-            const float in = s.in[st][t];
-            bool plain = true;
-            for (int J = 0; J <= quad; ++J) plain = plain && s.mask[st][J] == 0 && fabsf(s.total[st][J]) < kPlain;
-            wait(&s.qk_full, c);
-            if (c > 0) wait(&s.p_free, c - 1);
-            __syncwarp();
-            tc_fence_after();
-            float sum = in;
-            bool odd = false;
+        // ---- P, in the place of Q K^T
+        if constexpr (!kStates) {
 #pragma unroll 1
-            for (int J = quad; J >= 0 && plain; --J) {
-                float x[32];
-                tmem_ld32(lane_addr(tbase, quad, kColQK + 32 * J), x);
-                if (J < quad) sum += s.total[st][J];
-                const f32x2 f = dup2(decay_of(sum));
-                const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J]);
-                landed(x);
-                if (J == quad) {
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c & 1;
+                const uint32_t p = tbase + kColP + 128 * st;
+                wait(&s.dec_ready[st], c >> 1);
+                // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where J, the
+                // block of j, decays by less than 2^120; within a block without the middle factor.
+                float sum = s.in[st][t];
+                bool odd = false;
+#pragma unroll 1
+                for (int J = 0; J <= quad; ++J) odd |= s.mask[st][J] || !(fabsf(s.total[st][J]) < kPlain);
+                wait(&s.qk_full[st], c >> 1);
+                __syncwarp();
+                tc_fence_after();
+                int J = quad;
+#pragma unroll 1
+                for (; J >= 0 && !odd; --J) {
+                    float x[32];
+                    if (J < quad) sum += s.total[st][J];
+                    const f32x2 f = dup2(decay_of(sum));
+                    const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J]);
+                    ld_cols(lane_addr(p, quad, 32 * J), x);
+                    if (J == quad) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
-                }
-                uint32_t hi[16], lo[16];
-                f32x2 sign = 0;
+                        for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
+                    }
+                    uint32_t hi[16], lo[16];
+                    f32x2 sign = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 w = inverse[j];
-                    split(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), hi[2 * j], lo[2 * j], sign);
-                    split(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), hi[2 * j + 1],
-                          lo[2 * j + 1], sign);
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 w = inverse[j];
+                        split(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), hi[2 * j], lo[2 * j], sign);
+                        split(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), hi[2 * j + 1],
+                              lo[2 * j + 1], sign);
+                    }
+                    odd = __any_sync(0xffffffffu, is_odd(sign));
+                    if (odd) break;  // this block's products are still in place
+                    st_p(p, quad, J, hi, lo);
                 }
-                odd |= is_odd(sign);
-                tmem_st16(lane_addr(tbase, quad, kColP + 16 * J), hi);
-                tmem_st16(lane_addr(tbase, quad, kColP + 64 + 16 * J), lo);
+                if (odd) odd_decays(p, quad, lane, J, s.in[st], s.total[st], s.mask[st]);
+                const uint32_t zero[16] = {};
+#pragma unroll 1
+                for (int J = quad + 1; J < 4; ++J) st_p(p, quad, J, zero, zero);
+                mbar_arrive(&s.dec_free[st]);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&s.p_ready[st]);
             }
-            if (__any_sync(0xffffffffu, odd || !plain)) odd_decays(tbase, quad, lane, s.in[st], s.total[st], s.mask[st]);
-            mbar_arrive(&s.dec_free[st]);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&s.p_ready);
         }
     } else if (warp < 8) {
         // ---- the state: row t of S^T
         f32x2 S[kDVT / 2];
-        const int64_t at = (int64_t)v0 * dk + t;
         const int nv = min(kDVT, a.dv - v0);
+        const bool mine = 32 * quad < dk;  // the others' rows are not part of S: K^T has nothing there
+        {
+            const float *p = u.in + (int64_t)v0 * dk + t;
+            const int cols = u.in && t < dk ? nv : 0;
 #pragma unroll
-        for (int d = 0; d < kDVT; d += 2) {
-            const bool is = u.in && t < dk;
-            S[d / 2] = pack2(is && d < nv ? u.in[at + (int64_t)d * dk] : 0.f,
-                             is && d + 1 < nv ? u.in[at + (int64_t)(d + 1) * dk] : 0.f);
-        }
-        auto hand_over = [&] {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
-                st_parts(sm + kOffS, t, q, x);
+            for (int d = 0; d < kDVT; d += 2) {
+                const float x = d < cols ? *p : 0.f;
+                p += dk;
+                S[d / 2] = pack2(x, d + 1 < cols ? *p : 0.f);
+                p += dk;
             }
-            fence_async_smem();
-            mbar_arrive(&s.s_ready);
-        };
-        if (chunks > 0 && !states_only) hand_over();
-        for (int c = 0; c < chunks; ++c) {
+        }
+#pragma unroll 1
+        for (int c = -1; c < chunks; ++c) {
             const int st = c & 1;
-            wait(&s.dec_ready[st], c >> 1);
-            const float4 total = *reinterpret_cast<const float4 *>(s.total[st]);
-            const uint4 mask = *reinterpret_cast<const uint4 *>(s.mask[st]);
-            const float all = mask.x | mask.y | mask.z | mask.w ? 0.f : decay_of(total.x + total.y + total.z + total.w);
-            mbar_arrive(&s.dec_free[st]);
-            if (all == 0.f)
+            if (c >= 0) {
+                wait(&s.dec_ready[st], c >> 1);
+                const float4 total = *reinterpret_cast<const float4 *>(s.total[st]);
+                const uint4 mask = *reinterpret_cast<const uint4 *>(s.mask[st]);
+                const float all = mask.x | mask.y | mask.z | mask.w ? 0.f : decay_of(total.x + total.y + total.z + total.w);
+                mbar_arrive(&s.dec_free[st]);
+                if (all == 0.f)
 #pragma unroll
-                for (int d = 0; d < kDVT / 2; ++d) S[d] = 0;  // forgotten, infinite or not
-            wait(&s.u_full, c);
-            __syncwarp();
-            tc_fence_after();
+                    for (int d = 0; d < kDVT / 2; ++d) S[d] = 0;  // forgotten, infinite or not
+                wait(&s.u_full, c);
+                __syncwarp();
+                tc_fence_after();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[32];
-                tmem_ld32(lane_addr(tbase, quad, kColU + 32 * half), x);
-                landed(x);
+                for (int q = 0; q < 4 && mine; ++q) {
+                    float x[16];
+                    ld_cols(lane_addr(tbase, quad, kColU + 16 * q), x);
 #pragma unroll
-                for (int d = 0; d < 16; ++d) S[16 * half + d] = fma2(dup2(all), S[16 * half + d], pack2(x[2 * d], x[2 * d + 1]));
+                    for (int d = 0; d < 8; ++d) S[8 * q + d] = fma2(dup2(all), S[8 * q + d], pack2(x[2 * d], x[2 * d + 1]));
+                }
+                tc_fence_before();
+                mbar_arrive(&s.u_free);
             }
-            tc_fence_before();
-            mbar_arrive(&s.u_free);
-            if (c + 1 < chunks && !states_only) {
-                wait(&s.kq_free[st], c >> 1);  // Q S^T of this chunk has read the parts
-                hand_over();
+            if (!kStates && c + 1 < chunks) {
+                if (c >= 0) wait(&s.kq_free[st], c >> 1);  // Q S^T of this chunk has read the parts
+                f32x2 sign = 0;
+#pragma unroll
+                for (int q = 0; q < 8 && (mine || c < 0); ++q) {
+                    const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
+                    st_parts(sm + kOffS, t, q, x, sign);
+                }
+                if (is_odd(sign)) mend_row(sm + kOffS, t);
+                fence_async_smem();
+                mbar_arrive(&s.s_ready);
             }
         }
-        if (u.out && !*abort_flag)
+        if (u.out && !*abort_flag) {
+            float *p = u.out + (int64_t)v0 * dk + t;
+            const int cols = t < dk ? nv : 0;
 #pragma unroll
             for (int d = 0; d < kDVT; d += 2) {
                 float x, y;
                 unpack2(S[d / 2], x, y);
-                if (t < dk && d < nv) u.out[at + (int64_t)d * dk] = x;
-                if (t < dk && d + 1 < nv) u.out[at + (int64_t)(d + 1) * dk] = y;
+                if (d < cols) *p = x;
+                p += dk;
+                if (d + 1 < cols) *p = y;
+                p += dk;
             }
+        }
     } else if (warp < 12) {
         // ---- decays, and V times the decay to the chunk's end
         const float *decay = a.log_decay + (u.row + t) * a.ld_decay + h;
         float next = t < u.len ? *decay : 0.f;
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1, n = min(kC, u.len - c * kC);
             Decays d;
@@ -394,40 +486,46 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
             named_sync(1, 128);
             bool cut = d.cut_behind(lane);
             float sum = d.after;
-#pragma unroll
-            for (int J = 1; J < 4; ++J)
-                if (J > quad) {
-                    cut = cut || s.mask[st][J];
-                    sum += s.total[st][J];
-                }
+#pragma unroll 1
+            for (int J = quad + 1; J < 4; ++J) {
+                cut = cut || s.mask[st][J];
+                sum += s.total[st][J];
+            }
             const float w = cut ? 0.f : decay_of(sum);
-            wait(&s.full[st], c >> 1);
+            wait(&s.v_full[st], c >> 1);
+            if (n < kC) wait(&s.full[st], c >> 1);  // K's rows past the end, below
             if (c > 0) wait(&s.u_full, c - 1);  // the product has read the last chunk's
             uint8_t *V = sm + kOffV + st * kTile, *W = sm + kOffW;
             if (t < n) {
-                f32x2 sign = 0;
-#pragma unroll 2
-                for (int q = 0; q < 8; ++q) {
-                    float f[8];
-                    widen(*reinterpret_cast<const uint4 *>(V + sw128(t, q)), f);
-                    f32x2 x[4];
+                f32x2 sign = 0, raw = 0;
+#pragma unroll 1
+                for (int q = 0; q < 8; q += 2)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = pack2(f[2 * e], f[2 * e + 1]);
-                        sign = fma2(x[e], dup2(0.f), sign);
-                        x[e] = w == 0.f ? 0 : mul2(x[e], dup2(w));
+                    for (int r = 0; r < 2; ++r) {
+                        float f[8];
+                        widen(*reinterpret_cast<const uint4 *>(V + sw128(t, q + r)), f);
+                        f32x2 x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = pack2(f[2 * e], f[2 * e + 1]);
+                            raw = fma2(x[e], dup2(0.f), raw);
+                            x[e] = mul2(x[e], dup2(w));
+                        }
+                        st_parts(W, t, q + r, x, sign);
                     }
-                    st_parts(W, t, q, x);
+                if (is_odd(raw)) s.odd[st] = 1;
+                if (is_odd(sign)) {
+                    mend_row(W, t);
+                    if (w == 0.f) zero_row(W, t);  // what comes after has forgotten it
                 }
-                if (is_odd(sign)) s.odd[st] = 1;
             } else {  // rows past the end may be another sequence's
-                const uint4 zero = make_uint4(0, 0, 0, 0);
+                zero_row(W, t);
                 uint8_t *K = sm + kOffK + st * 2 * kTile;
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
                 for (int q = 0; q < 8; ++q) {
                     const uint32_t off = sw128(t, q);
                     *reinterpret_cast<uint4 *>(V + off) = zero;
-                    *reinterpret_cast<uint4 *>(W + off) = zero;
-                    *reinterpret_cast<uint4 *>(W + kTile + off) = zero;
                     *reinterpret_cast<uint4 *>(K + off) = zero;
                     if (dk > 64) *reinterpret_cast<uint4 *>(K + kTile + off) = zero;
                 }
@@ -437,168 +535,173 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, int states_only, const 
         }
     } else if (warp < 16) {
         // ---- outputs: row t
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (u.row + t) * a.ld_o + (int64_t)h * a.dv + v0;
-        const int nv = min(kDVT, a.dv - v0);
-        for (int c = 0; c < chunks && !states_only; ++c, o += kC * a.ld_o) {
-            const int st = c & 1, n = min(kC, u.len - c * kC);
-            wait(&s.dec_ready[st], c >> 1);
-            const unsigned mask = s.mask[st][quad];
-            float sum = s.in[st][t];
-            bool cut = mask & (0xffffffffu >> (31 - lane));
-            int first = 32 * quad + first_seen(mask, lane);
-#pragma unroll
-            for (int J = 2; J >= 0; --J)
-                if (J < quad) {
-                    if (!cut) first = 32 * J + (s.mask[st][J] ? 31 - __clz(s.mask[st][J]) : 0);
+        if constexpr (!kStates) {
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (u.row + t) * a.ld_o + (int64_t)h * a.dv + v0;
+            const int nv = min(kDVT, a.dv - v0);
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c, o += kC * a.ld_o) {
+                const int st = c & 1, n = min(kC, u.len - c * kC);
+                wait(&s.dec_ready[st], c >> 1);
+                const unsigned mask = s.mask[st][quad];
+                float sum = s.in[st][t];
+                bool cut = mask & (0xffffffffu >> (31 - lane));
+                int first = 32 * quad + first_seen(mask, lane);  // the first token this one sees
+#pragma unroll 1
+                for (int J = quad - 1; J >= 0; --J) {
+                    if (!cut) first = 32 * J + first_seen(s.mask[st][J], 31);
                     cut = cut || s.mask[st][J];
                     sum += s.total[st][J];
                 }
-            const float start = cut ? 0.f : a.scale * decay_of(sum);
-            wait(&s.w_ready[st], c >> 1);
-            const bool odd = s.odd[st];
-            mbar_arrive(&s.dec_free[st]);
-            wait(&s.o_full, c);
-            tc_fence_after();
-            if (!odd && t == 0) {
-                mbar_arrive(&s.v_free[st]);
-                mbar_arrive(&s.p_free);
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[32], y[32];
-                __syncwarp();
-                tmem_ld32(lane_addr(tbase, quad, kColI + 64 * st + 32 * half), x);
-                if (odd)
-                    odd_row(tbase, quad, t, first, sm + kOffV + st * kTile, half, y);
-                else
-                    tmem_ld32(lane_addr(tbase, quad, kColO + 32 * half), y);
-                landed(x);
-                landed(y);
-                if (half == 1) {
-                    tc_fence_before();
-                    mbar_arrive(&s.o_free);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t f[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = 8 * q + 2 * e;
-                        const f32x2 w = mul2(pack2(y[i], y[i + 1]), dup2(a.scale));
-                        float lo, hi;
-                        unpack2(start == 0.f ? w : fma2(pack2(x[i], x[i + 1]), dup2(start), w), lo, hi);
-                        f[e] = narrow_pair(lo, hi);
-                    }
-                    if (t < n && 32 * half + 8 * q < nv) 
-                        *reinterpret_cast<uint4 *>(o + 32 * half + 8 * q) = make_uint4(f[0], f[1], f[2], f[3]);
-                }
-            }
-            if (odd) {
-                named_sync(2, 128);
-                if (t == 0) {
+                const f32x2 start = dup2(a.scale * decay_of(sum)), scale = dup2(a.scale);
+                wait(&s.w_ready[st], c >> 1);
+                const bool odd = s.odd[st];
+                mbar_arrive(&s.dec_free[st]);
+                wait(&s.kq_free[st], c >> 1);
+                wait(&s.o_full, c);
+                tc_fence_after();
+                if (!odd && t == 0) {
                     mbar_arrive(&s.v_free[st]);
                     mbar_arrive(&s.p_free);
+                }
+                const int cols = t < n ? nv : 0;
+                if (odd) odd_row(tbase + kColP + 128 * st, tbase + kColO, quad, t, first, sm + kOffV + st * kTile);
+#pragma unroll 1
+                for (int q = 0; q < kDVT; q += 16) {
+                    float x[16], y[16];
+                    __syncwarp();
+                    ld_cols(lane_addr(tbase, quad, kColI + 64 * st + q), lane_addr(tbase, quad, kColO + q), x, y);
+                    uint32_t f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const f32x2 w = mul2(pack2(y[2 * e], y[2 * e + 1]), scale);
+                        float lo, hi;
+                        unpack2(cut ? w : fma2(pack2(x[2 * e], x[2 * e + 1]), start, w), lo, hi);
+                        f[e] = narrow_pair(lo, hi);
+                    }
+                    if (q < cols) *reinterpret_cast<uint4 *>(o + q) = make_uint4(f[0], f[1], f[2], f[3]);
+                    if (q + 8 < cols) *reinterpret_cast<uint4 *>(o + q + 8) = make_uint4(f[4], f[5], f[6], f[7]);
+                }
+                tc_fence_before();
+                mbar_arrive(&s.o_free[st]);
+                if (odd) {
+                    named_sync(2, 128);
+                    if (t == 0) {
+                        mbar_arrive(&s.v_free[st]);
+                        mbar_arrive(&s.p_free);
+                    }
                 }
             }
         }
     } else if (warp == 16) {
-        // ---- products
-        if (lane == 0 && chunks > 0) {
+        // ---- Q K^T and P V, the former two chunks ahead: it takes the place of the latter's P
+        if (!kStates && elect_one()) {
             const uint32_t base = smem_u32(sm);
-            const int steps = (dk + 15) / 16;  // of d_k
-            const uint32_t id_qk = idesc_bf16_f32(128, 128, 0, 0), id_s = idesc_bf16_f32(128, 64, 0, 1),
-                           id_u = idesc_bf16_f32(128, 64, 1, 1);
-            auto k_step = [](int k) { return (uint32_t)(((k >> 2) * kTile + (k & 3) * 32) >> 4); };
-            auto mn_step = [](int k) { return (uint32_t)(k * 2048 >> 4); };
-            auto qk = [&](int st) {
-                const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
-                const uint64_t k = sdesc_sw128(base + kOffK + st * 2 * kTile, 16, 1024);
-                for (int i = 0; i < steps; ++i) mma_f16kind(tbase + kColQK, q + k_step(i), k + k_step(i), id_qk, i > 0);
-                mma_commit(&s.qk_full);
-            };
-            auto add = [&](int st) {
-                const uint64_t k = sdesc_sw128(base + kOffK + st * 2 * kTile, kTile, 1024);
-                for (int part = 0; part < 2; ++part) {
-                    const uint64_t w = sdesc_sw128(base + kOffW + part * kTile, kTile, 1024);
-                    for (int i = 0; i < 8; ++i)
-                        mma_f16kind(tbase + kColU, k + mn_step(i), w + mn_step(i), id_u, part + i > 0);
-                }
-                mma_commit(&s.u_full);
-            };
-            auto inter = [&](int st) {
-                const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
-                for (int part = 0; part < 2; ++part) {
-                    const uint64_t S = sdesc_sw128(base + kOffS + part * kTile, kTile, 1024);
-                    for (int i = 0; i < steps; ++i)
-                        mma_f16kind(tbase + kColI + 64 * st, q + k_step(i), S + mn_step(i), id_s, part + i > 0);
-                }
-                mma_commit(&s.kq_free[st]);
-            };
-            auto intra = [&](int st) {
-                const uint64_t v = sdesc_sw128(base + kOffV + st * kTile, kTile, 1024);
-                for (int part = 0; part < 2; ++part)
-                    for (int i = 0; i < 8; ++i)
-                        mma_f16kind_ts(tbase + kColO, tbase + kColP + 64 * part + 8 * i, v + mn_step(i), id_s, part + i > 0);
-                mma_commit(&s.o_full);
-            };
-            if (states_only) {
-                for (int c = 0; c < chunks; ++c) {
-                    const int st = c & 1;
-                    wait(&s.full[st], c >> 1);
-                    wait(&s.w_ready[st], c >> 1);
-                    if (c > 0) wait(&s.u_free, c - 1);
+#pragma unroll 1
+            for (int c = -2; c < chunks; ++c) {
+                const int st = c & 1;
+                const uint32_t p = tbase + kColP + 128 * st;
+                if (c >= 0) {
+                    wait(&s.p_ready[st], c >> 1);
+                    wait(&s.w_ready[st], c >> 1);  // rows of V past the end are zero
+                    if (c > 0) wait(&s.o_free[st ^ 1], (c - 1) >> 1);
                     tc_fence_after();
-                    add(st);
+                    const uint64_t v = sdesc_sw128(base + kOffV + st * kTile, kTile, 1024);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mma_f16kind_ts(tbase + kColO, p + 32 * (i >> 1) + 16 * part + 8 * (i & 1), v + mn_step(i),
+                                           idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
+                    mma_commit(&s.o_full);
+                }
+                if (c + 2 < chunks) {
+                    wait(&s.full[st], (c + 2) >> 1);
+                    if (c >= 0) wait(&s.p_free, c);
+                    tc_fence_after();
+                    const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
+                    const uint64_t k = sdesc_sw128(base + kOffK + st * 2 * kTile, 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                            mma_f16kind(p, q + k_step(i), k + k_step(i), idesc_bf16_f32(128, 128, 0, 0), i > 0);
+                    mma_commit(&s.qk_full[st]);
                     mma_commit(&s.kq_free[st]);
-                    mma_commit(&s.v_free[st]);
-                }
-            } else {
-                auto ahead = [&](int c) {  // what chunk c needs beside P
-                    const int st = c & 1;
-                    wait(&s.w_ready[st], c >> 1);
-                    if (c > 0) wait(&s.u_free, c - 1);
-                    tc_fence_after();
-                    add(st);
-                    wait(&s.s_ready, c);
-                    tc_fence_after();
-                    inter(st);
-                };
-                wait(&s.full[0], 0);
-                tc_fence_after();
-                qk(0);
-                ahead(0);
-                for (int c = 0; c < chunks; ++c) {
-                    const int st = c & 1;
-                    wait(&s.p_ready, c);
-                    if (c + 1 < chunks) {
-                        wait(&s.full[st ^ 1], (c + 1) >> 1);
-                        tc_fence_after();
-                        qk(st ^ 1);
-                    }
-                    if (c > 0) wait(&s.o_free, c - 1);
-                    tc_fence_after();
-                    intra(st);
-                    if (c + 1 < chunks) ahead(c + 1);
                 }
             }
         }
-    } else if (warp == 17 && lane == 0) {
-        // ---- tensor copies
-        const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
-        const uint32_t bytes = (uint32_t)(halves * (states_only ? 1 : 2) + 1) * kTile;
-        for (int c = 0; c < chunks; ++c) {
+    } else if (warp == 17) {
+        // ---- K^T V, decayed, and Q S^T
+        if (elect_one()) {
+            const uint32_t base = smem_u32(sm);
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c & 1;
+                wait(&s.full[st], c >> 1);
+                wait(&s.w_ready[st], c >> 1);
+                if (c > 0) wait(&s.u_free, c - 1);
+                tc_fence_after();
+                const uint64_t k = sdesc_sw128(base + kOffK + st * 2 * kTile, kTile, 1024);
+                const uint64_t w = sdesc_sw128(base + kOffW, kTile, 1024);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mma_f16kind(tbase + kColU, k + mn_step(i), w + part * (kTile >> 4) + mn_step(i),
+                                    idesc_bf16_f32(128, 64, 1, 1), part + i > 0);
+                mma_commit(&s.u_full);
+                if constexpr (kStates) {
+                    mma_commit(&s.kq_free[st]);
+                    mma_commit(&s.v_free[st]);
+                } else {
+                    wait(&s.s_ready, c);
+                    if (c > 1) wait(&s.o_free[st], (c - 2) >> 1);
+                    tc_fence_after();
+                    const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
+                    const uint64_t S = sdesc_sw128(base + kOffS, kTile, 1024);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+                                mma_f16kind(tbase + kColI + 64 * st, q + k_step(i), S + part * (kTile >> 4) + mn_step(i),
+                                            idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
+                    mma_commit(&s.kq_free[st]);
+                }
+            }
+        }
+    } else if (warp == 18) {
+        // ---- tensor copies of K and Q; those of chunks ahead of the ring go to L2
+        if (elect_one()) {
+            const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
+#pragma unroll 1
+            for (int c = -kAhead; c < chunks; ++c) {
+                const int st = c & 1, row = (int)(u.row + (int64_t)c * kC);
+                if (c + kAhead < chunks)
+#pragma unroll 1
+                    for (int i = 0; i < halves; ++i) {
+                        fetch_l2(&tm_k, 64 * i, g, row + kAhead * kC);
+                        if (!kStates) fetch_l2(&tm_q, 64 * i, g, row + kAhead * kC);
+                    }
+                if (c < 0) continue;
+                if (c > 1) wait(&s.kq_free[st], (c - 2) >> 1);
+                if (*abort_flag) break;
+                mbar_arrive_expect_tx(&s.full[st], (uint32_t)(halves * (kStates ? 1 : 2)) * kTile);
+#pragma unroll 1
+                for (int i = 0; i < halves; ++i) {
+                    tma_load_3d(sm + kOffK + (st * 2 + i) * kTile, &tm_k, &s.full[st], 64 * i, g, row);
+                    if (!kStates) tma_load_3d(sm + kOffQ + (st * 2 + i) * kTile, &tm_q, &s.full[st], 64 * i, g, row);
+                }
+            }
+        }
+    } else if (elect_one()) {
+        // ---- and of V
+#pragma unroll 1
+        for (int c = -kAhead; c < chunks; ++c) {
             const int st = c & 1, row = (int)(u.row + (int64_t)c * kC);
-            if (c > 1) {
-                wait(&s.kq_free[st], (c - 2) >> 1);
-                wait(&s.v_free[st], (c - 2) >> 1);
-            }
+            if (c + kAhead < chunks) fetch_l2(&tm_v, v0, h, row + kAhead * kC);
+            if (c < 0) continue;
+            if (c > 1) wait(&s.v_free[st], (c - 2) >> 1);
             if (*abort_flag) break;
-            mbar_arrive_expect_tx(&s.full[st], bytes);
-            for (int i = 0; i < halves; ++i) {
-                tma_load_3d(sm + kOffK + (st * 2 + i) * kTile, &tm_k, &s.full[st], 64 * i, g, row);
-                if (!states_only) tma_load_3d(sm + kOffQ + (st * 2 + i) * kTile, &tm_q, &s.full[st], 64 * i, g, row);
-            }
-            tma_load_3d(sm + kOffV + st * kTile, &tm_v, &s.full[st], v0, h, row);
+            mbar_arrive_expect_tx(&s.v_full[st], kTile);
+            tma_load_3d(sm + kOffV + st * kTile, &tm_v, &s.v_full[st], v0, h, row);
         }
     }
     __syncwarp();
@@ -657,8 +760,12 @@ cudaError_t gdn_linattn_tc(const GdnLinattnArgs &a, bool states_only, cudaStream
     if (!make_map(&q, a.q, rows, a.groups, a.dk, a.ld_q) || !make_map(&k, a.k, rows, a.groups, a.dk, a.ld_k) ||
         !make_map(&v, a.v, rows, a.heads, a.dv, a.ld_v))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(gdn_linattn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    auto *kernel = states_only  ? gdn_linattn_tc_kernel<true, 8>
+                   : a.dk <= 64 ? gdn_linattn_tc_kernel<false, 4>
+                   : a.dk <= 96 ? gdn_linattn_tc_kernel<false, 6>
+                                : gdn_linattn_tc_kernel<false, 8>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    gdn_linattn_tc_kernel<<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(a, tiles, states_only, q, k, v);
+    kernel<<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(a, tiles, q, k, v);
     return cudaGetLastError();
 }
