@@ -5,8 +5,8 @@
 // chunks of 128 tokens.  With b the sum of log decays up to and with a token of
 // the chunk, and S^T (d_k x 64) the state before it:
 //
-//   P   = Lower(Q K^T e^{b_i - b_j})                  [128 x 128]
-//   O   = scale (e^{b_i} Q S^T + P V)                 [128 x 64]
+//   P   = scale Lower(Q K^T e^{b_i - b_j})            [128 x 128]
+//   O   = scale e^{b_i} Q S^T + P V                   [128 x 64]
 //   U   = K^T (V e^{b_n - b_j})                       [d_k x 64]
 //   S^T <- e^{b_n} S^T + U
 //
@@ -17,11 +17,12 @@
 // the decayed V, enters as two bf16 parts whose sum keeps 16 bits and more, so that
 // the final states are right to 2e-6 and the outputs but for their own rounding.
 //
-// Roles: warps 0-3 form P (tensor memory to tensor memory, a row per thread),
-// warps 4-7 keep the state and write its parts for the next chunk, warps 8-11 sum
-// the decays and form the decayed V, warps 12-15 write the outputs, warps 16 and 17
-// issue the products with P and those with the state, warps 18 and 19 the tensor
-// copies into rings of two stages, with later chunks fetched to L2 ahead.  All loops over chunks are kept small: together they have to
+// Roles: warps 0-7 form P (tensor memory to tensor memory; a row per thread, every
+// other block of 32 columns), warps 8-15 keep the state, 32 columns each, and write
+// its parts for the next chunk, warps 16-19 sum the decays and form the decayed V,
+// warps 20-23 write the outputs, warps 24 and 25 issue the products with P and those
+// with the state, warps 26 and 27 the tensor copies into rings of two stages, with
+// later chunks fetched to L2 ahead.  All loops over chunks are kept small: together they have to
 // stay in the instruction cache.
 //
 // Every wait is bounded: on timeout the block raises GDN_DEV_WAIT_TIMEOUT, issues
@@ -40,7 +41,7 @@ using namespace sm100;
 
 constexpr int kC = 128;     // tokens per chunk
 constexpr int kDVT = 64;    // columns of v per block
-constexpr int kThreads = 20 * 32;
+constexpr int kThreads = 28 * 32;
 constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one that is copied
 constexpr float kPlain = 120.f;  // decays of a block of 32, log 2, that go as products of two factors
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -73,12 +74,29 @@ static_assert(kSmemBytes <= 232448, "shared memory per block");
 // The parts of P of 32 tokens take the columns of their 32 products: 16 and 16.
 constexpr uint32_t kColP = 0, kColI = 256, kColO = 384, kColU = 448;
 
-__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *status)
+// A wait suspends the warp for as long as the hardware lets it; the clock is looked at
+// now and then.
+__device__ __noinline__ void wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *status)
 {
-    if (mbar_wait(bar, parity, *abort_flag ? kDrainNs : kWaitLimitNs)) return true;
+    const uint64_t limit = *abort_flag ? kDrainNs : kWaitLimitNs;
+    uint64_t from = 0;
+    for (unsigned i = 0;; ++i) {
+        if (mbar_try_wait(bar, parity)) return;
+        if (i % 16 == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (i == 0) from = now;
+            if (now - from > limit) break;
+        }
+    }
     *abort_flag = 1;
     atomicOr(status, GDN_DEV_WAIT_TIMEOUT);
-    return false;
+}
+
+// One arrival for the warp, after all of its lanes.
+__device__ __forceinline__ void arrive_warp(uint64_t *bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 struct Waiter {
@@ -86,7 +104,7 @@ struct Waiter {
     unsigned int *status;
     __device__ __forceinline__ void operator()(uint64_t *bar, int phase) const
     {
-        if (!mbar_test_wait(bar, phase & 1)) wait_long(bar, phase & 1, abort_flag, status);
+        if (!mbar_try_wait(bar, phase & 1)) wait_long(bar, phase & 1, abort_flag, status);
     }
 };
 
@@ -176,10 +194,11 @@ __device__ __forceinline__ uint32_t mend(uint32_t hi, uint32_t lo)
     return lo;
 }
 
-__device__ __noinline__ void mend_row(uint8_t *tiles, int r)
+// 32 columns of row r, from the pair w0.
+__device__ __noinline__ void mend_row(uint8_t *tiles, int r, int w0)
 {
 #pragma unroll 1
-    for (int w = 0; w < 32; ++w) {
+    for (int w = w0; w < w0 + 16; ++w) {
         const uint32_t at = sw128(r, w / 4) + w % 4 * 4;
         uint32_t *lo = reinterpret_cast<uint32_t *>(tiles + kTile + at);
         *lo = mend(*reinterpret_cast<const uint32_t *>(tiles + at), *lo);
@@ -212,9 +231,9 @@ __device__ __forceinline__ void st_p(uint32_t p, int quad, int J, const uint32_t
 }
 
 // P of one row in the cases that the plain path leaves: tokens that forget, blocks
-// that decay by more than 2^120, and products that are infinite or NaN.  Blocks
-// from `last` down.
-__device__ __noinline__ void odd_decays(uint32_t p, int quad, int lane, int last, const float *in, const float *total,
+// that decay by more than 2^120, and products that are infinite or NaN.  Every
+// other block from `last` down.
+__device__ __noinline__ void odd_decays(uint32_t p, int quad, int lane, int last, float scale, const float *in, const float *total,
                                         const unsigned *mask)
 {
     const float mine = in[32 * quad + lane];
@@ -223,7 +242,7 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int lane, int last
     const int first = first_seen(mask[quad], lane);
 #pragma unroll 1
     for (int J = quad; J >= 0; --J) {
-        if (J > last) {  // done
+        if (J > last || (last - J) % 2) {  // done, or the other warp's
             if (J < quad) {
                 sum += total[J];
                 cut = cut || mask[J];
@@ -239,7 +258,7 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int lane, int last
             const float w = in[32 * J + j];
             const bool seen = J == quad ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
             const float f = decay_of(J == quad ? mine - w : sum + (total[J] - w));
-            x[j] = seen && f != 0.f ? x[j] * f : 0.f;
+            x[j] = seen && f != 0.f ? x[j] * (f * scale) : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -316,17 +335,17 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             mbar_init(&s.v_full[i], 1);
             mbar_init(&s.kq_free[i], kStates ? 1 : 2);
             mbar_init(&s.v_free[i], 1);
-            mbar_init(&s.dec_ready[i], 128);
-            mbar_init(&s.dec_free[i], kStates ? 128 : 384);
-            mbar_init(&s.w_ready[i], 128);
-            mbar_init(&s.o_free[i], 128);
+            mbar_init(&s.dec_ready[i], 4);
+            mbar_init(&s.dec_free[i], kStates ? 8 : 20);
+            mbar_init(&s.w_ready[i], 4);
+            mbar_init(&s.o_free[i], 4);
             mbar_init(&s.qk_full[i], 1);
-            mbar_init(&s.p_ready[i], 128);
+            mbar_init(&s.p_ready[i], 8);
         }
         mbar_init(&s.p_free, 1);
         mbar_init(&s.u_full, 1);
-        mbar_init(&s.u_free, 128);
-        mbar_init(&s.s_ready, 128);
+        mbar_init(&s.u_free, 8);
+        mbar_init(&s.s_ready, 8);
         mbar_init(&s.o_full, 1);
         s.abort_flag = 0;
         fence_mbar_init();
@@ -345,9 +364,10 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     volatile int *abort_flag = &s.abort_flag;
     const Waiter wait = {abort_flag, a.status};
 
-    if (warp < 4) {
-        // ---- P, in the place of Q K^T
+    if (warp < 8) {
+        // ---- P, in the place of Q K^T: blocks quad - side, quad - side - 2, ..
         if constexpr (!kStates) {
+            const int side = warp >> 2;
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
@@ -362,54 +382,63 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 wait(&s.qk_full[st], c >> 1);
                 __syncwarp();
                 tc_fence_after();
-                int J = quad;
+                int J = quad - side;
+                if (side && J >= 0) sum += s.total[st][J];
 #pragma unroll 1
-                for (; J >= 0 && !odd; --J) {
-                    float x[32];
-                    if (J < quad) sum += s.total[st][J];
-                    const f32x2 f = dup2(decay_of(sum));
-                    const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J]);
-                    ld_cols(lane_addr(p, quad, 32 * J), x);
-                    if (J == quad) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
-                    }
+                for (; J >= 0 && !odd; J -= 2) {
+                    const f32x2 f = dup2(decay_of(sum) * a.scale);
+                    const bool diagonal = J == quad;
                     uint32_t hi[16], lo[16];
                     f32x2 sign = 0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 w = inverse[j];
-                        split(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), hi[2 * j], lo[2 * j], sign);
-                        split(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), hi[2 * j + 1],
-                              lo[2 * j + 1], sign);
+                    for (int half = 0; half < 2; ++half) {
+                        float x[16];
+                        const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J + 16 * half]);
+                        ld_cols(lane_addr(p, quad, 32 * J + 16 * half), x);
+                        if (diagonal) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) x[j] = 16 * half + j <= lane ? x[j] : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 w = inverse[j];
+                            const int e = 8 * half + 2 * j;
+                            split(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), hi[e], lo[e], sign);
+                            split(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), hi[e + 1], lo[e + 1],
+                                  sign);
+                        }
                     }
                     odd = __any_sync(0xffffffffu, is_odd(sign));
                     if (odd) break;  // this block's products are still in place
                     st_p(p, quad, J, hi, lo);
+                    if (J >= 2) sum += s.total[st][J - 1] + s.total[st][J - 2];
                 }
-                if (odd) odd_decays(p, quad, lane, J, s.in[st], s.total[st], s.mask[st]);
+                if (odd) odd_decays(p, quad, lane, J, a.scale, s.in[st], s.total[st], s.mask[st]);
                 const uint32_t zero[16] = {};
 #pragma unroll 1
-                for (int J = quad + 1; J < 4; ++J) st_p(p, quad, J, zero, zero);
-                mbar_arrive(&s.dec_free[st]);
+                for (J = quad + 2 - side; J < 4; J += 2) st_p(p, quad, J, zero, zero);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&s.p_ready[st]);
+                arrive_warp(&s.dec_free[st]);
+                arrive_warp(&s.p_ready[st]);
             }
         }
-    } else if (warp < 8) {
-        // ---- the state: row t of S^T
-        f32x2 S[kDVT / 2];
-        const int nv = min(kDVT, a.dv - v0);
+    } else if (warp < 16) {
+        // ---- the state: 32 columns of row t of S^T
+        constexpr int kCols = kDVT / 2;
+        const int c0 = (warp >> 2 & 1) * kCols;
+        f32x2 S[kCols / 2];
         const bool mine = 32 * quad < dk;  // the others' rows are not part of S: K^T has nothing there
+        const int64_t at = (int64_t)(v0 + c0) * dk + t;
+        const int cols = t < dk ? a.dv - v0 - c0 : 0;
         {
-            const float *p = u.in + (int64_t)v0 * dk + t;
-            const int cols = u.in && t < dk ? nv : 0;
+            const float *p = u.in + at;
+            const int n = u.in ? cols : 0;
 #pragma unroll
-            for (int d = 0; d < kDVT; d += 2) {
-                const float x = d < cols ? *p : 0.f;
+            for (int d = 0; d < kCols; d += 2) {
+                const float x = d < n ? *p : 0.f;
                 p += dk;
-                S[d / 2] = pack2(x, d + 1 < cols ? *p : 0.f);
+                S[d / 2] = pack2(x, d + 1 < n ? *p : 0.f);
                 p += dk;
             }
         }
@@ -421,41 +450,41 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 const float4 total = *reinterpret_cast<const float4 *>(s.total[st]);
                 const uint4 mask = *reinterpret_cast<const uint4 *>(s.mask[st]);
                 const float all = mask.x | mask.y | mask.z | mask.w ? 0.f : decay_of(total.x + total.y + total.z + total.w);
-                mbar_arrive(&s.dec_free[st]);
+                arrive_warp(&s.dec_free[st]);
                 if (all == 0.f)
 #pragma unroll
-                    for (int d = 0; d < kDVT / 2; ++d) S[d] = 0;  // forgotten, infinite or not
+                    for (int d = 0; d < kCols / 2; ++d) S[d] = 0;  // forgotten, infinite or not
                 wait(&s.u_full, c);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int q = 0; q < 4 && mine; ++q) {
+                for (int q = 0; q < kCols && mine; q += 16) {
                     float x[16];
-                    ld_cols(lane_addr(tbase, quad, kColU + 16 * q), x);
+                    ld_cols(lane_addr(tbase, quad, kColU + c0 + q), x);
 #pragma unroll
-                    for (int d = 0; d < 8; ++d) S[8 * q + d] = fma2(dup2(all), S[8 * q + d], pack2(x[2 * d], x[2 * d + 1]));
+                    for (int d = 0; d < 8; ++d)
+                        S[q / 2 + d] = fma2(dup2(all), S[q / 2 + d], pack2(x[2 * d], x[2 * d + 1]));
                 }
                 tc_fence_before();
-                mbar_arrive(&s.u_free);
+                arrive_warp(&s.u_free);
             }
             if (!kStates && c + 1 < chunks) {
                 if (c >= 0) wait(&s.kq_free[st], c >> 1);  // Q S^T of this chunk has read the parts
                 f32x2 sign = 0;
 #pragma unroll
-                for (int q = 0; q < 8 && (mine || c < 0); ++q) {
+                for (int q = 0; q < kCols / 8 && (mine || c < 0); ++q) {
                     const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
-                    st_parts(sm + kOffS, t, q, x, sign);
+                    st_parts(sm + kOffS, t, c0 / 8 + q, x, sign);
                 }
-                if (is_odd(sign)) mend_row(sm + kOffS, t);
+                if (is_odd(sign)) mend_row(sm + kOffS, t, c0 / 2);
                 fence_async_smem();
-                mbar_arrive(&s.s_ready);
+                arrive_warp(&s.s_ready);
             }
         }
         if (u.out && !*abort_flag) {
-            float *p = u.out + (int64_t)v0 * dk + t;
-            const int cols = t < dk ? nv : 0;
+            float *p = u.out + at;
 #pragma unroll
-            for (int d = 0; d < kDVT; d += 2) {
+            for (int d = 0; d < kCols; d += 2) {
                 float x, y;
                 unpack2(S[d / 2], x, y);
                 if (d < cols) *p = x;
@@ -464,7 +493,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 p += dk;
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 20) {
         // ---- decays, and V times the decay to the chunk's end
         const float *decay = a.log_decay + (u.row + t) * a.ld_decay + h;
         float next = t < u.len ? *decay : 0.f;
@@ -482,7 +511,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 s.mask[st][quad] = d.mask;
             }
             if (t == 0) s.odd[st] = 0;
-            mbar_arrive(&s.dec_ready[st]);
+            arrive_warp(&s.dec_ready[st]);
             named_sync(1, 128);
             bool cut = d.cut_behind(lane);
             float sum = d.after;
@@ -497,7 +526,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             if (c > 0) wait(&s.u_full, c - 1);  // the product has read the last chunk's
             uint8_t *V = sm + kOffV + st * kTile, *W = sm + kOffW;
             if (t < n) {
-                f32x2 sign = 0, raw = 0;
+                f32x2 sign = 0;
 #pragma unroll 1
                 for (int q = 0; q < 8; q += 2)
 #pragma unroll
@@ -508,14 +537,14 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             x[e] = pack2(f[2 * e], f[2 * e + 1]);
-                            raw = fma2(x[e], dup2(0.f), raw);
                             x[e] = mul2(x[e], dup2(w));
                         }
                         st_parts(W, t, q + r, x, sign);
                     }
-                if (is_odd(raw)) s.odd[st] = 1;
-                if (is_odd(sign)) {
-                    mend_row(W, t);
+                if (is_odd(sign)) {  // infinite or NaN, decayed or not
+                    s.odd[st] = 1;
+                    mend_row(W, t, 0);
+                    mend_row(W, t, 16);
                     if (w == 0.f) zero_row(W, t);  // what comes after has forgotten it
                 }
             } else {  // rows past the end may be another sequence's
@@ -531,9 +560,9 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             }
             fence_async_smem();
-            mbar_arrive(&s.w_ready[st]);
+            arrive_warp(&s.w_ready[st]);
         }
-    } else if (warp < 16) {
+    } else if (warp < 24) {
         // ---- outputs: row t
         if constexpr (!kStates) {
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (u.row + t) * a.ld_o + (int64_t)h * a.dv + v0;
@@ -552,10 +581,10 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     cut = cut || s.mask[st][J];
                     sum += s.total[st][J];
                 }
-                const f32x2 start = dup2(a.scale * decay_of(sum)), scale = dup2(a.scale);
+                const f32x2 start = dup2(a.scale * decay_of(sum));
                 wait(&s.w_ready[st], c >> 1);
                 const bool odd = s.odd[st];
-                mbar_arrive(&s.dec_free[st]);
+                arrive_warp(&s.dec_free[st]);
                 wait(&s.kq_free[st], c >> 1);
                 wait(&s.o_full, c);
                 tc_fence_after();
@@ -570,19 +599,21 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     float x[16], y[16];
                     __syncwarp();
                     ld_cols(lane_addr(tbase, quad, kColI + 64 * st + q), lane_addr(tbase, quad, kColO + q), x, y);
+                    if (cut)  // nothing of the state before, infinite or not
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = 0.f;
                     uint32_t f[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const f32x2 w = mul2(pack2(y[2 * e], y[2 * e + 1]), scale);
                         float lo, hi;
-                        unpack2(cut ? w : fma2(pack2(x[2 * e], x[2 * e + 1]), start, w), lo, hi);
+                        unpack2(fma2(pack2(x[2 * e], x[2 * e + 1]), start, pack2(y[2 * e], y[2 * e + 1])), lo, hi);
                         f[e] = narrow_pair(lo, hi);
                     }
                     if (q < cols) *reinterpret_cast<uint4 *>(o + q) = make_uint4(f[0], f[1], f[2], f[3]);
                     if (q + 8 < cols) *reinterpret_cast<uint4 *>(o + q + 8) = make_uint4(f[4], f[5], f[6], f[7]);
                 }
                 tc_fence_before();
-                mbar_arrive(&s.o_free[st]);
+                arrive_warp(&s.o_free[st]);
                 if (odd) {
                     named_sync(2, 128);
                     if (t == 0) {
@@ -592,7 +623,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             }
         }
-    } else if (warp == 16) {
+    } else if (warp == 24) {
         // ---- Q K^T and P V, the former two chunks ahead: it takes the place of the latter's P
         if (!kStates && elect_one()) {
             const uint32_t base = smem_u32(sm);
@@ -628,7 +659,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             }
         }
-    } else if (warp == 17) {
+    } else if (warp == 25) {
         // ---- K^T V, decayed, and Q S^T
         if (elect_one()) {
             const uint32_t base = smem_u32(sm);
@@ -667,7 +698,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             }
         }
-    } else if (warp == 18) {
+    } else if (warp == 26) {
         // ---- tensor copies of K and Q; those of chunks ahead of the ring go to L2
         if (elect_one()) {
             const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
