@@ -17,12 +17,12 @@
 // the decayed V, enters as two bf16 parts whose sum keeps 16 bits and more, so that
 // the final states are right to 2e-6 and the outputs but for their own rounding.
 //
-// Roles: warps 0-7 form P (tensor memory to tensor memory; a row per thread, every
-// other block of 32 columns), warps 8-15 keep the state, 32 columns each, and write
-// its parts for the next chunk, warps 16-19 sum the decays and form the decayed V,
-// warps 20-23 write the outputs, warps 24 and 25 issue the products with P and those
-// with the state, warps 26 and 27 the tensor copies into rings of two stages, with
-// later chunks fetched to L2 ahead.  All loops over chunks are kept small: together they have to
+// Roles, in groups of four warps: forming P (tensor memory to tensor memory, a row per
+// thread), keeping the state and writing its parts for the next chunk, summing the
+// decays and forming the decayed V, writing the outputs; then single warps that issue
+// the products with P, those with the state, and the tensor copies into rings of two
+// stages, with later chunks fetched to L2 ahead.
+// All loops over chunks are kept small: together they have to
 // stay in the instruction cache.
 //
 // Every wait is bounded: on timeout the block raises GDN_DEV_WAIT_TIMEOUT, issues
@@ -41,7 +41,11 @@ using namespace sm100;
 
 constexpr int kC = 128;     // tokens per chunk
 constexpr int kDVT = 64;    // columns of v per block
-constexpr int kThreads = 28 * 32;
+// Groups of four warps that form P (every kPG-th block of columns each) and that keep
+// the state (kDVT / kSG columns each).
+constexpr int kPG = 1, kSG = 1;
+constexpr int kWarpS = 4 * kPG, kWarpW = kWarpS + 4 * kSG, kWarpO = kWarpW + 4, kWarpIssue = kWarpO + 4;
+constexpr int kThreads = (kWarpIssue + 4) * 32;
 constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one that is copied
 constexpr float kPlain = 120.f;  // decays of a block of 32, log 2, that go as products of two factors
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -62,7 +66,8 @@ struct Small {
     float in[2][kC], inverse[2][kC], total[2][4];
     unsigned mask[2][4];
     int odd[2];             // V has infinities or NaN
-    uint64_t full[2], v_full[2], kq_free[2], v_free[2], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2];
+    uint64_t full[2], v_full[2], kq_free[2], v_free[2], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2],
+        o_staged[2];
     uint64_t p_free, u_full, u_free, s_ready, o_full;
     uint32_t tmem;
     int abort_flag;
@@ -194,11 +199,11 @@ __device__ __forceinline__ uint32_t mend(uint32_t hi, uint32_t lo)
     return lo;
 }
 
-// 32 columns of row r, from the pair w0.
-__device__ __noinline__ void mend_row(uint8_t *tiles, int r, int w0)
+// n pairs of row r from the pair w0.
+__device__ __noinline__ void mend_row(uint8_t *tiles, int r, int w0, int n)
 {
 #pragma unroll 1
-    for (int w = w0; w < w0 + 16; ++w) {
+    for (int w = w0; w < w0 + n; ++w) {
         const uint32_t at = sw128(r, w / 4) + w % 4 * 4;
         uint32_t *lo = reinterpret_cast<uint32_t *>(tiles + kTile + at);
         *lo = mend(*reinterpret_cast<const uint32_t *>(tiles + at), *lo);
@@ -231,19 +236,19 @@ __device__ __forceinline__ void st_p(uint32_t p, int quad, int J, const uint32_t
 }
 
 // P of one row in the cases that the plain path leaves: tokens that forget, blocks
-// that decay by more than 2^120, and products that are infinite or NaN.  Every
-// other block from `last` down.
-__device__ __noinline__ void odd_decays(uint32_t p, int quad, int lane, int last, float scale, const float *in, const float *total,
+// that decay by more than 2^120, and products that are infinite or NaN.  The warp's
+// blocks from `last` down.
+__device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, int last, float scale, const float *in, const float *total,
                                         const unsigned *mask)
 {
-    const float mine = in[32 * quad + lane];
+    const float mine = in[32 * I + lane];
     float sum = mine;
-    bool cut = mask[quad] & (0xffffffffu >> (31 - lane));
-    const int first = first_seen(mask[quad], lane);
+    bool cut = mask[I] & (0xffffffffu >> (31 - lane));
+    const int first = first_seen(mask[I], lane);
 #pragma unroll 1
-    for (int J = quad; J >= 0; --J) {
-        if (J > last || (last - J) % 2) {  // done, or the other warp's
-            if (J < quad) {
+    for (int J = I; J >= 0; --J) {
+        if (J > last || (last - J) % kPG) {  // done, or another warp's
+            if (J < I) {
                 sum += total[J];
                 cut = cut || mask[J];
             }
@@ -256,8 +261,8 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int lane, int last
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float w = in[32 * J + j];
-            const bool seen = J == quad ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
-            const float f = decay_of(J == quad ? mine - w : sum + (total[J] - w));
+            const bool seen = J == I ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
+            const float f = decay_of(J == I ? mine - w : sum + (total[J] - w));
             x[j] = seen && f != 0.f ? x[j] * (f * scale) : 0.f;
         }
 #pragma unroll
@@ -267,7 +272,7 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int lane, int last
         }
         __syncwarp();
         st_p(p, quad, J, hi, lo);
-        if (J < quad) {
+        if (J < I) {
             sum += total[J];
             cut = cut || mask[J];
         }
@@ -285,7 +290,7 @@ __device__ __noinline__ void odd_row(uint32_t p, uint32_t o, int quad, int i, in
 #pragma unroll
     for (int d = 0; d < 32; ++d) acc[d] = 0.f;
 #pragma unroll 1
-    for (int w = 0; w < 16 * (quad + 1); ++w) {
+    for (int w = 0; w < 64; ++w) {
         __syncwarp();
         const uint32_t hi = ld_col(lane_addr(p, quad, w / 16 * 32 + w % 16)), lo = ld_col(lane_addr(p, quad, w / 16 * 32 + 16 + w % 16));
 #pragma unroll 1
@@ -309,6 +314,12 @@ __device__ __noinline__ void odd_row(uint32_t p, uint32_t o, int quad, int i, in
     }
 }
 
+// The 32 tokens of a chunk whose rows of Q, P and O are in the lanes of a quarter of
+// tensor memory, which only every fourth warp, those of one scheduler, can reach.  The
+// last tokens have four blocks of P to form, the first one: they change places in every
+// other chunk.
+__device__ __forceinline__ int row_block(int quad, int chunk) { return chunk & 1 ? 3 - quad : quad; }
+
 // Descriptor steps of 16 along K, K-major (64 to a row) and MN-major (rows).
 __device__ __forceinline__ constexpr uint32_t k_step(int k) { return ((k >> 2) * kTile + (k & 3) * 32) >> 4; }
 __device__ __forceinline__ constexpr uint32_t mn_step(int k) { return k * 2048 >> 4; }
@@ -318,7 +329,8 @@ __device__ __forceinline__ constexpr uint32_t mn_step(int k) { return k * 2048 >
 template <bool kStates, int KS>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__ CUtensorMap tm_q,
-                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v)
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_o)
 {
     extern __shared__ __align__(1024) uint8_t sm[];
     Small &s = *reinterpret_cast<Small *>(sm + kOffSmall);
@@ -336,22 +348,24 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             mbar_init(&s.kq_free[i], kStates ? 1 : 2);
             mbar_init(&s.v_free[i], 1);
             mbar_init(&s.dec_ready[i], 4);
-            mbar_init(&s.dec_free[i], kStates ? 8 : 20);
+            mbar_init(&s.dec_free[i], 4 * (kStates ? kSG : kPG + kSG + 1));
             mbar_init(&s.w_ready[i], 4);
             mbar_init(&s.o_free[i], 4);
             mbar_init(&s.qk_full[i], 1);
-            mbar_init(&s.p_ready[i], 8);
+            mbar_init(&s.o_staged[i], 4);
+            mbar_init(&s.p_ready[i], 4 * kPG);
         }
         mbar_init(&s.p_free, 1);
         mbar_init(&s.u_full, 1);
-        mbar_init(&s.u_free, 8);
-        mbar_init(&s.s_ready, 8);
+        mbar_init(&s.u_free, 4 * kSG);
+        mbar_init(&s.s_ready, 4 * kSG);
         mbar_init(&s.o_full, 1);
         s.abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_o);
     }
     if (warp == 0) {
         tmem_alloc(&s.tmem, 512);
@@ -364,30 +378,30 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     volatile int *abort_flag = &s.abort_flag;
     const Waiter wait = {abort_flag, a.status};
 
-    if (warp < 8) {
-        // ---- P, in the place of Q K^T: blocks quad - side, quad - side - 2, ..
+    if (warp < kWarpS) {
+        // ---- P, in the place of Q K^T: a row per thread, every kPG-th block of columns up to its own
         if constexpr (!kStates) {
             const int side = warp >> 2;
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
-                const int st = c & 1;
+                const int st = c & 1, I = row_block(quad, c);
                 const uint32_t p = tbase + kColP + 128 * st;
                 wait(&s.dec_ready[st], c >> 1);
                 // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where J, the
                 // block of j, decays by less than 2^120; within a block without the middle factor.
-                float sum = s.in[st][t];
+                float sum = s.in[st][32 * I + lane];
                 bool odd = false;
 #pragma unroll 1
-                for (int J = 0; J <= quad; ++J) odd |= s.mask[st][J] || !(fabsf(s.total[st][J]) < kPlain);
+                for (int J = 0; J <= I; ++J) odd |= s.mask[st][J] || !(fabsf(s.total[st][J]) < kPlain);
                 wait(&s.qk_full[st], c >> 1);
                 __syncwarp();
                 tc_fence_after();
-                int J = quad - side;
+                int J = I - side;
                 if (side && J >= 0) sum += s.total[st][J];
 #pragma unroll 1
-                for (; J >= 0 && !odd; J -= 2) {
+                for (; J >= 0 && !odd; J -= kPG) {
                     const f32x2 f = dup2(decay_of(sum) * a.scale);
-                    const bool diagonal = J == quad;
+                    const bool diagonal = J == I;
                     uint32_t hi[16], lo[16];
                     f32x2 sign = 0;
 #pragma unroll
@@ -411,22 +425,24 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     odd = __any_sync(0xffffffffu, is_odd(sign));
                     if (odd) break;  // this block's products are still in place
                     st_p(p, quad, J, hi, lo);
-                    if (J >= 2) sum += s.total[st][J - 1] + s.total[st][J - 2];
+                    if (J >= kPG)
+#pragma unroll
+                        for (int e = 1; e <= kPG; ++e) sum += s.total[st][J - e];
                 }
-                if (odd) odd_decays(p, quad, lane, J, a.scale, s.in[st], s.total[st], s.mask[st]);
+                if (odd) odd_decays(p, quad, I, lane, J, a.scale, s.in[st], s.total[st], s.mask[st]);
                 const uint32_t zero[16] = {};
 #pragma unroll 1
-                for (J = quad + 2 - side; J < 4; J += 2) st_p(p, quad, J, zero, zero);
+                for (J = I + kPG - side; J < 4; J += kPG) st_p(p, quad, J, zero, zero);
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_warp(&s.dec_free[st]);
                 arrive_warp(&s.p_ready[st]);
             }
         }
-    } else if (warp < 16) {
-        // ---- the state: 32 columns of row t of S^T
-        constexpr int kCols = kDVT / 2;
-        const int c0 = (warp >> 2 & 1) * kCols;
+    } else if (warp < kWarpW) {
+        // ---- the state: kCols columns of row t of S^T
+        constexpr int kCols = kDVT / kSG;
+        const int c0 = (warp - kWarpS) / 4 * kCols;
         f32x2 S[kCols / 2];
         const bool mine = 32 * quad < dk;  // the others' rows are not part of S: K^T has nothing there
         const int64_t at = (int64_t)(v0 + c0) * dk + t;
@@ -476,7 +492,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
                     st_parts(sm + kOffS, t, c0 / 8 + q, x, sign);
                 }
-                if (is_odd(sign)) mend_row(sm + kOffS, t, c0 / 2);
+                if (is_odd(sign)) mend_row(sm + kOffS, t, c0 / 2, kCols / 2);
                 fence_async_smem();
                 arrive_warp(&s.s_ready);
             }
@@ -493,7 +509,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 p += dk;
             }
         }
-    } else if (warp < 20) {
+    } else if (warp < kWarpO) {
         // ---- decays, and V times the decay to the chunk's end
         const float *decay = a.log_decay + (u.row + t) * a.ld_decay + h;
         float next = t < u.len ? *decay : 0.f;
@@ -543,8 +559,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     }
                 if (is_odd(sign)) {  // infinite or NaN, decayed or not
                     s.odd[st] = 1;
-                    mend_row(W, t, 0);
-                    mend_row(W, t, 16);
+                    mend_row(W, t, 0, 32);
                     if (w == 0.f) zero_row(W, t);  // what comes after has forgotten it
                 }
             } else {  // rows past the end may be another sequence's
@@ -562,21 +577,21 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             fence_async_smem();
             arrive_warp(&s.w_ready[st]);
         }
-    } else if (warp < 24) {
-        // ---- outputs: row t
+    } else if (warp < kWarpIssue) {
+        // ---- outputs: a row per thread
         if constexpr (!kStates) {
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (u.row + t) * a.ld_o + (int64_t)h * a.dv + v0;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + u.row * a.ld_o + (int64_t)h * a.dv + v0;
             const int nv = min(kDVT, a.dv - v0);
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, o += kC * a.ld_o) {
-                const int st = c & 1, n = min(kC, u.len - c * kC);
+                const int st = c & 1, n = min(kC, u.len - c * kC), I = row_block(quad, c), i = 32 * I + lane;
                 wait(&s.dec_ready[st], c >> 1);
-                const unsigned mask = s.mask[st][quad];
-                float sum = s.in[st][t];
+                const unsigned mask = s.mask[st][I];
+                float sum = s.in[st][i];
                 bool cut = mask & (0xffffffffu >> (31 - lane));
-                int first = 32 * quad + first_seen(mask, lane);  // the first token this one sees
+                int first = 32 * I + first_seen(mask, lane);  // the first token this one sees
 #pragma unroll 1
-                for (int J = quad - 1; J >= 0; --J) {
+                for (int J = I - 1; J >= 0; --J) {
                     if (!cut) first = 32 * J + first_seen(s.mask[st][J], 31);
                     cut = cut || s.mask[st][J];
                     sum += s.total[st][J];
@@ -588,12 +603,17 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 wait(&s.kq_free[st], c >> 1);
                 wait(&s.o_full, c);
                 tc_fence_after();
-                if (!odd && t == 0) {
-                    mbar_arrive(&s.v_free[st]);
-                    mbar_arrive(&s.p_free);
+                uint8_t *stage = sm + kOffV + st * kTile;  // V is through, but for odd_row
+                if (odd) {
+                    odd_row(tbase + kColP + 128 * st, tbase + kColO, quad, i, first, stage);
+                    named_sync(2, 128);
                 }
-                const int cols = t < n ? nv : 0;
-                if (odd) odd_row(tbase + kColP + 128 * st, tbase + kColO, quad, t, first, sm + kOffV + st * kTile);
+                if (t == 0) mbar_arrive(&s.p_free);
+                // Whole chunks go through the place of V and a tensor copy: rows stored from here would take a
+                // transaction per row and store, half of what the memory pipe can do.
+                const bool whole = n == kC;
+                const int cols = i < n ? nv : 0;
+                __nv_bfloat16 *row = o + i * a.ld_o;
 #pragma unroll 1
                 for (int q = 0; q < kDVT; q += 16) {
                     float x[16], y[16];
@@ -609,21 +629,22 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                         unpack2(fma2(pack2(x[2 * e], x[2 * e + 1]), start, pack2(y[2 * e], y[2 * e + 1])), lo, hi);
                         f[e] = narrow_pair(lo, hi);
                     }
-                    if (q < cols) *reinterpret_cast<uint4 *>(o + q) = make_uint4(f[0], f[1], f[2], f[3]);
-                    if (q + 8 < cols) *reinterpret_cast<uint4 *>(o + q + 8) = make_uint4(f[4], f[5], f[6], f[7]);
+                    const uint4 f0 = make_uint4(f[0], f[1], f[2], f[3]), f1 = make_uint4(f[4], f[5], f[6], f[7]);
+                    if (whole) {
+                        *reinterpret_cast<uint4 *>(stage + sw128(i, q / 8)) = f0;
+                        *reinterpret_cast<uint4 *>(stage + sw128(i, q / 8 + 1)) = f1;
+                    } else {
+                        if (q < cols) *reinterpret_cast<uint4 *>(row + q) = f0;
+                        if (q + 8 < cols) *reinterpret_cast<uint4 *>(row + q + 8) = f1;
+                    }
                 }
                 tc_fence_before();
                 arrive_warp(&s.o_free[st]);
-                if (odd) {
-                    named_sync(2, 128);
-                    if (t == 0) {
-                        mbar_arrive(&s.v_free[st]);
-                        mbar_arrive(&s.p_free);
-                    }
-                }
+                fence_async_smem();
+                arrive_warp(&s.o_staged[st]);
             }
         }
-    } else if (warp == 24) {
+    } else if (warp == kWarpIssue) {
         // ---- Q K^T and P V, the former two chunks ahead: it takes the place of the latter's P
         if (!kStates && elect_one()) {
             const uint32_t base = smem_u32(sm);
@@ -659,7 +680,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             }
         }
-    } else if (warp == 25) {
+    } else if (warp == kWarpIssue + 1) {
         // ---- K^T V, decayed, and Q S^T
         if (elect_one()) {
             const uint32_t base = smem_u32(sm);
@@ -698,7 +719,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             }
         }
-    } else if (warp == 26) {
+    } else if (warp == kWarpIssue + 2) {
         // ---- tensor copies of K and Q; those of chunks ahead of the ring go to L2
         if (elect_one()) {
             const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
@@ -709,7 +730,9 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
 #pragma unroll 1
                     for (int i = 0; i < halves; ++i) {
                         fetch_l2(&tm_k, 64 * i, g, row + kAhead * kC);
-                        if (!kStates) fetch_l2(&tm_q, 64 * i, g, row + kAhead * kC);
+                        if (!kStates)
+#pragma unroll 1
+                            for (int b = 0; b < 4; ++b) fetch_l2(&tm_q, 64 * i, g, row + kAhead * kC + 32 * b);
                     }
                 if (c < 0) continue;
                 if (c > 1) wait(&s.kq_free[st], (c - 2) >> 1);
@@ -718,22 +741,38 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
 #pragma unroll 1
                 for (int i = 0; i < halves; ++i) {
                     tma_load_3d(sm + kOffK + (st * 2 + i) * kTile, &tm_k, &s.full[st], 64 * i, g, row);
-                    if (!kStates) tma_load_3d(sm + kOffQ + (st * 2 + i) * kTile, &tm_q, &s.full[st], 64 * i, g, row);
+                    if (!kStates)
+#pragma unroll 1
+                        for (int b = 0; b < 4; ++b)
+                            tma_load_3d(sm + kOffQ + (st * 2 + i) * kTile + b * (kTile / 4), &tm_q, &s.full[st], 64 * i, g,
+                                        row + 32 * row_block(b, c));
                 }
             }
         }
     } else if (elect_one()) {
-        // ---- and of V
+        // ---- of V, and of the outputs that take its place
+        auto put = [&](int c) {
+            if constexpr (kStates) {
+                wait(&s.v_free[c & 1], c >> 1);
+            } else {
+                wait(&s.o_staged[c & 1], c >> 1);
+                if (u.len - c * kC >= kC && !*abort_flag)
+                    tma_store_3d(&tm_o, sm + kOffV + (c & 1) * kTile, v0, h, (int)(u.row + (int64_t)c * kC));
+                bulk_commit();
+            }
+        };
 #pragma unroll 1
-        for (int c = -kAhead; c < chunks; ++c) {
+        for (int c = -kAhead; c < chunks + 2; ++c) {
             const int st = c & 1, row = (int)(u.row + (int64_t)c * kC);
             if (c + kAhead < chunks) fetch_l2(&tm_v, v0, h, row + kAhead * kC);
             if (c < 0) continue;
-            if (c > 1) wait(&s.v_free[st], (c - 2) >> 1);
-            if (*abort_flag) break;
+            if (c > 1 && c - 2 < chunks) put(c - 2);
+            if (c >= chunks || *abort_flag) continue;
+            bulk_wait_read();
             mbar_arrive_expect_tx(&s.v_full[st], kTile);
             tma_load_3d(sm + kOffV + st * kTile, &tm_v, &s.v_full[st], v0, h, row);
         }
+        bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before();
@@ -758,12 +797,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-// [rows][heads][width] bf16 with a row stride, in boxes of 128 rows x 1 head x 64.
-bool make_map(CUtensorMap *m, const void *base, int64_t rows, int heads, int width, int64_t ld)
+// [rows][heads][width] bf16 with a row stride, in boxes of `high` rows x 1 head x 64.
+bool make_map(CUtensorMap *m, const void *base, int64_t rows, int heads, int width, int64_t ld, int high)
 {
     const cuuint64_t dim[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t stride[2] = {(cuuint64_t)width * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kC}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)high}, es[3] = {1, 1, 1};
     return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dim, stride, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -776,7 +815,7 @@ bool gdn_linattn_tc_supported(const GdnLinattnArgs &a)
     const int64_t rows = a.cu_seqlens ? a.T : (int64_t)a.N * a.T;
     // tensor copies take strides that are multiples of 16 bytes, below 2^40
     return a.dtype == 1 && a.dk % 8 == 0 && a.dv % 8 == 0 && (a.ld_q | a.ld_k | a.ld_v | a.ld_o) % 8 == 0 &&
-           a.ld_q < ((int64_t)1 << 38) && a.ld_k < ((int64_t)1 << 38) && a.ld_v < ((int64_t)1 << 38) && rows > 0 &&
+           a.ld_q < ((int64_t)1 << 38) && a.ld_k < ((int64_t)1 << 38) && a.ld_v < ((int64_t)1 << 38) && a.ld_o < ((int64_t)1 << 38) && rows > 0 &&
            rows < ((int64_t)1 << 31) - 2 * kC && aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned16(a.o) &&
            encoder();
 }
@@ -787,9 +826,9 @@ cudaError_t gdn_linattn_tc(const GdnLinattnArgs &a, bool states_only, cudaStream
     const int tiles = (a.dv + kDVT - 1) / kDVT;
     const int64_t blocks = (a.segment ? a.pieces : a.N) * a.heads * tiles;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    CUtensorMap q, k, v;
-    if (!make_map(&q, a.q, rows, a.groups, a.dk, a.ld_q) || !make_map(&k, a.k, rows, a.groups, a.dk, a.ld_k) ||
-        !make_map(&v, a.v, rows, a.heads, a.dv, a.ld_v))
+    CUtensorMap q, k, v, o;
+    if (!make_map(&q, a.q, rows, a.groups, a.dk, a.ld_q, kC / 4) || !make_map(&k, a.k, rows, a.groups, a.dk, a.ld_k, kC) ||
+        !make_map(&v, a.v, rows, a.heads, a.dv, a.ld_v, kC) || !make_map(&o, a.o, rows, a.heads, a.dv, a.ld_o, kC))
         return cudaErrorInvalidValue;
     auto *kernel = states_only  ? gdn_linattn_tc_kernel<true, 8>
                    : a.dk <= 64 ? gdn_linattn_tc_kernel<false, 4>
@@ -797,6 +836,6 @@ cudaError_t gdn_linattn_tc(const GdnLinattnArgs &a, bool states_only, cudaStream
                                 : gdn_linattn_tc_kernel<false, 8>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(a, tiles, q, k, v);
+    kernel<<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(a, tiles, q, k, v, o);
     return cudaGetLastError();
 }
