@@ -20,10 +20,9 @@
 // Roles, in groups of four warps: forming P (tensor memory to tensor memory, a row per
 // thread), keeping the state and writing its parts for the next chunk, summing the
 // decays and forming the decayed V, writing the outputs; then single warps that issue
-// the products with P, those with the state, and the tensor copies into rings of two
-// stages, with later chunks fetched to L2 ahead.
-// All loops over chunks are kept small: together they have to
-// stay in the instruction cache.
+// the products with P, K^T V, Q S^T, and the tensor copies into rings of two
+// stages, with later chunks fetched to L2 ahead.  All loops over chunks are kept
+// small: together they have to stay in the instruction cache.
 //
 // Every wait is bounded: on timeout the block raises GDN_DEV_WAIT_TIMEOUT, issues
 // no more copies and winds down with waits of 50 us, enough for what is in flight.
@@ -67,7 +66,7 @@ struct Small {
     unsigned mask[2][4];
     int odd[2];             // V has infinities or NaN
     uint64_t full[2], v_full[2], kq_free[2], v_free[2], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2],
-        o_staged[2];
+        o_staged[2], i_full[2];
     uint64_t p_free, u_full, u_free, s_ready, o_full;
     uint32_t tmem;
     int abort_flag;
@@ -345,7 +344,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.kq_free[i], kStates ? 1 : 2);
+            mbar_init(&s.kq_free[i], kStates ? 1 : 3);
             mbar_init(&s.v_free[i], 1);
             mbar_init(&s.dec_ready[i], 4);
             mbar_init(&s.dec_free[i], 4 * (kStates ? kSG : kPG + kSG + 1));
@@ -353,6 +352,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             mbar_init(&s.o_free[i], 4);
             mbar_init(&s.qk_full[i], 1);
             mbar_init(&s.o_staged[i], 4);
+            mbar_init(&s.i_full[i], 1);
             mbar_init(&s.p_ready[i], 4 * kPG);
         }
         mbar_init(&s.p_free, 1);
@@ -485,7 +485,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 arrive_warp(&s.u_free);
             }
             if (!kStates && c + 1 < chunks) {
-                if (c >= 0) wait(&s.kq_free[st], c >> 1);  // Q S^T of this chunk has read the parts
+                if (c >= 0) wait(&s.i_full[st], c >> 1);  // Q S^T of this chunk has read the parts
                 f32x2 sign = 0;
 #pragma unroll
                 for (int q = 0; q < kCols / 8 && (mine || c < 0); ++q) {
@@ -600,7 +600,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 wait(&s.w_ready[st], c >> 1);
                 const bool odd = s.odd[st];
                 arrive_warp(&s.dec_free[st]);
-                wait(&s.kq_free[st], c >> 1);
+                wait(&s.i_full[st], c >> 1);
                 wait(&s.o_full, c);
                 tc_fence_after();
                 uint8_t *stage = sm + kOffV + st * kTile;  // V is through, but for odd_row
@@ -654,7 +654,8 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 const uint32_t p = tbase + kColP + 128 * st;
                 if (c >= 0) {
                     wait(&s.p_ready[st], c >> 1);
-                    wait(&s.w_ready[st], c >> 1);  // rows of V past the end are zero
+                    wait(&s.v_full[st], c >> 1);
+                    if (u.len - c * kC < kC) wait(&s.w_ready[st], c >> 1);  // rows past the end are zero
                     if (c > 0) wait(&s.o_free[st ^ 1], (c - 1) >> 1);
                     tc_fence_after();
                     const uint64_t v = sdesc_sw128(base + kOffV + st * kTile, kTile, 1024);
@@ -681,7 +682,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             }
         }
     } else if (warp == kWarpIssue + 1) {
-        // ---- K^T V, decayed, and Q S^T
+        // ---- K^T V, decayed
         if (elect_one()) {
             const uint32_t base = smem_u32(sm);
 #pragma unroll 1
@@ -700,77 +701,92 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                         mma_f16kind(tbase + kColU, k + mn_step(i), w + part * (kTile >> 4) + mn_step(i),
                                     idesc_bf16_f32(128, 64, 1, 1), part + i > 0);
                 mma_commit(&s.u_full);
-                if constexpr (kStates) {
-                    mma_commit(&s.kq_free[st]);
-                    mma_commit(&s.v_free[st]);
-                } else {
-                    wait(&s.s_ready, c);
-                    if (c > 1) wait(&s.o_free[st], (c - 2) >> 1);
-                    tc_fence_after();
-                    const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
-                    const uint64_t S = sdesc_sw128(base + kOffS, kTile, 1024);
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int i = 0; i < KS; ++i)
-                                mma_f16kind(tbase + kColI + 64 * st, q + k_step(i), S + part * (kTile >> 4) + mn_step(i),
-                                            idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
-                    mma_commit(&s.kq_free[st]);
-                }
+                mma_commit(&s.kq_free[st]);
+                if (kStates) mma_commit(&s.v_free[st]);
             }
         }
     } else if (warp == kWarpIssue + 2) {
-        // ---- tensor copies of K and Q; those of chunks ahead of the ring go to L2
-        if (elect_one()) {
-            const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
+        // ---- Q S^T
+        if (!kStates && elect_one()) {
+            const uint32_t base = smem_u32(sm);
 #pragma unroll 1
-            for (int c = -kAhead; c < chunks; ++c) {
-                const int st = c & 1, row = (int)(u.row + (int64_t)c * kC);
-                if (c + kAhead < chunks)
-#pragma unroll 1
-                    for (int i = 0; i < halves; ++i) {
-                        fetch_l2(&tm_k, 64 * i, g, row + kAhead * kC);
-                        if (!kStates)
-#pragma unroll 1
-                            for (int b = 0; b < 4; ++b) fetch_l2(&tm_q, 64 * i, g, row + kAhead * kC + 32 * b);
-                    }
-                if (c < 0) continue;
-                if (c > 1) wait(&s.kq_free[st], (c - 2) >> 1);
-                if (*abort_flag) break;
-                mbar_arrive_expect_tx(&s.full[st], (uint32_t)(halves * (kStates ? 1 : 2)) * kTile);
-#pragma unroll 1
-                for (int i = 0; i < halves; ++i) {
-                    tma_load_3d(sm + kOffK + (st * 2 + i) * kTile, &tm_k, &s.full[st], 64 * i, g, row);
-                    if (!kStates)
-#pragma unroll 1
-                        for (int b = 0; b < 4; ++b)
-                            tma_load_3d(sm + kOffQ + (st * 2 + i) * kTile + b * (kTile / 4), &tm_q, &s.full[st], 64 * i, g,
-                                        row + 32 * row_block(b, c));
-                }
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c & 1;
+                wait(&s.full[st], c >> 1);
+                wait(&s.s_ready, c);
+                if (c > 1) wait(&s.o_free[st], (c - 2) >> 1);
+                tc_fence_after();
+                const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
+                const uint64_t S = sdesc_sw128(base + kOffS, kTile, 1024);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        mma_f16kind(tbase + kColI + 64 * st, q + k_step(i), S + part * (kTile >> 4) + mn_step(i),
+                                    idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
+                mma_commit(&s.kq_free[st]);
+                mma_commit(&s.i_full[st]);
             }
         }
     } else if (elect_one()) {
-        // ---- of V, and of the outputs that take its place
-        auto put = [&](int c) {
-            if constexpr (kStates) {
-                wait(&s.v_free[c & 1], c >> 1);
-            } else {
-                wait(&s.o_staged[c & 1], c >> 1);
-                if (u.len - c * kC >= kC && !*abort_flag)
-                    tma_store_3d(&tm_o, sm + kOffV + (c & 1) * kTile, v0, h, (int)(u.row + (int64_t)c * kC));
-                bulk_commit();
+        // ---- tensor copies: K and Q, V, and the outputs that take the place of V, whichever can go on.  Chunks
+        // ahead of the rings are fetched to L2.
+        const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
+        auto row = [&](int c) { return (int)(u.row + (int64_t)c * kC); };
+        auto load_kq = [&](int c, bool ahead) {
+            uint64_t *bar = &s.full[c & 1];
+            if (!ahead) mbar_arrive_expect_tx(bar, (uint32_t)(halves * (kStates ? 1 : 2)) * kTile);
+#pragma unroll 1
+            for (int i = 0; i < halves; ++i) {
+                const int at = ((c & 1) * 2 + i) * kTile;
+                if (ahead) fetch_l2(&tm_k, 64 * i, g, row(c));
+                else tma_load_3d(sm + kOffK + at, &tm_k, bar, 64 * i, g, row(c));
+                if (kStates) continue;
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    const int from = row(c) + 32 * row_block(b, c);
+                    if (ahead) fetch_l2(&tm_q, 64 * i, g, from);
+                    else tma_load_3d(sm + kOffQ + at + b * (kTile / 4), &tm_q, bar, 64 * i, g, from);
+                }
             }
         };
+        auto load_v = [&](int c) {
+            mbar_arrive_expect_tx(&s.v_full[c & 1], kTile);
+            tma_load_3d(sm + kOffV + (c & 1) * kTile, &tm_v, &s.v_full[c & 1], v0, h, row(c));
+            if (c + kAhead < chunks) fetch_l2(&tm_v, v0, h, row(c + kAhead));
+        };
 #pragma unroll 1
-        for (int c = -kAhead; c < chunks + 2; ++c) {
-            const int st = c & 1, row = (int)(u.row + (int64_t)c * kC);
-            if (c + kAhead < chunks) fetch_l2(&tm_v, v0, h, row + kAhead * kC);
-            if (c < 0) continue;
-            if (c > 1 && c - 2 < chunks) put(c - 2);
-            if (c >= chunks || *abort_flag) continue;
-            bulk_wait_read();
-            mbar_arrive_expect_tx(&s.v_full[st], kTile);
-            tma_load_3d(sm + kOffV + st * kTile, &tm_v, &s.v_full[st], v0, h, row);
+        for (int c = 0; c < 2 && c < chunks; ++c) load_v(c);
+        int kq = 0, put = 0;  // chunks loaded; chunks whose V is through and whose outputs are stored
+        uint64_t idle = 0;    // since when there is nothing to do
+        while ((kq < chunks || put < chunks) && !*abort_flag) {
+            bool moved = false;
+            if (kq < chunks && (kq < 2 || mbar_test_wait(&s.kq_free[kq & 1], (kq - 2) >> 1 & 1))) {
+                load_kq(kq, false);
+                if (kq + kAhead < chunks) load_kq(kq + kAhead, true);
+                ++kq;
+                moved = true;
+            }
+            if (put < chunks && mbar_test_wait(kStates ? &s.v_free[put & 1] : &s.o_staged[put & 1], put >> 1 & 1)) {
+                if (!kStates && u.len - put * kC >= kC) {
+                    tma_store_3d(&tm_o, sm + kOffV + (put & 1) * kTile, v0, h, row(put));
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+                if (put + 2 < chunks) load_v(put + 2);
+                ++put;
+                moved = true;
+            }
+            if (moved) {
+                idle = 0;
+            } else {
+                const uint64_t now = globaltimer_ns();
+                if (!idle) idle = now;
+                if (now - idle > kWaitLimitNs) {
+                    *abort_flag = 1;
+                    atomicOr(a.status, GDN_DEV_WAIT_TIMEOUT);
+                }
+            }
         }
         bulk_wait_all();
     }
