@@ -13,9 +13,11 @@
 // Only the last line is serial, and it is 64 fused multiply-adds a thread: the
 // state stays in the registers of four warps, fp32, for the whole walk, and none
 // of the products waits for more than the one before it.  Q, K and V enter as they
-// are (products of bf16 are exact in fp32); what is formed on the way, P, S and
-// the decayed V, enters as two bf16 parts whose sum keeps 16 bits and more, so that
-// the final states are right to 2e-6 and the outputs but for their own rounding.
+// are (products of bf16 are exact in fp32), and sums are fp32.  The decayed V enters
+// as two bf16 parts whose sum keeps 16 bits: final states are right to 2e-6.  P and
+// the state enter the outputs' products rounded once to bf16, which is what the
+// outputs themselves are rounded to: 2.0e-3 off in the 2-norm, 1.7e-3 of it from the
+// outputs' own rounding (in two parts each: 1.7e-3, and twice the work on P and S).
 //
 // Roles, in groups of four warps: forming P (tensor memory to tensor memory, a row per
 // thread), keeping the state and writing its parts for the next chunk, summing the
@@ -40,11 +42,12 @@ using namespace sm100;
 
 constexpr int kC = 128;     // tokens per chunk
 constexpr int kDVT = 64;    // columns of v per block
-// Groups of four warps that form P (every kPG-th block of columns each) and that keep
-// the state (kDVT / kSG columns each).
-constexpr int kPG = 1, kSG = 1;
-constexpr int kWarpS = 4 * kPG, kWarpW = kWarpS + 4 * kSG, kWarpO = kWarpW + 4, kWarpIssue = kWarpO + 4;
+// Warps: four that form P, kSG groups of four that keep the state (kDVT / kSG columns
+// each), and so on.
+constexpr int kSG = 1;
+constexpr int kWarpS = 4, kWarpW = kWarpS + 4 * kSG, kWarpO = kWarpW + 4, kWarpIssue = kWarpO + 4;
 constexpr int kThreads = (kWarpIssue + 4) * 32;
+constexpr int kRing = 3;    // stages of V, which the outputs take over: two of them wait for each other
 constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one that is copied
 constexpr float kPlain = 120.f;  // decays of a block of 32, log 2, that go as products of two factors
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -54,10 +57,10 @@ constexpr uint64_t kDrainNs = 50000;  // a wait's bound once the block has given
 constexpr int kTile = kC * 128;           // 128 rows
 constexpr int kOffQ = 0;                  // 2 stages x 2 halves of d_k
 constexpr int kOffK = kOffQ + 4 * kTile;
-constexpr int kOffV = kOffK + 4 * kTile;  // 2 stages
-constexpr int kOffW = kOffV + 2 * kTile;  // decayed V: high and low parts
-constexpr int kOffS = kOffW + 2 * kTile;  // S^T: high and low parts
-constexpr int kOffSmall = kOffS + 2 * kTile;
+constexpr int kOffV = kOffK + 4 * kTile;  // kRing stages
+constexpr int kOffW = kOffV + kRing * kTile;  // decayed V: high and low parts
+constexpr int kOffS = kOffW + 2 * kTile;      // S^T
+constexpr int kOffSmall = kOffS + kTile;
 
 struct Small {
     // decays of two chunks: sums up to and with a token within its block of 32, their
@@ -65,8 +68,8 @@ struct Small {
     float in[2][kC], inverse[2][kC], total[2][4];
     unsigned mask[2][4];
     int odd[2];             // V has infinities or NaN
-    uint64_t full[2], v_full[2], kq_free[2], v_free[2], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2],
-        o_staged[2], i_full[2];
+    uint64_t full[2], v_full[kRing], kq_free[2], v_free[kRing], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2],
+        o_staged[kRing], i_full[2];
     uint64_t p_free, u_full, u_free, s_ready, o_full;
     uint32_t tmem;
     int abort_flag;
@@ -75,7 +78,7 @@ constexpr int kSmemBytes = kOffSmall + (int)sizeof(Small);
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
 // Tensor memory, 512 columns: Q K^T, then P in its place, x 2 | Q S^T x 2 | P V | U.
-// The parts of P of 32 tokens take the columns of their 32 products: 16 and 16.
+// P of 32 tokens takes the first 16 columns of their 32 products.
 constexpr uint32_t kColP = 0, kColI = 256, kColO = 384, kColU = 448;
 
 // A wait suspends the warp for as long as the hardware lets it; the clock is looked at
@@ -198,11 +201,10 @@ __device__ __forceinline__ uint32_t mend(uint32_t hi, uint32_t lo)
     return lo;
 }
 
-// n pairs of row r from the pair w0.
-__device__ __noinline__ void mend_row(uint8_t *tiles, int r, int w0, int n)
+__device__ __noinline__ void mend_row(uint8_t *tiles, int r)
 {
 #pragma unroll 1
-    for (int w = w0; w < w0 + n; ++w) {
+    for (int w = 0; w < 32; ++w) {
         const uint32_t at = sw128(r, w / 4) + w % 4 * 4;
         uint32_t *lo = reinterpret_cast<uint32_t *>(tiles + kTile + at);
         *lo = mend(*reinterpret_cast<const uint32_t *>(tiles + at), *lo);
@@ -227,17 +229,9 @@ __device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32
     *reinterpret_cast<uint4 *>(tiles + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
-// The parts of P of a row and 32 tokens, buffer p.
-__device__ __forceinline__ void st_p(uint32_t p, int quad, int J, const uint32_t (&hi)[16], const uint32_t (&lo)[16])
-{
-    tmem_st16(lane_addr(p, quad, 32 * J), hi);
-    tmem_st16(lane_addr(p, quad, 32 * J + 16), lo);
-}
-
-// P of one row in the cases that the plain path leaves: tokens that forget, blocks
-// that decay by more than 2^120, and products that are infinite or NaN.  The warp's
-// blocks from `last` down.
-__device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, int last, float scale, const float *in, const float *total,
+// P of one row in the cases that the plain path leaves: tokens that forget, and blocks
+// that decay by more than 2^120.
+__device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, float scale, const float *in, const float *total,
                                         const unsigned *mask)
 {
     const float mine = in[32 * I + lane];
@@ -246,17 +240,9 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, i
     const int first = first_seen(mask[I], lane);
 #pragma unroll 1
     for (int J = I; J >= 0; --J) {
-        if (J > last || (last - J) % kPG) {  // done, or another warp's
-            if (J < I) {
-                sum += total[J];
-                cut = cut || mask[J];
-            }
-            continue;
-        }
         float x[32];
         ld_cols(lane_addr(p, quad, 32 * J), x);
-        uint32_t hi[16], lo[16];
-        f32x2 sign = 0;
+        uint32_t w16[16];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float w = in[32 * J + j];
@@ -265,12 +251,9 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, i
             x[j] = seen && f != 0.f ? x[j] * (f * scale) : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            split(pack2(x[2 * j], x[2 * j + 1]), hi[j], lo[j], sign);
-            lo[j] = mend(hi[j], lo[j]);
-        }
+        for (int j = 0; j < 16; ++j) w16[j] = narrow_pair(x[2 * j], x[2 * j + 1]);
         __syncwarp();
-        st_p(p, quad, J, hi, lo);
+        tmem_st16(lane_addr(p, quad, 32 * J), w16);
         if (J < I) {
             sum += total[J];
             cut = cut || mask[J];
@@ -291,12 +274,11 @@ __device__ __noinline__ void odd_row(uint32_t p, uint32_t o, int quad, int i, in
 #pragma unroll 1
     for (int w = 0; w < 64; ++w) {
         __syncwarp();
-        const uint32_t hi = ld_col(lane_addr(p, quad, w / 16 * 32 + w % 16)), lo = ld_col(lane_addr(p, quad, w / 16 * 32 + 16 + w % 16));
+        const uint32_t pair = ld_col(lane_addr(p, quad, w / 16 * 32 + w % 16));
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
             const int j = 2 * w + e;
-            const float f = e ? __uint_as_float(hi & 0xffff0000u) + __uint_as_float(lo & 0xffff0000u)
-                              : __uint_as_float(hi << 16) + __uint_as_float(lo << 16);
+            const float f = __uint_as_float(e ? pair & 0xffff0000u : pair << 16);
             if (j > i || j < first) continue;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -343,17 +325,19 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.v_full[i], 1);
             mbar_init(&s.kq_free[i], kStates ? 1 : 3);
-            mbar_init(&s.v_free[i], 1);
             mbar_init(&s.dec_ready[i], 4);
-            mbar_init(&s.dec_free[i], 4 * (kStates ? kSG : kPG + kSG + 1));
+            mbar_init(&s.dec_free[i], 4 * (kStates ? kSG : kSG + 2));
             mbar_init(&s.w_ready[i], 4);
             mbar_init(&s.o_free[i], 4);
             mbar_init(&s.qk_full[i], 1);
-            mbar_init(&s.o_staged[i], 4);
             mbar_init(&s.i_full[i], 1);
-            mbar_init(&s.p_ready[i], 4 * kPG);
+            mbar_init(&s.p_ready[i], 4);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.v_free[i], 1);
+            mbar_init(&s.o_staged[i], 4);
         }
         mbar_init(&s.p_free, 1);
         mbar_init(&s.u_full, 1);
@@ -379,9 +363,8 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     const Waiter wait = {abort_flag, a.status};
 
     if (warp < kWarpS) {
-        // ---- P, in the place of Q K^T: a row per thread, every kPG-th block of columns up to its own
+        // ---- P, in the place of Q K^T: a row per thread, blocks of 32 columns up to its own
         if constexpr (!kStates) {
-            const int side = warp >> 2;
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1, I = row_block(quad, c);
@@ -396,43 +379,33 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 wait(&s.qk_full[st], c >> 1);
                 __syncwarp();
                 tc_fence_after();
-                int J = I - side;
-                if (side && J >= 0) sum += s.total[st][J];
+                if (odd) odd_decays(p, quad, I, lane, a.scale, s.in[st], s.total[st], s.mask[st]);
 #pragma unroll 1
-                for (; J >= 0 && !odd; J -= kPG) {
+                for (int J = I; J >= 0 && !odd; --J) {
                     const f32x2 f = dup2(decay_of(sum) * a.scale);
-                    const bool diagonal = J == I;
-                    uint32_t hi[16], lo[16];
-                    f32x2 sign = 0;
+                    const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J]);
+                    float x[32];
+                    ld_cols(lane_addr(p, quad, 32 * J), x);
+                    if (J == I) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float x[16];
-                        const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J + 16 * half]);
-                        ld_cols(lane_addr(p, quad, 32 * J + 16 * half), x);
-                        if (diagonal) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) x[j] = 16 * half + j <= lane ? x[j] : 0.f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 w = inverse[j];
-                            const int e = 8 * half + 2 * j;
-                            split(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), hi[e], lo[e], sign);
-                            split(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), hi[e + 1], lo[e + 1],
-                                  sign);
-                        }
+                        for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
                     }
-                    odd = __any_sync(0xffffffffu, is_odd(sign));
-                    if (odd) break;  // this block's products are still in place
-                    st_p(p, quad, J, hi, lo);
-                    if (J >= kPG)
+                    uint32_t w16[16];
 #pragma unroll
-                        for (int e = 1; e <= kPG; ++e) sum += s.total[st][J - e];
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 w = inverse[j];
+                        float lo, hi;
+                        unpack2(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), lo, hi);
+                        w16[2 * j] = narrow_pair(lo, hi);
+                        unpack2(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), lo, hi);
+                        w16[2 * j + 1] = narrow_pair(lo, hi);
+                    }
+                    tmem_st16(lane_addr(p, quad, 32 * J), w16);
+                    if (J > 0) sum += s.total[st][J - 1];
                 }
-                if (odd) odd_decays(p, quad, I, lane, J, a.scale, s.in[st], s.total[st], s.mask[st]);
                 const uint32_t zero[16] = {};
 #pragma unroll 1
-                for (J = I + kPG - side; J < 4; J += kPG) st_p(p, quad, J, zero, zero);
+                for (int J = I + 1; J < 4; ++J) tmem_st16(lane_addr(p, quad, 32 * J), zero);
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_warp(&s.dec_free[st]);
@@ -485,14 +458,18 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 arrive_warp(&s.u_free);
             }
             if (!kStates && c + 1 < chunks) {
-                if (c >= 0) wait(&s.i_full[st], c >> 1);  // Q S^T of this chunk has read the parts
-                f32x2 sign = 0;
+                if (c >= 0) wait(&s.i_full[st], c >> 1);  // Q S^T of this chunk has read it
 #pragma unroll
                 for (int q = 0; q < kCols / 8 && (mine || c < 0); ++q) {
-                    const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
-                    st_parts(sm + kOffS, t, c0 / 8 + q, x, sign);
+                    uint32_t w16[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float lo, hi;
+                        unpack2(S[4 * q + e], lo, hi);
+                        w16[e] = narrow_pair(lo, hi);
+                    }
+                    *reinterpret_cast<uint4 *>(sm + kOffS + sw128(t, c0 / 8 + q)) = make_uint4(w16[0], w16[1], w16[2], w16[3]);
                 }
-                if (is_odd(sign)) mend_row(sm + kOffS, t, c0 / 2, kCols / 2);
                 fence_async_smem();
                 arrive_warp(&s.s_ready);
             }
@@ -537,10 +514,10 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 sum += s.total[st][J];
             }
             const float w = cut ? 0.f : decay_of(sum);
-            wait(&s.v_full[st], c >> 1);
+            wait(&s.v_full[c % kRing], c / kRing);
             if (n < kC) wait(&s.full[st], c >> 1);  // K's rows past the end, below
             if (c > 0) wait(&s.u_full, c - 1);  // the product has read the last chunk's
-            uint8_t *V = sm + kOffV + st * kTile, *W = sm + kOffW;
+            uint8_t *V = sm + kOffV + c % kRing * kTile, *W = sm + kOffW;
             if (t < n) {
                 f32x2 sign = 0;
 #pragma unroll 1
@@ -559,7 +536,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     }
                 if (is_odd(sign)) {  // infinite or NaN, decayed or not
                     s.odd[st] = 1;
-                    mend_row(W, t, 0, 32);
+                    mend_row(W, t);
                     if (w == 0.f) zero_row(W, t);  // what comes after has forgotten it
                 }
             } else {  // rows past the end may be another sequence's
@@ -603,7 +580,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 wait(&s.i_full[st], c >> 1);
                 wait(&s.o_full, c);
                 tc_fence_after();
-                uint8_t *stage = sm + kOffV + st * kTile;  // V is through, but for odd_row
+                uint8_t *stage = sm + kOffV + c % kRing * kTile;  // V is through, but for odd_row
                 if (odd) {
                     odd_row(tbase + kColP + 128 * st, tbase + kColO, quad, i, first, stage);
                     named_sync(2, 128);
@@ -641,7 +618,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 tc_fence_before();
                 arrive_warp(&s.o_free[st]);
                 fence_async_smem();
-                arrive_warp(&s.o_staged[st]);
+                arrive_warp(&s.o_staged[c % kRing]);
             }
         }
     } else if (warp == kWarpIssue) {
@@ -654,17 +631,15 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 const uint32_t p = tbase + kColP + 128 * st;
                 if (c >= 0) {
                     wait(&s.p_ready[st], c >> 1);
-                    wait(&s.v_full[st], c >> 1);
+                    wait(&s.v_full[c % kRing], c / kRing);
                     if (u.len - c * kC < kC) wait(&s.w_ready[st], c >> 1);  // rows past the end are zero
                     if (c > 0) wait(&s.o_free[st ^ 1], (c - 1) >> 1);
                     tc_fence_after();
-                    const uint64_t v = sdesc_sw128(base + kOffV + st * kTile, kTile, 1024);
+                    const uint64_t v = sdesc_sw128(base + kOffV + c % kRing * kTile, kTile, 1024);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            mma_f16kind_ts(tbase + kColO, p + 32 * (i >> 1) + 16 * part + 8 * (i & 1), v + mn_step(i),
-                                           idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
+                    for (int i = 0; i < 8; ++i)
+                        mma_f16kind_ts(tbase + kColO, p + 32 * (i >> 1) + 8 * (i & 1), v + mn_step(i),
+                                       idesc_bf16_f32(128, 64, 0, 1), i > 0);
                     mma_commit(&s.o_full);
                 }
                 if (c + 2 < chunks) {
@@ -702,7 +677,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                                     idesc_bf16_f32(128, 64, 1, 1), part + i > 0);
                 mma_commit(&s.u_full);
                 mma_commit(&s.kq_free[st]);
-                if (kStates) mma_commit(&s.v_free[st]);
+                if (kStates) mma_commit(&s.v_free[c % kRing]);
             }
         }
     } else if (warp == kWarpIssue + 2) {
@@ -719,11 +694,8 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
                 const uint64_t S = sdesc_sw128(base + kOffS, kTile, 1024);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-                        mma_f16kind(tbase + kColI + 64 * st, q + k_step(i), S + part * (kTile >> 4) + mn_step(i),
-                                    idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
+                for (int i = 0; i < KS; ++i)
+                    mma_f16kind(tbase + kColI + 64 * st, q + k_step(i), S + mn_step(i), idesc_bf16_f32(128, 64, 0, 1), i > 0);
                 mma_commit(&s.kq_free[st]);
                 mma_commit(&s.i_full[st]);
             }
@@ -751,12 +723,12 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             }
         };
         auto load_v = [&](int c) {
-            mbar_arrive_expect_tx(&s.v_full[c & 1], kTile);
-            tma_load_3d(sm + kOffV + (c & 1) * kTile, &tm_v, &s.v_full[c & 1], v0, h, row(c));
+            mbar_arrive_expect_tx(&s.v_full[c % kRing], kTile);
+            tma_load_3d(sm + kOffV + c % kRing * kTile, &tm_v, &s.v_full[c % kRing], v0, h, row(c));
             if (c + kAhead < chunks) fetch_l2(&tm_v, v0, h, row(c + kAhead));
         };
 #pragma unroll 1
-        for (int c = 0; c < 2 && c < chunks; ++c) load_v(c);
+        for (int c = 0; c < kRing && c < chunks; ++c) load_v(c);
         int kq = 0, put = 0;  // chunks loaded; chunks whose V is through and whose outputs are stored
         uint64_t idle = 0;    // since when there is nothing to do
         while ((kq < chunks || put < chunks) && !*abort_flag) {
@@ -767,13 +739,13 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 ++kq;
                 moved = true;
             }
-            if (put < chunks && mbar_test_wait(kStates ? &s.v_free[put & 1] : &s.o_staged[put & 1], put >> 1 & 1)) {
+            if (put < chunks && mbar_test_wait(kStates ? &s.v_free[put % kRing] : &s.o_staged[put % kRing], put / kRing & 1)) {
                 if (!kStates && u.len - put * kC >= kC) {
-                    tma_store_3d(&tm_o, sm + kOffV + (put & 1) * kTile, v0, h, row(put));
+                    tma_store_3d(&tm_o, sm + kOffV + put % kRing * kTile, v0, h, row(put));
                     bulk_commit();
                     bulk_wait_read();
                 }
-                if (put + 2 < chunks) load_v(put + 2);
+                if (put + kRing < chunks) load_v(put + kRing);
                 ++put;
                 moved = true;
             }
