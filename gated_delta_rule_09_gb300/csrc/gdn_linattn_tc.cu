@@ -69,7 +69,8 @@ struct Small {
     unsigned mask[2][4];
     int odd[2];             // V has infinities or NaN
     uint64_t full[2], v_full[kRing], kq_free[2], v_free[kRing], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2],
-        o_staged[kRing], i_full[2];
+        o_staged[kRing], i_full[2],
+        w_half[2], w_gone[2];
     uint64_t p_free, u_full, u_free, s_ready, o_full;
     uint32_t tmem;
     int abort_flag;
@@ -332,6 +333,8 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             mbar_init(&s.o_free[i], 4);
             mbar_init(&s.qk_full[i], 1);
             mbar_init(&s.i_full[i], 1);
+            mbar_init(&s.w_half[i], 2);
+            mbar_init(&s.w_gone[i], 1);
             mbar_init(&s.p_ready[i], 4);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -516,7 +519,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             const float w = cut ? 0.f : decay_of(sum);
             wait(&s.v_full[c % kRing], c / kRing);
             if (n < kC) wait(&s.full[st], c >> 1);  // K's rows past the end, below
-            if (c > 0) wait(&s.u_full, c - 1);  // the product has read the last chunk's
+            if (c > 0) wait(&s.w_gone[quad >> 1], c - 1);  // the product has read the last chunk's
             uint8_t *V = sm + kOffV + c % kRing * kTile, *W = sm + kOffW;
             if (t < n) {
                 f32x2 sign = 0;
@@ -552,6 +555,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             }
             fence_async_smem();
+            arrive_warp(&s.w_half[quad >> 1]);
             arrive_warp(&s.w_ready[st]);
         }
     } else if (warp < kWarpIssue) {
@@ -664,17 +668,22 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
                 wait(&s.full[st], c >> 1);
-                wait(&s.w_ready[st], c >> 1);
                 if (c > 0) wait(&s.u_free, c - 1);
-                tc_fence_after();
                 const uint64_t k = sdesc_sw128(base + kOffK + st * 2 * kTile, kTile, 1024);
                 const uint64_t w = sdesc_sw128(base + kOffW, kTile, 1024);
+                // 64 tokens at a time: the next chunk's take their place while the others are still read
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                for (int half = 0; half < 2; ++half) {
+                    wait(&s.w_half[half], c);
+                    tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mma_f16kind(tbase + kColU, k + mn_step(i), w + part * (kTile >> 4) + mn_step(i),
-                                    idesc_bf16_f32(128, 64, 1, 1), part + i > 0);
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int i = 4 * half; i < 4 * half + 4; ++i)
+                            mma_f16kind(tbase + kColU, k + mn_step(i), w + part * (kTile >> 4) + mn_step(i),
+                                        idesc_bf16_f32(128, 64, 1, 1), half + part + i > 0);
+                    mma_commit(&s.w_gone[half]);
+                }
                 mma_commit(&s.u_full);
                 mma_commit(&s.kq_free[st]);
                 if (kStates) mma_commit(&s.v_free[c % kRing]);
