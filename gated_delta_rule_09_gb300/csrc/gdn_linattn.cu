@@ -33,6 +33,21 @@ template <int DK> struct Smem {
     float all;
 };
 
+// kC rows of W columns to shared memory, zeros past n rows and `cols` columns.  All of
+// a thread's loads are in flight together.
+template <typename E, int W>
+__device__ __forceinline__ void rows(float (*to)[W + 4], const E *from, int64_t ld, int n, int cols)
+{
+    constexpr int kStep = kThreads / W, kLoads = kC / kStep;
+    const int c = threadIdx.x % W, r0 = threadIdx.x / W;
+    E x[kLoads];
+    from += r0 * ld + c;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i, from += kStep * ld) x[i] = r0 + i * kStep < n && c < cols ? *from : from_f<E>(0.f);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) to[r0 + i * kStep][c] = to_f(x[i]);
+}
+
 template <typename E, int DK>
 __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinattnArgs a, int tiles, int states_only)
 {
@@ -60,16 +75,9 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
     for (int c = 0; c < u.len; c += kC) {
         const int n = min(kC, u.len - c);
         __syncthreads();
-        for (int i = t; i < kC * DK; i += kThreads) {
-            const int r = i / DK, kk = i % DK;
-            const bool is = r < n && kk < dk;
-            if (!states_only) m.q[r][kk] = is ? to_f(q[(c + r) * a.ld_q + kk]) : 0.f;
-            m.k[r][kk] = is ? to_f(k[(c + r) * a.ld_k + kk]) : 0.f;
-        }
-        for (int i = t; i < kC * kDVT; i += kThreads) {
-            const int r = i / kDVT, d = i % kDVT;
-            m.v[r][d] = r < n && d < nv ? to_f(v[(c + r) * a.ld_v + d]) : 0.f;
-        }
+        rows<E, DK>(m.k, k + c * a.ld_k, a.ld_k, n, dk);
+        rows<E, kDVT>(m.v, v + c * a.ld_v, a.ld_v, n, nv);
+        if (!states_only) rows<E, DK>(m.q, q + c * a.ld_q, a.ld_q, n, dk);
         if (t < 32) {
             Decays d;
             d.scan(lane < n ? decay[(c + lane) * a.ld_decay] : 0.f);
@@ -390,15 +398,50 @@ cudaError_t pass(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 
 }  // namespace
 
+// Whole sequences or pieces.  Times of the tensor-core kernel on one multiprocessor,
+// us per chunk of 128 tokens and beside them (one document of 131 072 tokens x 8
+// heads: whole 1743, 9 pieces 369; 4096 tokens x 16 heads: whole 65, 4 pieces 50; 1024
+// tokens x 8 heads: whole 26, 2 pieces 40).  Pieces are chosen to fill the
+// multiprocessors once, twice or three times.
 void gdn_linattn_plan(int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment, int64_t *piece_slots)
 {
+    constexpr double kWhole = 1.7, kWholeStart = 10, kCut = 3.0, kCutStart = 26, kBytesPerUs = 6e6;
+    constexpr int64_t kChunk = 128, kLeast = 4;  // chunks of a piece
     *segment = 0;
     *piece_slots = 0;
-    if (asked <= 0) return;
-    const int seg = (int)(((int64_t)asked + 127) / 128 * 128);
-    if (seg >= T) return;
-    *segment = seg;
-    *piece_slots = packed ? (int64_t)T / seg + N : (int64_t)N * (((int64_t)T + seg - 1) / seg);
+    if (N < 1 || T < 1) return;
+    int64_t seg = ((int64_t)asked + kChunk - 1) / kChunk;
+    if (asked <= 0) {
+        const int sms = gdn_ssm_sms();
+        const bool uneven = packed && N > 1;
+        const int64_t per = (int64_t)heads * ((dv + 63) / 64), seqs = uneven ? 1 : N;
+        // a packed sequence may be the longest by far; twice the mean is taken for it
+        const int64_t all = (T + kChunk - 1) / kChunk, longest = uneven ? (2 * all + N - 1) / N : all;
+        const double share = (double)all * seqs * per / sms;  // chunks per multiprocessor
+        auto waves = [&](int64_t blocks) { return (double)((blocks + sms - 1) / sms); };
+        const double chain = (double)heads * dk * dv * 16 / kBytesPerUs;  // per piece: its state written, read, written, read
+        double best = kWholeStart + kWhole * (!uneven ? waves(N * per) * all : share > longest ? share : longest);
+        seg = all;
+        for (int k = 1; k <= 3; ++k) {
+            int64_t s = uneven ? (int64_t)(share / k) + 1 : (all * N * per + (int64_t)k * sms - 1) / ((int64_t)k * sms);
+            if (!uneven) {  // as many pieces of a sequence as fit
+                const int64_t p = (int64_t)k * sms / (N * per);
+                if (p < 2) continue;
+                s = (all + p - 1) / p;
+            }
+            if (s < kLeast) s = kLeast;
+            if (s >= longest) continue;
+            const int64_t pieces = uneven ? all / s + N : N * ((all + s - 1) / s);
+            const double t = kCutStart + chain * pieces + kCut * (uneven ? share + s : waves(pieces * per) * s);
+            if (t < best) {
+                best = t;
+                seg = s;
+            }
+        }
+    }
+    if (seg * kChunk >= T) return;
+    *segment = (int)(seg * kChunk);
+    *piece_slots = packed ? (int64_t)T / *segment + N : (int64_t)N * (((int64_t)T + *segment - 1) / *segment);
 }
 
 cudaError_t gdn_launch_linattn_fwd(const GdnLinattnArgs &a, cudaStream_t s, int *launches)
