@@ -53,7 +53,7 @@ SIGNATURES = {
     "gdn_ssm_step": (ctypes.c_int, [_vp] * 12 + [_i] * 4 + [_l] * 6 + [_i, _i, _i, _vp]),
     "gdn_group_norm": (ctypes.c_int, [_vp] * 5 + [_l, _i, _i, _l, _l, _l, ctypes.c_float,
                                                   _i, _i, _i, _vp]),
-    "gdn_linattn_fwd_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i, _i, _vp, _i]),
+    "gdn_linattn_fwd_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i, _i, _vp, _i, _i]),
     "gdn_linattn_fwd": (ctypes.c_int, [_vp] * 8 + [_i] * 6 + [_l] * 5
                         + [_i, _vp, ctypes.c_float, _i, _i, _vp, ctypes.c_size_t, _vp]),
     "gdn_linattn_step": (ctypes.c_int, [_vp] * 8 + [_i] * 5 + [_l] * 5

@@ -99,8 +99,8 @@ struct GdnLinattnArgs {
     float *piece_decay;          // [piece slot, heads] decay over the piece
 };
 
-// Pieces a call is cut into, as gdn_ssm_plan; no more slots for a larger dv or other strides.
-void gdn_linattn_plan(int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment,
+// Pieces a call is cut into, as gdn_ssm_plan, by the kernel it runs on.
+void gdn_linattn_plan(bool tensor_cores, int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment,
                       int64_t *piece_slots);
 cudaError_t gdn_launch_linattn_fwd(const GdnLinattnArgs &a, cudaStream_t s, int *launches);
 cudaError_t gdn_launch_linattn_step(const GdnLinattnArgs &a, cudaStream_t s);

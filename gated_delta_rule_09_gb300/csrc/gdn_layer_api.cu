@@ -262,9 +262,9 @@ gdn_status_t check_linattn(bool step, GdnLinattnArgs &a, int dtype, bool *nothin
     if (step && a.N > 0 && !a.state_out)
         return gdn_fail(GDN_ERR_INVALID_ARG, "state_out must be non-NULL");
     GDN_TRY(check_pool(a.state_in, a.state_out, a.slots, a.N, a.pool));
-    // Blocks are numbered in 31 bits: one per sequence, head and 64 columns of v.
-    if ((double)a.N * a.heads * ((a.dv + 63) / 64) > 0x7fffffff)
-        return gdn_fail(GDN_ERR_UNSUPPORTED, "%d sequences x %d heads x %d (supported: up to 2^31 - 1 tiles of 64)",
+    // Blocks are numbered in 31 bits: one per sequence, head and 32 columns of v.
+    if ((double)a.N * a.heads * ((a.dv + 31) / 32) > 0x7fffffff)
+        return gdn_fail(GDN_ERR_UNSUPPORTED, "%d sequences x %d heads x %d (supported: up to 2^31 - 1 tiles of 32)",
                         a.N, a.heads, a.dv);
     View v[kLinViews];
     linattn_views(a, rows, v);
@@ -296,10 +296,10 @@ size_t linattn_workspace(int64_t slots, int heads, int dk, int dv)
 
 gdn_status_t take_workspace(GdnLinattnArgs &a, int asked, void *workspace, size_t bytes)
 {
-    gdn_linattn_plan(a.N, a.T, a.heads, a.dk, a.dv, a.cu_seqlens != nullptr, asked, &a.segment, &a.pieces);
+    gdn_linattn_plan(gdn_linattn_tc_supported(a), a.N, a.T, a.heads, a.dk, a.dv, a.cu_seqlens != nullptr, asked, &a.segment, &a.pieces);
     if (!a.segment) return GDN_OK;
-    if ((double)a.pieces * a.heads * ((a.dv + 63) / 64) > 0x7fffffff)
-        return gdn_fail(GDN_ERR_UNSUPPORTED, "%lld pieces x %d heads x %d (supported: up to 2^31 - 1 tiles of 64)",
+    if ((double)a.pieces * a.heads * ((a.dv + 31) / 32) > 0x7fffffff)
+        return gdn_fail(GDN_ERR_UNSUPPORTED, "%lld pieces x %d heads x %d (supported: up to 2^31 - 1 tiles of 32)",
                         (long long)a.pieces, a.heads, a.dv);
     const size_t need = linattn_workspace(a.pieces, a.heads, a.dk, a.dv);
     if (!workspace || bytes < need)
@@ -439,13 +439,19 @@ gdn_status_t gdn_group_norm(const void *x, const void *gate, const float *weight
 }
 
 size_t gdn_linattn_fwd_workspace_size(int B, int T, int heads, int d_k, int d_v,
-                                      const int32_t *cu_seqlens, int segment)
+                                      const int32_t *cu_seqlens, int segment, int tensor_cores)
 {
     if (B < 1 || T < 1 || heads < 1 || d_k < 1 || d_k > 128 || d_v < 1) return 0;
-    int seg = 0;
-    int64_t slots = 0;
-    gdn_linattn_plan(B, T, heads, d_k, d_v, cu_seqlens != nullptr, segment, &seg, &slots);
-    return seg ? linattn_workspace(slots, heads, d_k, d_v) : 0;
+    size_t most = 0;
+    for (int tc = 0; tc < 2; ++tc) {
+        if (tensor_cores >= 0 && (tensor_cores != 0) != (tc != 0)) continue;
+        int seg = 0;
+        int64_t slots = 0;
+        gdn_linattn_plan(tc != 0, B, T, heads, d_k, d_v, cu_seqlens != nullptr, segment, &seg, &slots);
+        const size_t need = seg ? linattn_workspace(slots, heads, d_k, d_v) : 0;
+        if (need > most) most = need;
+    }
+    return most;
 }
 
 gdn_status_t gdn_linattn_fwd(const void *q, const void *k, const void *v, const float *log_decay,

@@ -21,66 +21,87 @@ namespace {
 using namespace gdn_linattn;
 
 constexpr int kC = 32;        // tokens per chunk: one warp's worth of decays
-constexpr int kDVT = 64;      // columns of v per block
 constexpr int kThreads = 256;
-constexpr int kLdS = kDVT + 4;
 
-template <int DK> struct Smem {
-    float q[kC][DK + 4], k[kC][DK + 4], v[kC][kLdS], P[kC][kC + 1];
-    float S[DK][kLdS];        // the state's slice, transposed
+// Tiles of a block: DK columns of q and k (d_k filled up with zeros), DV of v.
+template <int DK, int DV> struct Smem {
+    float q[kC][DK + 4], k[kC][DK + 4], v[kC][DV + 4], P[kC][kC + 1];
+    float S[DK][DV + 4];      // the state's slice, transposed
     float in[kC], start[kC], add[kC];
     int first[kC];
     float all;
 };
 
-// kC rows of W columns to shared memory, zeros past n rows and `cols` columns.  All of
-// a thread's loads are in flight together.
-template <typename E, int W>
-__device__ __forceinline__ void rows(float (*to)[W + 4], const E *from, int64_t ld, int n, int cols)
-{
-    constexpr int kStep = kThreads / W, kLoads = kC / kStep;
-    const int c = threadIdx.x % W, r0 = threadIdx.x / W;
+// kC rows of W columns, on their way from memory: all of a thread's loads are in
+// flight together.  Zeros past n rows and `cols` columns.
+template <typename E, int W> struct Rows {
+    static constexpr int kLoads = (kC * W + kThreads - 1) / kThreads;
     E x[kLoads];
-    from += r0 * ld + c;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i, from += kStep * ld) x[i] = r0 + i * kStep < n && c < cols ? *from : from_f<E>(0.f);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) to[r0 + i * kStep][c] = to_f(x[i]);
-}
 
-template <typename E, int DK>
+    __device__ __forceinline__ void load(const E *from, int64_t ld, int n, int cols)
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int e = threadIdx.x + i * kThreads, r = e / W, c = e % W;
+            x[i] = r < n && c < cols ? from[r * ld + c] : from_f<E>(0.f);
+        }
+    }
+    __device__ __forceinline__ void store(float (*to)[W + 4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            if (kC * W % kThreads == 0 || e < kC * W) to[e / W][e % W] = to_f(x[i]);
+        }
+    }
+};
+
+// Two and two blocks per multiprocessor; the next chunk's rows are loaded while this
+// one's are worked on.
+template <typename E, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinattnArgs a, int tiles, int states_only)
 {
     extern __shared__ __align__(16) uint8_t raw[];
-    Smem<DK> &m = *reinterpret_cast<Smem<DK> *>(raw);
+    Smem<DK, DV> &m = *reinterpret_cast<Smem<DK, DV> *>(raw);
     const int t = threadIdx.x, lane = t & 31;
     const int64_t unit = blockIdx.x;
-    const int v0 = (int)(unit % tiles) * kDVT, h = (int)(unit / tiles % a.heads);
+    const int v0 = (int)(unit % tiles) * DV, h = (int)(unit / tiles % a.heads);
     Unit u;
     if (!find_unit(a, unit / tiles / a.heads, h, states_only, u)) return;
-    const int dk = a.dk, nv = min(kDVT, a.dv - v0), g = h / (a.heads / a.groups);
+    const int dk = a.dk, nv = min(DV, a.dv - v0), g = h / (a.heads / a.groups);
     const E *q = static_cast<const E *>(a.q) + u.row * a.ld_q + (int64_t)g * dk;
     const E *k = static_cast<const E *>(a.k) + u.row * a.ld_k + (int64_t)g * dk;
     const E *v = static_cast<const E *>(a.v) + u.row * a.ld_v + (int64_t)h * a.dv + v0;
     const float *decay = a.log_decay + u.row * a.ld_decay + h;
     E *o = static_cast<E *>(a.o) + u.row * a.ld_o + (int64_t)h * a.dv + v0;
 
-    for (int i = t; i < DK * kDVT; i += kThreads) {  // d_k along the lanes, as the state lies
+    Rows<E, DK> qr, kr;
+    Rows<E, DV> vr;
+    float decay_next = 0.f;
+    auto load = [&](int c) {
+        const int n = u.len - c;
+        kr.load(k + c * a.ld_k, a.ld_k, n, dk);
+        vr.load(v + c * a.ld_v, a.ld_v, n, nv);
+        if (!states_only) qr.load(q + c * a.ld_q, a.ld_q, n, dk);
+        if (t < 32) decay_next = lane < n ? decay[(int64_t)(c + lane) * a.ld_decay] : 0.f;
+    };
+    load(0);
+    for (int i = t; i < DK * DV; i += kThreads) {  // d_k along the lanes, as the state lies
         const int kk = i % DK, d = i / DK;
         m.S[kk][d] = u.in && kk < dk && d < nv ? u.in[(int64_t)(v0 + d) * dk + kk] : 0.f;
     }
-    const int i0 = t / 16 * 2, j0 = t % 16 * 2, d0 = t % 16 * 4;  // 2 x 2 of P, 2 x 4 of o
-    constexpr int KP = DK / 32;
-    const int k0 = t / 8 * KP, e0 = t % 8 * 8;                    // KP x 8 of S
+    constexpr int OV = DV / 16, SV = DV / 8, KP = DK / 32;
+    const int i0 = t / 16 * 2, j0 = t % 16 * 2, d0 = t % 16 * OV;  // 2 x 2 of P, 2 x OV of o
+    const int k0 = t / 8 * KP, e0 = t % 8 * SV;                    // KP x SV of S
     for (int c = 0; c < u.len; c += kC) {
         const int n = min(kC, u.len - c);
         __syncthreads();
-        rows<E, DK>(m.k, k + c * a.ld_k, a.ld_k, n, dk);
-        rows<E, kDVT>(m.v, v + c * a.ld_v, a.ld_v, n, nv);
-        if (!states_only) rows<E, DK>(m.q, q + c * a.ld_q, a.ld_q, n, dk);
+        kr.store(m.k);
+        vr.store(m.v);
+        if (!states_only) qr.store(m.q);
         if (t < 32) {
             Decays d;
-            d.scan(lane < n ? decay[(c + lane) * a.ld_decay] : 0.f);
+            d.scan(decay_next);
             m.in[lane] = d.in;
             m.first[lane] = first_seen(d.mask, lane);
             m.start[lane] = d.cut_upto(lane) ? 0.f : decay_of(d.in);
@@ -88,94 +109,111 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             if (lane == 0) m.all = d.mask ? 0.f : decay_of(d.total);
         }
         __syncthreads();
-        float acc[2][4] = {};
+        load(c + kC);
+        float acc[2][OV] = {};
         if (!states_only) {
             if (j0 <= i0 + 1) {
-                float p[2][2] = {};
-#pragma unroll 8
-                for (int kk = 0; kk < DK; kk += 4) {
-                    const float4 q0 = *reinterpret_cast<const float4 *>(&m.q[i0][kk]);
-                    const float4 q1 = *reinterpret_cast<const float4 *>(&m.q[i0 + 1][kk]);
-                    const float4 k0 = *reinterpret_cast<const float4 *>(&m.k[j0][kk]);
-                    const float4 k1 = *reinterpret_cast<const float4 *>(&m.k[j0 + 1][kk]);
-                    p[0][0] += q0.x * k0.x + q0.y * k0.y + q0.z * k0.z + q0.w * k0.w;
-                    p[0][1] += q0.x * k1.x + q0.y * k1.y + q0.z * k1.z + q0.w * k1.w;
-                    p[1][0] += q1.x * k0.x + q1.y * k0.y + q1.z * k0.z + q1.w * k0.w;
-                    p[1][1] += q1.x * k1.x + q1.y * k1.y + q1.z * k1.z + q1.w * k1.w;
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int i = i0 + x, j = j0 + y;
-                        m.P[i][j] = j <= i && j >= m.first[i] ? p[x][y] * decay_of(m.in[i] - m.in[j]) : 0.f;
-                    }
-            }
+                f32x2 p[2][2] = {};
 #pragma unroll 4
+                for (int kk = 0; kk < DK; kk += 4) {
+                    float4 x[2], y[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = *reinterpret_cast<const float4 *>(&m.q[i0 + e][kk]);
+                        y[e] = *reinterpret_cast<const float4 *>(&m.k[j0 + e][kk]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            p[e][f] = fma2(pack2(x[e].x, x[e].y), pack2(y[f].x, y[f].y), p[e][f]);
+                            p[e][f] = fma2(pack2(x[e].z, x[e].w), pack2(y[f].z, y[f].w), p[e][f]);
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const int i = i0 + e, j = j0 + f;
+                        float lo, hi;
+                        unpack2(p[e][f], lo, hi);
+                        m.P[i][j] = j <= i && j >= m.first[i] ? (lo + hi) * decay_of(m.in[i] - m.in[j]) : 0.f;
+                    }
+            }
+#pragma unroll 2
             for (int kk = 0; kk < DK; kk += 4) {
-                float q0[4], q1[4], s[4][4];
-                ld_vec<float, 4>(&m.q[i0][kk], q0);
-                ld_vec<float, 4>(&m.q[i0 + 1][kk], q1);
+                float x[2][4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    ld_vec<float, 4>(&m.S[kk + x][d0], s[x]);
+                for (int e = 0; e < 2; ++e) ld_vec<float, 4>(&m.q[i0 + e][kk], x[e]);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        acc[0][y] = fmaf(q0[x], s[x][y], acc[0][y]);
-                        acc[1][y] = fmaf(q1[x], s[x][y], acc[1][y]);
+                for (int f = 0; f < 4; ++f) {
+                    float s[OV];
+                    ld_vec<float, OV>(&m.S[kk + f][d0], s);
+#pragma unroll
+                    for (int y = 0; y < OV; ++y) {
+                        acc[0][y] = fmaf(x[0][f], s[y], acc[0][y]);
+                        acc[1][y] = fmaf(x[1][f], s[y], acc[1][y]);
                     }
                 }
             }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float w = m.start[i0 + x];
+            for (int e = 0; e < 2; ++e) {
+                const float w = m.start[i0 + e];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) acc[x][y] = w == 0.f ? 0.f : w * acc[x][y];
+                for (int y = 0; y < OV; ++y) acc[e][y] = w == 0.f ? 0.f : w * acc[e][y];
             }
         }
         __syncthreads();
         if (!states_only) {
-            for (int j = 0; j <= i0 + 1; ++j) {
-                float w[4];
-                ld_vec<float, 4>(&m.v[j][d0], w);
+            // a token sees nothing of those behind it, infinite or not
+#pragma unroll 4
+            for (int j = 0; j <= i0; ++j) {
+                float w[OV];
+                ld_vec<float, OV>(&m.v[j][d0], w);
                 const float p0 = m.P[i0][j], p1 = m.P[i0 + 1][j];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {  // a token sees nothing of those behind it, infinite or not
-                    acc[0][y] = j <= i0 ? fmaf(p0, w[y], acc[0][y]) : acc[0][y];
+                for (int y = 0; y < OV; ++y) {
+                    acc[0][y] = fmaf(p0, w[y], acc[0][y]);
                     acc[1][y] = fmaf(p1, w[y], acc[1][y]);
                 }
             }
+            float w[OV];
+            ld_vec<float, OV>(&m.v[i0 + 1][d0], w);
+            const float p1 = m.P[i0 + 1][i0 + 1];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int y = 0; y < OV; ++y) acc[1][y] = fmaf(p1, w[y], acc[1][y]);
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    if (i0 + x < n && d0 + y < nv) o[(c + i0 + x) * a.ld_o + d0 + y] = from_f<E>(a.scale * acc[x][y]);
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int y = 0; y < OV; ++y)
+                    if (i0 + e < n && d0 + y < nv) o[(c + i0 + e) * a.ld_o + d0 + y] = from_f<E>(a.scale * acc[e][y]);
         }
-        float s[KP][8] = {};
+        float s[KP][SV] = {};
+#pragma unroll 2
         for (int j = 0; j < n; ++j) {
-            float kk[KP], w[8];
-            ld_vec<float, KP>(&m.k[j][k0], kk);
-            ld_vec<float, 8>(&m.v[j][e0], w);
+            float w[SV];
+            ld_vec<float, SV>(&m.v[j][e0], w);
             const float f = m.add[j];
 #pragma unroll
             for (int x = 0; x < KP; ++x) {
-                const float fk = f * kk[x];
+                const float fk = f * m.k[j][k0 + x];
 #pragma unroll
-                for (int y = 0; y < 8; ++y) s[x][y] = fmaf(fk, w[y], s[x][y]);
+                for (int y = 0; y < SV; ++y) s[x][y] = fmaf(fk, w[y], s[x][y]);
             }
         }
         const float all = m.all;
 #pragma unroll
-        for (int x = 0; x < KP; ++x)
+        for (int x = 0; x < KP; ++x) {
+            float S[SV];
+            ld_vec<float, SV>(&m.S[k0 + x][e0], S);
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                float &S = m.S[k0 + x][e0 + y];
-                S = all == 0.f ? s[x][y] : fmaf(all, S, s[x][y]);
-            }
+            for (int y = 0; y < SV; ++y) S[y] = all == 0.f ? s[x][y] : fmaf(all, S[y], s[x][y]);
+            st_vec<float, SV>(&m.S[k0 + x][e0], S);
+        }
     }
     __syncthreads();
     if (u.out)
-        for (int i = t; i < DK * kDVT; i += kThreads) {
+        for (int i = t; i < DK * DV; i += kThreads) {
             const int kk = i % DK, d = i / DK;
             if (kk < dk && d < nv) u.out[(int64_t)(v0 + d) * dk + kk] = m.S[kk][d];
         }
@@ -377,36 +415,58 @@ template <typename E> cudaError_t step_by_width(const GdnLinattnArgs &a, cudaStr
 
 int64_t spans(const GdnLinattnArgs &a) { return a.segment ? a.pieces : a.N; }
 
-template <typename E, int DK> cudaError_t simt(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
+template <typename E, int DK, int DV> cudaError_t simt_of(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 {
-    const int tiles = (a.dv + kDVT - 1) / kDVT;
+    const int tiles = (a.dv + DV - 1) / DV;
     const int64_t blocks = spans(a) * a.heads * tiles;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = cudaFuncSetAttribute(gdn_linattn_kernel<E, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sizeof(Smem<DK>));
+    const cudaError_t e = cudaFuncSetAttribute(gdn_linattn_kernel<E, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)sizeof(Smem<DK, DV>));
     if (e != cudaSuccess) return e;
-    gdn_linattn_kernel<E, DK><<<(unsigned)blocks, kThreads, sizeof(Smem<DK>), s>>>(a, tiles, states_only);
+    gdn_linattn_kernel<E, DK, DV><<<(unsigned)blocks, kThreads, sizeof(Smem<DK, DV>), s>>>(a, tiles, states_only);
     return cudaGetLastError();
+}
+
+// 32 columns of v per block where 64 would leave room for more blocks (4 x 4096 tokens
+// x 16 heads fp32: 256 blocks instead of 128).
+template <typename E, int DK> cudaError_t simt(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
+{
+    const int64_t blocks = spans(a) * a.heads * ((a.dv + 63) / 64);
+    return a.dv <= 32 || blocks < 2 * gdn_ssm_sms() ? simt_of<E, DK, 32>(a, states_only, s) : simt_of<E, DK, 64>(a, states_only, s);
+}
+
+template <typename E> cudaError_t simt_by_width(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
+{
+    if (a.dk <= 32) return simt<E, 32>(a, states_only, s);
+    if (a.dk <= 64) return simt<E, 64>(a, states_only, s);
+    if (a.dk <= 96) return simt<E, 96>(a, states_only, s);
+    return simt<E, 128>(a, states_only, s);
 }
 
 cudaError_t pass(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 {
     if (gdn_linattn_tc_supported(a)) return gdn_linattn_tc(a, states_only, s);
-    if (a.dtype == 1) return a.dk > 64 ? simt<__nv_bfloat16, 128>(a, states_only, s) : simt<__nv_bfloat16, 64>(a, states_only, s);
-    return a.dk > 64 ? simt<float, 128>(a, states_only, s) : simt<float, 64>(a, states_only, s);
+    return a.dtype == 1 ? simt_by_width<__nv_bfloat16>(a, states_only, s) : simt_by_width<float>(a, states_only, s);
 }
 
 }  // namespace
 
-// Whole sequences or pieces.  Times of the tensor-core kernel on one multiprocessor,
-// us per chunk of 128 tokens and beside them (one document of 131 072 tokens x 8
-// heads: whole 1743, 9 pieces 369; 4096 tokens x 16 heads: whole 65, 4 pieces 50; 1024
-// tokens x 8 heads: whole 26, 2 pieces 40).  Pieces are chosen to fill the
-// multiprocessors once, twice or three times.
-void gdn_linattn_plan(int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment, int64_t *piece_slots)
+// Whole sequences or pieces: the quicker by what was measured, us per chunk of 128
+// tokens of a block that has a multiprocessor to itself, and beside all chunks.
+// Tensor cores: one document of 131 072 tokens x 8 heads whole 1743, 9 pieces 370; 4096
+// tokens x 16 heads whole 65, 4 pieces 50; 1024 tokens x 8 heads whole 26, 2 pieces 40.
+// CUDA cores: 517 tokens x 2 heads whole 124, 5 pieces 64; 3 x 517 tokens x 6 heads of
+// 77 and 45 whole 207, pieces of 128 69; 4 x 4096 tokens x 16 heads of 64 whole 543, 2
+// pieces 702.  Pieces are chosen to fill the multiprocessors once, twice or three times.
+void gdn_linattn_plan(bool tensor_cores, int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment,
+                      int64_t *piece_slots)
 {
-    constexpr double kWhole = 1.7, kWholeStart = 10, kCut = 3.0, kCutStart = 26, kBytesPerUs = 6e6;
-    constexpr int64_t kChunk = 128, kLeast = 4;  // chunks of a piece
+    const double wide = 0.3 + 0.7 * ((dk + 31) / 32) / 4;  // tiles of d_k on CUDA cores
+    const double kWhole = tensor_cores ? 1.7 : 24 * wide, kWholeStart = 10;
+    const double kCut = tensor_cores ? 3.0 : 36 * wide, kCutStart = 26;
+    constexpr double kBytesPerUs = 6e6;
+    constexpr int64_t kChunk = 128;
+    const int64_t least = tensor_cores ? 4 : 1;  // chunks of a piece
     *segment = 0;
     *piece_slots = 0;
     if (N < 1 || T < 1) return;
@@ -414,7 +474,7 @@ void gdn_linattn_plan(int N, int T, int heads, int dk, int dv, bool packed, int 
     if (asked <= 0) {
         const int sms = gdn_ssm_sms();
         const bool uneven = packed && N > 1;
-        const int64_t per = (int64_t)heads * ((dv + 63) / 64), seqs = uneven ? 1 : N;
+        const int64_t per = (int64_t)heads * (tensor_cores ? (dv + 63) / 64 : (dv + 31) / 32), seqs = uneven ? 1 : N;
         // a packed sequence may be the longest by far; twice the mean is taken for it
         const int64_t all = (T + kChunk - 1) / kChunk, longest = uneven ? (2 * all + N - 1) / N : all;
         const double share = (double)all * seqs * per / sms;  // chunks per multiprocessor
@@ -429,7 +489,7 @@ void gdn_linattn_plan(int N, int T, int heads, int dk, int dv, bool packed, int 
                 if (p < 2) continue;
                 s = (all + p - 1) / p;
             }
-            if (s < kLeast) s = kLeast;
+            if (s < least) s = least;
             if (s >= longest) continue;
             const int64_t pieces = uneven ? all / s + N : N * ((all + s - 1) / s);
             const double t = kCutStart + chain * pieces + kCut * (uneven ? share + s : waves(pieces * per) * s);

@@ -72,6 +72,12 @@ def _rows(name, t, dtype, index, shape, inner=1):
     return ld
 
 
+def _dense(t, dtype, index, shape):
+    """Whether an argument is all that ``_param`` and ``_rows`` ask for, and contiguous."""
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous())
+
+
 def _empty(stream, like, shape=None, dtype=None):
     """A new tensor that belongs to the stream the call runs on."""
     if stream is None:
@@ -344,20 +350,25 @@ def gdn_group_norm(x, groups, weight=None, bias=None, gate=None, y=None, eps=1e-
 def _linattn_params(q, k, v, log_decay, index, dtype):
     """Checks shared by prompts and steps: (heads, groups, d_k, d_v, row strides
     of q, k, v and log_decay)."""
-    lead, (H, dv) = v.shape[:-2], v.shape[-2:]
-    if not isinstance(q, torch.Tensor) or q.dim() != v.dim():
+    shape = v.shape
+    lead, H, dv = shape[:-2], shape[-2], shape[-1]
+    if not isinstance(q, torch.Tensor) or q.dim() != len(shape):
         raise ValueError("q and k must be [..., groups, d_k]")
-    G, dk = q.shape[-2:]
-    qk = lead + (G, dk)
+    qk = q.shape
+    G, dk = qk[-2], qk[-1]
+    if qk[:-2] != lead:
+        raise ValueError("q must be %s, got %s" % (list(lead + (G, dk)), list(qk)))
     if not isinstance(log_decay, torch.Tensor):
         raise TypeError("log_decay must be a CUDA tensor")
     if log_decay.dim() == 1:
         _param("log_decay", log_decay, torch.float32, index, (H,))
         ld_decay = 0
     else:
-        ld_decay = _rows("log_decay", log_decay, torch.float32, index, lead + (H,))
-    return (H, G, dk, dv, _rows("q", q, dtype, index, qk, 2), _rows("k", k, dtype, index, qk, 2),
-            _rows("v", v, dtype, index, v.shape, 2), ld_decay)
+        ld_decay = H if _dense(log_decay, torch.float32, index, shape[:-1]) else _rows(
+            "log_decay", log_decay, torch.float32, index, lead + (H,))
+    return (H, G, dk, dv, G * dk if _dense(q, dtype, index, qk) else _rows("q", q, dtype, index, qk, 2),
+            G * dk if _dense(k, dtype, index, qk) else _rows("k", k, dtype, index, qk, 2),
+            H * dv if v.is_contiguous() else _rows("v", v, dtype, index, shape, 2), ld_decay)
 
 
 def _values(v, dims, layout):
@@ -396,7 +407,10 @@ def gdn_linattn_fwd(q, k, v, log_decay, scale=1.0, state_in=None, o=None, state_
         ld_o = _rows("o", o, dtype, index, shape, 2)
     segment = int(segment)
     if workspace is None:
-        need = lib.gdn_linattn_fwd_workspace_size(N, T, H, dk, dv, _ptr(cu_seqlens), segment)
+        tensor_cores = 0
+        if dtype is torch.bfloat16 and not (dk | dv | ld_q | ld_k | ld_v | ld_o) & 7:
+            tensor_cores = 1 if not (_ptr(q) | _ptr(k) | _ptr(v) | _ptr(o)) & 15 else -1
+        need = lib.gdn_linattn_fwd_workspace_size(N, T, H, dk, dv, _ptr(cu_seqlens), segment, tensor_cores)
         if need:
             workspace = _empty(stream, v, (need,), torch.uint8)
     else:
@@ -414,7 +428,7 @@ def gdn_linattn_fwd_workspace_size(N, T, heads, d_k, d_v, packed=False, segment=
     """Bytes of device workspace ``gdn_linattn_fwd`` needs for N sequences of T
     tokens (``packed``: T rows in all); 0 when it needs none."""
     marker = 1 if packed else None  # only NULL-ness reaches the library
-    return int(_lib.load().gdn_linattn_fwd_workspace_size(N, T, heads, d_k, d_v, marker, int(segment)))
+    return int(_lib.load().gdn_linattn_fwd_workspace_size(N, T, heads, d_k, d_v, marker, int(segment), -1))
 
 
 def gdn_linattn_step(q, k, v, log_decay, scale=1.0, state_in=None, o=None, state_out=None, slots=None,
@@ -467,17 +481,23 @@ def gdn_block_norm(y, residual=None, post_weight=None, post_bias=None, pre_weigh
         raise ValueError("post_weight and post_bias need post=True")
     if not pre and (pre_weight is not None or pre_bias is not None or h is not None):
         raise ValueError("pre_weight, pre_bias and h need pre=True")
-    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
-                    ("pre_bias", pre_bias), ("scale", scale)):
-        if t is not None:
-            _param(name, t, torch.float32, index, (C,))
+    row = (C,)
+    for t in (post_weight, post_bias, pre_weight, pre_bias, scale):
+        if t is not None and not _dense(t, torch.float32, index, row):
+            for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
+                            ("pre_bias", pre_bias), ("scale", scale)):
+                if t is not None:
+                    _param(name, t, torch.float32, index, row)
     given = residual if residual is not None else residual_out
     rtype = dtype if given is None else getattr(given, "dtype", None)
     if rtype is not dtype and rtype is not torch.float32:
         raise TypeError("residual must be %s or torch.float32, got %s" % (dtype, rtype))
-    ld_y = _rows("y", y, dtype, index, shape)
-    ld_g = 0 if gate is None else _rows("gate", gate, dtype, index, shape)
-    ld_r = 0 if residual is None else _rows("residual", residual, rtype, index, shape)
+    ld_y = C if y.is_contiguous() else _rows("y", y, dtype, index, shape)
+    ld_g = ld_r = C
+    if gate is not None and not _dense(gate, dtype, index, shape):
+        ld_g = _rows("gate", gate, dtype, index, shape)
+    if residual is not None and not _dense(residual, rtype, index, shape):
+        ld_r = _rows("residual", residual, rtype, index, shape)
     fn = _lib.load().gdn_block_norm
     if residual_out is None:
         residual_out, ld_ro = _empty(stream, y, shape, rtype), C

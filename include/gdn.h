@@ -451,7 +451,7 @@ gdn_status_t gdn_group_norm(const void *x, const void *gate, const float *weight
  * kernel, or four when sequences are cut; path 9.
  */
 size_t gdn_linattn_fwd_workspace_size(int B, int T, int heads, int d_k, int d_v,
-                                      const int32_t *cu_seqlens, int segment);
+                                      const int32_t *cu_seqlens, int segment, int tensor_cores);
 
 gdn_status_t gdn_linattn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
                              const float *state_in, const int32_t *slots, void *o, float *state_out,
