@@ -333,6 +333,15 @@ cudaError_t launch(const GdnBlockNormArgs &a, int T, cudaStream_t s)
     return cudaGetLastError();
 }
 
+// The team by the row's words.  us, bf16, gated and scaled, both norms, a team of T
+// threads, K words each, R rows at a time as T x K x R.
+// 16-byte words: 16 384 rows of 4096 256 x 2 x 1 119 (5.6 TB/s), 128 x 4 x 1 125, 512 x
+// 1 x 2 133, 256 x 2 x 2 148; 32 768 rows of 1024 128 x 1 x 2 57 (5.9 TB/s), 64 x 2 x 1
+// 57; 8192 rows of 8192 512 x 2 x 1 145, 256 x 4 x 1 189; 5000 rows of 12 288 512 x 3 x 1
+// 142, element by element from memory 521.  8192 rows of 2048 with an fp32 stream, mean
+// and variance: 256 x 1 x 2 45 (4.5 TB/s), 256 x 1 x 1 47, 128 x 2 x 1 47.
+// Single elements, 16 384 rows: of 1925 512 x 4 x 1 229, 256 x 8 x 1 262; of 4093 from
+// memory 448, 512 x 8 x 1 545 (issue slots).
 template <typename E, typename R, int VEC> cudaError_t by_width(const GdnBlockNormArgs &a, cudaStream_t s)
 {
     const int words = (a.channels + VEC - 1) / VEC;
@@ -344,10 +353,10 @@ template <typename E, typename R, int VEC> cudaError_t by_width(const GdnBlockNo
     if (words <= 64) return launch<E, R, VEC, 1, 2, 64>(a, 64, s);
     if (words <= 128) return launch<E, R, VEC, 1, 2, 128>(a, 128, s);
     if (words <= 256) return launch<E, R, VEC, 1, 2, 256>(a, 256, s);
-    if (words <= 512) return launch<E, R, VEC, 1, 2, 512>(a, 512, s);
+    if (words <= 512) return launch<E, R, VEC, 2, 1, 256>(a, 256, s);
     if (words <= 1024) return launch<E, R, VEC, 2, 1, 512>(a, 512, s);
-    if constexpr (VEC < 8)
-        if (words <= 2048) return launch<E, R, VEC, 4, 1, 512>(a, 512, s);
+    if (words <= 1536) return launch<E, R, VEC, 3, 1, 512>(a, 512, s);
+    if (words <= 2048) return launch<E, R, VEC, 4, 1, 512>(a, 512, s);
     if (a.rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
     gdn_block_norm_wide_kernel<E, R><<<(unsigned)a.rows, 512, 0, s>>>(a);
     return cudaGetLastError();
