@@ -1,4 +1,4 @@
-"""Two sequence-mixing layers on the package's entry points, as a server runs
+"""Three sequence-mixing layers on the package's entry points, as a server runs
 them: a packed prompt of several sequences first, then token by token with the
 states kept in pools, and the same tokens as one longer prompt to compare with.
 
@@ -6,6 +6,9 @@ states kept in pools, and the same tokens as one longer prompt to compare with.
                      -> group norm of the heads, gated
   selective scan     convolution -> gdn_ssm_fwd / gdn_ssm_step (gated)
                      -> group norm of the heads
+  linear attention   norm before -> gdn_linattn_fwd / gdn_linattn_step
+                     -> group norm of the heads -> norm after, gate, scale,
+                     residual sum and the next block's norm before in one pass
 
     python examples/mixing_layers.py [--tokens 200] [--steps 8]
 """
@@ -19,7 +22,7 @@ import torch.nn.functional as F
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import gated_delta_rule_09_gb300 as gdn  # noqa: E402
 
-WIDTH, HEADS, DIM, TAPS, STATES = 256, 4, 64, 4, 16
+WIDTH, HEADS, GROUPS, DIM, TAPS, STATES = 256, 4, 2, 64, 4, 16
 INNER = HEADS * DIM
 
 
@@ -41,6 +44,12 @@ class Weights:
         step = torch.exp(torch.empty(INNER, device="cuda").uniform_(-6.9, -2.3, generator=g))
         self.delta_bias = step + torch.log(-torch.expm1(-step))
         self.scan_norm = 1 + 0.1 * self._normal(INNER)
+        self.linear_in = self._proj(WIDTH, 2 * GROUPS * DIM + INNER + WIDTH)            # q | k | v | gate
+        self.linear_decay = self._proj(WIDTH, HEADS)
+        self.linear_out = self._proj(INNER, WIDTH)
+        self.linear_norm = 1 + 0.1 * self._normal(INNER)
+        self.linear_before, self.linear_after, self.next_before = (1 + 0.1 * self._normal(WIDTH) for _ in range(3))
+        self.linear_scale = 0.5 + 0.1 * self._normal(WIDTH)
 
     def _normal(self, *shape):
         return torch.randn(*shape, generator=self._g, device="cuda")
@@ -58,6 +67,7 @@ class Pools:
         self.delta = z(slots, HEADS, DIM, DIM)
         self.scan_conv = z(slots, TAPS - 1, INNER, dt=torch.bfloat16)
         self.scan = z(slots, INNER, STATES)
+        self.linear = z(slots, HEADS, DIM, DIM)
 
 
 def _delta_inputs(p, conv):
@@ -108,7 +118,27 @@ def scan_step(w, pools, u, slots):
     return gdn.gdn_group_norm(y, HEADS, w.scan_norm, y=y)
 
 
-LAYERS = {"gated delta rule": (delta_prompt, delta_step), "selective scan": (scan_prompt, scan_step)}
+def _linear(w, u, mix):
+    """One block of a residual stream: ``mix`` is the attention of a prompt or a step."""
+    stream, h = gdn.gdn_block_norm(u, pre_weight=w.linear_before, post=False)
+    p = h @ w.linear_in
+    q, k, v, gate = p.split((GROUPS * DIM, GROUPS * DIM, INNER, WIDTH), -1)
+    o, _ = mix(q.unflatten(-1, (GROUPS, DIM)), k.unflatten(-1, (GROUPS, DIM)), v.unflatten(-1, (HEADS, DIM)),
+               -0.1 * F.softplus((h @ w.linear_decay).float()), scale=DIM ** -0.5)
+    y = gdn.gdn_group_norm(o.flatten(-2), HEADS, w.linear_norm, rms=True) @ w.linear_out
+    return gdn.gdn_block_norm(y, stream, post_weight=w.linear_after, pre_weight=w.next_before, gate=gate, scale=w.linear_scale)[1]
+
+
+def linear_prompt(w, pools, u, slots, cu):
+    return _linear(w, u, lambda *a, **kw: gdn.gdn_linattn_fwd(*a, **kw, state_in=pools.linear, slots=slots, cu_seqlens=cu))
+
+
+def linear_step(w, pools, u, slots):
+    return _linear(w, u, lambda *a, **kw: gdn.gdn_linattn_step(*a, **kw, state_in=pools.linear, slots=slots))
+
+
+LAYERS = {"gated delta rule": (delta_prompt, delta_step), "selective scan": (scan_prompt, scan_step),
+          "linear attention": (linear_prompt, linear_step)}
 
 
 def _pack(seqs):
