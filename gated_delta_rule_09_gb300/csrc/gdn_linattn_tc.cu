@@ -323,7 +323,32 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     if (!find_unit(a, unit / tiles / a.heads, h, kStates, u)) return;
     const int chunks = (int)(((int64_t)u.len + kC - 1) / kC), dk = a.dk;
 
-    if (tid == 0) {
+    // Tensor copies of a chunk's K and Q, to the ring or ahead to L2, and of its V.
+    const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
+    auto row = [&](int c) { return (int)(u.row + (int64_t)c * kC); };
+    auto load_kq = [&](int c, bool ahead) {
+        uint64_t *bar = &s.full[c & 1];
+        if (!ahead) mbar_arrive_expect_tx(bar, (uint32_t)(halves * (kStates ? 1 : 2)) * kTile);
+#pragma unroll 1
+        for (int i = 0; i < halves; ++i) {
+            const int at = ((c & 1) * 2 + i) * kTile;
+            if (ahead) fetch_l2(&tm_k, 64 * i, g, row(c));
+            else tma_load_3d(sm + kOffK + at, &tm_k, bar, 64 * i, g, row(c));
+            if (kStates) continue;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                const int from = row(c) + 32 * row_block(b, c);
+                if (ahead) fetch_l2(&tm_q, 64 * i, g, from);
+                else tma_load_3d(sm + kOffQ + at + b * (kTile / 4), &tm_q, bar, 64 * i, g, from);
+            }
+        }
+    };
+    auto load_v = [&](int c) {
+        mbar_arrive_expect_tx(&s.v_full[c % kRing], kTile);
+        tma_load_3d(sm + kOffV + c % kRing * kTile, &tm_v, &s.v_full[c % kRing], v0, h, row(c));
+        if (c + kAhead < chunks) fetch_l2(&tm_v, v0, h, row(c + kAhead));
+    };
+    if (warp == kWarpIssue + 3 && elect_one()) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.kq_free[i], kStates ? 1 : 3);
@@ -349,9 +374,14 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
         mbar_init(&s.o_full, 1);
         s.abort_flag = 0;
         fence_mbar_init();
-        prefetch_tensormap(&tm_q);
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
+        fence_async_smem();
+        // the first chunks are on their way while tensor memory is allocated
+#pragma unroll 1
+        for (int c = 0; c < 2 && c < chunks; ++c) load_kq(c, false);
+#pragma unroll 1
+        for (int c = 0; c < kRing && c < chunks; ++c) load_v(c);
+#pragma unroll 1
+        for (int c = 2; c < 2 + kAhead && c < chunks; ++c) load_kq(c, true);
         prefetch_tensormap(&tm_o);
     }
     if (warp == 0) {
@@ -712,37 +742,11 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     } else if (elect_one()) {
         // ---- tensor copies: K and Q, V, and the outputs that take the place of V, whichever can go on.  Chunks
         // ahead of the rings are fetched to L2.
-        const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
-        auto row = [&](int c) { return (int)(u.row + (int64_t)c * kC); };
-        auto load_kq = [&](int c, bool ahead) {
-            uint64_t *bar = &s.full[c & 1];
-            if (!ahead) mbar_arrive_expect_tx(bar, (uint32_t)(halves * (kStates ? 1 : 2)) * kTile);
-#pragma unroll 1
-            for (int i = 0; i < halves; ++i) {
-                const int at = ((c & 1) * 2 + i) * kTile;
-                if (ahead) fetch_l2(&tm_k, 64 * i, g, row(c));
-                else tma_load_3d(sm + kOffK + at, &tm_k, bar, 64 * i, g, row(c));
-                if (kStates) continue;
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    const int from = row(c) + 32 * row_block(b, c);
-                    if (ahead) fetch_l2(&tm_q, 64 * i, g, from);
-                    else tma_load_3d(sm + kOffQ + at + b * (kTile / 4), &tm_q, bar, 64 * i, g, from);
-                }
-            }
-        };
-        auto load_v = [&](int c) {
-            mbar_arrive_expect_tx(&s.v_full[c % kRing], kTile);
-            tma_load_3d(sm + kOffV + c % kRing * kTile, &tm_v, &s.v_full[c % kRing], v0, h, row(c));
-            if (c + kAhead < chunks) fetch_l2(&tm_v, v0, h, row(c + kAhead));
-        };
-#pragma unroll 1
-        for (int c = 0; c < kRing && c < chunks; ++c) load_v(c);
-        int kq = 0, put = 0;  // chunks loaded; chunks whose V is through and whose outputs are stored
+        int kq = min(2, chunks), put = 0;  // chunks loaded; chunks whose V is through and whose outputs are stored
         uint64_t idle = 0;    // since when there is nothing to do
         while ((kq < chunks || put < chunks) && !*abort_flag) {
             bool moved = false;
-            if (kq < chunks && (kq < 2 || mbar_test_wait(&s.kq_free[kq & 1], (kq - 2) >> 1 & 1))) {
+            if (kq < chunks && mbar_test_wait(&s.kq_free[kq & 1], (kq - 2) >> 1 & 1)) {
                 load_kq(kq, false);
                 if (kq + kAhead < chunks) load_kq(kq + kAhead, true);
                 ++kq;
