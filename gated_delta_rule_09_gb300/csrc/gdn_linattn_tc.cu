@@ -47,7 +47,8 @@ constexpr int kDVT = 64;    // columns of v per block
 constexpr int kSG = 1;
 constexpr int kWarpS = 4, kWarpW = kWarpS + 4 * kSG, kWarpO = kWarpW + 4, kWarpIssue = kWarpO + 4;
 constexpr int kThreads = (kWarpIssue + 4) * 32;
-constexpr int kRing = 3;    // stages of V, which the outputs take over: two of them wait for each other
+constexpr int kParts = 3;   // of the decayed V
+constexpr int kRing = 2;    // stages of V, which the outputs take over: two of them wait for each other
 constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one that is copied
 constexpr float kPlain = 120.f;  // decays of a block of 32, log 2, that go as products of two factors
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -58,8 +59,8 @@ constexpr int kTile = kC * 128;           // 128 rows
 constexpr int kOffQ = 0;                  // 2 stages x 2 halves of d_k
 constexpr int kOffK = kOffQ + 4 * kTile;
 constexpr int kOffV = kOffK + 4 * kTile;  // kRing stages
-constexpr int kOffW = kOffV + kRing * kTile;  // decayed V: high and low parts
-constexpr int kOffS = kOffW + 2 * kTile;      // S^T
+constexpr int kOffW = kOffV + kRing * kTile;  // decayed V in parts
+constexpr int kOffS = kOffW + kParts * kTile;  // S^T
 constexpr int kOffSmall = kOffS + kTile;
 
 struct Small {
@@ -174,17 +175,20 @@ __device__ __forceinline__ uint32_t ld_col(uint32_t taddr)
     return v;
 }
 
-// Two values as two bf16 pairs, the first rounded, the second what that leaves.
-// `sign` becomes NaN where a value is infinite or NaN, whose second part then is NaN.
-__device__ __forceinline__ void split(f32x2 v, uint32_t &hi, uint32_t &lo, f32x2 &sign)
+// Two values as pairs of bf16 parts, each the rounded rest of those before it: their
+// sum is the value to 2^-26.  `sign` becomes NaN where a value is infinite or NaN, whose
+// other parts then are NaN.
+__device__ __forceinline__ void split(f32x2 v, uint32_t (&part)[kParts], f32x2 &sign)
 {
-    float x, y;
-    unpack2(v, x, y);
-    hi = narrow_pair(x, y);
-    const f32x2 d = fma2(pack2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), dup2(-1.f), v);
-    sign = fma2(d, dup2(0.f), sign);
-    unpack2(d, x, y);
-    lo = narrow_pair(x, y);
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+        float x, y;
+        unpack2(v, x, y);
+        part[p] = narrow_pair(x, y);
+        if (p + 1 < kParts)
+            v = fma2(pack2(__uint_as_float(part[p] << 16), __uint_as_float(part[p] & 0xffff0000u)), dup2(-1.f), v);
+        if (p == 0) sign = fma2(v, dup2(0.f), sign);
+    }
 }
 
 __device__ __forceinline__ bool is_odd(f32x2 sign)
@@ -194,7 +198,7 @@ __device__ __forceinline__ bool is_odd(f32x2 sign)
     return x + y != 0.f;
 }
 
-// Second parts where the first is infinite or NaN: zero.
+// Other parts where the first is infinite or NaN: zero.
 __device__ __forceinline__ uint32_t mend(uint32_t hi, uint32_t lo)
 {
     if ((hi & 0x7f80u) == 0x7f80u) lo &= 0xffff0000u;
@@ -207,27 +211,30 @@ __device__ __noinline__ void mend_row(uint8_t *tiles, int r)
 #pragma unroll 1
     for (int w = 0; w < 32; ++w) {
         const uint32_t at = sw128(r, w / 4) + w % 4 * 4;
-        uint32_t *lo = reinterpret_cast<uint32_t *>(tiles + kTile + at);
-        *lo = mend(*reinterpret_cast<const uint32_t *>(tiles + at), *lo);
+        for (int p = 1; p < kParts; ++p) {
+            uint32_t *lo = reinterpret_cast<uint32_t *>(tiles + p * kTile + at);
+            *lo = mend(*reinterpret_cast<const uint32_t *>(tiles + at), *lo);
+        }
     }
 }
 
 __device__ __noinline__ void zero_row(uint8_t *tiles, int r)
 {
 #pragma unroll 1
-    for (int c = 0; c < 16; ++c)
+    for (int c = 0; c < 8 * kParts; ++c)
         *reinterpret_cast<uint4 *>(tiles + (c >> 3) * kTile + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
 }
 
-// 8 values into 16-byte column c of row r of two tiles.
+// 8 values into 16-byte column c of row r of kParts tiles.
 __device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4], f32x2 &sign)
 {
-    uint32_t hi[4], lo[4];
+    uint32_t w[4][kParts];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split(x[i], hi[i], lo[i], sign);
+    for (int i = 0; i < 4; ++i) split(x[i], w[i], sign);
     const uint32_t at = sw128(r, c);
-    *reinterpret_cast<uint4 *>(tiles + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4 *>(tiles + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+        *reinterpret_cast<uint4 *>(tiles + p * kTile + at) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
 }
 
 // P of one row in the cases that the plain path leaves: tokens that forget, and blocks
@@ -707,7 +714,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     wait(&s.w_half[half], c);
                     tc_fence_after();
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < kParts; ++part)
 #pragma unroll
                         for (int i = 4 * half; i < 4 * half + 4; ++i)
                             mma_f16kind(tbase + kColU, k + mn_step(i), w + part * (kTile >> 4) + mn_step(i),
