@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             m.first[lane] = first_seen(d.mask, lane);
             m.start[lane] = d.cut_upto(lane) ? 0.f : decay_of(d.in);
             m.add[lane] = d.cut_behind(lane) ? 0.f : decay_of(d.after);
-            if (lane == 0) m.all = d.mask ? 0.f : decay_of(d.total);
+            if (lane == 0) m.all = d.mask ? 0.f : chained_decay_of(d.total);
         }
         __syncthreads();
         load(c + kC);
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_step_kernel(const GdnLin
             }
         }
         const int row = lane / 4;
-        const float d = decay_of(a.log_decay[n * a.ld_decay + h] * kLog2e);
+        const float d = chained_decay_of(a.log_decay[n * a.ld_decay + h] * kLog2e);
         float kk[V], qq[V];
         ld_part<E, V>(static_cast<const E *>(a.k) + n * a.ld_k + (int64_t)(h / share) * dk, dk, lane, VEC, kk);
         ld_part<E, V>(static_cast<const E *>(a.q) + n * a.ld_q + (int64_t)(h / share) * dk, dk, lane, VEC, qq);

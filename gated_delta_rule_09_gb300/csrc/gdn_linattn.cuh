@@ -58,6 +58,25 @@ __device__ __forceinline__ int first_seen(unsigned mask, int i)
 // 2^x of a sum of decays; kDecayShift as in the scan's decays.
 __device__ __forceinline__ float decay_of(float x) { return ex2(x + kDecayShift); }
 
+// The same to half a step of fp32 and a little more, for the factors that follow one
+// another in a state: what ex2.approx is off, 2 steps at most, adds up over the chunks
+// (131 072 tokens in chunks of 32, heads that keep 8192: 2.0e-6 off with it).  2^f of the
+// fraction f, |f| <= 1/2, by the series of e^(f ln 2), whose ninth term is below 2^-32.
+__device__ __forceinline__ float chained_decay_of(float x)
+{
+    const float n = rintf(fmaxf(x, -127.f)), f = fmaxf(x, -127.f) - n;
+    float p = 1.321548679e-06f;
+    p = fmaf(p, f, 1.525273380e-05f);
+    p = fmaf(p, f, 1.540353039e-04f);
+    p = fmaf(p, f, 1.333355815e-03f);
+    p = fmaf(p, f, 9.618129108e-03f);
+    p = fmaf(p, f, 5.550410866e-02f);
+    p = fmaf(p, f, 2.402265070e-01f);
+    p = fmaf(p, f, 6.931471806e-01f);
+    p = fmaf(p, f, 1.f);
+    return x < -126.f ? 0.f : x != x ? x : x > 127.f ? ex2(x) : p * __int_as_float(((int)n + 127) << 23);
+}
+
 // What a block works on: a whole sequence or a piece of one, and the states it
 // reads and writes.
 struct Unit {

@@ -14,10 +14,17 @@
 // state stays in the registers of four warps, fp32, for the whole walk, and none
 // of the products waits for more than the one before it.  Q, K and V enter as they
 // are (products of bf16 are exact in fp32), and sums are fp32.  The decayed V enters
-// as two bf16 parts whose sum keeps 16 bits: final states are right to 2e-6.  P and
-// the state enter the outputs' products rounded once to bf16, which is what the
-// outputs themselves are rounded to: 2.0e-3 off in the 2-norm, 1.7e-3 of it from the
-// outputs' own rounding (in two parts each: 1.7e-3, and twice the work on P and S).
+// as three bf16 parts, whose sum is the value to fp32: final states are 3e-7 to 6e-7 off
+// in the 2-norm (two parts: 2.0e-6, and 67.5 us instead of 78).  P and the state enter
+// the outputs' products rounded once to bf16, which is what the outputs themselves are
+// rounded to: 2.3e-3 off, 1.7e-3 of it from the outputs' own rounding (in two parts each
+// 1.7e-3; that took 85 us where one part took 72, everything else alike).
+//
+// 4 x 4096 tokens x 16 heads of 128: 78 us, 3.5 TB/s, 52 % of the HBM copy rate; a chunk
+// takes 1.9 us.  No one thing bounds it: of the 67.5 us that it took with two parts, P
+// left out gave back 4 us, the outputs 1, the state's hand-over 1, the decayed V 7; the
+// tensor pipe was busy for about half of the time (46 cycles for a product of 128 x 64 x
+// 16), each scheduler issued in half of its cycles, and the rest is hand-overs.
 //
 // Roles, in groups of four warps: forming P (tensor memory to tensor memory, a row per
 // thread), keeping the state and writing its parts for the next chunk, summing the
@@ -478,7 +485,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 wait(&s.dec_ready[st], c >> 1);
                 const float4 total = *reinterpret_cast<const float4 *>(s.total[st]);
                 const uint4 mask = *reinterpret_cast<const uint4 *>(s.mask[st]);
-                const float all = mask.x | mask.y | mask.z | mask.w ? 0.f : decay_of(total.x + total.y + total.z + total.w);
+                const float all = mask.x | mask.y | mask.z | mask.w ? 0.f : chained_decay_of(total.x + total.y + total.z + total.w);
                 arrive_warp(&s.dec_free[st]);
                 if (all == 0.f)
 #pragma unroll
