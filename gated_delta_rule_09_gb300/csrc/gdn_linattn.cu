@@ -56,7 +56,7 @@ template <typename E, int W> struct Rows {
     }
 };
 
-// Two and two blocks per multiprocessor; the next chunk's rows are loaded while this
+// Two blocks per multiprocessor; the next chunk's rows are loaded while this
 // one's are worked on.
 template <typename E, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinattnArgs a, int tiles, int states_only)
@@ -453,8 +453,9 @@ cudaError_t pass(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 
 // Whole sequences or pieces: the quicker by what was measured, us per chunk of 128
 // tokens of a block that has a multiprocessor to itself, and beside all chunks.
-// Tensor cores: one document of 131 072 tokens x 8 heads whole 1743, 9 pieces 370; 4096
-// tokens x 16 heads whole 65, 4 pieces 50; 1024 tokens x 8 heads whole 26, 2 pieces 40.
+// Tensor cores: one document of 131 072 tokens x 8 heads whole 2114, 9 pieces 425; 4096
+// tokens x 16 heads whole 75, 4 pieces 55; 2048 tokens whole 42, 4 pieces 41; 1024 tokens
+// x 8 heads whole 26, 2 pieces 40; 4096 tokens x 32 heads whole 77, 2 pieces 88.
 // CUDA cores: 517 tokens x 2 heads whole 124, 5 pieces 64; 3 x 517 tokens x 6 heads of
 // 77 and 45 whole 207, pieces of 128 69; 4 x 4096 tokens x 16 heads of 64 whole 543, 2
 // pieces 702.  Pieces are chosen to fill the multiprocessors once, twice or three times.
@@ -462,8 +463,8 @@ void gdn_linattn_plan(bool tensor_cores, int N, int T, int heads, int dk, int dv
                       int64_t *piece_slots)
 {
     const double wide = 0.3 + 0.7 * ((dk + 31) / 32) / 4;  // tiles of d_k on CUDA cores
-    const double kWhole = tensor_cores ? 1.7 : 24 * wide, kWholeStart = 10;
-    const double kCut = tensor_cores ? 3.0 : 36 * wide, kCutStart = 26;
+    const double kWhole = tensor_cores ? 2.05 : 24 * wide, kWholeStart = 10;
+    const double kCut = tensor_cores ? 3.5 : 36 * wide, kCutStart = 26;
     constexpr double kBytesPerUs = 6e6;
     constexpr int64_t kChunk = 128;
     const int64_t least = tensor_cores ? 4 : 1;  // chunks of a piece

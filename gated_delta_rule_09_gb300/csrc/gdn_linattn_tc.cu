@@ -283,30 +283,30 @@ __device__ __noinline__ void odd_row(uint32_t p, uint32_t o, int quad, int i, in
 {
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-    float acc[32];
+        float acc[32];
 #pragma unroll
-    for (int d = 0; d < 32; ++d) acc[d] = 0.f;
+        for (int d = 0; d < 32; ++d) acc[d] = 0.f;
 #pragma unroll 1
-    for (int w = 0; w < 64; ++w) {
-        __syncwarp();
-        const uint32_t pair = ld_col(lane_addr(p, quad, w / 16 * 32 + w % 16));
+        for (int w = 0; w < 64; ++w) {
+            __syncwarp();
+            const uint32_t pair = ld_col(lane_addr(p, quad, w / 16 * 32 + w % 16));
 #pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-            const int j = 2 * w + e;
-            const float f = __uint_as_float(e ? pair & 0xffff0000u : pair << 16);
-            if (j > i || j < first) continue;
+            for (int e = 0; e < 2; ++e) {
+                const int j = 2 * w + e;
+                const float f = __uint_as_float(e ? pair & 0xffff0000u : pair << 16);
+                if (j > i || j < first) continue;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[8];
-                widen(*reinterpret_cast<const uint4 *>(V + sw128(j, half * 4 + q)), v);
+                for (int q = 0; q < 4; ++q) {
+                    float v[8];
+                    widen(*reinterpret_cast<const uint4 *>(V + sw128(j, half * 4 + q)), v);
 #pragma unroll
-                for (int d = 0; d < 8; ++d) acc[q * 8 + d] = fmaf(f, v[d], acc[q * 8 + d]);
+                    for (int d = 0; d < 8; ++d) acc[q * 8 + d] = fmaf(f, v[d], acc[q * 8 + d]);
+                }
             }
         }
-    }
-    __syncwarp();
-    tmem_st32(lane_addr(o, quad, 32 * half), acc);
-    tmem_st_wait();
+        __syncwarp();
+        tmem_st32(lane_addr(o, quad, 32 * half), acc);
+        tmem_st_wait();
     }
 }
 

@@ -83,7 +83,7 @@ def _empty(stream, like, shape=None, dtype=None):
     if stream is None:
         if shape is None:
             return torch.empty_like(like, memory_format=torch.contiguous_format)
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
@@ -152,10 +152,11 @@ def _states(state_in, state_out, slots, N, entry, dtype, index, want, x, stream)
             raise ValueError("a pool of states must be [pool, %s]" % ", ".join(map(str, entry)))
         pool = given.shape[0]
     shape = (pool,) + entry
-    if state_in is not None:
+    if state_in is not None and not _dense(state_in, dtype, index, shape):
         _param("state_in", state_in, dtype, index, shape)
     if state_out is not None:
-        _param("state_out", state_out, dtype, index, shape)
+        if not _dense(state_out, dtype, index, shape):
+            _param("state_out", state_out, dtype, index, shape)
     elif want:
         state_out = state_in if slots is not None else _empty(stream, x, shape, dtype)
     return state_out, pool
@@ -347,28 +348,41 @@ def gdn_group_norm(x, groups, weight=None, bias=None, gate=None, y=None, eps=1e-
     return y
 
 
-def _linattn_params(q, k, v, log_decay, index, dtype):
+def _heads(name, t, dtype, index, shape):
+    """``_rows`` of [..., heads, width] slices, the usual layouts first."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        width = shape[-1] * shape[-2]
+        if t.is_contiguous():
+            return width
+        st = t.stride()
+        if st[-1] == 1 and st[-2] == shape[-1] and st[-3] >= width and (len(st) == 3 or st[0] == st[1] * shape[1]):
+            return st[-3]
+    return _rows(name, t, dtype, index, shape, 2)
+
+
+def _linattn_params(q, k, v, log_decay, index, dtype, shape):
     """Checks shared by prompts and steps: (heads, groups, d_k, d_v, row strides
     of q, k, v and log_decay)."""
-    shape = v.shape
-    lead, H, dv = shape[:-2], shape[-2], shape[-1]
+    H, dv = shape[-2], shape[-1]
     if not isinstance(q, torch.Tensor) or q.dim() != len(shape):
         raise ValueError("q and k must be [..., groups, d_k]")
+    if not isinstance(k, torch.Tensor):
+        raise TypeError("k must be a CUDA tensor")
     qk = q.shape
     G, dk = qk[-2], qk[-1]
-    if qk[:-2] != lead:
-        raise ValueError("q must be %s, got %s" % (list(lead + (G, dk)), list(qk)))
+    if qk[:-2] != shape[:-2]:
+        raise ValueError("q must be %s, got %s" % (list(shape[:-2] + (G, dk)), list(qk)))
     if not isinstance(log_decay, torch.Tensor):
         raise TypeError("log_decay must be a CUDA tensor")
     if log_decay.dim() == 1:
         _param("log_decay", log_decay, torch.float32, index, (H,))
         ld_decay = 0
+    elif _dense(log_decay, torch.float32, index, shape[:-1]):
+        ld_decay = H
     else:
-        ld_decay = H if _dense(log_decay, torch.float32, index, shape[:-1]) else _rows(
-            "log_decay", log_decay, torch.float32, index, lead + (H,))
-    return (H, G, dk, dv, G * dk if _dense(q, dtype, index, qk) else _rows("q", q, dtype, index, qk, 2),
-            G * dk if _dense(k, dtype, index, qk) else _rows("k", k, dtype, index, qk, 2),
-            H * dv if v.is_contiguous() else _rows("v", v, dtype, index, shape, 2), ld_decay)
+        ld_decay = _rows("log_decay", log_decay, torch.float32, index, shape[:-1])
+    return (H, G, dk, dv, _heads("q", q, dtype, index, qk), _heads("k", k, dtype, index, qk),
+            _heads("v", v, dtype, index, shape), ld_decay)
 
 
 def _values(v, dims, layout):
@@ -397,7 +411,7 @@ def gdn_linattn_fwd(q, k, v, log_decay, scale=1.0, state_in=None, o=None, state_
     """
     shape, dtype, index = _values(v, 4, "[B,T,H,d_v]")
     N, T = _sequences(shape, cu_seqlens, index)
-    H, G, dk, dv, ld_q, ld_k, ld_v, ld_d = _linattn_params(q, k, v, log_decay, index, dtype)
+    H, G, dk, dv, ld_q, ld_k, ld_v, ld_d = _linattn_params(q, k, v, log_decay, index, dtype, shape)
     lib = _lib.load()
     state_out, pool = _states(state_in, state_out, slots, N, (H, dv, dk), torch.float32, index,
                               want_final_state, v, stream)
@@ -409,7 +423,7 @@ def gdn_linattn_fwd(q, k, v, log_decay, scale=1.0, state_in=None, o=None, state_
     if workspace is None:
         tensor_cores = 0
         if dtype is torch.bfloat16 and not (dk | dv | ld_q | ld_k | ld_v | ld_o) & 7:
-            tensor_cores = 1 if not (_ptr(q) | _ptr(k) | _ptr(v) | _ptr(o)) & 15 else -1
+            tensor_cores = -1 if (q.data_ptr() | k.data_ptr() | v.data_ptr() | o.data_ptr()) & 15 else 1
         need = lib.gdn_linattn_fwd_workspace_size(N, T, H, dk, dv, _ptr(cu_seqlens), segment, tensor_cores)
         if need:
             workspace = _empty(stream, v, (need,), torch.uint8)
@@ -438,7 +452,7 @@ def gdn_linattn_step(q, k, v, log_decay, scale=1.0, state_in=None, o=None, state
     ``state_out`` may be ``state_in``."""
     shape, dtype, index = _values(v, 3, "[N,H,d_v]")
     N = shape[0]
-    H, G, dk, dv, ld_q, ld_k, ld_v, ld_d = _linattn_params(q, k, v, log_decay, index, dtype)
+    H, G, dk, dv, ld_q, ld_k, ld_v, ld_d = _linattn_params(q, k, v, log_decay, index, dtype, shape)
     fn = _lib.load().gdn_linattn_step
     state_out, pool = _states(state_in, state_out, slots, N, (H, dv, dk), torch.float32, index, True, v,
                               stream)
@@ -481,7 +495,7 @@ def gdn_block_norm(y, residual=None, post_weight=None, post_bias=None, pre_weigh
         raise ValueError("post_weight and post_bias need post=True")
     if not pre and (pre_weight is not None or pre_bias is not None or h is not None):
         raise ValueError("pre_weight, pre_bias and h need pre=True")
-    row = (C,)
+    row = shape[-1:]
     for t in (post_weight, post_bias, pre_weight, pre_bias, scale):
         if t is not None and not _dense(t, torch.float32, index, row):
             for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
@@ -500,7 +514,7 @@ def gdn_block_norm(y, residual=None, post_weight=None, post_bias=None, pre_weigh
         ld_r = _rows("residual", residual, rtype, index, shape)
     fn = _lib.load().gdn_block_norm
     if residual_out is None:
-        residual_out, ld_ro = _empty(stream, y, shape, rtype), C
+        residual_out, ld_ro = _empty(stream, y) if rtype is dtype else _empty(stream, y, shape, rtype), C
     else:
         ld_ro = _rows("residual_out", residual_out, rtype, index, shape)
     ld_h = 0

@@ -17,7 +17,7 @@ FORGET = -126 * np.log(2)
 def linattn(q, k, v, log_decay, scale, state_in, slots, cu, parts=False, steps=False, pieces=1):
     """q, k [B,T,G,dk], v [B,T,H,dv] (steps: [N,...]); returns o, its bound, the
     new states and their bounds.  ``parts``: the tensor-core kernel, where the
-    decayed v enters products as two bf16 parts, P and S rounded to bf16 once."""
+    decayed v enters products as three bf16 parts, P and S rounded to bf16 once."""
     H, dv = v.shape[-2:]
     G, dk = q.shape[-2:]
     cu = list(range(v.shape[0] + 1)) if steps else offsets(v, cu)
@@ -27,8 +27,9 @@ def linattn(q, k, v, log_decay, scale, state_in, slots, cu, parts=False, steps=F
     g = np.broadcast_to(g, (len(V), H)) if g.ndim == 1 else g.reshape(-1, H)
     o, bound, new, eb = np.zeros_like(V), np.zeros_like(V), [], []
     S0 = f64(state_in)
-    # two bf16 parts: what the first leaves, 2^-9, is rounded to 8 bits; half a step of bf16
-    cut, half_step = (2.0 ** -17, 2.0 ** -9) if parts else (0.0, 0.0)
+    # a rounding to bf16 (8 bits) is off by at most half a step, 2^-8 of the value (eps = 2^-7): three parts,
+    # each the rounding of what those before it leave, leave 2^-24; P and S are rounded once, one of the two a term
+    cut, half_step = (2.0 ** -24, 2.0 ** -8) if parts else (0.0, 0.0)
     for i, e in enumerate(entries(slots, len(cu) - 1)):
         S = np.zeros((H, dv, dk)) if S0 is None or not 0 <= e < len(S0) else S0[e].copy()
         m, err = np.abs(S), np.zeros_like(S)       # sum of magnitudes; error of the decays' chain so far
