@@ -23,47 +23,77 @@ using namespace gdn_linattn;
 constexpr int kC = 32;        // tokens per chunk: one warp's worth of decays
 constexpr int kThreads = 256;
 
-// Tiles of a block: DK columns of q and k (d_k filled up with zeros), DV of v.
+// Tiles of a block: DK columns of q and k (d_k filled up with zeros), DV of v.  The
+// state's rows follow those of k, and v lies along the tokens: every product reads both
+// of its factors as words of four along the sum.  Rows are 4 words longer than a
+// multiple of 32: eight rows' words of 16 bytes lie in different banks.
 template <int DK, int DV> struct Smem {
-    float q[kC][DK + 4], k[kC][DK + 4], v[kC][DV + 4], P[kC][kC + 1];
-    float S[DK][DV + 4];      // the state's slice, transposed
-    float in[kC], start[kC], add[kC];
+    float q[kC][DK + 4], k[kC + DV][DK + 4];
+    float v[DV][kC + 4], P[kC][kC + 4];
+    float add[kC], in[kC], start[kC];
     int first[kC];
     float all;
 };
 
 // kC rows of W columns, on their way from memory: all of a thread's loads are in
-// flight together.  Zeros past n rows and `cols` columns.
+// flight together.  A warp takes every eighth row.  Zeros past n rows and `cols` columns.
 template <typename E, int W> struct Rows {
-    static constexpr int kLoads = (kC * W + kThreads - 1) / kThreads;
-    E x[kLoads];
-
+    static constexpr int kRowsOf = kC * 32 / kThreads, kStep = kThreads / 32, kCols = W / 32;
+    E x[kRowsOf][kCols];
     __device__ __forceinline__ void load(const E *from, int64_t ld, int n, int cols)
     {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        const E *row = from + warp * ld + lane;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int e = threadIdx.x + i * kThreads, r = e / W, c = e % W;
-            x[i] = r < n && c < cols ? from[r * ld + c] : from_f<E>(0.f);
-        }
+        for (int i = 0; i < kRowsOf; ++i, row += kStep * ld)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+                x[i][c] = warp + kStep * i < n && lane + 32 * c < cols ? row[32 * c] : from_f<E>(0.f);
     }
-    __device__ __forceinline__ void store(float (*to)[W + 4]) const
+    template <int L> __device__ __forceinline__ void store(float (*to)[L]) const
     {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int e = threadIdx.x + i * kThreads;
-            if (kC * W % kThreads == 0 || e < kC * W) to[e / W][e % W] = to_f(x[i]);
-        }
+        for (int i = 0; i < kRowsOf; ++i)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) to[warp + kStep * i][lane + 32 * c] = to_f(x[i][c]);
+    }
+    // Transposed; whether something of it is infinite or NaN.
+    template <int L> __device__ __forceinline__ bool turn(float (*to)[L]) const
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < kRowsOf; ++i)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                const float f = to_f(x[i][c]);
+                to[lane + 32 * c][warp + kStep * i] = f;
+                odd |= !(fabsf(f) <= 3.402823466e38f);
+            }
+        return odd;
     }
 };
 
-// Two blocks per multiprocessor; the next chunk's rows are loaded while this
-// one's are worked on.
+__device__ __forceinline__ void dot4(const float4 &x, const float4 &y, f32x2 &sum)
+{
+    sum = fma2(pack2(x.x, x.y), pack2(y.x, y.y), sum);
+    sum = fma2(pack2(x.z, x.w), pack2(y.z, y.w), sum);
+}
+
+// A warp's lanes are 4 rows by 8 columns of a product: its loads of either factor are
+// free of bank conflicts, 4 x 3 sums a thread of Q [K; S]^T for 7 words of 16 bytes, 4 x
+// 8 of V^T K for 12 floats a token.  Bound by what shared memory gives to registers, 128
+// bytes a cycle (4 x 4096 tokens x 16 heads fp32: 1005 us, about 12 000 of a chunk's
+// 16 000 cycles; fused multiply-adds 6000).  512 threads with half the sums each, and so
+// more words for them, took 1352; one sum a thread along rows of o 1395.  The next
+// chunk's rows are loaded while this one's are worked on.
 template <typename E, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinattnArgs a, int tiles, int states_only)
 {
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<DK, DV> &m = *reinterpret_cast<Smem<DK, DV> *>(raw);
-    const int t = threadIdx.x, lane = t & 31;
+    const int t = threadIdx.x, lane = t & 31, warp = t / 32;
     const int64_t unit = blockIdx.x;
     const int v0 = (int)(unit % tiles) * DV, h = (int)(unit / tiles % a.heads);
     Unit u;
@@ -86,18 +116,19 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
         if (t < 32) decay_next = lane < n ? decay[(int64_t)(c + lane) * a.ld_decay] : 0.f;
     };
     load(0);
-    for (int i = t; i < DK * DV; i += kThreads) {  // d_k along the lanes, as the state lies
+    for (int i = t; i < DK * DV; i += kThreads) {
         const int kk = i % DK, d = i / DK;
-        m.S[kk][d] = u.in && kk < dk && d < nv ? u.in[(int64_t)(v0 + d) * dk + kk] : 0.f;
+        m.k[kC + d][kk] = u.in && kk < dk && d < nv ? u.in[(int64_t)(v0 + d) * dk + kk] : 0.f;
     }
-    constexpr int OV = DV / 16, SV = DV / 8, KP = DK / 32;
-    const int i0 = t / 16 * 2, j0 = t % 16 * 2, d0 = t % 16 * OV;  // 2 x 2 of P, 2 x OV of o
-    const int k0 = t / 8 * KP, e0 = t % 8 * SV;                    // KP x SV of S
+    constexpr int OV = DV / 32;                                              // columns of o of a thread
+    const int i0 = lane / 8 + warp % 2 * 4, j0 = lane % 8 + warp / 2 * 8;    // rows 8 apart; columns 32 apart
+    constexpr int SV = DV / 16, SK = DK / 32;                                // rows and pairs of columns of S
+    const int d0 = lane / 8 + warp / 2 * 4, k0 = 2 * (lane % 8 + warp % 2 * 8);  // 16 and 32 apart
     for (int c = 0; c < u.len; c += kC) {
         const int n = min(kC, u.len - c);
         __syncthreads();
         kr.store(m.k);
-        vr.store(m.v);
+        const bool inf = vr.turn(m.v);
         if (!states_only) qr.store(m.q);
         if (t < 32) {
             Decays d;
@@ -108,114 +139,123 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             m.add[lane] = d.cut_behind(lane) ? 0.f : decay_of(d.after);
             if (lane == 0) m.all = d.mask ? 0.f : chained_decay_of(d.total);
         }
-        __syncthreads();
+        const bool odd = __syncthreads_or(inf);
         load(c + kC);
-        float acc[2][OV] = {};
+        float acc[4][OV];
         if (!states_only) {
-            if (j0 <= i0 + 1) {
-                f32x2 p[2][2] = {};
-#pragma unroll 4
-                for (int kk = 0; kk < DK; kk += 4) {
-                    float4 x[2], y[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[e] = *reinterpret_cast<const float4 *>(&m.q[i0 + e][kk]);
-                        y[e] = *reinterpret_cast<const float4 *>(&m.k[j0 + e][kk]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            p[e][f] = fma2(pack2(x[e].x, x[e].y), pack2(y[f].x, y[f].y), p[e][f]);
-                            p[e][f] = fma2(pack2(x[e].z, x[e].w), pack2(y[f].z, y[f].w), p[e][f]);
-                        }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const int i = i0 + e, j = j0 + f;
-                        float lo, hi;
-                        unpack2(p[e][f], lo, hi);
-                        m.P[i][j] = j <= i && j >= m.first[i] ? (lo + hi) * decay_of(m.in[i] - m.in[j]) : 0.f;
-                    }
-            }
+            f32x2 sum[4][1 + OV] = {};
 #pragma unroll 2
             for (int kk = 0; kk < DK; kk += 4) {
-                float x[2][4];
+                float4 x[4], y[1 + OV];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) ld_vec<float, 4>(&m.q[i0 + e][kk], x[e]);
+                for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float4 *>(&m.q[i0 + 8 * e][kk]);
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    float s[OV];
-                    ld_vec<float, OV>(&m.S[kk + f][d0], s);
+                for (int f = 0; f <= OV; ++f) y[f] = *reinterpret_cast<const float4 *>(&m.k[j0 + 32 * f][kk]);
 #pragma unroll
-                    for (int y = 0; y < OV; ++y) {
-                        acc[0][y] = fmaf(x[0][f], s[y], acc[0][y]);
-                        acc[1][y] = fmaf(x[1][f], s[y], acc[1][y]);
-                    }
-                }
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int f = 0; f <= OV; ++f) dot4(x[e], y[f], sum[e][f]);
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float w = m.start[i0 + e];
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + 8 * e;
+                const float w = m.start[i];
+                float lo, hi;
+                unpack2(sum[e][0], lo, hi);
+                m.P[i][j0] = j0 <= i && j0 >= m.first[i] ? (lo + hi) * decay_of(m.in[i] - m.in[j0]) : 0.f;
 #pragma unroll
-                for (int y = 0; y < OV; ++y) acc[e][y] = w == 0.f ? 0.f : w * acc[e][y];
+                for (int f = 0; f < OV; ++f) {
+                    unpack2(sum[e][1 + f], lo, hi);
+                    acc[e][f] = w == 0.f ? 0.f : w * (lo + hi);
+                }
             }
         }
         __syncthreads();
         if (!states_only) {
-            // a token sees nothing of those behind it, infinite or not
-#pragma unroll 4
-            for (int j = 0; j <= i0; ++j) {
-                float w[OV];
-                ld_vec<float, OV>(&m.v[j][d0], w);
-                const float p0 = m.P[i0][j], p1 = m.P[i0 + 1][j];
+            if (!odd) {
+                f32x2 sum[4][OV] = {};
+#pragma unroll 2
+                for (int j = 0; j < kC; j += 4) {
+                    float4 x[4], y[OV];
 #pragma unroll
-                for (int y = 0; y < OV; ++y) {
-                    acc[0][y] = fmaf(p0, w[y], acc[0][y]);
-                    acc[1][y] = fmaf(p1, w[y], acc[1][y]);
+                    for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float4 *>(&m.P[i0 + 8 * e][j]);
+#pragma unroll
+                    for (int f = 0; f < OV; ++f) y[f] = *reinterpret_cast<const float4 *>(&m.v[j0 + 32 * f][j]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int f = 0; f < OV; ++f) dot4(x[e], y[f], sum[e][f]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int f = 0; f < OV; ++f) {
+                        float lo, hi;
+                        unpack2(sum[e][f], lo, hi);
+                        acc[e][f] += lo + hi;
+                    }
+            } else {  // a token sees nothing of those behind it, infinite or not; same order of sums
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + 8 * e;
+#pragma unroll
+                    for (int f = 0; f < OV; ++f) {
+                        float sum[2] = {};
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll 1
+                            for (int j = r; j <= i; j += 2)
+                                if (j >= m.first[i]) sum[r] = fmaf(m.P[i][j], m.v[j0 + 32 * f][j], sum[r]);
+                        acc[e][f] += sum[0] + sum[1];
+                    }
                 }
             }
-            float w[OV];
-            ld_vec<float, OV>(&m.v[i0 + 1][d0], w);
-            const float p1 = m.P[i0 + 1][i0 + 1];
 #pragma unroll
-            for (int y = 0; y < OV; ++y) acc[1][y] = fmaf(p1, w[y], acc[1][y]);
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int y = 0; y < OV; ++y)
-                    if (i0 + e < n && d0 + y < nv) o[(c + i0 + e) * a.ld_o + d0 + y] = from_f<E>(a.scale * acc[e][y]);
+                for (int f = 0; f < OV; ++f) {
+                    const int i = i0 + 8 * e, d = j0 + 32 * f;
+                    if (i < n && d < nv) o[(c + i) * a.ld_o + d] = from_f<E>(a.scale * acc[e][f]);
+                }
         }
-        float s[KP][SV] = {};
-#pragma unroll 2
-        for (int j = 0; j < n; ++j) {
-            float w[SV];
-            ld_vec<float, SV>(&m.v[j][e0], w);
-            const float f = m.add[j];
+        f32x2 s[SV][SK] = {};
+#pragma unroll 1
+        for (int j = 0; j < n; j += 4) {
+            float w[SV][4], f[4];
+            ld_vec<float, 4>(&m.add[j], f);
 #pragma unroll
-            for (int x = 0; x < KP; ++x) {
-                const float fk = f * m.k[j][k0 + x];
+            for (int x = 0; x < SV; ++x) {
+                ld_vec<float, 4>(&m.v[d0 + 16 * x][j], w[x]);
 #pragma unroll
-                for (int y = 0; y < SV; ++y) s[x][y] = fmaf(fk, w[y], s[x][y]);
+                for (int e = 0; e < 4; ++e) w[x][e] *= f[e];
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int y = 0; y < SK; ++y) {
+                    const float2 kk = *reinterpret_cast<const float2 *>(&m.k[j + e][k0 + 32 * y]);
+#pragma unroll
+                    for (int x = 0; x < SV; ++x)
+                        s[x][y] = fma2(pack2(w[x][e], w[x][e]), pack2(kk.x, kk.y), s[x][y]);
+                }
         }
         const float all = m.all;
 #pragma unroll
-        for (int x = 0; x < KP; ++x) {
-            float S[SV];
-            ld_vec<float, SV>(&m.S[k0 + x][e0], S);
+        for (int x = 0; x < SV; ++x)
 #pragma unroll
-            for (int y = 0; y < SV; ++y) S[y] = all == 0.f ? s[x][y] : fmaf(all, S[y], s[x][y]);
-            st_vec<float, SV>(&m.S[k0 + x][e0], S);
-        }
+            for (int y = 0; y < SK; ++y) {
+                float2 *S = reinterpret_cast<float2 *>(&m.k[kC + d0 + 16 * x][k0 + 32 * y]);
+                const float2 before = *S;
+                float lo, hi;
+                unpack2(s[x][y], lo, hi);
+                *S = make_float2(all == 0.f ? lo : fmaf(all, before.x, lo), all == 0.f ? hi : fmaf(all, before.y, hi));
+            }
     }
     __syncthreads();
     if (u.out)
         for (int i = t; i < DK * DV; i += kThreads) {
             const int kk = i % DK, d = i / DK;
-            if (kk < dk && d < nv) u.out[(int64_t)(v0 + d) * dk + kk] = m.S[kk][d];
+            if (kk < dk && d < nv) u.out[(int64_t)(v0 + d) * dk + kk] = m.k[kC + d][kk];
         }
 }
 
@@ -427,12 +467,13 @@ template <typename E, int DK, int DV> cudaError_t simt_of(const GdnLinattnArgs &
     return cudaGetLastError();
 }
 
-// 32 columns of v per block where 64 would leave room for more blocks (4 x 4096 tokens
-// x 16 heads fp32: 256 blocks instead of 128).
+// 32 columns of v per block where 64 would leave multiprocessors empty.  us, fp32, d_k
+// 128, of 32 and of 64: 4096 tokens x 16 heads (32 blocks of 64) 705, 1000; 4 x 4096 x 16
+// (128) 1202, 1005; 4 x 4096 x 16 of 64 (64) 487, 601.
 template <typename E, int DK> cudaError_t simt(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 {
     const int64_t blocks = spans(a) * a.heads * ((a.dv + 63) / 64);
-    return a.dv <= 32 || blocks < 2 * gdn_ssm_sms() ? simt_of<E, DK, 32>(a, states_only, s) : simt_of<E, DK, 64>(a, states_only, s);
+    return a.dv <= 32 || 5 * blocks < 4 * gdn_ssm_sms() ? simt_of<E, DK, 32>(a, states_only, s) : simt_of<E, DK, 64>(a, states_only, s);
 }
 
 template <typename E> cudaError_t simt_by_width(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
@@ -452,19 +493,22 @@ cudaError_t pass(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 }  // namespace
 
 // Whole sequences or pieces: the quicker by what was measured, us per chunk of 128
-// tokens of a block that has a multiprocessor to itself, and beside all chunks.
+// tokens for the first block of a multiprocessor and for each more, and beside all
+// chunks.
 // Tensor cores: one document of 131 072 tokens x 8 heads whole 2114, 9 pieces 425; 4096
 // tokens x 16 heads whole 75, 4 pieces 55; 2048 tokens whole 42, 4 pieces 41; 1024 tokens
 // x 8 heads whole 26, 2 pieces 40; 4096 tokens x 32 heads whole 77, 2 pieces 88.
-// CUDA cores: 517 tokens x 2 heads whole 124, 5 pieces 64; 3 x 517 tokens x 6 heads of
-// 77 and 45 whole 207, pieces of 128 69; 4 x 4096 tokens x 16 heads of 64 whole 543, 2
-// pieces 702.  Pieces are chosen to fill the multiprocessors once, twice or three times.
+// CUDA cores, fp32 (blocks of 32 columns; one of 64 takes the time of two): 4096 tokens x
+// 4 heads whole 695, pieces of 512 153, of 128 108; 16 heads whole 705, pieces of 2048 530,
+// 512 327; 4 x 4096 x 16 whole 1005, 4 pieces each 1139; 517 x 2 heads whole 97, 5 pieces 58.
+// Pieces are chosen to fill the multiprocessors once or up to as often as there is room.
 void gdn_linattn_plan(bool tensor_cores, int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment,
                       int64_t *piece_slots)
 {
-    const double wide = 0.3 + 0.7 * ((dk + 31) / 32) / 4;  // tiles of d_k on CUDA cores
-    const double kWhole = tensor_cores ? 2.05 : 24 * wide, kWholeStart = 10;
-    const double kCut = tensor_cores ? 3.5 : 36 * wide, kCutStart = 26;
+    const double wide = 0.4 + 0.6 * ((dk + 31) / 32) / 4;  // tiles of d_k on CUDA cores
+    const double kWhole = tensor_cores ? 2.05 : 21.5 * wide, kWholeMore = tensor_cores ? kWhole : 10 * wide, kWholeStart = 10;
+    const double kCut = tensor_cores ? 3.5 : 31.5 * wide, kCutMore = tensor_cores ? kCut : 14 * wide, kCutStart = 26;
+    const int kFills = tensor_cores ? 3 : 4;
     constexpr double kBytesPerUs = 6e6;
     constexpr int64_t kChunk = 128;
     const int64_t least = tensor_cores ? 4 : 1;  // chunks of a piece
@@ -479,11 +523,12 @@ void gdn_linattn_plan(bool tensor_cores, int N, int T, int heads, int dk, int dv
         // a packed sequence may be the longest by far; twice the mean is taken for it
         const int64_t all = (T + kChunk - 1) / kChunk, longest = uneven ? (2 * all + N - 1) / N : all;
         const double share = (double)all * seqs * per / sms;  // chunks per multiprocessor
-        auto waves = [&](int64_t blocks) { return (double)((blocks + sms - 1) / sms); };
+        auto more = [&](int64_t blocks) { return (double)((blocks + sms - 1) / sms - 1); };
         const double chain = (double)heads * dk * dv * 16 / kBytesPerUs;  // per piece: its state written, read, written, read
-        double best = kWholeStart + kWhole * (!uneven ? waves(N * per) * all : share > longest ? share : longest);
+        double best = kWholeStart + (!uneven ? (kWhole + kWholeMore * more(N * per)) * all
+                                     : kWholeMore * share > kWhole * longest ? kWholeMore * share : kWhole * longest);
         seg = all;
-        for (int k = 1; k <= 3; ++k) {
+        for (int k = 1; k <= kFills; ++k) {
             int64_t s = uneven ? (int64_t)(share / k) + 1 : (all * N * per + (int64_t)k * sms - 1) / ((int64_t)k * sms);
             if (!uneven) {  // as many pieces of a sequence as fit
                 const int64_t p = (int64_t)k * sms / (N * per);
@@ -493,7 +538,8 @@ void gdn_linattn_plan(bool tensor_cores, int N, int T, int heads, int dk, int dv
             if (s < least) s = least;
             if (s >= longest) continue;
             const int64_t pieces = uneven ? all / s + N : N * ((all + s - 1) / s);
-            const double t = kCutStart + chain * pieces + kCut * (uneven ? share + s : waves(pieces * per) * s);
+            const double t = kCutStart + chain * pieces +
+                             (uneven ? kCut * s + kCutMore * share : (kCut + kCutMore * more(pieces * per)) * s);
             if (t < best) {
                 best = t;
                 seg = s;
