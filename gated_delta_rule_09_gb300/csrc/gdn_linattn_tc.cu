@@ -74,7 +74,7 @@ struct Small {
     // decays of two chunks: sums up to and with a token within its block of 32, their
     // inverse factors 2^-in, and the blocks' sums
     float in[2][kC], inverse[2][kC], total[2][4];
-    unsigned mask[2][4];
+    unsigned mask[2][4], steep[2][4];  // tokens that forget; a sum on the way is 2^kPlain or more
     int odd[2];             // V has infinities or NaN
     uint64_t full[2], v_full[kRing], kq_free[2], v_free[kRing], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2],
         o_staged[kRing], i_full[2],
@@ -245,7 +245,7 @@ __device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32
 }
 
 // P of one row in the cases that the plain path leaves: tokens that forget, and blocks
-// that decay by more than 2^120.
+// with a decay of 2^120 or more on the way.
 __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, float scale, const float *in, const float *total,
                                         const unsigned *mask)
 {
@@ -348,9 +348,8 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             const int at = ((c & 1) * 2 + i) * kTile;
             if (ahead) fetch_l2(&tm_k, 64 * i, g, row(c));
             else tma_load_3d(sm + kOffK + at, &tm_k, bar, 64 * i, g, row(c));
-            if (kStates) continue;
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < (kStates ? 0 : 4); ++b) {
                 const int from = row(c) + 32 * row_block(b, c);
                 if (ahead) fetch_l2(&tm_q, 64 * i, g, from);
                 else tma_load_3d(sm + kOffQ + at + b * (kTile / 4), &tm_q, bar, 64 * i, g, from);
@@ -417,12 +416,12 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 const int st = c & 1, I = row_block(quad, c);
                 const uint32_t p = tbase + kColP + 128 * st;
                 wait(&s.dec_ready[st], c >> 1);
-                // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where J, the
-                // block of j, decays by less than 2^120; within a block without the middle factor.
+                // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where no sum
+                // in J, the block of j, reaches 120; within a block without the middle factor.
                 float sum = s.in[st][32 * I + lane];
                 bool odd = false;
 #pragma unroll 1
-                for (int J = 0; J <= I; ++J) odd |= s.mask[st][J] || !(fabsf(s.total[st][J]) < kPlain);
+                for (int J = 0; J <= I; ++J) odd |= s.mask[st][J] || s.steep[st][J];
                 wait(&s.qk_full[st], c >> 1);
                 __syncwarp();
                 tc_fence_after();
@@ -546,9 +545,11 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             if (c > 1) wait(&s.dec_free[st], (c - 2) >> 1);
             s.in[st][t] = d.in;
             s.inverse[st][t] = ex2(-d.in);
+            const bool steep = __any_sync(0xffffffffu, !(fabsf(d.in) < kPlain));
             if (lane == 0) {
                 s.total[st][quad] = d.total;
                 s.mask[st][quad] = d.mask;
+                s.steep[st][quad] = steep;
             }
             if (t == 0) s.odd[st] = 0;
             arrive_warp(&s.dec_ready[st]);
@@ -698,7 +699,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     const uint64_t k = sdesc_sw128(base + kOffK + st * 2 * kTile, 16, 1024);
 #pragma unroll
                     for (int i = 0; i < KS; ++i)
-                            mma_f16kind(p, q + k_step(i), k + k_step(i), idesc_bf16_f32(128, 128, 0, 0), i > 0);
+                        mma_f16kind(p, q + k_step(i), k + k_step(i), idesc_bf16_f32(128, 128, 0, 0), i > 0);
                     mma_commit(&s.qk_full[st]);
                     mma_commit(&s.kq_free[st]);
                 }

@@ -116,6 +116,15 @@ def test_decays_of_every_size(dtype, rate):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decays_that_fall_and_rise_within_a_block(dtype):
+    """Sums that pass 2^-126 on the way, though the block's own does not; growth up to e^40."""
+    x = make((1, 200), 2, 1, 64, 64, dtype, seed=17)
+    for at, g in ((40, -60.0), (41, -60.0), (44, 20.0), (45, 20.0), (130, -70.0), (131, -20.0), (132, 9.0), (133, 8.0)):
+        x["log_decay"][:, at, 0] = g
+    check(x, state_in=torch.randn(1, 2, 64, 64, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("name", ["q", "k", "v", "log_decay"])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")])
 def test_a_token_sees_nothing_of_those_behind_it(dtype, name, value):
