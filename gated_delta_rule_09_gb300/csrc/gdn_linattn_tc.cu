@@ -57,7 +57,10 @@ constexpr int kThreads = (kWarpIssue + 4) * 32;
 constexpr int kParts = 3;   // of the decayed V
 constexpr int kRing = 2;    // stages of V, which the outputs take over: two of them wait for each other
 constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one that is copied
-constexpr float kPlain = 120.f;  // decays of a block of 32, log 2, that go as products of two factors
+// Sums of decays within a block of 32, log 2, that go as products of two factors, 2^-in_j
+// and one that is zero below 2^-126: what is lost is below 2^(90 - 126) of a product (with
+// 120, 1 % of one).
+constexpr float kPlain = 90.f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 50000;  // a wait's bound once the block has given up on one
 
@@ -245,7 +248,8 @@ __device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32
 }
 
 // P of one row in the cases that the plain path leaves: tokens that forget, and blocks
-// with a decay of 2^120 or more on the way.
+// with a decay of 2^90 or more on the way.  An exponential an entry: 217 us where the
+// plain path takes 78, if every block of 32 goes this way.
 __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, float scale, const float *in, const float *total,
                                         const unsigned *mask)
 {
@@ -417,7 +421,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 const uint32_t p = tbase + kColP + 128 * st;
                 wait(&s.dec_ready[st], c >> 1);
                 // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where no sum
-                // in J, the block of j, reaches 120; within a block without the middle factor.
+                // in J, the block of j, reaches 90; within a block without the middle factor.
                 float sum = s.in[st][32 * I + lane];
                 bool odd = false;
 #pragma unroll 1

@@ -125,6 +125,18 @@ def test_decays_that_fall_and_rise_within_a_block(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fall", [-40.0, -62.0, -70.0, -82.0])
+def test_tokens_behind_a_steep_decay_are_seen(dtype, fall):
+    """A token that all but forgets, then tokens whose outputs come from those just behind it alone."""
+    x = make((1, 200), 2, 1, 64, 64, dtype, seed=19)
+    x = {n: t.clone() for n, t in x.items()}
+    x["log_decay"][:, 1] = fall
+    x["log_decay"][:, 32] = -5.7
+    x["v"][:, 32:60] = 0
+    check(x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("name", ["q", "k", "v", "log_decay"])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")])
 def test_a_token_sees_nothing_of_those_behind_it(dtype, name, value):
