@@ -11,7 +11,7 @@
 // bf16 calls whose rows tensor copies can take run on the tensor cores
 // (gdn_linattn_tc.cu); this file has the kernel for every other call, in fp32 on
 // CUDA cores, the step for single tokens, and what joins the pieces of a long
-// sequence: a first pass forms what each piece adds to the state and its decay, a
+// sequence: a first pass forms what each piece adds to the state, and its decay, a
 // chain over a sequence's pieces turns these into the states they start from, and
 // the second pass is the ordinary one over all pieces at once.
 #include "gdn_linattn.cuh"
@@ -84,7 +84,7 @@ __device__ __forceinline__ void dot4(const float4 &x, const float4 &y, f32x2 &su
 // A warp's lanes are 4 rows by 8 columns of a product: its loads of either factor are
 // free of bank conflicts, 4 x 3 sums a thread of Q [K; S]^T for 7 words of 16 bytes, 4 x
 // 8 of V^T K for 12 floats a token.  Bound by what shared memory gives to registers, 128
-// bytes a cycle (4 x 4096 tokens x 16 heads fp32: 1005 us, about 12 000 of a chunk's
+// bytes a cycle (4 x 4096 tokens x 16 heads fp32: 977 us, about 12 000 of a chunk's
 // 16 000 cycles; fused multiply-adds 6000).  512 threads with half the sums each, and so
 // more words for them, took 1352; one sum a thread along rows of o 1395.  The next
 // chunk's rows are loaded while this one's are worked on.
@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
     const int i0 = lane / 8 + warp % 2 * 4, j0 = lane % 8 + warp / 2 * 8;    // rows 8 apart; columns 32 apart
     constexpr int SV = DV / 16, SK = DK / 32;                                // rows and pairs of columns of S
     const int d0 = lane / 8 + warp / 2 * 4, k0 = 2 * (lane % 8 + warp % 2 * 8);  // 16 and 32 apart
+    PieceDecay piece;
     for (int c = 0; c < u.len; c += kC) {
         const int n = min(kC, u.len - c);
         __syncthreads();
@@ -137,7 +138,10 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             m.first[lane] = first_seen(d.mask, lane);
             m.start[lane] = d.cut_upto(lane) ? 0.f : decay_of(d.in);
             m.add[lane] = d.cut_behind(lane) ? 0.f : decay_of(d.after);
-            if (lane == 0) m.all = d.mask ? 0.f : chained_decay_of(d.total);
+            if (lane == 0) {
+                m.all = d.mask ? 0.f : chained_decay_of(d.total);
+                if (states_only) piece.add(d.total, d.mask);
+            }
         }
         const bool odd = __syncthreads_or(inf);
         load(c + kC);
@@ -252,37 +256,12 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             }
     }
     __syncthreads();
+    if (states_only && v0 == 0 && t == 0) a.piece_decay[unit / tiles] = piece.all();
     if (u.out)
         for (int i = t; i < DK * DV; i += kThreads) {
             const int kk = i % DK, d = i / DK;
             if (kk < dk && d < nv) u.out[(int64_t)(v0 + d) * dk + kk] = m.k[kC + d][kk];
         }
-}
-
-// Decay of each piece but a sequence's last, one warp each.
-__global__ void __launch_bounds__(kThreads) gdn_linattn_decay_kernel(const GdnLinattnArgs a)
-{
-    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    if (item >= a.pieces * a.heads) return;
-    const int64_t slot = item / a.heads;
-    const int h = (int)(item % a.heads), lane = threadIdx.x & 31;
-    Unit u;
-    if (!find_unit(a, slot, h, true, u)) return;
-    double sum = 0.;
-    bool cut = false;
-    if (a.ld_decay == 0) {
-        sum = (double)a.log_decay[h] * u.len;
-    } else {
-        for (int i = lane; i < u.len; i += 32) {
-            const float g = a.log_decay[(u.row + i) * a.ld_decay + h];
-            cut |= g * kLog2e <= kForget;
-            sum += g;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        cut = __any_sync(0xffffffffu, cut);
-    }
-    if (lane == 0) a.piece_decay[item] = cut ? 0.f : (float)exp(sum);
 }
 
 // The states that the pieces of each sequence start from, in place of what the
@@ -469,7 +448,7 @@ template <typename E, int DK, int DV> cudaError_t simt_of(const GdnLinattnArgs &
 
 // 32 columns of v per block where 64 would leave multiprocessors empty.  us, fp32, d_k
 // 128, of 32 and of 64: 4096 tokens x 16 heads (32 blocks of 64) 705, 1000; 4 x 4096 x 16
-// (128) 1202, 1005; 4 x 4096 x 16 of 64 (64) 487, 601.
+// (128) 1202, 977; 4 x 4096 x 16 of 64 (64) 486, 601.
 template <typename E, int DK> cudaError_t simt(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 {
     const int64_t blocks = spans(a) * a.heads * ((a.dv + 63) / 64);
@@ -495,19 +474,19 @@ cudaError_t pass(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 // Whole sequences or pieces: the quicker by what was measured, us per chunk of 128
 // tokens for the first block of a multiprocessor and for each more, and beside all
 // chunks.
-// Tensor cores: one document of 131 072 tokens x 8 heads whole 2114, 9 pieces 425; 4096
-// tokens x 16 heads whole 75, 4 pieces 55; 2048 tokens whole 42, 4 pieces 41; 1024 tokens
-// x 8 heads whole 26, 2 pieces 40; 4096 tokens x 32 heads whole 77, 2 pieces 88.
+// Tensor cores: one document of 131 072 tokens x 8 heads whole 2121, in pieces 418; 4096
+// tokens x 16 heads whole 75, 4 pieces 50; 2048 tokens whole 42, 4 pieces 36; 1024 tokens
+// x 8 heads whole 26, 2 pieces 33; 4096 tokens x 32 heads whole 77, 2 pieces 82.
 // CUDA cores, fp32 (blocks of 32 columns; one of 64 takes the time of two): 4096 tokens x
-// 4 heads whole 695, pieces of 512 153, of 128 108; 16 heads whole 705, pieces of 2048 530,
-// 512 327; 4 x 4096 x 16 whole 1005, 4 pieces each 1139; 517 x 2 heads whole 97, 5 pieces 58.
+// 4 heads whole 726, pieces of 512 148, of 128 102; 16 heads whole 736, pieces of 2048 531,
+// 512 317; 4 x 4096 x 16 whole 977, 4 pieces each 1117; 517 x 2 heads whole 102, 5 pieces 52.
 // Pieces are chosen to fill the multiprocessors once or up to as often as there is room.
 void gdn_linattn_plan(bool tensor_cores, int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment,
                       int64_t *piece_slots)
 {
     const double wide = 0.4 + 0.6 * ((dk + 31) / 32) / 4;  // tiles of d_k on CUDA cores
     const double kWhole = tensor_cores ? 2.05 : 21.5 * wide, kWholeMore = tensor_cores ? kWhole : 10 * wide, kWholeStart = 10;
-    const double kCut = tensor_cores ? 3.5 : 31.5 * wide, kCutMore = tensor_cores ? kCut : 14 * wide, kCutStart = 26;
+    const double kCut = tensor_cores ? 3.5 : 31.5 * wide, kCutMore = tensor_cores ? kCut : 14 * wide, kCutStart = 20;
     const int kFills = tensor_cores ? 3 : 4;
     constexpr double kBytesPerUs = 6e6;
     constexpr int64_t kChunk = 128;
@@ -557,15 +536,13 @@ cudaError_t gdn_launch_linattn_fwd(const GdnLinattnArgs &a, cudaStream_t s, int 
     if (a.segment) {
         cudaError_t e = pass(a, true, s);
         if (e != cudaSuccess) return e;
-        const int64_t warps = a.pieces * a.heads, blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
         const int per_head = (int)(((int64_t)a.dv * a.dk + 4 * kThreads - 1) / (4 * kThreads));
         const int64_t chains = (int64_t)a.N * a.heads * per_head;
-        if (blocks > 0x7fffffff || chains > 0x7fffffff) return cudaErrorInvalidConfiguration;
-        gdn_linattn_decay_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a);
+        if (chains > 0x7fffffff) return cudaErrorInvalidConfiguration;
         gdn_linattn_chain_kernel<<<(unsigned)chains, kThreads, 0, s>>>(a, per_head);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        *launches = 3;
+        *launches = 2;
     }
     *launches += 1;
     return pass(a, false, s);

@@ -77,6 +77,18 @@ __device__ __forceinline__ float chained_decay_of(float x)
     return x < -126.f ? 0.f : x != x ? x : x > 127.f ? ex2(x) : p * __int_as_float(((int)n + 127) << 23);
 }
 
+// The decay over a piece, from its chunks' sums as they come.
+struct PieceDecay {
+    double sum = 0.;
+    bool cut = false;
+    __device__ __forceinline__ void add(float total, unsigned mask)
+    {
+        sum += total;
+        cut |= mask != 0;
+    }
+    __device__ __forceinline__ float all() const { return cut ? 0.f : chained_decay_of((float)sum); }
+};
+
 // What a block works on: a whole sequence or a piece of one, and the states it
 // reads and writes.
 struct Unit {

@@ -481,6 +481,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 p += dk;
             }
         }
+        PieceDecay piece;
 #pragma unroll 1
         for (int c = -1; c < chunks; ++c) {
             const int st = c & 1;
@@ -488,7 +489,10 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 wait(&s.dec_ready[st], c >> 1);
                 const float4 total = *reinterpret_cast<const float4 *>(s.total[st]);
                 const uint4 mask = *reinterpret_cast<const uint4 *>(s.mask[st]);
-                const float all = mask.x | mask.y | mask.z | mask.w ? 0.f : chained_decay_of(total.x + total.y + total.z + total.w);
+                const float sum = total.x + total.y + total.z + total.w;
+                const unsigned cut = mask.x | mask.y | mask.z | mask.w;
+                const float all = cut ? 0.f : chained_decay_of(sum);
+                if (kStates && t == 0) piece.add(sum, cut);
                 arrive_warp(&s.dec_free[st]);
                 if (all == 0.f)
 #pragma unroll
@@ -524,6 +528,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 arrive_warp(&s.s_ready);
             }
         }
+        if (kStates && v0 + c0 == 0 && t == 0) a.piece_decay[unit / tiles] = piece.all();
         if (u.out && !*abort_flag) {
             float *p = u.out + at;
 #pragma unroll

@@ -448,7 +448,7 @@ gdn_status_t gdn_group_norm(const void *x, const void *gate, const float *weight
  *               time; NULL allowed when that size is 0
  * bf16 with d_k, d_v and row strides multiples of 8 and q, k, v, o aligned to 16
  * bytes runs on the tensor cores; everything else in fp32 on CUDA cores.  One
- * kernel, or four when sequences are cut; path 9.
+ * kernel, or three when sequences are cut; path 9.
  */
 size_t gdn_linattn_fwd_workspace_size(int B, int T, int heads, int d_k, int d_v,
                                       const int32_t *cu_seqlens, int segment, int tensor_cores);
