@@ -145,7 +145,7 @@ def test_a_token_sees_nothing_of_those_behind_it(dtype, name, value):
     cu = torch.tensor([0, 150, 250], dtype=torch.int32, device="cuda")
     x = make((1, 250), 2, 1, 64, 64, dtype, seed=13)
     x = {n: t.clone() for n, t in x.items()}
-    want, _ = gdn.gdn_linattn_fwd(**x, cu_seqlens=cu)
+    want, states = gdn.gdn_linattn_fwd(**x, cu_seqlens=cu)
     for t, first, last in ((140, 0, 140), (150, 0, 150)):
         y = {n: v.clone() for n, v in x.items()}
         y[name][0, t] = value
@@ -153,8 +153,25 @@ def test_a_token_sees_nothing_of_those_behind_it(dtype, name, value):
         assert torch.equal(o[0, first:last], want[0, first:last])
         if t == 140:
             assert torch.equal(o[0, 150:], want[0, 150:])
-            assert bool(torch.isfinite(S[1]).all())
+            assert torch.equal(S[1], states[1])
+        else:
+            assert torch.equal(S[0], states[0])
     assert gdn.gdn_get_device_status() == 0 and sum(lengths) == 250
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["k", "v", "log_decay"])
+def test_a_piece_sees_nothing_of_those_behind_it(dtype, name):
+    """The same where the sequence is cut: outputs ahead of the token, and the other sequences' outputs and states."""
+    cu = torch.tensor([0, 300, 640], dtype=torch.int32, device="cuda")
+    x = {n: t.clone() for n, t in make((1, 640), 2, 1, 64, 64, dtype, seed=23).items()}
+    want, states = gdn.gdn_linattn_fwd(**x, cu_seqlens=cu, segment=128)
+    for t, first, last, other in ((290, 0, 290, 1), (300, 0, 300, 0), (200, 0, 200, 1)):
+        y = {n: v.clone() for n, v in x.items()}
+        y[name][0, t] = float("inf")
+        o, S = gdn.gdn_linattn_fwd(**y, cu_seqlens=cu, segment=128)
+        assert torch.equal(o[0, first:last], want[0, first:last]) and torch.equal(S[other], states[other])
+    assert gdn.gdn_get_device_status() == 0
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
