@@ -436,20 +436,19 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J]);
                     float x[32];
                     ld_cols(lane_addr(p, quad, 32 * J), x);
-                    if (J == I) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 w = inverse[j];
+                        unpack2(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), x[4 * j], x[4 * j + 1]);
+                        unpack2(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), x[4 * j + 2], x[4 * j + 3]);
+                    }
+                    if (J == I) {  // the factor of a token behind may be infinite: a rise, then a fall
 #pragma unroll
                         for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
                     }
                     uint32_t w16[16];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 w = inverse[j];
-                        float lo, hi;
-                        unpack2(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), lo, hi);
-                        w16[2 * j] = narrow_pair(lo, hi);
-                        unpack2(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), lo, hi);
-                        w16[2 * j + 1] = narrow_pair(lo, hi);
-                    }
+                    for (int j = 0; j < 16; ++j) w16[j] = narrow_pair(x[2 * j], x[2 * j + 1]);
                     tmem_st16(lane_addr(p, quad, 32 * J), w16);
                     if (J > 0) sum += s.total[st][J - 1];
                 }
