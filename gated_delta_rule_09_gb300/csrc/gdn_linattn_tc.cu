@@ -15,23 +15,23 @@
 // of the products waits for more than the one before it.  Q, K and V enter as they
 // are (products of bf16 are exact in fp32), and sums are fp32.  The decayed V enters
 // as three bf16 parts, whose sum is the value to fp32: final states are 3e-7 to 6e-7 off
-// in the 2-norm (two parts: 2.0e-6, and 67.5 us instead of 78).  P and the state enter
-// the outputs' products rounded once to bf16, which is what the outputs themselves are
-// rounded to: 2.3e-3 off, 1.7e-3 of it from the outputs' own rounding (in two parts each
-// 1.7e-3; that took 85 us where one part took 72, everything else alike).
+// in the 2-norm (two parts: 2.0e-6).  P and the state enter the outputs' products as two
+// bf16 parts each, which leave 2^-16: outputs are off by their own rounding, 1.7e-3 (one
+// part each: 2.3e-3).
 //
-// 4 x 4096 tokens x 16 heads of 128: 78 us, 3.5 TB/s, 52 % of the HBM copy rate; a chunk
-// takes 1.9 us.  No one thing bounds it: of the 67.5 us that it took with two parts, P
-// left out gave back 4 us, the outputs 1, the state's hand-over 1, the decayed V 7; the
-// tensor pipe was busy for about half of the time (46 cycles for a product of 128 x 64 x
-// 16), each scheduler issued in half of its cycles, and the rest is hand-overs.
+// 4 x 4096 tokens x 16 heads of 128: 94 us, 2.9 TB/s, 43 % of the HBM copy rate; a chunk
+// takes 2.4 us.  No one thing bounds it: P unsplit gave back 4 us, the second parts'
+// products 7, the outputs 5, the copies of Q 4, and shared memory moves some 510 KB a
+// chunk, most of what 128 bytes a cycle are.  Both parts of S^T as one product of 128
+// columns, Q read once, took 96: its sums then have one stage.
 //
 // Roles, in groups of four warps: forming P (tensor memory to tensor memory, a row per
 // thread), keeping the state and writing its parts for the next chunk, summing the
 // decays and forming the decayed V, writing the outputs; then single warps that issue
-// the products with P, K^T V, Q S^T, and the tensor copies into rings of two
-// stages, with later chunks fetched to L2 ahead.  All loops over chunks are kept
-// small: together they have to stay in the instruction cache.
+// P V, K^T V, Q S^T and Q K^T, and the tensor copies into rings of two stages (K and V)
+// and one (Q, whose next tile comes after Q S^T: the second part of S^T has the room),
+// with later chunks fetched to L2 ahead.  All loops over chunks are kept small: together
+// they have to stay in the instruction cache.
 //
 // Every wait is bounded: on timeout the block raises GDN_DEV_WAIT_TIMEOUT, issues
 // no more copies and winds down with waits of 50 us, enough for what is in flight.
@@ -55,7 +55,8 @@ constexpr int kSG = 1;
 constexpr int kWarpS = 4, kWarpW = kWarpS + 4 * kSG, kWarpO = kWarpW + 4, kWarpIssue = kWarpO + 4;
 constexpr int kThreads = (kWarpIssue + 4) * 32;
 constexpr int kParts = 3;   // of the decayed V
-constexpr int kRing = 2;    // stages of V, which the outputs take over: two of them wait for each other
+constexpr int kHalves = 2;  // parts of P and of the state
+constexpr int kRing = 3;    // stages of V, which the outputs take over: two of them wait for each other (98 us, three 94)
 constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one that is copied
 // Sums of decays within a block of 32, log 2, that go as products of two factors, 2^-in_j
 // and one that is zero below 2^-126: what is lost is below 2^(90 - 126) of a product (with
@@ -66,23 +67,22 @@ constexpr uint64_t kDrainNs = 50000;  // a wait's bound once the block has given
 
 // Shared memory: tiles of 128-byte rows, 128-byte swizzle.
 constexpr int kTile = kC * 128;           // 128 rows
-constexpr int kOffQ = 0;                  // 2 stages x 2 halves of d_k
-constexpr int kOffK = kOffQ + 4 * kTile;
+constexpr int kOffQ = 0;                  // 2 halves of d_k
+constexpr int kOffK = kOffQ + 2 * kTile;  // 2 stages of them
 constexpr int kOffV = kOffK + 4 * kTile;  // kRing stages
 constexpr int kOffW = kOffV + kRing * kTile;  // decayed V in parts
-constexpr int kOffS = kOffW + kParts * kTile;  // S^T
-constexpr int kOffSmall = kOffS + kTile;
+constexpr int kOffS = kOffW + kParts * kTile;  // S^T in parts
+constexpr int kOffSmall = kOffS + kHalves * kTile;
 
 struct Small {
     // decays of two chunks: sums up to and with a token within its block of 32, their
     // inverse factors 2^-in, and the blocks' sums
     float in[2][kC], inverse[2][kC], total[2][4];
-    unsigned mask[2][4], steep[2][4];  // tokens that forget; a sum on the way is 2^kPlain or more
-    int odd[2];             // V has infinities or NaN
-    uint64_t full[2], v_full[kRing], kq_free[2], v_free[kRing], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2], p_ready[2],
-        o_staged[kRing], i_full[2],
-        w_half[2], w_gone[2];
-    uint64_t p_free, u_full, u_free, s_ready, o_full;
+    unsigned mask[2][4], steep[2][4];  // tokens that forget; whose sum is 2^kPlain or more
+    unsigned odd[2][4];     // tokens whose V has infinities or NaN
+    uint64_t k_full[2], v_full[kRing], k_free[2], v_free[kRing], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2],
+        p_ready[2], p_free[2], o_staged[kRing], i_full[2], w_half[2], w_gone[2];
+    uint64_t q_full, q_free, u_full, u_free, s_ready, o_full;
     uint32_t tmem;
     int abort_flag;
 };
@@ -90,7 +90,7 @@ constexpr int kSmemBytes = kOffSmall + (int)sizeof(Small);
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
 // Tensor memory, 512 columns: Q K^T, then P in its place, x 2 | Q S^T x 2 | P V | U.
-// P of 32 tokens takes the first 16 columns of their 32 products.
+// The parts of P of 32 tokens take the columns of their 32 products: 16 and 16.
 constexpr uint32_t kColP = 0, kColI = 256, kColO = 384, kColU = 448;
 
 // A wait suspends the warp for as long as the hardware lets it; the clock is looked at
@@ -185,17 +185,17 @@ __device__ __forceinline__ uint32_t ld_col(uint32_t taddr)
     return v;
 }
 
-// Two values as pairs of bf16 parts, each the rounded rest of those before it: their
-// sum is the value to 2^-26.  `sign` becomes NaN where a value is infinite or NaN, whose
-// other parts then are NaN.
-__device__ __forceinline__ void split(f32x2 v, uint32_t (&part)[kParts], f32x2 &sign)
+// Two values as pairs of N bf16 parts, each the rounded rest of those before it: what
+// their sum leaves of the value is 2^-8N.  `sign` becomes NaN where a value is infinite or
+// NaN, whose other parts then are NaN.
+template <int N> __device__ __forceinline__ void split(f32x2 v, uint32_t (&part)[N], f32x2 &sign)
 {
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
+    for (int p = 0; p < N; ++p) {
         float x, y;
         unpack2(v, x, y);
         part[p] = narrow_pair(x, y);
-        if (p + 1 < kParts)
+        if (p + 1 < N)
             v = fma2(pack2(__uint_as_float(part[p] << 16), __uint_as_float(part[p] & 0xffff0000u)), dup2(-1.f), v);
         if (p == 0) sign = fma2(v, dup2(0.f), sign);
     }
@@ -216,12 +216,12 @@ __device__ __forceinline__ uint32_t mend(uint32_t hi, uint32_t lo)
     return lo;
 }
 
-__device__ __noinline__ void mend_row(uint8_t *tiles, int r)
+__device__ __noinline__ void mend_row(uint8_t *tiles, int parts, int r)
 {
 #pragma unroll 1
     for (int w = 0; w < 32; ++w) {
         const uint32_t at = sw128(r, w / 4) + w % 4 * 4;
-        for (int p = 1; p < kParts; ++p) {
+        for (int p = 1; p < parts; ++p) {
             uint32_t *lo = reinterpret_cast<uint32_t *>(tiles + p * kTile + at);
             *lo = mend(*reinterpret_cast<const uint32_t *>(tiles + at), *lo);
         }
@@ -235,23 +235,31 @@ __device__ __noinline__ void zero_row(uint8_t *tiles, int r)
         *reinterpret_cast<uint4 *>(tiles + (c >> 3) * kTile + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
 }
 
-// 8 values into 16-byte column c of row r of kParts tiles.
-__device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4], f32x2 &sign)
+// 8 values into 16-byte column c of row r of N tiles.
+template <int N> __device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4], f32x2 &sign)
 {
-    uint32_t w[4][kParts];
+    uint32_t w[4][N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split(x[i], w[i], sign);
+    for (int i = 0; i < 4; ++i) split<N>(x[i], w[i], sign);
     const uint32_t at = sw128(r, c);
 #pragma unroll
-    for (int p = 0; p < kParts; ++p)
+    for (int p = 0; p < N; ++p)
         *reinterpret_cast<uint4 *>(tiles + p * kTile + at) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+}
+
+// The parts of P of a row and 32 tokens.
+__device__ __forceinline__ void st_p(uint32_t p, int quad, int J, const uint32_t (&hi)[16], const uint32_t (&lo)[16])
+{
+    tmem_st16(lane_addr(p, quad, 32 * J), hi);
+    tmem_st16(lane_addr(p, quad, 32 * J + 16), lo);
 }
 
 // P of one row in the cases that the plain path leaves: tokens that forget, and blocks
 // with a decay of 2^90 or more on the way.  An exponential an entry: 217 us where the
-// plain path takes 78, if every block of 32 goes this way.
-__device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, float scale, const float *in, const float *total,
-                                        const unsigned *mask)
+// plain path takes 78, if every block of 32 goes this way.  Rows that come before any such
+// token (`own` false) have the plain path's factors: the same bits, whatever comes later.
+__device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, bool own, float scale, const float *in,
+                                        const float *inverse, const float *total, const unsigned *mask)
 {
     const float mine = in[32 * I + lane];
     float sum = mine;
@@ -261,18 +269,25 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, f
     for (int J = I; J >= 0; --J) {
         float x[32];
         ld_cols(lane_addr(p, quad, 32 * J), x);
-        uint32_t w16[16];
+        uint32_t hi[16], lo[16];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float w = in[32 * J + j];
             const bool seen = J == I ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
-            const float f = decay_of(J == I ? mine - w : sum + (total[J] - w));
-            x[j] = seen && f != 0.f ? x[j] * (f * scale) : 0.f;
+            const float f = own ? decay_of(J == I ? mine - w : sum + (total[J] - w)) * scale
+                                : decay_of(J == I ? sum : sum + total[J]) * scale * inverse[32 * J + j];
+            x[j] = seen && f != 0.f ? x[j] * f : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) w16[j] = narrow_pair(x[2 * j], x[2 * j + 1]);
+        for (int j = 0; j < 16; ++j) {
+            uint32_t part[kHalves];
+            f32x2 sign = 0;
+            split<kHalves>(pack2(x[2 * j], x[2 * j + 1]), part, sign);
+            hi[j] = part[0];
+            lo[j] = mend(part[0], part[1]);
+        }
         __syncwarp();
-        tmem_st16(lane_addr(p, quad, 32 * J), w16);
+        st_p(p, quad, J, hi, lo);
         if (J < I) {
             sum += total[J];
             cut = cut || mask[J];
@@ -280,32 +295,46 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, f
     }
 }
 
-// P V of one row and 32 columns for a chunk whose V is infinite or NaN somewhere: a
-// token must see nothing of those behind it, and zero times infinity is NaN.  To the
-// columns at o, in place of what the product left there.
-__device__ __noinline__ void odd_row(uint32_t p, uint32_t o, int quad, int i, int first, const uint8_t *V)
+// A row of V that has infinities or NaN, as P V gets it: in their place the smallest
+// numbers there are, one for each kind, which are lost in any sum.  A token must see
+// nothing of those behind it, and zero times infinity is NaN; who sees the row gets its
+// infinities from odd_row.
+__device__ __noinline__ void code_row(uint8_t *V, int r)
+{
+#pragma unroll 1
+    for (int w = 0; w < 32; ++w) {
+        uint32_t *at = reinterpret_cast<uint32_t *>(V + sw128(r, w / 4) + w % 4 * 4);
+        uint32_t out = 0;
+#pragma unroll
+        for (int e = 0; e < 32; e += 16) {
+            const uint32_t h = *at >> e & 0xffffu, m = h & 0x7fffu;
+            out |= (m > 0x7f80u ? 2u : m == 0x7f80u ? (h & 0x8000u) | 1u : m < 3u ? 0u : h) << e;
+        }
+        *at = out;
+    }
+}
+
+// What the coded rows of V add to P V of a token that sees them, tokens `first` to i: to the
+// columns at o.
+__device__ __noinline__ void odd_row(uint32_t p, uint32_t o, int quad, int i, int first, const unsigned *rows, const uint8_t *V)
 {
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
         float acc[32];
-#pragma unroll
-        for (int d = 0; d < 32; ++d) acc[d] = 0.f;
+        ld_cols(lane_addr(o, quad, 32 * half), acc);
 #pragma unroll 1
-        for (int w = 0; w < 64; ++w) {
+        for (int j = 0; j < kC; ++j) {
+            if (!(rows[j >> 5] >> (j & 31) & 1)) continue;
             __syncwarp();
-            const uint32_t pair = ld_col(lane_addr(p, quad, w / 16 * 32 + w % 16));
-#pragma unroll 1
-            for (int e = 0; e < 2; ++e) {
-                const int j = 2 * w + e;
-                const float f = __uint_as_float(e ? pair & 0xffff0000u : pair << 16);
-                if (j > i || j < first) continue;
+            const int w = j >> 1, at = w / 16 * 32 + w % 16;
+            const uint32_t hi = ld_col(lane_addr(p, quad, at)), lo = ld_col(lane_addr(p, quad, at + 16));
+            if (j > i || j < first) continue;
+            const float h = __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16);
+            const float f = h == 0.f ? copysignf(1.f, h) : h + __uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[8];
-                    widen(*reinterpret_cast<const uint4 *>(V + sw128(j, half * 4 + q)), v);
-#pragma unroll
-                    for (int d = 0; d < 8; ++d) acc[q * 8 + d] = fmaf(f, v[d], acc[q * 8 + d]);
-                }
+            for (int d = 0; d < 32; ++d) {
+                const uint32_t v = *reinterpret_cast<const unsigned short *>(V + sw128(j, half * 4 + d / 8) + d % 8 * 2);
+                if ((v & 0x7fffu) - 1u < 2u) acc[d] = fmaf(f, __uint_as_float(v == 2u ? 0x7fc00000u : (v & 0x8000u) << 16 | 0x7f800000u), acc[d]);
             }
         }
         __syncwarp();
@@ -341,24 +370,27 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     if (!find_unit(a, unit / tiles / a.heads, h, kStates, u)) return;
     const int chunks = (int)(((int64_t)u.len + kC - 1) / kC), dk = a.dk;
 
-    // Tensor copies of a chunk's K and Q, to the ring or ahead to L2, and of its V.
+    // Tensor copies of a chunk's K or Q, to shared memory or ahead to L2, and of its V.
     const int g = h / (a.heads / a.groups), halves = dk > 64 ? 2 : 1;
     auto row = [&](int c) { return (int)(u.row + (int64_t)c * kC); };
-    auto load_kq = [&](int c, bool ahead) {
-        uint64_t *bar = &s.full[c & 1];
-        if (!ahead) mbar_arrive_expect_tx(bar, (uint32_t)(halves * (kStates ? 1 : 2)) * kTile);
+    auto load_k = [&](int c, bool ahead) {
+        uint64_t *bar = &s.k_full[c & 1];
+        if (!ahead) mbar_arrive_expect_tx(bar, (uint32_t)halves * kTile);
 #pragma unroll 1
-        for (int i = 0; i < halves; ++i) {
-            const int at = ((c & 1) * 2 + i) * kTile;
+        for (int i = 0; i < halves; ++i)
             if (ahead) fetch_l2(&tm_k, 64 * i, g, row(c));
-            else tma_load_3d(sm + kOffK + at, &tm_k, bar, 64 * i, g, row(c));
+            else tma_load_3d(sm + kOffK + ((c & 1) * 2 + i) * kTile, &tm_k, bar, 64 * i, g, row(c));
+    };
+    auto load_q = [&](int c, bool ahead) {
+        if (!ahead) mbar_arrive_expect_tx(&s.q_full, (uint32_t)halves * kTile);
 #pragma unroll 1
-            for (int b = 0; b < (kStates ? 0 : 4); ++b) {
+        for (int i = 0; i < halves; ++i)
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
                 const int from = row(c) + 32 * row_block(b, c);
                 if (ahead) fetch_l2(&tm_q, 64 * i, g, from);
-                else tma_load_3d(sm + kOffQ + at + b * (kTile / 4), &tm_q, bar, 64 * i, g, from);
+                else tma_load_3d(sm + kOffQ + i * kTile + b * (kTile / 4), &tm_q, &s.q_full, 64 * i, g, from);
             }
-        }
     };
     auto load_v = [&](int c) {
         mbar_arrive_expect_tx(&s.v_full[c % kRing], kTile);
@@ -367,8 +399,9 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     };
     if (warp == kWarpIssue + 3 && elect_one()) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.kq_free[i], kStates ? 1 : 3);
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_free[i], kStates ? 1 : 2);
+            mbar_init(&s.p_free[i], 1);
             mbar_init(&s.dec_ready[i], 4);
             mbar_init(&s.dec_free[i], 4 * (kStates ? kSG : kSG + 2));
             mbar_init(&s.w_ready[i], 4);
@@ -384,7 +417,8 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             mbar_init(&s.v_free[i], 1);
             mbar_init(&s.o_staged[i], 4);
         }
-        mbar_init(&s.p_free, 1);
+        mbar_init(&s.q_full, 1);
+        mbar_init(&s.q_free, 1);
         mbar_init(&s.u_full, 1);
         mbar_init(&s.u_free, 4 * kSG);
         mbar_init(&s.s_ready, 4 * kSG);
@@ -394,11 +428,15 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
         fence_async_smem();
         // the first chunks are on their way while tensor memory is allocated
 #pragma unroll 1
-        for (int c = 0; c < 2 && c < chunks; ++c) load_kq(c, false);
+        for (int c = 0; c < 2 && c < chunks; ++c) load_k(c, false);
+        if (!kStates) load_q(0, false);
 #pragma unroll 1
         for (int c = 0; c < kRing && c < chunks; ++c) load_v(c);
 #pragma unroll 1
-        for (int c = 2; c < 2 + kAhead && c < chunks; ++c) load_kq(c, true);
+        for (int c = 1; c < 2 + kAhead && c < chunks; ++c) {
+            if (c > 1) load_k(c, true);
+            if (!kStates && c < 1 + kAhead) load_q(c, true);
+        }
         prefetch_tensormap(&tm_o);
     }
     if (warp == 0) {
@@ -423,38 +461,53 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where no sum
                 // in J, the block of j, reaches 90; within a block without the middle factor.
                 float sum = s.in[st][32 * I + lane];
-                bool odd = false;
+                const unsigned here = s.mask[st][I] | s.steep[st][I];
+                bool own = here & (0xffffffffu >> (31 - lane));
 #pragma unroll 1
-                for (int J = 0; J <= I; ++J) odd |= s.mask[st][J] || s.steep[st][J];
+                for (int J = 0; J < I; ++J) own |= s.mask[st][J] || s.steep[st][J];
+                const bool odd = own || here;
                 wait(&s.qk_full[st], c >> 1);
                 __syncwarp();
                 tc_fence_after();
-                if (odd) odd_decays(p, quad, I, lane, a.scale, s.in[st], s.total[st], s.mask[st]);
+                if (odd) odd_decays(p, quad, I, lane, own, a.scale, s.in[st], s.inverse[st], s.total[st], s.mask[st]);
 #pragma unroll 1
                 for (int J = I; J >= 0 && !odd; --J) {
                     const f32x2 f = dup2(decay_of(sum) * a.scale);
-                    const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J]);
-                    float x[32];
-                    ld_cols(lane_addr(p, quad, 32 * J), x);
+                    uint32_t hi[16], lo[16];
+                    f32x2 sign = 0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 w = inverse[j];
-                        unpack2(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), x[4 * j], x[4 * j + 1]);
-                        unpack2(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), x[4 * j + 2], x[4 * j + 3]);
+                    for (int half = 0; half < 2; ++half) {
+                        const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J + 16 * half]);
+                        float x[16];
+                        ld_cols(lane_addr(p, quad, 32 * J + 16 * half), x);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 w = inverse[j];
+                            unpack2(mul2(pack2(x[4 * j], x[4 * j + 1]), mul2(f, pack2(w.x, w.y))), x[4 * j], x[4 * j + 1]);
+                            unpack2(mul2(pack2(x[4 * j + 2], x[4 * j + 3]), mul2(f, pack2(w.z, w.w))), x[4 * j + 2], x[4 * j + 3]);
+                        }
+                        if (J == I) {  // the factor of a token behind may be infinite: a rise, then a fall
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) x[j] = 16 * half + j <= lane ? x[j] : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            uint32_t part[kHalves];
+                            split<kHalves>(pack2(x[2 * j], x[2 * j + 1]), part, sign);
+                            hi[8 * half + j] = part[0];
+                            lo[8 * half + j] = part[1];
+                        }
                     }
-                    if (J == I) {  // the factor of a token behind may be infinite: a rise, then a fall
+                    if (is_odd(sign))
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
-                    }
-                    uint32_t w16[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w16[j] = narrow_pair(x[2 * j], x[2 * j + 1]);
-                    tmem_st16(lane_addr(p, quad, 32 * J), w16);
+                        for (int j = 0; j < 16; ++j) lo[j] = mend(hi[j], lo[j]);
+                    __syncwarp();
+                    st_p(p, quad, J, hi, lo);
                     if (J > 0) sum += s.total[st][J - 1];
                 }
-                const uint32_t zero[16] = {};
+                const float zero[32] = {};
 #pragma unroll 1
-                for (int J = I + 1; J < 4; ++J) tmem_st16(lane_addr(p, quad, 32 * J), zero);
+                for (int J = I + 1; J < 4; ++J) tmem_st32(lane_addr(p, quad, 32 * J), zero);
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_warp(&s.dec_free[st]);
@@ -512,17 +565,13 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             }
             if (!kStates && c + 1 < chunks) {
                 if (c >= 0) wait(&s.i_full[st], c >> 1);  // Q S^T of this chunk has read it
+                f32x2 sign = 0;
 #pragma unroll
                 for (int q = 0; q < kCols / 8 && (mine || c < 0); ++q) {
-                    uint32_t w16[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float lo, hi;
-                        unpack2(S[4 * q + e], lo, hi);
-                        w16[e] = narrow_pair(lo, hi);
-                    }
-                    *reinterpret_cast<uint4 *>(sm + kOffS + sw128(t, c0 / 8 + q)) = make_uint4(w16[0], w16[1], w16[2], w16[3]);
+                    const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
+                    st_parts<kHalves>(sm + kOffS, t, c0 / 8 + q, x, sign);
                 }
+                if (is_odd(sign)) mend_row(sm + kOffS, kHalves, t);
                 fence_async_smem();
                 arrive_warp(&s.s_ready);
             }
@@ -553,13 +602,13 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             if (c > 1) wait(&s.dec_free[st], (c - 2) >> 1);
             s.in[st][t] = d.in;
             s.inverse[st][t] = ex2(-d.in);
-            const bool steep = __any_sync(0xffffffffu, !(fabsf(d.in) < kPlain));
+            const unsigned steep = __ballot_sync(0xffffffffu, !(fabsf(d.in) < kPlain));
             if (lane == 0) {
                 s.total[st][quad] = d.total;
                 s.mask[st][quad] = d.mask;
                 s.steep[st][quad] = steep;
+                s.odd[st][quad] = 0;
             }
-            if (t == 0) s.odd[st] = 0;
             arrive_warp(&s.dec_ready[st]);
             named_sync(1, 128);
             bool cut = d.cut_behind(lane);
@@ -571,7 +620,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             }
             const float w = cut ? 0.f : decay_of(sum);
             wait(&s.v_full[c % kRing], c / kRing);
-            if (n < kC) wait(&s.full[st], c >> 1);  // K's rows past the end, below
+            if (n < kC) wait(&s.k_full[st], c >> 1);  // K's rows past the end, below
             if (c > 0) wait(&s.w_gone[quad >> 1], c - 1);  // the product has read the last chunk's
             uint8_t *V = sm + kOffV + c % kRing * kTile, *W = sm + kOffW;
             if (t < n) {
@@ -588,11 +637,14 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                             x[e] = pack2(f[2 * e], f[2 * e + 1]);
                             x[e] = mul2(x[e], dup2(w));
                         }
-                        st_parts(W, t, q + r, x, sign);
+                        st_parts<kParts>(W, t, q + r, x, sign);
                     }
                 if (is_odd(sign)) {  // infinite or NaN, decayed or not
-                    s.odd[st] = 1;
-                    mend_row(W, t);
+                    if (!kStates) {
+                        atomicOr(&s.odd[st][quad], 1u << lane);
+                        code_row(V, t);
+                    }
+                    mend_row(W, kParts, t);
                     if (w == 0.f) zero_row(W, t);  // what comes after has forgotten it
                 }
             } else {  // rows past the end may be another sequence's
@@ -632,17 +684,18 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
                 const f32x2 start = dup2(a.scale * decay_of(sum));
                 wait(&s.w_ready[st], c >> 1);
-                const bool odd = s.odd[st];
+                const uint4 odd = *reinterpret_cast<const uint4 *>(s.odd[st]);
                 arrive_warp(&s.dec_free[st]);
                 wait(&s.i_full[st], c >> 1);
                 wait(&s.o_full, c);
                 tc_fence_after();
                 uint8_t *stage = sm + kOffV + c % kRing * kTile;  // V is through, but for odd_row
-                if (odd) {
-                    odd_row(tbase + kColP + 128 * st, tbase + kColO, quad, i, first, stage);
+                if (odd.x | odd.y | odd.z | odd.w) {
+                    const unsigned rows[4] = {odd.x, odd.y, odd.z, odd.w};
+                    odd_row(tbase + kColP + 128 * st, tbase + kColO, quad, i, first, rows, stage);
                     named_sync(2, 128);
                 }
-                if (t == 0) mbar_arrive(&s.p_free);
+                if (t == 0) mbar_arrive(&s.p_free[st]);
                 // Whole chunks go through the place of V and a tensor copy: rows stored from here would take a
                 // transaction per row and store, half of what the memory pipe can do.
                 const bool whole = n == kC;
@@ -679,38 +732,26 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             }
         }
     } else if (warp == kWarpIssue) {
-        // ---- Q K^T and P V, the former two chunks ahead: it takes the place of the latter's P
+        // ---- P V
         if (!kStates && elect_one()) {
             const uint32_t base = smem_u32(sm);
 #pragma unroll 1
-            for (int c = -2; c < chunks; ++c) {
+            for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
                 const uint32_t p = tbase + kColP + 128 * st;
-                if (c >= 0) {
-                    wait(&s.p_ready[st], c >> 1);
-                    wait(&s.v_full[c % kRing], c / kRing);
-                    if (u.len - c * kC < kC) wait(&s.w_ready[st], c >> 1);  // rows past the end are zero
-                    if (c > 0) wait(&s.o_free[st ^ 1], (c - 1) >> 1);
-                    tc_fence_after();
-                    const uint64_t v = sdesc_sw128(base + kOffV + c % kRing * kTile, kTile, 1024);
+                wait(&s.p_ready[st], c >> 1);
+                wait(&s.v_full[c % kRing], c / kRing);
+                wait(&s.w_ready[st], c >> 1);  // V is finite, and zero past the end
+                if (c > 0) wait(&s.o_free[st ^ 1], (c - 1) >> 1);
+                tc_fence_after();
+                const uint64_t v = sdesc_sw128(base + kOffV + c % kRing * kTile, kTile, 1024);
+#pragma unroll
+                for (int part = 0; part < kHalves; ++part)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        mma_f16kind_ts(tbase + kColO, p + 32 * (i >> 1) + 8 * (i & 1), v + mn_step(i),
-                                       idesc_bf16_f32(128, 64, 0, 1), i > 0);
-                    mma_commit(&s.o_full);
-                }
-                if (c + 2 < chunks) {
-                    wait(&s.full[st], (c + 2) >> 1);
-                    if (c >= 0) wait(&s.p_free, c);
-                    tc_fence_after();
-                    const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
-                    const uint64_t k = sdesc_sw128(base + kOffK + st * 2 * kTile, 16, 1024);
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-                        mma_f16kind(p, q + k_step(i), k + k_step(i), idesc_bf16_f32(128, 128, 0, 0), i > 0);
-                    mma_commit(&s.qk_full[st]);
-                    mma_commit(&s.kq_free[st]);
-                }
+                        mma_f16kind_ts(tbase + kColO, p + 32 * (i >> 1) + 16 * part + 8 * (i & 1), v + mn_step(i),
+                                       idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
+                mma_commit(&s.o_full);
             }
         }
     } else if (warp == kWarpIssue + 1) {
@@ -720,7 +761,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
-                wait(&s.full[st], c >> 1);
+                wait(&s.k_full[st], c >> 1);
                 if (c > 0) wait(&s.u_free, c - 1);
                 const uint64_t k = sdesc_sw128(base + kOffK + st * 2 * kTile, kTile, 1024);
                 const uint64_t w = sdesc_sw128(base + kOffW, kTile, 1024);
@@ -738,41 +779,64 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     mma_commit(&s.w_gone[half]);
                 }
                 mma_commit(&s.u_full);
-                mma_commit(&s.kq_free[st]);
+                mma_commit(&s.k_free[st]);
                 if (kStates) mma_commit(&s.v_free[c % kRing]);
             }
         }
     } else if (warp == kWarpIssue + 2) {
-        // ---- Q S^T
+        // ---- Q S^T of a chunk, then Q K^T of the next in the place of P of the one before: Q has one stage
         if (!kStates && elect_one()) {
             const uint32_t base = smem_u32(sm);
+            const uint64_t q = sdesc_sw128(base + kOffQ, 16, 1024);
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                const int st = c & 1;
-                wait(&s.full[st], c >> 1);
-                wait(&s.s_ready, c);
-                if (c > 1) wait(&s.o_free[st], (c - 2) >> 1);
-                tc_fence_after();
-                const uint64_t q = sdesc_sw128(base + kOffQ + st * 2 * kTile, 16, 1024);
-                const uint64_t S = sdesc_sw128(base + kOffS, kTile, 1024);
+            for (int c = -1; c < chunks; ++c) {
+                const int st = c & 1, to = st ^ 1;
+                if (c >= 0) {
+                    wait(&s.s_ready, c);
+                    if (c > 1) wait(&s.o_free[st], (c - 2) >> 1);
+                    tc_fence_after();
+                    const uint64_t S = sdesc_sw128(base + kOffS, kTile, 1024);
 #pragma unroll
-                for (int i = 0; i < KS; ++i)
-                    mma_f16kind(tbase + kColI + 64 * st, q + k_step(i), S + mn_step(i), idesc_bf16_f32(128, 64, 0, 1), i > 0);
-                mma_commit(&s.kq_free[st]);
-                mma_commit(&s.i_full[st]);
+                    for (int part = 0; part < kHalves; ++part)
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+                            mma_f16kind(tbase + kColI + 64 * st, q + k_step(i), S + part * (kTile >> 4) + mn_step(i),
+                                        idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
+                    mma_commit(&s.q_free);
+                    mma_commit(&s.i_full[st]);
+                }
+                if (c + 1 < chunks) {
+                    wait(&s.k_full[to], (c + 1) >> 1);
+                    wait(&s.q_full, c + 1);
+                    if (c > 0) wait(&s.p_free[to], (c - 1) >> 1);
+                    tc_fence_after();
+                    const uint64_t k = sdesc_sw128(base + kOffK + to * 2 * kTile, 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        mma_f16kind(tbase + kColP + 128 * to, q + k_step(i), k + k_step(i), idesc_bf16_f32(128, 128, 0, 0), i > 0);
+                    mma_commit(&s.qk_full[to]);
+                    mma_commit(&s.k_free[to]);
+                }
             }
         }
     } else if (elect_one()) {
-        // ---- tensor copies: K and Q, V, and the outputs that take the place of V, whichever can go on.  Chunks
+        // ---- tensor copies: K, Q, V, and the outputs that take the place of V, whichever can go on.  Chunks
         // ahead of the rings are fetched to L2.
-        int kq = min(2, chunks), put = 0;  // chunks loaded; chunks whose V is through and whose outputs are stored
+        int k = min(2, chunks), q = kStates ? chunks : 1;  // chunks loaded
+        int put = 0;          // chunks whose V is through and whose outputs are stored
         uint64_t idle = 0;    // since when there is nothing to do
-        while ((kq < chunks || put < chunks) && !*abort_flag) {
+        while ((k < chunks || q < chunks || put < chunks) && !*abort_flag) {
             bool moved = false;
-            if (kq < chunks && mbar_test_wait(&s.kq_free[kq & 1], (kq - 2) >> 1 & 1)) {
-                load_kq(kq, false);
-                if (kq + kAhead < chunks) load_kq(kq + kAhead, true);
-                ++kq;
+            if (q < chunks && mbar_test_wait(&s.q_free, (q - 1) & 1)) {
+                load_q(q, false);
+                if (q + kAhead < chunks) load_q(q + kAhead, true);
+                ++q;
+                moved = true;
+            }
+            if (k < chunks && mbar_test_wait(&s.k_free[k & 1], (k - 2) >> 1 & 1)) {
+                load_k(k, false);
+                if (k + kAhead < chunks) load_k(k + kAhead, true);
+                ++k;
                 moved = true;
             }
             if (put < chunks && mbar_test_wait(kStates ? &s.v_free[put % kRing] : &s.o_staged[put % kRing], put / kRing & 1)) {
