@@ -58,10 +58,10 @@ constexpr int kParts = 3;   // of the decayed V
 constexpr int kHalves = 2;  // parts of P and of the state
 constexpr int kRing = 3;    // stages of V, which the outputs take over: two of them wait for each other (98 us, three 94)
 constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one that is copied
-// Sums of decays within a block of 32, log 2, that go as products of two factors, 2^-in_j
-// and one that is zero below 2^-126: what is lost is below 2^(90 - 126) of a product (with
-// 120, 1 % of one).
-constexpr float kPlain = 90.f;
+// Sums of decays within a block of 32, log 2, that go as products of two factors: from
+// -kFall to kRise.  The factors are 2^-in_j 2^-kShift and 2^(sum up to i) 2^kShift, so that
+// neither leaves what fp32 holds before their product is below 2^(kFall - 222).
+constexpr float kFall = 90.f, kRise = 24.f, kShift = 96.f, kTwoShift = 7.9228162514264338e28f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 50000;  // a wait's bound once the block has given up on one
 
@@ -76,9 +76,9 @@ constexpr int kOffSmall = kOffS + kHalves * kTile;
 
 struct Small {
     // decays of two chunks: sums up to and with a token within its block of 32, their
-    // inverse factors 2^-in, and the blocks' sums
+    // inverse factors 2^(-in - kShift), and the blocks' sums
     float in[2][kC], inverse[2][kC], total[2][4];
-    unsigned mask[2][4], steep[2][4];  // tokens that forget; whose sum is 2^kPlain or more
+    unsigned mask[2][4], steep[2][4];  // tokens that forget; whose sum is beyond kFall or kRise
     unsigned odd[2][4];     // tokens whose V has infinities or NaN
     uint64_t k_full[2], v_full[kRing], k_free[2], v_free[kRing], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2],
         p_ready[2], p_free[2], o_staged[kRing], i_full[2], w_half[2], w_gone[2];
@@ -254,8 +254,17 @@ __device__ __forceinline__ void st_p(uint32_t p, int quad, int J, const uint32_t
     tmem_st16(lane_addr(p, quad, 32 * J + 16), lo);
 }
 
-// P of one row in the cases that the plain path leaves: tokens that forget, and blocks
-// with a decay of 2^90 or more on the way.  An exponential an entry: 217 us where the
+// The factor of a row whose sum of decays is x, and of the scale, times 2^kShift.  The
+// exponent is shifted only where that costs none of its digits.
+__device__ __forceinline__ float row_factor(float x, float scale)
+{
+    const bool far = x < -64.f;
+    const float f = decay_of(far ? x + kShift : x) * scale;
+    return far ? f : f * kTwoShift;
+}
+
+// P of one row in the cases that the plain path leaves: tokens that forget, and sums of
+// decays beyond kFall and kRise, over blocks too.  An exponential an entry: 217 us where the
 // plain path takes 78, if every block of 32 goes this way.  Rows that come before any such
 // token (`own` false) have the plain path's factors: the same bits, whatever comes later.
 __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, bool own, float scale, const float *in,
@@ -275,7 +284,7 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, b
             const float w = in[32 * J + j];
             const bool seen = J == I ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
             const float f = own ? decay_of(J == I ? mine - w : sum + (total[J] - w)) * scale
-                                : decay_of(J == I ? sum : sum + total[J]) * scale * inverse[32 * J + j];
+                                : row_factor(J == I ? sum : sum + total[J], scale) * inverse[32 * J + j];
             x[j] = seen && f != 0.f ? x[j] * f : 0.f;
         }
 #pragma unroll
@@ -453,26 +462,31 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     if (warp < kWarpS) {
         // ---- P, in the place of Q K^T: a row per thread, blocks of 32 columns up to its own
         if constexpr (!kStates) {
+            const float limit = 28.f - log2f(fabsf(a.scale));  // row_factor stays below 2^124
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1, I = row_block(quad, c);
                 const uint32_t p = tbase + kColP + 128 * st;
                 wait(&s.dec_ready[st], c >> 1);
-                // The factor of tokens i and j is 2^(in_i + the blocks between) 2^(total_J) 2^-in_j, where no sum
-                // in J, the block of j, reaches 90; within a block without the middle factor.
+                // The factor of tokens i and j is 2^(in_i + the blocks between + total_J) 2^-in_j, where J is the
+                // block of j; within a block without the other sums.
                 float sum = s.in[st][32 * I + lane];
                 const unsigned here = s.mask[st][I] | s.steep[st][I];
                 bool own = here & (0xffffffffu >> (31 - lane));
+                float most = sum;
 #pragma unroll 1
-                for (int J = 0; J < I; ++J) own |= s.mask[st][J] || s.steep[st][J];
-                const bool odd = own || here;
+                for (int J = I; J >= 0; --J) {
+                    if (J < I) most += s.total[st][J], own |= s.mask[st][J] || s.steep[st][J];
+                    own |= !(most <= limit);
+                }
+                const bool odd = __any_sync(0xffffffffu, own);
                 wait(&s.qk_full[st], c >> 1);
                 __syncwarp();
                 tc_fence_after();
                 if (odd) odd_decays(p, quad, I, lane, own, a.scale, s.in[st], s.inverse[st], s.total[st], s.mask[st]);
 #pragma unroll 1
                 for (int J = I; J >= 0 && !odd; --J) {
-                    const f32x2 f = dup2(decay_of(sum) * a.scale);
+                    const f32x2 f = dup2(row_factor(sum, a.scale));
                     uint32_t hi[16], lo[16];
                     f32x2 sign = 0;
 #pragma unroll
@@ -601,8 +615,8 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             next = t + (int64_t)(c + 1) * kC < u.len ? decay[(int64_t)(c + 1) * kC * a.ld_decay] : 0.f;
             if (c > 1) wait(&s.dec_free[st], (c - 2) >> 1);
             s.in[st][t] = d.in;
-            s.inverse[st][t] = ex2(-d.in);
-            const unsigned steep = __ballot_sync(0xffffffffu, !(fabsf(d.in) < kPlain));
+            s.inverse[st][t] = ex2(-d.in) * (1.f / kTwoShift);
+            const unsigned steep = __ballot_sync(0xffffffffu, !(d.in > -kFall && d.in < kRise));
             if (lane == 0) {
                 s.total[st][quad] = d.total;
                 s.mask[st][quad] = d.mask;

@@ -1,8 +1,11 @@
 """Decays that rise, fall and fall again within a block of 32 tokens: finite inputs
-give finite outputs.  Against the definition in fp64."""
+give finite outputs, and what lies behind a steep token is not lost.  Against the
+definition in fp64."""
 import pytest
 
-from test_gpu_linattn import check, make
+import gated_delta_rule_09_gb300 as gdn
+from linattn_exact import agrees, walk
+from test_gpu_linattn import check, make, on_tensor_cores
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +27,25 @@ def test_a_rise_then_a_fall_within_a_block(dtype, at):
     for t in at:                                  # what the rise multiplies stays of ordinary size
         x["k"][0, :t] *= 2.0 ** -30 if at[t] > 0 else 1.0
     check(x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fall,second", [(-62.0, -28.0), (-40.0, -60.0), (-61.0, -61.0), (-30.0, -62.0)])
+def test_tokens_seen_over_two_steep_ones(dtype, fall, second):
+    """A fall early in a block and another early in the next: what is left of the tokens between is all there is."""
+    x = decayed(dtype, 200, {1: fall, 33: second}, seed=33, base=-0.01)
+    x["v"][0, :2] = 0
+    x["v"][0, 32:64] = 0
+    o, S = gdn.gdn_linattn_fwd(**x, scale=0.25)
+    assert gdn.gdn_get_device_status() == 0
+    ro, bo, rS, bS = walk(**x, scale=0.25, parts=on_tensor_cores(x))
+    assert agrees(o, ro, bo) <= 1 and agrees(S[0], rS[0], bS[0] + 1e-37) <= 1
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 40, 2.0 ** -60, -3.0, 0.0])
+def test_scales_of_every_size(scale):
+    """Steep and flat decays under a scale that no factor may take along past what fp32 holds."""
+    x = decayed("bf16", 200, {1: -61.0, 40: 10.0, 70: -30.0}, seed=37)
+    o, _ = gdn.gdn_linattn_fwd(**x, scale=scale)
+    ro, bo, _, _ = walk(**x, scale=scale, parts=True)
+    assert agrees(o, ro, bo) <= 1 and gdn.gdn_get_device_status() == 0
