@@ -32,8 +32,11 @@ template <int DK, int DV> struct Smem {
     float v[DV][kC + 4], P[kC][kC + 4];
     float add[kC], in[kC], start[kC];
     int first[kC];
+    int kept;    // tokens before this one are forgotten by the end of the chunk
     float all;
 };
+
+__device__ __forceinline__ bool not_finite(float f) { return !(fabsf(f) <= 3.402823466e38f); }
 
 // kC rows of W columns, on their way from memory: all of a thread's loads are in
 // flight together.  A warp takes every eighth row.  Zeros past n rows and `cols` columns.
@@ -50,15 +53,22 @@ template <typename E, int W> struct Rows {
             for (int c = 0; c < kCols; ++c)
                 x[i][c] = warp + kStep * i < n && lane + 32 * c < cols ? row[32 * c] : from_f<E>(0.f);
     }
-    template <int L> __device__ __forceinline__ void store(float (*to)[L]) const
+    // To shared memory; whether something of it is infinite or NaN.
+    template <int L> __device__ __forceinline__ bool store(float (*to)[L]) const
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        bool odd = false;
 #pragma unroll
         for (int i = 0; i < kRowsOf; ++i)
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) to[warp + kStep * i][lane + 32 * c] = to_f(x[i][c]);
+            for (int c = 0; c < kCols; ++c) {
+                const float f = to_f(x[i][c]);
+                to[warp + kStep * i][lane + 32 * c] = f;
+                odd |= not_finite(f);
+            }
+        return odd;
     }
-    // Transposed; whether something of it is infinite or NaN.
+    // The same transposed.
     template <int L> __device__ __forceinline__ bool turn(float (*to)[L]) const
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -69,7 +79,7 @@ template <typename E, int W> struct Rows {
             for (int c = 0; c < kCols; ++c) {
                 const float f = to_f(x[i][c]);
                 to[lane + 32 * c][warp + kStep * i] = f;
-                odd |= !(fabsf(f) <= 3.402823466e38f);
+                odd |= not_finite(f);
             }
         return odd;
     }
@@ -128,8 +138,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
     for (int c = 0; c < u.len; c += kC) {
         const int n = min(kC, u.len - c);
         __syncthreads();
-        kr.store(m.k);
-        const bool inf = vr.turn(m.v);
+        const bool inf_k = kr.store(m.k), inf_v = vr.turn(m.v);
         if (!states_only) qr.store(m.q);
         if (t < 32) {
             Decays d;
@@ -139,11 +148,12 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             m.start[lane] = d.cut_upto(lane) ? 0.f : decay_of(d.in);
             m.add[lane] = d.cut_behind(lane) ? 0.f : decay_of(d.after);
             if (lane == 0) {
+                m.kept = first_seen(d.mask, 31);
                 m.all = d.mask ? 0.f : chained_decay_of(d.total);
                 if (states_only) piece.add(d.total, d.mask);
             }
         }
-        const bool odd = __syncthreads_or(inf);
+        const bool odd = __syncthreads_or(inf_k || inf_v);
         load(c + kC);
         float acc[4][OV];
         if (!states_only) {
@@ -221,6 +231,12 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
                     const int i = i0 + 8 * e, d = j0 + 32 * f;
                     if (i < n && d < nv) o[(c + i) * a.ld_o + d] = from_f<E>(a.scale * acc[e][f]);
                 }
+        }
+        if (odd) {  // what is forgotten adds nothing, where its factor of zero would make NaN
+            __syncthreads();
+            for (int i = t; i < m.kept * DK; i += kThreads) m.k[i / DK][i % DK] = 0.f;
+            for (int i = t; i < m.kept * DV; i += kThreads) m.v[i % DV][i / DV] = 0.f;
+            __syncthreads();
         }
         f32x2 s[SV][SK] = {};
 #pragma unroll 1

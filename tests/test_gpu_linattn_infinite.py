@@ -1,0 +1,65 @@
+"""Infinities and NaN in linear attention: forgotten ones do not come back, whole or in pieces."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_09_gb300 as gdn
+from linattn_exact import agrees, walk
+from test_gpu_linattn import make, on_tensor_cores
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+def positive(T, H, G, dk, dv, dtype, seed=0, rate=0.05, extra=0, lead=1):
+    """q and k above zero: an infinity meets no other of the other sign."""
+    x = {n: t.clone() for n, t in make((lead, T), H, G, dk, dv, dtype, seed=seed, rate=rate).items()}
+    for n in "qk":
+        x[n].abs_().add_(0.5)
+    if extra:                                     # rows that tensor copies cannot take
+        for n in "qkv":
+            t = x[n]
+            wide = torch.zeros(*t.shape[:2], t[0, 0].numel() + extra, dtype=t.dtype, device="cuda")
+            wide[..., extra:] = t.flatten(2)
+            x[n] = wide[..., extra:].unflatten(-1, t.shape[2:])
+    return x
+
+
+def check(x, odd=(), state=None, segment=0, pieces=1):
+    """``odd``: (name, index, value).  Bounds are those of the same call without the odd values, whose finite
+    results are the same."""
+    y = {n: t.clone() if t.is_contiguous() else t for n, t in x.items()}
+    for name, at, value in odd:
+        y[name] = y[name].clone() if y[name] is x[name] else y[name]
+        y[name][at] = value
+    plain = {n: t.clone() for n, t in x.items()}
+    for name, at, _ in odd:
+        plain[name][at] = 0
+    tc = on_tensor_cores(y)
+    S0 = None if state is None else torch.nan_to_num(state, nan=0, posinf=0, neginf=0)
+    ro, _, rS, _ = walk(**y, state_in=state)
+    so, bo, sS, bS = walk(**plain, state_in=S0, parts=tc, pieces=pieces)
+    fin = np.isfinite(ro)
+    assert np.allclose(ro[fin], so[fin], rtol=1e-9, atol=1e-30)
+    # an infinite k meets the parts of what it multiplies, on tensor cores, which may have both signs
+    kinds = not (tc and any(name == "k" for name, _, _ in odd))
+    o, S = gdn.gdn_linattn_fwd(**y, state_in=state, segment=segment)
+    assert gdn.gdn_get_device_status() == 0
+    assert agrees(o, ro, bo, kinds) <= 1
+    for i in range(len(rS)):
+        assert agrees(S[i], rS[i], bS[i] + 1e-37, kinds) <= 1
+
+
+FORMS = [("f32", 64, 64, 0), ("bf16", 64, 64, 3), ("f32", 128, 32, 0)]
+
+
+@pytest.mark.parametrize("dtype,dk,dv,extra", FORMS)
+@pytest.mark.parametrize("name", ["k", "v"])
+@pytest.mark.parametrize("value", [INF, NAN])
+@pytest.mark.parametrize("t,forget", [(70, 73), (70, 100), (70, 130), (70, 200), (127, 128), (130, 131), (131, 160)])
+@pytest.mark.parametrize("segment", [0, 128])
+def test_what_is_forgotten_does_not_come_back(dtype, dk, dv, extra, name, value, t, forget, segment):
+    """An odd value, then a token that forgets: in the same 32 tokens, the same chunk, the next, the next piece."""
+    x = positive(300, 2, 1, dk, dv, dtype, seed=t, extra=extra)
+    x["log_decay"][0, forget] = -INF if t % 2 else -100.0
+    check(x, [(name, (0, t, 0, 3), value)], segment=segment, pieces=1 + segment // 128)
