@@ -235,6 +235,25 @@ __device__ __noinline__ void zero_row(uint8_t *tiles, int r)
         *reinterpret_cast<uint4 *>(tiles + (c >> 3) * kTile + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
 }
 
+// Whether a row of K, in `halves` tiles, has infinities or NaN; and zeros in its place.
+__device__ __noinline__ bool odd_k_row(const uint8_t *K, int r, int halves)
+{
+    bool odd = false;
+#pragma unroll 1
+    for (int c = 0; c < 8 * halves; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(K + (c >> 3) * kTile + sw128(r, c & 7));
+        for (uint32_t w : {x.x, x.y, x.z, x.w}) odd |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    }
+    return odd;
+}
+
+__device__ __noinline__ void zero_k_row(uint8_t *K, int r, int halves)
+{
+#pragma unroll 1
+    for (int c = 0; c < 8 * halves; ++c)
+        *reinterpret_cast<uint4 *>(K + (c >> 3) * kTile + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
+}
+
 // 8 values into 16-byte column c of row r of N tiles.
 template <int N> __device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4], f32x2 &sign)
 {
@@ -636,7 +655,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             wait(&s.v_full[c % kRing], c / kRing);
             if (n < kC) wait(&s.k_full[st], c >> 1);  // K's rows past the end, below
             if (c > 0) wait(&s.w_gone[quad >> 1], c - 1);  // the product has read the last chunk's
-            uint8_t *V = sm + kOffV + c % kRing * kTile, *W = sm + kOffW;
+            uint8_t *V = sm + kOffV + c % kRing * kTile, *W = sm + kOffW, *K = sm + kOffK + st * 2 * kTile;
             if (t < n) {
                 f32x2 sign = 0;
 #pragma unroll 1
@@ -663,15 +682,14 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             } else {  // rows past the end may be another sequence's
                 zero_row(W, t);
-                uint8_t *K = sm + kOffK + st * 2 * kTile;
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t off = sw128(t, q);
-                    *reinterpret_cast<uint4 *>(V + off) = zero;
-                    *reinterpret_cast<uint4 *>(K + off) = zero;
-                    if (dk > 64) *reinterpret_cast<uint4 *>(K + kTile + off) = zero;
-                }
+                zero_k_row(V, t, 1);
+                zero_k_row(K, t, halves);
+            }
+            if (__any_sync(0xffffffffu, cut)) {  // an infinite K that is forgotten meets zeros of W: NaN
+                wait(&s.k_full[st], c >> 1);
+                const bool odd = cut && t < n && odd_k_row(K, t, halves);
+                if (!kStates && __any_sync(0xffffffffu, odd)) wait(&s.qk_full[st], c >> 1);
+                if (odd) zero_k_row(K, t, halves);
             }
             fence_async_smem();
             arrive_warp(&s.w_half[quad >> 1]);

@@ -50,7 +50,7 @@ def check(x, odd=(), state=None, segment=0, pieces=1):
         assert agrees(S[i], rS[i], bS[i] + 1e-37, kinds) <= 1
 
 
-FORMS = [("f32", 64, 64, 0), ("bf16", 64, 64, 3), ("f32", 128, 32, 0)]
+FORMS = [("f32", 64, 64, 0), ("bf16", 64, 64, 3), ("f32", 128, 32, 0), ("bf16", 64, 64, 0), ("bf16", 128, 72, 0)]
 
 
 @pytest.mark.parametrize("dtype,dk,dv,extra", FORMS)
