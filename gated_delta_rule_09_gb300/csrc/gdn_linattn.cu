@@ -268,7 +268,10 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
                 const float2 before = *S;
                 float lo, hi;
                 unpack2(s[x][y], lo, hi);
-                *S = make_float2(all == 0.f ? lo : fmaf(all, before.x, lo), all == 0.f ? hi : fmaf(all, before.y, hi));
+                // columns past d_k stay zero: an infinite v makes NaN of their zeros
+                lo = all == 0.f ? lo : fmaf(all, before.x, lo);
+                hi = all == 0.f ? hi : fmaf(all, before.y, hi);
+                *S = make_float2(k0 + 32 * y < dk ? lo : 0.f, k0 + 32 * y + 1 < dk ? hi : 0.f);
             }
     }
     __syncthreads();

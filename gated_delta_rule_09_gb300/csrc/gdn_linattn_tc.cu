@@ -552,7 +552,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
         constexpr int kCols = kDVT / kSG;
         const int c0 = (warp - kWarpS) / 4 * kCols;
         f32x2 S[kCols / 2];
-        const bool mine = 32 * quad < dk;  // the others' rows are not part of S: K^T has nothing there
+        const bool mine = 32 * quad < dk;  // the others' rows are not part of S
         const int64_t at = (int64_t)(v0 + c0) * dk + t;
         const int cols = t < dk ? a.dv - v0 - c0 : 0;
         {
@@ -600,7 +600,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 if (c >= 0) wait(&s.i_full[st], c >> 1);  // Q S^T of this chunk has read it
                 f32x2 sign = 0;
 #pragma unroll
-                for (int q = 0; q < kCols / 8 && (mine || c < 0); ++q) {
+                for (int q = 0; q < kCols / 8 && (t < dk || c < 0); ++q) {  // the rows past d_k stay zero
                     const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
                     st_parts<kHalves>(sm + kOffS, t, c0 / 8 + q, x, sign);
                 }

@@ -1,4 +1,5 @@
-"""Infinities and NaN in linear attention: forgotten ones do not come back, whole or in pieces."""
+"""Infinities and NaN in linear attention: forgotten ones do not come back, whole or in
+pieces, and columns that fill up a tile make none."""
 import numpy as np
 import pytest
 import torch
@@ -63,3 +64,11 @@ def test_what_is_forgotten_does_not_come_back(dtype, dk, dv, extra, name, value,
     x = positive(300, 2, 1, dk, dv, dtype, seed=t, extra=extra)
     x["log_decay"][0, forget] = -INF if t % 2 else -100.0
     check(x, [(name, (0, t, 0, 3), value)], segment=segment, pieces=1 + segment // 128)
+
+
+@pytest.mark.parametrize("dtype,dk,dv,extra", [("f32", 77, 45, 0), ("f32", 40, 64, 0), ("bf16", 40, 64, 0), ("bf16", 72, 72, 0),
+                                               ("bf16", 8, 8, 0), ("bf16", 120, 64, 0), ("bf16", 77, 45, 3)])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+def test_columns_that_fill_up_a_tile_stay_out(dtype, dk, dv, extra, value):
+    """d_k that is no whole tile: an infinite v makes its column infinite from there on, not NaN."""
+    check(positive(300, 2, 2, dk, dv, dtype, seed=dk, extra=extra), [("v", (0, 70, 0, 3), value)])
