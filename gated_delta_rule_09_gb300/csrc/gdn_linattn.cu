@@ -402,7 +402,9 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_step_kernel(const GdnLin
             dot[r] = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                s[r][j] = d == 0.f ? w * kk[j] : fmaf(d, s[r][j], w * kk[j]);
+                // a lane without this column keeps zero: an infinite v would make NaN of it
+                const float add = (VEC ? V * lane : lane + 32 * j) < dk ? w * kk[j] : 0.f;
+                s[r][j] = d == 0.f ? add : fmaf(d, s[r][j], add);
                 dot[r] = fmaf(s[r][j], qq[j], dot[r]);
             }
         }

@@ -1,5 +1,5 @@
 """Infinities and NaN in linear attention: forgotten ones do not come back, whole or in
-pieces, and columns that fill up a tile make none."""
+pieces, and columns that fill up a tile, or lanes without one in a step, make none."""
 import numpy as np
 import pytest
 import torch
@@ -72,3 +72,21 @@ def test_what_is_forgotten_does_not_come_back(dtype, dk, dv, extra, name, value,
 def test_columns_that_fill_up_a_tile_stay_out(dtype, dk, dv, extra, value):
     """d_k that is no whole tile: an infinite v makes its column infinite from there on, not NaN."""
     check(positive(300, 2, 2, dk, dv, dtype, seed=dk, extra=extra), [("v", (0, 70, 0, 3), value)])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(96, 64), (40, 7), (64, 64), (128, 128), (33, 5), (1, 1)])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+def test_steps_of_an_infinite_value(dtype, dk, dv, value):
+    """d_k that leaves lanes of a warp without a column."""
+    x = {n: t[:, 0].contiguous() for n, t in positive(1, 2, 2, dk, dv, dtype, seed=dk, lead=3).items()}
+    y = {n: t.clone() for n, t in x.items()}
+    y["v"][1, 0, 0] = value
+    S0 = torch.randn(3, 2, dv, dk, device="cuda")
+    o, S = gdn.gdn_linattn_step(**y, state_in=S0)
+    lay = lambda z: {n: t[:, None] for n, t in z.items()}  # noqa: E731
+    ro, _, rS, _ = walk(**lay(y), state_in=S0)
+    x["v"][1, 0, 0] = 0
+    _, bo, _, bS = walk(**lay(x), state_in=S0)
+    assert agrees(o[:, None], ro, bo) <= 1
+    assert all(agrees(S[i], rS[i], bS[i]) <= 1 for i in range(3))
