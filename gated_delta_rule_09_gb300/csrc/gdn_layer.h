@@ -96,7 +96,7 @@ struct GdnLinattnArgs {
     int segment;                 // tokens per piece; 0: one piece per sequence
     int64_t pieces;              // piece slots of the whole call, segment > 0
     float *piece_state;          // [piece slot, heads, dv, dk]: what a piece adds, then the state it starts from
-    float *piece_decay;          // [piece slot, heads] decay over the piece
+    float *piece_decay;          // [piece slot, heads] root of the decay over the piece; 0: forgotten
 };
 
 // Pieces a call is cut into, as gdn_ssm_plan, by the kernel it runs on.

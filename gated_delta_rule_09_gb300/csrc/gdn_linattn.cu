@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
 }
 
 // The states that the pieces of each sequence start from, in place of what the
-// pieces add.  A block walks 4 x kThreads elements of one head's state through
+// pieces add; a piece's decay by its root, twice.  A block walks 4 x kThreads elements of one head's state through
 // the pieces; the next piece's are in flight while this one's are added.
 __global__ void __launch_bounds__(kThreads) gdn_linattn_chain_kernel(const GdnLinattnArgs a, int blocks)
 {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_chain_kernel(const GdnLi
             add[x] = next[x];
             if (more && i < per) next[x] = at[a.heads * per + i];
             if (i < per) at[i] = S[x];
-            S[x] = f == 0.f ? add[x] : fmaf(f, S[x], add[x]);
+            S[x] = f == 0.f ? add[x] : fmaf(f * S[x], f, add[x]);
         }
     }
 }

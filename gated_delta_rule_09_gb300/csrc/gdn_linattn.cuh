@@ -77,7 +77,16 @@ __device__ __forceinline__ float chained_decay_of(float x)
     return x < -126.f ? 0.f : x != x ? x : x > 127.f ? ex2(x) : p * __int_as_float(((int)n + 127) << 23);
 }
 
-// The decay over a piece, from its chunks' sums as they come.
+// 2^(x / 2), twice of which takes a state over a sum of decays x whose own 2^x is zero or
+// infinite, though what it multiplies to need not be.  Kept from zero and, for a finite x,
+// from infinity: an infinite state stays infinite and a zero one zero, as token by token.
+__device__ __forceinline__ float half_decay_of(float x)
+{
+    const float h = 0.5f * x;
+    return chained_decay_of(h < -126.f ? -126.f : h > 127.f && h < 3e38f ? 127.f : h);
+}
+
+// The root of the decay over a piece, from its chunks' sums as they come; zero where a token forgets.
 struct PieceDecay {
     double sum = 0.;
     bool cut = false;
@@ -86,7 +95,7 @@ struct PieceDecay {
         sum += total;
         cut |= mask != 0;
     }
-    __device__ __forceinline__ float all() const { return cut ? 0.f : chained_decay_of((float)sum); }
+    __device__ __forceinline__ float all() const { return cut ? 0.f : half_decay_of((float)sum); }
 };
 
 // What a block works on: a whole sequence or a piece of one, and the states it

@@ -1,5 +1,6 @@
 """Infinities and NaN in linear attention: forgotten ones do not come back, whole or in
-pieces, and columns that fill up a tile, or lanes without one in a step, make none."""
+pieces, columns that fill up a tile, or lanes without one in a step, make none, and
+states stay what they are from piece to piece."""
 import numpy as np
 import pytest
 import torch
@@ -90,3 +91,40 @@ def test_steps_of_an_infinite_value(dtype, dk, dv, value):
     _, bo, _, bS = walk(**lay(x), state_in=S0)
     assert agrees(o[:, None], ro, bo) <= 1
     assert all(agrees(S[i], rS[i], bS[i]) <= 1 for i in range(3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rate", [-0.2])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+@pytest.mark.parametrize("segment", [0, 512])
+def test_odd_states_stay_until_a_token_forgets(dtype, rate, value, segment):
+    """Decays whose product over a chunk or a piece is below 2^-126, none of which is by itself."""
+    x = positive(1200, 2, 1, 64, 64, dtype, seed=5)
+    x["log_decay"][:] = rate
+    S0 = torch.randn(1, 2, 64, 64, device="cuda")
+    S0[0, 0, 3] = value
+    S0[0, 1, 7] = value
+    x["log_decay"][0, 900, 1] = -INF              # head 1 forgets, head 0 does not
+    check(x, state=S0, segment=segment, pieces=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rate", [0.2, 0.6])
+def test_growth_over_a_piece_leaves_zero_states_zero(dtype, rate):
+    """Pieces that grow past the largest number, chunks of 128 that do not."""
+    x = positive(1200, 2, 1, 64, 64, dtype, seed=7)
+    x["log_decay"][:] = rate
+    x["v"].zero_()
+    o, S = gdn.gdn_linattn_fwd(**x, segment=512)
+    assert bool((o == 0).all()) and bool((S == 0).all()) and gdn.gdn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pieces_that_grow_and_fall_again(dtype):
+    """Half a piece up by e^60, the other half down again: states in between are finite, and so is the rest."""
+    x = positive(1024, 2, 1, 64, 64, dtype, seed=9)
+    x["log_decay"][:] = -60.0 / 256
+    x["log_decay"][:, :256] = x["log_decay"][:, 512:768] = 60.0 / 256
+    S0 = torch.randn(1, 2, 64, 64, device="cuda")
+    for segment, pieces in ((0, 1), (512, 2)):
+        check(x, state=S0, segment=segment, pieces=pieces)
