@@ -30,10 +30,10 @@ constexpr int kThreads = 256;
 template <int DK, int DV> struct Smem {
     float q[kC][DK + 4], k[kC + DV][DK + 4];
     float v[DV][kC + 4], P[kC][kC + 4];
-    float add[kC], in[kC], start[kC];
+    float add[kC], in[kC], start[kC], early[kC];  // early: a second factor of start
     int first[kC];
     int kept;    // tokens before this one are forgotten by the end of the chunk
-    float all;
+    float all, before;  // the decay over the chunk, in two factors; 0 when it forgets
 };
 
 __device__ __forceinline__ bool not_finite(float f) { return !(fabsf(f) <= 3.402823466e38f); }
@@ -145,11 +145,15 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             d.scan(decay_next);
             m.in[lane] = d.in;
             m.first[lane] = first_seen(d.mask, lane);
-            m.start[lane] = d.cut_upto(lane) ? 0.f : decay_of(d.in);
+            const float start = decay_of(once(d.in));
+            m.start[lane] = d.cut_upto(lane) ? 0.f : start;
+            m.early[lane] = is_far(d.in) ? start : 1.f;
             m.add[lane] = d.cut_behind(lane) ? 0.f : decay_of(d.after);
             if (lane == 0) {
                 m.kept = first_seen(d.mask, 31);
-                m.all = d.mask ? 0.f : chained_decay_of(d.total);
+                const float all = chained_decay_of(once(d.total));
+                m.all = d.mask ? 0.f : all;
+                m.before = is_far(d.total) ? all : 1.f;
                 if (states_only) piece.add(d.total, d.mask);
             }
         }
@@ -173,14 +177,14 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = i0 + 8 * e;
-                const float w = m.start[i];
+                const float w = m.start[i], early = m.early[i];
                 float lo, hi;
                 unpack2(sum[e][0], lo, hi);
                 m.P[i][j0] = j0 <= i && j0 >= m.first[i] ? (lo + hi) * decay_of(m.in[i] - m.in[j0]) : 0.f;
 #pragma unroll
                 for (int f = 0; f < OV; ++f) {
                     unpack2(sum[e][1 + f], lo, hi);
-                    acc[e][f] = w == 0.f ? 0.f : w * (lo + hi);
+                    acc[e][f] = w == 0.f ? 0.f : w * (early * (lo + hi));
                 }
             }
         }
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
                         s[x][y] = fma2(pack2(w[x][e], w[x][e]), pack2(kk.x, kk.y), s[x][y]);
                 }
         }
-        const float all = m.all;
+        const float all = m.all, again = m.before;
 #pragma unroll
         for (int x = 0; x < SV; ++x)
 #pragma unroll
@@ -269,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
                 float lo, hi;
                 unpack2(s[x][y], lo, hi);
                 // columns past d_k stay zero: an infinite v makes NaN of their zeros
-                lo = all == 0.f ? lo : fmaf(all, before.x, lo);
-                hi = all == 0.f ? hi : fmaf(all, before.y, hi);
+                lo = all == 0.f ? lo : fmaf(all, again * before.x, lo);
+                hi = all == 0.f ? hi : fmaf(all, again * before.y, hi);
                 *S = make_float2(k0 + 32 * y < dk ? lo : 0.f, k0 + 32 * y + 1 < dk ? hi : 0.f);
             }
     }

@@ -111,6 +111,12 @@ __device__ __noinline__ void wait_long(uint64_t *bar, uint32_t parity, volatile 
     atomicOr(status, GDN_DEV_WAIT_TIMEOUT);
 }
 
+// Products in place in rare branches: as statements of their own they stay there, where the
+// compiler would form them beside the old values, and registers do not hold both.
+__device__ __forceinline__ void mul_here(float &x, float f) { asm volatile("mul.rn.f32 %0, %0, %1;" : "+f"(x) : "f"(f)); }
+__device__ __forceinline__ void opaque(float &x) { asm volatile("" : "+f"(x)); }  // no path of its own for each value
+__device__ __forceinline__ void mul2_here(f32x2 &x, f32x2 f) { asm volatile("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(f)); }
+
 // One arrival for the warp, after all of its lanes.
 __device__ __forceinline__ void arrive_warp(uint64_t *bar)
 {
@@ -576,12 +582,17 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 const uint4 mask = *reinterpret_cast<const uint4 *>(s.mask[st]);
                 const float sum = total.x + total.y + total.z + total.w;
                 const unsigned cut = mask.x | mask.y | mask.z | mask.w;
-                const float all = cut ? 0.f : chained_decay_of(sum);
                 if (kStates && t == 0) piece.add(sum, cut);
                 arrive_warp(&s.dec_free[st]);
+                float all = cut ? 0.f : chained_decay_of(once(sum)), again = is_far(sum) ? all : 1.f;
+                opaque(all), opaque(again);
                 if (all == 0.f)
 #pragma unroll
                     for (int d = 0; d < kCols / 2; ++d) S[d] = 0;  // forgotten, infinite or not
+                if (again != 1.f) {
+#pragma unroll
+                    for (int d = 0; d < kCols / 2; ++d) mul2_here(S[d], dup2(again));
+                }
                 wait(&s.u_full, c);
                 __syncwarp();
                 tc_fence_after();
@@ -714,7 +725,10 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     cut = cut || s.mask[st][J];
                     sum += s.total[st][J];
                 }
-                const f32x2 start = dup2(a.scale * decay_of(sum));
+                const float from = decay_of(once(sum));
+                float again = is_far(sum) ? from : 1.f;
+                opaque(again);
+                const f32x2 start = dup2(a.scale * from);
                 wait(&s.w_ready[st], c >> 1);
                 const uint4 odd = *reinterpret_cast<const uint4 *>(s.odd[st]);
                 arrive_warp(&s.dec_free[st]);
@@ -738,6 +752,9 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     float x[16], y[16];
                     __syncwarp();
                     ld_cols(lane_addr(tbase, quad, kColI + 64 * st + q), lane_addr(tbase, quad, kColO + q), x, y);
+                    if (again != 1.f)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) mul_here(x[e], again);
                     if (cut)  // nothing of the state before, infinite or not
 #pragma unroll
                         for (int e = 0; e < 16; ++e) x[e] = 0.f;

@@ -94,7 +94,7 @@ def test_steps_of_an_infinite_value(dtype, dk, dv, value):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rate", [-0.2])
+@pytest.mark.parametrize("rate", [-0.2, -1.0, -3.0])
 @pytest.mark.parametrize("value", [INF, -INF, NAN])
 @pytest.mark.parametrize("segment", [0, 512])
 def test_odd_states_stay_until_a_token_forgets(dtype, rate, value, segment):
