@@ -437,7 +437,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             mbar_init(&s.k_free[i], kStates ? 1 : 2);
             mbar_init(&s.p_free[i], 1);
             mbar_init(&s.dec_ready[i], 4);
-            mbar_init(&s.dec_free[i], 4 * (kStates ? kSG : kSG + 2));
+            mbar_init(&s.dec_free[i], 4 * (kStates ? kSG : kSG + 2) + (kStates ? 0 : 1));
             mbar_init(&s.w_ready[i], 4);
             mbar_init(&s.o_free[i], 4);
             mbar_init(&s.qk_full[i], 1);
@@ -788,9 +788,10 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
                 const uint32_t p = tbase + kColP + 128 * st;
+                wait(&s.w_ready[st], c >> 1);  // V is finite, and zero past the end
+                mbar_arrive(&s.dec_free[st]);  // seen: two chunks on the barrier's phase would look like this one's
                 wait(&s.p_ready[st], c >> 1);
                 wait(&s.v_full[c % kRing], c / kRing);
-                wait(&s.w_ready[st], c >> 1);  // V is finite, and zero past the end
                 if (c > 0) wait(&s.o_free[st ^ 1], (c - 1) >> 1);
                 tc_fence_after();
                 const uint64_t v = sdesc_sw128(base + kOffV + c % kRing * kTile, kTile, 1024);
