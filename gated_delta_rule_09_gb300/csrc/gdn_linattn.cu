@@ -38,6 +38,13 @@ template <int DK, int DV> struct Smem {
 
 __device__ __forceinline__ bool not_finite(float f) { return !(fabsf(f) <= 3.402823466e38f); }
 
+// What a decay below 2^-126 leaves of x beside infinities: those stay, and what is finite
+// still has its sign in their products.
+__device__ __forceinline__ float least_of(float x)
+{
+    return not_finite(x) || x == 0.f ? x : copysignf(1.175494351e-38f, x);
+}
+
 // kC rows of W columns, on their way from memory: all of a thread's loads are in
 // flight together.  A warp takes every eighth row.  Zeros past n rows and `cols` columns.
 template <typename E, int W> struct Rows {
@@ -180,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
                 const float w = m.start[i], early = m.early[i];
                 float lo, hi;
                 unpack2(sum[e][0], lo, hi);
-                m.P[i][j0] = j0 <= i && j0 >= m.first[i] ? (lo + hi) * decay_of(m.in[i] - m.in[j0]) : 0.f;
+                const float x = lo + hi, f = decay_of(m.in[i] - m.in[j0]);
+                m.P[i][j0] = j0 <= i && j0 >= m.first[i] ? (odd && f == 0.f ? least_of(x) : x * f) : 0.f;
 #pragma unroll
                 for (int f = 0; f < OV; ++f) {
                     unpack2(sum[e][1 + f], lo, hi);
@@ -240,6 +248,10 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             __syncthreads();
             for (int i = t; i < m.kept * DK; i += kThreads) m.k[i / DK][i % DK] = 0.f;
             for (int i = t; i < m.kept * DV; i += kThreads) m.v[i % DV][i / DV] = 0.f;
+            for (int i = m.kept * DV + t; i < kC * DV; i += kThreads)
+                if (m.add[i / DV] == 0.f) m.v[i % DV][i / DV] = least_of(m.v[i % DV][i / DV]);
+            __syncthreads();
+            if (t < kC && t >= m.kept && m.add[t] == 0.f) m.add[t] = 1.f;
             __syncthreads();
         }
         f32x2 s[SV][SK] = {};

@@ -234,6 +234,19 @@ __device__ __noinline__ void mend_row(uint8_t *tiles, int parts, int r)
     }
 }
 
+// The decayed row where the decay is zero but no token forgets: the infinities and NaN of V stay.
+__device__ __noinline__ void keep_odd_row(uint8_t *tiles, const uint8_t *V, int r)
+{
+#pragma unroll 1
+    for (int w = 0; w < 32; ++w) {
+        const uint32_t at = sw128(r, w / 4) + w % 4 * 4;
+        uint32_t hi = *reinterpret_cast<const uint32_t *>(V + at);
+        if ((hi & 0x7f80u) != 0x7f80u) hi &= 0xffff0000u;
+        if ((hi & 0x7f800000u) != 0x7f800000u) hi &= 0xffffu;
+        for (int p = 0; p < kParts; ++p) *reinterpret_cast<uint32_t *>(tiles + p * kTile + at) = p ? 0u : hi;
+    }
+}
+
 __device__ __noinline__ void zero_row(uint8_t *tiles, int r)
 {
 #pragma unroll 1
@@ -310,7 +323,7 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, b
             const bool seen = J == I ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
             const float f = own ? decay_of(J == I ? mine - w : sum + (total[J] - w)) * scale
                                 : row_factor(J == I ? sum : sum + total[J], scale) * inverse[32 * J + j];
-            x[j] = seen && f != 0.f ? x[j] * f : 0.f;
+            x[j] = !seen ? 0.f : f != 0.f ? x[j] * f : copysignf(0.f, x[j] * copysignf(1.f, f));  // zeros keep their sign
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -684,12 +697,13 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                         st_parts<kParts>(W, t, q + r, x, sign);
                     }
                 if (is_odd(sign)) {  // infinite or NaN, decayed or not
+                    if (cut) zero_row(W, t);  // what comes after has forgotten it
+                    else if (w == 0.f) keep_odd_row(W, V, t);
+                    else mend_row(W, kParts, t);
                     if (!kStates) {
                         atomicOr(&s.odd[st][quad], 1u << lane);
                         code_row(V, t);
                     }
-                    mend_row(W, kParts, t);
-                    if (w == 0.f) zero_row(W, t);  // what comes after has forgotten it
                 }
             } else {  // rows past the end may be another sequence's
                 zero_row(W, t);

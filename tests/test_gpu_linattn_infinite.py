@@ -1,6 +1,6 @@
 """Infinities and NaN in linear attention: forgotten ones do not come back, whole or in
 pieces, columns that fill up a tile, or lanes without one in a step, make none, and
-states stay what they are from piece to piece."""
+states and values stay what they are under decays that forget nothing."""
 import numpy as np
 import pytest
 import torch
@@ -106,6 +106,17 @@ def test_odd_states_stay_until_a_token_forgets(dtype, rate, value, segment):
     S0[0, 1, 7] = value
     x["log_decay"][0, 900, 1] = -INF              # head 1 forgets, head 0 does not
     check(x, state=S0, segment=segment, pieces=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rate", [-1.0, -3.0])
+@pytest.mark.parametrize("value", [INF, NAN])
+@pytest.mark.parametrize("t", [10, 100, 130])
+def test_odd_values_stay_until_a_token_forgets(dtype, rate, value, t):
+    x = positive(300, 2, 1, 64, 64, dtype, seed=t)
+    x["log_decay"][:] = rate
+    x["log_decay"][0, 280, 1] = -INF
+    check(x, [("v", (0, t, 0, 3), value), ("v", (0, t, 1, 5), value)])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
