@@ -30,7 +30,7 @@ constexpr int kThreads = 256;
 template <int DK, int DV> struct Smem {
     float q[kC][DK + 4], k[kC + DV][DK + 4];
     float v[DV][kC + 4], P[kC][kC + 4];
-    float add[kC], in[kC], start[kC], early[kC];  // early: a second factor of start
+    float add[kC], in[kC], rest[kC], start[kC], early[kC];  // early: a second factor of start
     int first[kC];
     int kept;    // tokens before this one are forgotten by the end of the chunk
     float all, before;  // the decay over the chunk, in two factors; 0 when it forgets
@@ -149,7 +149,9 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
         if (!states_only) qr.store(m.q);
         if (t < 32) {
             Decays d;
-            d.scan(decay_next);
+            const float decay_now = decay_next;
+            d.scan(decay_now);
+            m.rest[lane] = d.exact(decay_now);
             m.in[lane] = d.in;
             m.first[lane] = first_seen(d.mask, lane);
             const float start = decay_of(once(d.in));
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
                 const float w = m.start[i], early = m.early[i];
                 float lo, hi;
                 unpack2(sum[e][0], lo, hi);
-                const float x = lo + hi, f = decay_of(m.in[i] - m.in[j0]);
+                const float x = lo + hi, f = decay_of(m.in[i] - m.in[j0] + (m.rest[i] - m.rest[j0]));
                 m.P[i][j0] = j0 <= i && j0 >= m.first[i] ? (odd && f == 0.f ? least_of(x) : x * f) : 0.f;
 #pragma unroll
                 for (int f = 0; f < OV; ++f) {

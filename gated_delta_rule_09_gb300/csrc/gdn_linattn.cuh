@@ -15,9 +15,9 @@ constexpr float kForget = -126.f;
 // Decays of 32 consecutive tokens, one per lane, as base-2 logarithms.  Factors
 // between two tokens are products over the tokens between; every one used here is
 // a sum of terms that are added up, never a difference of two long sums, but for
-// pairs within the block (`in` of one minus `in` of the other).  Tokens that
-// forget count as zero in the sums and stand in `mask`, so that an infinite decay
-// makes no NaN.
+// pairs within the block (`in` of one minus `in` of the other), which have `rest` beside
+// them.  Tokens that forget count as zero in the sums and stand in `mask`, so that an
+// infinite decay makes no NaN.
 struct Decays {
     float in;       // sum over the block's tokens up to and with the lane's
     float after;    // sum over the block's tokens behind the lane's
@@ -41,6 +41,29 @@ struct Decays {
         total = __shfl_sync(0xffffffffu, in, 31);
         after = __shfl_down_sync(0xffffffffu, back, 1);
         if (lane == 31) after = 0.f;
+    }
+
+    // `in` anew with what its rounding leaves out, for differences between tokens behind a
+    // steep one: they depend on what lies between, not on how far the block has come (eight
+    // tokens of e^-60, then flat: 7e-5 off without).  Sums in fixed point, steps of 2^-40, are
+    // exact, where fp64 has a sixtieth of the rate.  Lanes behind a decay that does not fit, 2^17
+    // and more or NaN, keep what they have.
+    __device__ __forceinline__ float exact(float log_decay)
+    {
+        const int lane = threadIdx.x & 31;
+        const float g = log_decay * kLog2e;
+        const bool fits = fabsf(g) < 131072.f;
+        long long x = fits && g > kForget ? __float2ll_rn(g * 1099511627776.f) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        const unsigned out = __ballot_sync(0xffffffffu, !fits && !(g <= kForget));
+        if (out & (0xffffffffu >> (31 - lane))) return 0.f;
+        const float high = __ll2float_rn(x);
+        in = high * 9.094947017729282e-13f;
+        return __ll2float_rn(x - __float2ll_rn(high)) * 9.094947017729282e-13f;
     }
 
     // Whether some token up to and with lane i, or behind it, forgets.

@@ -76,7 +76,8 @@ constexpr int kOffSmall = kOffS + kHalves * kTile;
 
 struct Small {
     // decays of two chunks: sums up to and with a token within its block of 32, their
-    // inverse factors 2^(-in - kShift), and the blocks' sums
+    // inverse factors 2^(-in - kShift), for steep tokens and those behind them what the sum's
+    // rounding leaves out, and the blocks' sums
     float in[2][kC], inverse[2][kC], total[2][4];
     unsigned mask[2][4], steep[2][4];  // tokens that forget; whose sum is beyond kFall or kRise
     unsigned odd[2][4];     // tokens whose V has infinities or NaN
@@ -306,9 +307,10 @@ __device__ __forceinline__ float row_factor(float x, float scale)
 // plain path takes 78, if every block of 32 goes this way.  Rows that come before any such
 // token (`own` false) have the plain path's factors: the same bits, whatever comes later.
 __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, bool own, float scale, const float *in,
-                                        const float *inverse, const float *total, const unsigned *mask)
+                                        const float *inverse, const float *total, const unsigned *mask, const unsigned *steep)
 {
-    const float mine = in[32 * I + lane];
+    auto rest = [&](int J, int j) { return (mask[J] | steep[J]) & (0xffffffffu >> (31 - j)) ? inverse[32 * J + j] : 0.f; };
+    const float mine = in[32 * I + lane], mine_rest = rest(I, lane);
     float sum = mine;
     bool cut = mask[I] & (0xffffffffu >> (31 - lane));
     const int first = first_seen(mask[I], lane);
@@ -321,7 +323,8 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, b
         for (int j = 0; j < 32; ++j) {
             const float w = in[32 * J + j];
             const bool seen = J == I ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
-            const float f = own ? decay_of(J == I ? mine - w : sum + (total[J] - w)) * scale
+            const float f = own ? decay_of(J == I ? mine - w + (mine_rest - rest(J, j))
+                                                  : sum + (in[32 * J + 31] - w + (rest(J, 31) - rest(J, j)))) * scale
                                 : row_factor(J == I ? sum : sum + total[J], scale) * inverse[32 * J + j];
             x[j] = !seen ? 0.f : f != 0.f ? x[j] * f : copysignf(0.f, x[j] * copysignf(1.f, f));  // zeros keep their sign
         }
@@ -521,7 +524,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 wait(&s.qk_full[st], c >> 1);
                 __syncwarp();
                 tc_fence_after();
-                if (odd) odd_decays(p, quad, I, lane, own, a.scale, s.in[st], s.inverse[st], s.total[st], s.mask[st]);
+                if (odd) odd_decays(p, quad, I, lane, own, a.scale, s.in[st], s.inverse[st], s.total[st], s.mask[st], s.steep[st]);
 #pragma unroll 1
                 for (int J = I; J >= 0 && !odd; --J) {
                     const f32x2 f = dup2(row_factor(sum, a.scale));
@@ -654,12 +657,18 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1, n = min(kC, u.len - c * kC);
             Decays d;
-            d.scan(next);
+            const float now = next;
+            d.scan(now);
             next = t + (int64_t)(c + 1) * kC < u.len ? decay[(int64_t)(c + 1) * kC * a.ld_decay] : 0.f;
             if (c > 1) wait(&s.dec_free[st], (c - 2) >> 1);
-            s.in[st][t] = d.in;
-            s.inverse[st][t] = ex2(-d.in) * (1.f / kTwoShift);
             const unsigned steep = __ballot_sync(0xffffffffu, !(d.in > -kFall && d.in < kRise));
+            float inverse = ex2(-d.in) * (1.f / kTwoShift);
+            if (steep || d.mask) {
+                const float rest = d.exact(now);
+                if ((steep | d.mask) & (0xffffffffu >> (31 - lane))) inverse = rest;
+            }
+            s.in[st][t] = d.in;
+            s.inverse[st][t] = inverse;
             if (lane == 0) {
                 s.total[st][quad] = d.total;
                 s.mask[st][quad] = d.mask;

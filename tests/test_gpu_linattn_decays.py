@@ -1,9 +1,12 @@
 """Decays that rise, fall and fall again within a block of 32 tokens: finite inputs
-give finite outputs, and what lies behind a steep token is not lost.  Against the
-definition in fp64."""
+give finite outputs, and what lies behind a steep token is neither lost nor less
+precise.  Against the definition in fp64."""
+import numpy as np
 import pytest
+import torch
 
 import gated_delta_rule_09_gb300 as gdn
+from layer_reference import EX, U, stored
 from linattn_exact import agrees, walk
 from test_gpu_linattn import check, make, on_tensor_cores
 
@@ -49,3 +52,28 @@ def test_scales_of_every_size(scale):
     o, _ = gdn.gdn_linattn_fwd(**x, scale=scale)
     ro, bo, _, _ = walk(**x, scale=scale, parts=True)
     assert agrees(o, ro, bo) <= 1 and gdn.gdn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("steep", [-50.0, -60.0, -80.0, -87.0])
+@pytest.mark.parametrize("where", [range(8), range(0, 16, 2), range(1), range(0, 24, 3)])
+def test_flat_decays_behind_steep_ones(dtype, steep, where):
+    """Outputs of a single term: the factor of two tokens depends on what lies between them, not on what the
+    block of 32 began with."""
+    T, at, dk, dv = 96, 25, 8, 64
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = torch.Generator("cuda").manual_seed(41)
+    q = torch.zeros(1, T, 1, dk, device="cuda", dtype=dt)
+    q[..., 0] = 1
+    v = torch.zeros(1, T, 1, dv, device="cuda", dtype=dt)
+    v[0, at, 0] = torch.randn(dv, generator=gen, device="cuda").to(dt)
+    g = -0.05 * torch.rand(1, T, 1, generator=gen, device="cuda")
+    g[0, list(where)] = steep
+    o, _ = gdn.gdn_linattn_fwd(q, q, v, g)
+    sums = np.cumsum(g[0, :, 0].double().cpu().numpy())
+    D = np.maximum(sums[at] - sums, 0)                       # between the token and the output
+    want = np.where(np.arange(T) >= at, np.exp(-D), 0)[:, None] * v[0, at, 0].double().cpu().numpy()
+    # the factor's exponential and those that carry a state on (twice a block: 6 and 6), the roundings of the sum
+    # between, and three products; on tensor cores what two parts leave, twice
+    rel = (14 * EX + 12 * U * D + 16 * U + (2.0 ** -15 if dtype == "bf16" else 0))[:, None]
+    assert agrees(o[0, :, 0], want, stored(want, rel * np.abs(want), dt)) <= 1
