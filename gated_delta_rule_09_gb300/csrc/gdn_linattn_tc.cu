@@ -83,7 +83,7 @@ struct Small {
     unsigned odd[2][4];     // tokens whose V has infinities or NaN
     uint64_t k_full[2], v_full[kRing], k_free[2], v_free[kRing], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2],
         p_ready[2], p_free[2], o_staged[kRing], i_full[2], w_half[2], w_gone[2];
-    uint64_t q_full, q_free, u_full, u_free, s_ready, o_full;
+    uint64_t odd_read, q_full, q_free, u_full, u_free, s_ready, o_full;
     uint32_t tmem;
     int abort_flag;
 };
@@ -467,6 +467,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             mbar_init(&s.v_free[i], 1);
             mbar_init(&s.o_staged[i], 4);
         }
+        mbar_init(&s.odd_read, 4);
         mbar_init(&s.q_full, 1);
         mbar_init(&s.q_free, 1);
         mbar_init(&s.u_full, 1);
@@ -762,8 +763,10 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 if (odd.x | odd.y | odd.z | odd.w) {
                     const unsigned rows[4] = {odd.x, odd.y, odd.z, odd.w};
                     odd_row(tbase + kColP + 128 * st, tbase + kColO, quad, i, first, rows, stage);
-                    named_sync(2, 128);
+                    tc_fence_before();  // Q K^T takes the place of the P that was read
                 }
+                arrive_warp(&s.odd_read);
+                if (odd.x | odd.y | odd.z | odd.w) wait(&s.odd_read, c);  // a bounded wait, where warps that gave up differ
                 if (t == 0) mbar_arrive(&s.p_free[st]);
                 // Whole chunks go through the place of V and a tensor copy: rows stored from here would take a
                 // transaction per row and store, half of what the memory pipe can do.
