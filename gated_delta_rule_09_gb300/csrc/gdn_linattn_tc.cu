@@ -480,7 +480,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
         // the first chunks are on their way while tensor memory is allocated
 #pragma unroll 1
         for (int c = 0; c < 2 && c < chunks; ++c) load_k(c, false);
-        if (!kStates) load_q(0, false);
+        if (!kStates && chunks > 0) load_q(0, false);
 #pragma unroll 1
         for (int c = 0; c < kRing && c < chunks; ++c) load_v(c);
 #pragma unroll 1
@@ -898,7 +898,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
     } else if (elect_one()) {
         // ---- tensor copies: K, Q, V, and the outputs that take the place of V, whichever can go on.  Chunks
         // ahead of the rings are fetched to L2.
-        int k = min(2, chunks), q = kStates ? chunks : 1;  // chunks loaded
+        int k = min(2, chunks), q = kStates ? chunks : min(1, chunks);  // chunks loaded
         int put = 0;          // chunks whose V is through and whose outputs are stored
         uint64_t idle = 0;    // since when there is nothing to do
         while ((k < chunks || q < chunks || put < chunks) && !*abort_flag) {
