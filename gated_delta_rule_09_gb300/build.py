@@ -5,9 +5,9 @@ Each translation unit under ``csrc/`` compiles in parallel to an object in
 or header newer than the library triggers a rebuild.
 
 A second library, ``libgdn_waittest.so``, is the same code with the tensor-core
-kernel compiled under ``GDN_WAIT_TEST``: 5 ms wait limits and one withheld
-arrival in one unit, so the bounded-wait abort path can be run on purpose.
-Only its test loads it; nothing else does.
+kernels compiled under ``GDN_WAIT_TEST``: 5 ms wait limits and one withheld
+arrival in one unit, so the bounded-wait abort paths can be run on purpose.
+Only their tests load it; nothing else does.
 """
 from __future__ import annotations
 
@@ -24,7 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 WAITTEST_LIB = os.path.join(PKG, "libgdn_waittest.so")
-WAITTEST_SRC = "gdn_tc.cu"  # the translation unit the test build recompiles
+WAITTEST_SRCS = ("gdn_tc.cu", "gdn_linattn_tc.cu")  # the translation units the test build recompiles
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -68,9 +68,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         jobs.append((src, [cc, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]))
-    wt_obj = os.path.join(BUILD, WAITTEST_SRC[:-3] + "_waittest.o")
-    wt_src = os.path.join(CSRC, WAITTEST_SRC)
-    jobs.append((wt_src, [cc, *NVCC_FLAGS, *extra_flags, "-DGDN_WAIT_TEST", "-c", wt_src, "-o", wt_obj]))
+    wt_objs = list(objs)
+    for name in WAITTEST_SRCS:
+        src, obj = os.path.join(CSRC, name), os.path.join(BUILD, name[:-3] + "_waittest.o")
+        wt_objs[objs.index(os.path.join(BUILD, name[:-3] + ".o"))] = obj
+        jobs.append((src, [cc, *NVCC_FLAGS, *extra_flags, "-DGDN_WAIT_TEST", "-c", src, "-o", obj]))
     for src, cmd in jobs:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
@@ -85,7 +87,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             failed.append(os.path.basename(src))
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
-    wt_objs = [wt_obj if os.path.basename(o) == WAITTEST_SRC[:-3] + ".o" else o for o in objs]
     for lib, parts in ((WAITTEST_LIB, wt_objs), (LIB, objs)):
         tmp = lib + ".tmp.%d" % os.getpid()
         subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *parts], check=True)

@@ -33,8 +33,9 @@
 // with later chunks fetched to L2 ahead.  All loops over chunks are kept small: together
 // they have to stay in the instruction cache.
 //
-// Every wait is bounded: on timeout the block raises GDN_DEV_WAIT_TIMEOUT, issues
-// no more copies and winds down with waits of 50 us, enough for what is in flight.
+// Every wait is bounded: on timeout the block raises GDN_DEV_WAIT_TIMEOUT, issues no more
+// copies and winds down with waits of 50 us, enough for what is in flight; who issued
+// products or copies waits for the last of them.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <mutex>
@@ -62,7 +63,15 @@ constexpr int kAhead = 3;   // chunks that are fetched to L2 ahead of the one th
 // -kFall to kRise.  The factors are 2^-in_j 2^-kShift and 2^(sum up to i) 2^kShift, so that
 // neither leaves what fp32 holds before their product is below 2^(kFall - 222).
 constexpr float kFall = 90.f, kRise = 24.f, kShift = 96.f, kTwoShift = 7.9228162514264338e28f;
+#ifndef GDN_WAIT_TEST
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr bool kWaitTest = false;
+#else
+// Test build: 5 ms per wait, and one warp that keeps the state withholds one arrival in the
+// first block, the one that the state before chunk 1 is written.
+constexpr uint64_t kWaitLimitNs = 5000000ull;
+constexpr bool kWaitTest = true;
+#endif
 constexpr uint64_t kDrainNs = 50000;  // a wait's bound once the block has given up on one
 
 // Shared memory: tiles of 128-byte rows, 128-byte swizzle.
@@ -83,7 +92,7 @@ struct Small {
     unsigned odd[2][4];     // tokens whose V has infinities or NaN
     uint64_t k_full[2], v_full[kRing], k_free[2], v_free[kRing], dec_ready[2], dec_free[2], w_ready[2], o_free[2], qk_full[2],
         p_ready[2], p_free[2], o_staged[kRing], i_full[2], w_half[2], w_gone[2];
-    uint64_t odd_read, q_full, q_free, u_full, u_free, s_ready, o_full;
+    uint64_t drained[3], odd_read, q_full, q_free, u_full, u_free, s_ready, o_full;
     uint32_t tmem;
     int abort_flag;
 };
@@ -123,6 +132,14 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar)
 {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// This thread's products have ended before tensor memory is freed, also where the waits for
+// them gave up.
+__device__ __noinline__ void drain(uint64_t *bar, volatile int *abort_flag, unsigned int *status)
+{
+    mma_commit(bar);
+    if (!mbar_try_wait(bar, 0)) wait_long(bar, 0, abort_flag, status);
 }
 
 struct Waiter {
@@ -467,6 +484,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             mbar_init(&s.v_free[i], 1);
             mbar_init(&s.o_staged[i], 4);
         }
+        for (int i = 0; i < 3; ++i) mbar_init(&s.drained[i], 1);
         mbar_init(&s.odd_read, 4);
         mbar_init(&s.q_full, 1);
         mbar_init(&s.q_free, 1);
@@ -634,7 +652,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
                 if (is_odd(sign)) mend_row(sm + kOffS, kHalves, t);
                 fence_async_smem();
-                arrive_warp(&s.s_ready);
+                if (!(kWaitTest && blockIdx.x == 0 && c == 0 && warp == kWarpS)) arrive_warp(&s.s_ready);
             }
         }
         if (kStates && v0 + c0 == 0 && t == 0) a.piece_decay[unit / tiles] = piece.all();
@@ -829,6 +847,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                                        idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
                 mma_commit(&s.o_full);
             }
+            drain(&s.drained[0], abort_flag, a.status);
         }
     } else if (warp == kWarpIssue + 1) {
         // ---- K^T V, decayed
@@ -858,6 +877,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 mma_commit(&s.k_free[st]);
                 if (kStates) mma_commit(&s.v_free[c % kRing]);
             }
+            drain(&s.drained[1], abort_flag, a.status);
         }
     } else if (warp == kWarpIssue + 2) {
         // ---- Q S^T of a chunk, then Q K^T of the next in the place of P of the one before: Q has one stage
@@ -894,12 +914,13 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     mma_commit(&s.k_free[to]);
                 }
             }
+            drain(&s.drained[2], abort_flag, a.status);
         }
     } else if (elect_one()) {
         // ---- tensor copies: K, Q, V, and the outputs that take the place of V, whichever can go on.  Chunks
         // ahead of the rings are fetched to L2.
         int k = min(2, chunks), q = kStates ? chunks : min(1, chunks);  // chunks loaded
-        int put = 0;          // chunks whose V is through and whose outputs are stored
+        int v = min(kRing, chunks), put = 0;  // and chunks whose V is through and whose outputs are stored
         uint64_t idle = 0;    // since when there is nothing to do
         while ((k < chunks || q < chunks || put < chunks) && !*abort_flag) {
             bool moved = false;
@@ -921,7 +942,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     bulk_commit();
                     bulk_wait_read();
                 }
-                if (put + kRing < chunks) load_v(put + kRing);
+                if (v < chunks) load_v(v++);
                 ++put;
                 moved = true;
             }
@@ -936,6 +957,12 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 }
             }
         }
+        // no copy is on its way when the block ends, also where the waits for it gave up
+#pragma unroll 1
+        for (int c = max(0, k - 2); c < k; ++c) wait(&s.k_full[c & 1], c >> 1);
+        if (!kStates && q > 0) wait(&s.q_full, q - 1);
+#pragma unroll 1
+        for (int c = max(0, v - kRing); c < v; ++c) wait(&s.v_full[c % kRing], c / kRing);
         bulk_wait_all();
     }
     __syncwarp();
