@@ -30,8 +30,8 @@
 // decays and forming the decayed V, writing the outputs; then single warps that issue
 // P V, K^T V, Q S^T and Q K^T, and the tensor copies into rings of two stages (K and V)
 // and one (Q, whose next tile comes after Q S^T: the second part of S^T has the room),
-// with later chunks fetched to L2 ahead.  All loops over chunks are kept small: together
-// they have to stay in the instruction cache.
+// with later chunks fetched to L2 ahead.  All loops over chunks are kept small, rare paths
+// in functions of their own: together they have to stay in the instruction cache.
 //
 // Every wait is bounded: on timeout the block raises GDN_DEV_WAIT_TIMEOUT, issues no more
 // copies and winds down with waits of 50 us, enough for what is in flight; who issued
@@ -100,7 +100,7 @@ constexpr int kSmemBytes = kOffSmall + (int)sizeof(Small);
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
 // Tensor memory, 512 columns: Q K^T, then P in its place, x 2 | Q S^T x 2 | P V | U.
-// The parts of P of 32 tokens take the columns of their 32 products: 16 and 16.
+// The parts of P of 16 tokens take the columns of their 16 products: 8 and 8.
 constexpr uint32_t kColP = 0, kColI = 256, kColO = 384, kColU = 448;
 
 // A wait suspends the warp for as long as the hardware lets it; the clock is looked at
@@ -209,20 +209,39 @@ __device__ __forceinline__ uint32_t ld_col(uint32_t taddr)
     return v;
 }
 
-// Two values as pairs of N bf16 parts, each the rounded rest of those before it: what
-// their sum leaves of the value is 2^-8N.  `sign` becomes NaN where a value is infinite or
-// NaN, whose other parts then are NaN.
-template <int N> __device__ __forceinline__ void split(f32x2 v, uint32_t (&part)[N], f32x2 &sign)
+// What the rounding of two values to a pair of bf16 leaves.
+__device__ __forceinline__ f32x2 rest_of(f32x2 v, uint32_t part)
 {
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-        float x, y;
-        unpack2(v, x, y);
-        part[p] = narrow_pair(x, y);
-        if (p + 1 < N)
-            v = fma2(pack2(__uint_as_float(part[p] << 16), __uint_as_float(part[p] & 0xffff0000u)), dup2(-1.f), v);
-        if (p == 0) sign = fma2(v, dup2(0.f), sign);
-    }
+    return fma2(pack2(__uint_as_float(part << 16), __uint_as_float(part & 0xffff0000u)), dup2(-1.f), v);
+}
+
+__device__ __forceinline__ uint32_t narrow2(f32x2 v)
+{
+    float x, y;
+    unpack2(v, x, y);
+    return narrow_pair(x, y);
+}
+
+// Two values as pairs of three bf16 parts, each the rounded rest of those before it: their
+// sum is the value to 2^-24.  `sign` becomes NaN where a value is infinite or NaN, whose
+// other parts then are NaN.
+__device__ __forceinline__ void split3(f32x2 v, uint32_t (&part)[kParts], f32x2 &sign)
+{
+    part[0] = narrow2(v);
+    v = rest_of(v, part[0]);
+    sign = fma2(v, dup2(0.f), sign);
+    part[1] = narrow2(v);
+    part[2] = narrow2(rest_of(v, part[1]));
+}
+
+// The same as two parts, to 2^-16, for outputs.  The second of an infinite value would be
+// NaN: the greater of it and -2^112 is that number, which its products with the other
+// factor do not bring up to the first's infinity.  (Values beyond 2^120 lose their second part
+// to it at worst.)
+__device__ __forceinline__ void split2(f32x2 v, uint32_t &hi, uint32_t &lo)
+{
+    hi = narrow2(v);
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(narrow2(rest_of(v, hi))), "r"(0xf780f780u));
 }
 
 __device__ __forceinline__ bool is_odd(f32x2 sign)
@@ -240,12 +259,12 @@ __device__ __forceinline__ uint32_t mend(uint32_t hi, uint32_t lo)
     return lo;
 }
 
-__device__ __noinline__ void mend_row(uint8_t *tiles, int parts, int r)
+__device__ __noinline__ void mend_row(uint8_t *tiles, int r)
 {
 #pragma unroll 1
     for (int w = 0; w < 32; ++w) {
         const uint32_t at = sw128(r, w / 4) + w % 4 * 4;
-        for (int p = 1; p < parts; ++p) {
+        for (int p = 1; p < kParts; ++p) {
             uint32_t *lo = reinterpret_cast<uint32_t *>(tiles + p * kTile + at);
             *lo = mend(*reinterpret_cast<const uint32_t *>(tiles + at), *lo);
         }
@@ -291,23 +310,28 @@ __device__ __noinline__ void zero_k_row(uint8_t *K, int r, int halves)
         *reinterpret_cast<uint4 *>(K + (c >> 3) * kTile + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
 }
 
-// 8 values into 16-byte column c of row r of N tiles.
-template <int N> __device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4], f32x2 &sign)
+// 8 values into 16-byte column c of row r, in parts into tiles one after another.
+__device__ __forceinline__ void st_parts(uint8_t *tiles, int r, int c, const f32x2 (&x)[4], f32x2 &sign)
 {
-    uint32_t w[4][N];
+    uint32_t w[4][kParts];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split<N>(x[i], w[i], sign);
+    for (int i = 0; i < 4; ++i) split3(x[i], w[i], sign);
     const uint32_t at = sw128(r, c);
 #pragma unroll
-    for (int p = 0; p < N; ++p)
+    for (int p = 0; p < kParts; ++p)
         *reinterpret_cast<uint4 *>(tiles + p * kTile + at) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
 }
 
-// The parts of P of a row and 32 tokens.
-__device__ __forceinline__ void st_p(uint32_t p, int quad, int J, const uint32_t (&hi)[16], const uint32_t (&lo)[16])
+// The column of P's first part of token pair w; of the second, 8 more.
+__device__ __forceinline__ int pair_at(int w) { return w / 8 * 16 + w % 8; }
+
+// P of 16 tokens as parts, in place of the products.
+__device__ __forceinline__ void st_p(uint32_t at, const float (&x)[16])
 {
-    tmem_st16(lane_addr(p, quad, 32 * J), hi);
-    tmem_st16(lane_addr(p, quad, 32 * J + 16), lo);
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split2(pack2(x[2 * j], x[2 * j + 1]), w[j], w[8 + j]);
+    tmem_st16(at, w);
 }
 
 // The factor of a row whose sum of decays is x, and of the scale, times 2^kShift.  The
@@ -317,6 +341,12 @@ __device__ __forceinline__ float row_factor(float x, float scale)
     const bool far = x < -64.f;
     const float f = decay_of(far ? x + kShift : x) * scale;
     return far ? f : f * kTwoShift;
+}
+
+// A product with its factor, NaN where it is not seen.  A factor of zero leaves a zero of the right sign.
+__device__ __forceinline__ float decayed(float x, float f)
+{
+    return f != f ? 0.f : f != 0.f ? x * f : copysignf(0.f, x * copysignf(1.f, f));
 }
 
 // P of one row in the cases that the plain path leaves: tokens that forget, and sums of
@@ -333,28 +363,26 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, b
     const int first = first_seen(mask[I], lane);
 #pragma unroll 1
     for (int J = I; J >= 0; --J) {
-        float x[32];
-        ld_cols(lane_addr(p, quad, 32 * J), x);
-        uint32_t hi[16], lo[16];
+        const float last = in[32 * J + 31], last_rest = rest(J, 31), plain = row_factor(J == I ? sum : sum + total[J], scale);
+#pragma unroll 1
+        for (int from = 0; from < 32; from += 16) {
+            float x[16], factor[16];  // factors lie in local memory: unrolled, they would be half of the kernel's code
+            ld_cols(lane_addr(p, quad, 32 * J + from), x);
+#pragma unroll 2
+            for (int e = 0; e < 16; ++e) {
+                const int j = from + e;
+                const float w = in[32 * J + j];
+                const bool seen = J == I ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
+                const float f = own ? decay_of(J == I ? mine - w + (mine_rest - rest(J, j))
+                                                      : sum + (last - w + (last_rest - rest(J, j)))) * scale
+                                    : plain * inverse[32 * J + j];
+                factor[e] = seen ? f : __uint_as_float(0x7fc00000u);
+            }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float w = in[32 * J + j];
-            const bool seen = J == I ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
-            const float f = own ? decay_of(J == I ? mine - w + (mine_rest - rest(J, j))
-                                                  : sum + (in[32 * J + 31] - w + (rest(J, 31) - rest(J, j)))) * scale
-                                : row_factor(J == I ? sum : sum + total[J], scale) * inverse[32 * J + j];
-            x[j] = !seen ? 0.f : f != 0.f ? x[j] * f : copysignf(0.f, x[j] * copysignf(1.f, f));  // zeros keep their sign
+            for (int e = 0; e < 16; ++e) x[e] = decayed(x[e], factor[e]);
+            __syncwarp();
+            st_p(lane_addr(p, quad, 32 * J + from), x);
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            uint32_t part[kHalves];
-            f32x2 sign = 0;
-            split<kHalves>(pack2(x[2 * j], x[2 * j + 1]), part, sign);
-            hi[j] = part[0];
-            lo[j] = mend(part[0], part[1]);
-        }
-        __syncwarp();
-        st_p(p, quad, J, hi, lo);
         if (J < I) {
             sum += total[J];
             cut = cut || mask[J];
@@ -386,29 +414,33 @@ __device__ __noinline__ void code_row(uint8_t *V, int r)
 __device__ __noinline__ void odd_row(uint32_t p, uint32_t o, int quad, int i, int first, const unsigned *rows, const uint8_t *V)
 {
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        float acc[32];
-        ld_cols(lane_addr(o, quad, 32 * half), acc);
+    for (int part = 0; part < 4; ++part) {
+        float acc[16];
+        ld_cols(lane_addr(o, quad, 16 * part), acc);
 #pragma unroll 1
         for (int j = 0; j < kC; ++j) {
             if (!(rows[j >> 5] >> (j & 31) & 1)) continue;
             __syncwarp();
-            const int w = j >> 1, at = w / 16 * 32 + w % 16;
-            const uint32_t hi = ld_col(lane_addr(p, quad, at)), lo = ld_col(lane_addr(p, quad, at + 16));
+            const uint32_t hi = ld_col(lane_addr(p, quad, pair_at(j >> 1))), lo = ld_col(lane_addr(p, quad, pair_at(j >> 1) + 8));
             if (j > i || j < first) continue;
             const float h = __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16);
             const float f = h == 0.f ? copysignf(1.f, h) : h + __uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16);
 #pragma unroll
-            for (int d = 0; d < 32; ++d) {
-                const uint32_t v = *reinterpret_cast<const unsigned short *>(V + sw128(j, half * 4 + d / 8) + d % 8 * 2);
+            for (int d = 0; d < 16; ++d) {
+                const uint32_t v = *reinterpret_cast<const unsigned short *>(V + sw128(j, part * 2 + d / 8) + d % 8 * 2);
                 if ((v & 0x7fffu) - 1u < 2u) acc[d] = fmaf(f, __uint_as_float(v == 2u ? 0x7fc00000u : (v & 0x8000u) << 16 | 0x7f800000u), acc[d]);
             }
         }
         __syncwarp();
-        tmem_st32(lane_addr(o, quad, 32 * half), acc);
+        uint32_t out[16];
+#pragma unroll
+        for (int d = 0; d < 16; ++d) out[d] = __float_as_uint(acc[d]);
+        tmem_st16(lane_addr(o, quad, 16 * part), out);
         tmem_st_wait();
     }
 }
+
+__device__ __noinline__ float exact_sum(Decays &d, float log_decay) { return d.exact(log_decay); }
 
 // The 32 tokens of a chunk whose rows of Q, P and O are in the lanes of a quarter of
 // tensor memory, which only every fourth warp, those of one scheduler, can reach.  The
@@ -547,13 +579,12 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
 #pragma unroll 1
                 for (int J = I; J >= 0 && !odd; --J) {
                     const f32x2 f = dup2(row_factor(sum, a.scale));
-                    uint32_t hi[16], lo[16];
-                    f32x2 sign = 0;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J + 16 * half]);
+#pragma unroll 1
+                    for (int from = 0; from < 32; from += 16) {
+                        const uint32_t at = lane_addr(p, quad, 32 * J + from);
+                        const float4 *inverse = reinterpret_cast<const float4 *>(&s.inverse[st][32 * J + from]);
                         float x[16];
-                        ld_cols(lane_addr(p, quad, 32 * J + 16 * half), x);
+                        ld_cols(at, x);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float4 w = inverse[j];
@@ -562,21 +593,10 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                         }
                         if (J == I) {  // the factor of a token behind may be infinite: a rise, then a fall
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) x[j] = 16 * half + j <= lane ? x[j] : 0.f;
+                            for (int j = 0; j < 16; ++j) x[j] = from + j <= lane ? x[j] : 0.f;
                         }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            uint32_t part[kHalves];
-                            split<kHalves>(pack2(x[2 * j], x[2 * j + 1]), part, sign);
-                            hi[8 * half + j] = part[0];
-                            lo[8 * half + j] = part[1];
-                        }
+                        st_p(at, x);
                     }
-                    if (is_odd(sign))
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) lo[j] = mend(hi[j], lo[j]);
-                    __syncwarp();
-                    st_p(p, quad, J, hi, lo);
                     if (J > 0) sum += s.total[st][J - 1];
                 }
                 const float zero[32] = {};
@@ -644,13 +664,15 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             }
             if (!kStates && c + 1 < chunks) {
                 if (c >= 0) wait(&s.i_full[st], c >> 1);  // Q S^T of this chunk has read it
-                f32x2 sign = 0;
 #pragma unroll
                 for (int q = 0; q < kCols / 8 && (t < dk || c < 0); ++q) {  // the rows past d_k stay zero
-                    const f32x2 x[4] = {S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]};
-                    st_parts<kHalves>(sm + kOffS, t, c0 / 8 + q, x, sign);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split2(S[4 * q + e], hi[e], lo[e]);
+                    uint8_t *at = sm + kOffS + sw128(t, c0 / 8 + q);
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(at + kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                if (is_odd(sign)) mend_row(sm + kOffS, kHalves, t);
                 fence_async_smem();
                 if (!(kWaitTest && blockIdx.x == 0 && c == 0 && warp == kWarpS)) arrive_warp(&s.s_ready);
             }
@@ -683,7 +705,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             const unsigned steep = __ballot_sync(0xffffffffu, !(d.in > -kFall && d.in < kRise));
             float inverse = ex2(-d.in) * (1.f / kTwoShift);
             if (steep || d.mask) {
-                const float rest = d.exact(now);
+                const float rest = exact_sum(d, now);
                 if ((steep | d.mask) & (0xffffffffu >> (31 - lane))) inverse = rest;
             }
             s.in[st][t] = d.in;
@@ -711,23 +733,18 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
             if (t < n) {
                 f32x2 sign = 0;
 #pragma unroll 1
-                for (int q = 0; q < 8; q += 2)
+                for (int q = 0; q < 8; ++q) {
+                    float f[8];
+                    widen(*reinterpret_cast<const uint4 *>(V + sw128(t, q)), f);
+                    f32x2 x[4];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float f[8];
-                        widen(*reinterpret_cast<const uint4 *>(V + sw128(t, q + r)), f);
-                        f32x2 x[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] = pack2(f[2 * e], f[2 * e + 1]);
-                            x[e] = mul2(x[e], dup2(w));
-                        }
-                        st_parts<kParts>(W, t, q + r, x, sign);
-                    }
+                    for (int e = 0; e < 4; ++e) x[e] = mul2(pack2(f[2 * e], f[2 * e + 1]), dup2(w));
+                    st_parts(W, t, q, x, sign);
+                }
                 if (is_odd(sign)) {  // infinite or NaN, decayed or not
                     if (cut) zero_row(W, t);  // what comes after has forgotten it
                     else if (w == 0.f) keep_odd_row(W, V, t);
-                    else mend_row(W, kParts, t);
+                    else mend_row(W, t);
                     if (!kStates) {
                         atomicOr(&s.odd[st][quad], 1u << lane);
                         code_row(V, t);
@@ -839,11 +856,11 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 if (c > 0) wait(&s.o_free[st ^ 1], (c - 1) >> 1);
                 tc_fence_after();
                 const uint64_t v = sdesc_sw128(base + kOffV + c % kRing * kTile, kTile, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int part = 0; part < kHalves; ++part)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        mma_f16kind_ts(tbase + kColO, p + 32 * (i >> 1) + 16 * part + 8 * (i & 1), v + mn_step(i),
+                        mma_f16kind_ts(tbase + kColO, p + 16 * i + 8 * part, v + mn_step(i),
                                        idesc_bf16_f32(128, 64, 0, 1), part + i > 0);
                 mma_commit(&s.o_full);
             }
@@ -865,7 +882,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                 for (int half = 0; half < 2; ++half) {
                     wait(&s.w_half[half], c);
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < kParts; ++part)
 #pragma unroll
                         for (int i = 4 * half; i < 4 * half + 4; ++i)
@@ -892,7 +909,7 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     if (c > 1) wait(&s.o_free[st], (c - 2) >> 1);
                     tc_fence_after();
                     const uint64_t S = sdesc_sw128(base + kOffS, kTile, 1024);
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < kHalves; ++part)
 #pragma unroll
                         for (int i = 0; i < KS; ++i)
