@@ -38,6 +38,13 @@ template <int DK, int DV> struct Smem {
 
 __device__ __forceinline__ bool not_finite(float f) { return !(fabsf(f) <= 3.402823466e38f); }
 
+__device__ __forceinline__ float at_least(float x, float least)  // NaN stays
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(least));
+    return y;
+}
+
 // What a decay below 2^-126 leaves of x beside infinities: those stay, and what is finite
 // still has its sign in their products.
 __device__ __forceinline__ float least_of(float x)
@@ -151,7 +158,19 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
             Decays d;
             const float decay_now = decay_next;
             d.scan(decay_now);
-            m.rest[lane] = d.exact(decay_now);
+            // Sums up to 2^8 are off by 5e-7 at most.  Which lanes have the exact ones depends on no
+            // token behind them.
+            const unsigned steep = __ballot_sync(0xffffffffu, !(fabsf(d.in) <= 8.f));
+            float rest = 0.f;
+            if (steep) {
+                const float plain = d.in;
+                rest = d.exact(decay_now);
+                if (!(steep & (0xffffffffu >> (31 - lane)))) {
+                    d.in = plain;
+                    rest = 0.f;
+                }
+            }
+            m.rest[lane] = rest;
             m.in[lane] = d.in;
             m.first[lane] = first_seen(d.mask, lane);
             const float start = decay_of(once(d.in));
@@ -169,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
         const bool odd = __syncthreads_or(inf_k || inf_v);
         load(c + kC);
         float acc[4][OV];
+        const float least = odd ? 1.175494351e-38f : 0.f;  // a decay that no token forgets leaves infinities as they are
         if (!states_only) {
             f32x2 sum[4][1 + OV] = {};
 #pragma unroll 2
@@ -189,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linattn_kernel(const GdnLinat
                 const float w = m.start[i], early = m.early[i];
                 float lo, hi;
                 unpack2(sum[e][0], lo, hi);
-                const float x = lo + hi, f = decay_of(m.in[i] - m.in[j0] + (m.rest[i] - m.rest[j0]));
-                m.P[i][j0] = j0 <= i && j0 >= m.first[i] ? (odd && f == 0.f ? least_of(x) : x * f) : 0.f;
+                const float f = at_least(decay_of(m.in[i] - m.in[j0] + (m.rest[i] - m.rest[j0])), least);
+                m.P[i][j0] = j0 <= i && j0 >= m.first[i] ? (lo + hi) * f : 0.f;
 #pragma unroll
                 for (int f = 0; f < OV; ++f) {
                     unpack2(sum[e][1 + f], lo, hi);

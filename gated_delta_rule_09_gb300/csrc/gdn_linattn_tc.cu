@@ -343,12 +343,6 @@ __device__ __forceinline__ float row_factor(float x, float scale)
     return far ? f : f * kTwoShift;
 }
 
-// A product with its factor, NaN where it is not seen.  A factor of zero leaves a zero of the right sign.
-__device__ __forceinline__ float decayed(float x, float f)
-{
-    return f != f ? 0.f : f != 0.f ? x * f : copysignf(0.f, x * copysignf(1.f, f));
-}
-
 // P of one row in the cases that the plain path leaves: tokens that forget, and sums of
 // decays beyond kFall and kRise, over blocks too.  An exponential an entry: 217 us where the
 // plain path takes 78, if every block of 32 goes this way.  Rows that come before any such
@@ -366,20 +360,18 @@ __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, b
         const float last = in[32 * J + 31], last_rest = rest(J, 31), plain = row_factor(J == I ? sum : sum + total[J], scale);
 #pragma unroll 1
         for (int from = 0; from < 32; from += 16) {
-            float x[16], factor[16];  // factors lie in local memory: unrolled, they would be half of the kernel's code
+            float x[16];
             ld_cols(lane_addr(p, quad, 32 * J + from), x);
-#pragma unroll 2
+            const unsigned late = (mask[J] | steep[J]) ? ~0u << (__ffs(mask[J] | steep[J]) - 1) : 0;  // tokens with a rest
+#pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int j = from + e;
-                const float w = in[32 * J + j];
+                const float w = in[32 * J + j], other = inverse[32 * J + j], left = late >> j & 1 ? other : 0.f;
                 const bool seen = J == I ? j <= lane && j >= first : !cut && !(mask[J] & (0xfffffffeu << j));
-                const float f = own ? decay_of(J == I ? mine - w + (mine_rest - rest(J, j))
-                                                      : sum + (last - w + (last_rest - rest(J, j)))) * scale
-                                    : plain * inverse[32 * J + j];
-                factor[e] = seen ? f : __uint_as_float(0x7fc00000u);
+                const float f = own ? decay_of(J == I ? mine - w + (mine_rest - left) : sum + (last - w + (last_rest - left))) * scale
+                                    : plain * other;
+                x[e] = !seen ? 0.f : f != 0.f ? x[e] * f : copysignf(0.f, x[e] * copysignf(1.f, f));  // zeros keep their sign
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = decayed(x[e], factor[e]);
             __syncwarp();
             st_p(lane_addr(p, quad, 32 * J + from), x);
         }
