@@ -108,7 +108,7 @@ __device__ __forceinline__ void dot4(const float4 &x, const float4 &y, f32x2 &su
 // A warp's lanes are 4 rows by 8 columns of a product: its loads of either factor are
 // free of bank conflicts, 4 x 3 sums a thread of Q [K; S]^T for 7 words of 16 bytes, 4 x
 // 8 of V^T K for 12 floats a token.  Bound by what shared memory gives to registers, 128
-// bytes a cycle (4 x 4096 tokens x 16 heads fp32: 977 us, about 12 000 of a chunk's
+// bytes a cycle (4 x 4096 tokens x 16 heads fp32: 995 us, about 12 000 of a chunk's
 // 16 000 cycles; fused multiply-adds 6000).  512 threads with half the sums each, and so
 // more words for them, took 1352; one sum a thread along rows of o 1395.  The next
 // chunk's rows are loaded while this one's are worked on.
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_chain_kernel(const GdnLi
 
 // One new token per sequence.  Row i of S needs only itself, k, q and v_i: a warp
 // takes kRows rows of one head at a time, a row over its lanes.  Bound by HBM:
-// the state is read and written once (256 sequences x 16 heads of 128: 81 us, 6.05 TB/s).
+// the state is read and written once (256 sequences x 16 heads of 128, 541 MB: 81 us, 6.7 TB/s).
 constexpr int kRows = 8;
 
 template <typename T, int V> __device__ __forceinline__ void ld_part(const T *p, int dk, int lane, bool vec, float (&x)[V])
@@ -533,19 +533,21 @@ cudaError_t pass(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 // Whole sequences or pieces: the quicker by what was measured, us per chunk of 128
 // tokens for the first block of a multiprocessor and for each more, and beside all
 // chunks.
-// Tensor cores: one document of 131 072 tokens x 8 heads whole 2121, in pieces 418; 4096
-// tokens x 16 heads whole 75, 4 pieces 50; 2048 tokens whole 42, 4 pieces 36; 1024 tokens
-// x 8 heads whole 26, 2 pieces 33; 4096 tokens x 32 heads whole 77, 2 pieces 82.
+// Tensor cores: one document of 131 072 tokens x 8 heads whole 2592, in pieces 530; 4096
+// tokens x 16 heads whole 92, 4 pieces 59; 2048 tokens whole 51, 4 pieces 39.5; 1024 tokens
+// x 8 heads whole 29, 2 pieces 36; 4096 tokens x 32 heads whole 94.5, 2 pieces 98.
 // CUDA cores, fp32 (blocks of 32 columns; one of 64 takes the time of two): 4096 tokens x
-// 4 heads whole 726, pieces of 512 148, of 128 102; 16 heads whole 736, pieces of 2048 531,
-// 512 317; 4 x 4096 x 16 whole 977, 4 pieces each 1117; 517 x 2 heads whole 102, 5 pieces 52.
+// 4 heads whole 752, pieces of 512 156, of 128 101; 16 heads whole 756, pieces of 2048 550,
+// 512 320; 4 x 4096 x 16 whole 995; 517 x 2 heads whole 106, 5 pieces 53.
+// Sequences of a pack are not seen from here: one that has nearly all of its rows (131 072
+// rows x 8 heads, 8 sequences) is not cut, 2693, where pieces of 6912 take 554.
 // Pieces are chosen to fill the multiprocessors once or up to as often as there is room.
 void gdn_linattn_plan(bool tensor_cores, int N, int T, int heads, int dk, int dv, bool packed, int asked, int *segment,
                       int64_t *piece_slots)
 {
     const double wide = 0.4 + 0.6 * ((dk + 31) / 32) / 4;  // tiles of d_k on CUDA cores
-    const double kWhole = tensor_cores ? 2.05 : 21.5 * wide, kWholeMore = tensor_cores ? kWhole : 10 * wide, kWholeStart = 10;
-    const double kCut = tensor_cores ? 3.5 : 31.5 * wide, kCutMore = tensor_cores ? kCut : 14 * wide, kCutStart = 20;
+    const double kWhole = tensor_cores ? 2.55 : 21.5 * wide, kWholeMore = tensor_cores ? kWhole : 10 * wide, kWholeStart = 10;
+    const double kCut = tensor_cores ? 4.5 : 31.5 * wide, kCutMore = tensor_cores ? kCut : 14 * wide, kCutStart = 20;
     const int kFills = tensor_cores ? 3 : 4;
     constexpr double kBytesPerUs = 6e6;
     constexpr int64_t kChunk = 128;

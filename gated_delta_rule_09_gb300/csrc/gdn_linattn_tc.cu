@@ -344,8 +344,8 @@ __device__ __forceinline__ float row_factor(float x, float scale)
 }
 
 // P of one row in the cases that the plain path leaves: tokens that forget, and sums of
-// decays beyond kFall and kRise, over blocks too.  An exponential an entry: 217 us where the
-// plain path takes 78, if every block of 32 goes this way.  Rows that come before any such
+// decays beyond kFall and kRise, over blocks too.  An exponential an entry: 309 us where the
+// plain path takes 98, if every block of 32 goes this way.  Rows that come before any such
 // token (`own` false) have the plain path's factors: the same bits, whatever comes later.
 __device__ __noinline__ void odd_decays(uint32_t p, int quad, int I, int lane, bool own, float scale, const float *in,
                                         const float *inverse, const float *total, const unsigned *mask, const unsigned *steep)
