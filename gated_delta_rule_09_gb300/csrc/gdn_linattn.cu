@@ -506,8 +506,8 @@ template <typename E, int DK, int DV> cudaError_t simt_of(const GdnLinattnArgs &
 }
 
 // 32 columns of v per block where 64 would leave multiprocessors empty.  us, fp32, d_k
-// 128, of 32 and of 64: 4096 tokens x 16 heads (32 blocks of 64) 705, 1000; 4 x 4096 x 16
-// (128) 1202, 977; 4 x 4096 x 16 of 64 (64) 486, 601.
+// 128, of 32 and of 64: 4096 tokens x 16 heads (32 blocks of 64) 763, 998; 4 x 4096 x 16
+// with d_v 64 (64 blocks) 763, 1010; with d_v 128 (128) 1252, 999.
 template <typename E, int DK> cudaError_t simt(const GdnLinattnArgs &a, bool states_only, cudaStream_t s)
 {
     const int64_t blocks = spans(a) * a.heads * ((a.dv + 63) / 64);

@@ -139,3 +139,21 @@ def test_pieces_that_grow_and_fall_again(dtype):
     S0 = torch.randn(1, 2, 64, 64, device="cuda")
     for segment, pieces in ((0, 1), (512, 2)):
         check(x, state=S0, segment=segment, pieces=pieces)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.125, -2.0 ** -20, 2.0 ** 20])
+@pytest.mark.parametrize("rate", [-0.2, -3.0])
+def test_odd_states_under_a_scale(dtype, scale, rate):
+    """A scale does not take a decay that no token forgets below what fp32 holds."""
+    x = positive(300, 2, 1, 64, 64, dtype, seed=3)
+    x["log_decay"][:] = rate
+    x["v"][0, 40, 0, 5] = INF
+    S0 = torch.zeros(1, 2, 64, 64, device="cuda")
+    S0[0, 0, 3] = INF
+    S0[0, 1, 7] = -INF
+    o, S = gdn.gdn_linattn_fwd(**x, scale=scale, state_in=S0)
+    ro, _, rS, _ = walk(**x, scale=scale, state_in=S0)
+    odd = ~np.isfinite(ro)
+    assert np.array_equal(o.double().cpu().numpy()[odd], ro[odd]) and bool(torch.isfinite(o.cpu()[torch.from_numpy(~odd)]).all())
+    assert np.array_equal(np.isfinite(S[0].cpu().numpy()), np.isfinite(rS[0])) and gdn.gdn_get_device_status() == 0
