@@ -110,10 +110,10 @@ __device__ __forceinline__ float half_decay_of(float x)
 }
 
 // Sums of decays below -126, whose 2^x is zero in fp32 and would drop an infinite state that
-// no token forgets, are applied as two factors 2^once(x): 2^-100 at least, which a scale may
-// still go with.
-__device__ __forceinline__ bool is_far(float x) { return x < -126.f; }
-__device__ __forceinline__ float once(float x) { return is_far(x) ? fmaxf(0.5f * x, -100.f) : x; }
+// no token forgets, are applied as two factors 2^once(x); where a scale goes with them, sums
+// below -60, so that either factor has room for it.
+__device__ __forceinline__ bool is_far(float x, float from = -126.f) { return x < from; }
+__device__ __forceinline__ float once(float x, float from = -126.f) { return is_far(x, from) ? fmaxf(0.5f * x, -100.f) : x; }
 
 // The root of the decay over a piece, from its chunks' sums as they come; zero where a token forgets.
 struct PieceDecay {

@@ -776,8 +776,8 @@ gdn_linattn_tc_kernel(const GdnLinattnArgs a, int tiles, const __grid_constant__
                     cut = cut || s.mask[st][J];
                     sum += s.total[st][J];
                 }
-                const float from = decay_of(once(sum));
-                float again = is_far(sum) ? from : 1.f;
+                const float from = decay_of(once(sum, -60.f));
+                float again = is_far(sum, -60.f) ? from : 1.f;
                 opaque(again);
                 const f32x2 start = dup2(a.scale * from);
                 wait(&s.w_ready[st], c >> 1);
