@@ -19,11 +19,13 @@
 // bf16 parts each, which leave 2^-16: outputs are off by their own rounding, 1.7e-3 (one
 // part each: 2.3e-3).
 //
-// 4 x 4096 tokens x 16 heads of 128: 94 us, 2.9 TB/s, 43 % of the HBM copy rate; a chunk
-// takes 2.4 us.  No one thing bounds it: P unsplit gave back 4 us, the second parts'
-// products 7, the outputs 5, the copies of Q 4, and shared memory moves some 510 KB a
-// chunk, most of what 128 bytes a cycle are.  Both parts of S^T as one product of 128
-// columns, Q read once, took 96: its sums then have one stage.
+// 4 x 4096 tokens x 16 heads of 128: 98.6 us, 2.8 TB/s, 41 % of the HBM copy rate; a chunk
+// takes 2.6 us.  No one thing bounds it: with the tensor pipe busy for 49 % of the time on
+// the multiprocessors that have a block, each scheduler issues in 45 % of its cycles and
+// shared memory moves some 510 KB a chunk, most of what 128 bytes a cycle are.  Left out, P's
+// second parts gave back 4 us, the outputs' half 5, the copies of Q 4.  Both parts of S^T as
+// one product of 128 columns, Q read once, took 96 us where this took 94: its sums then have
+// one stage.  Larger loops took 108: warps waited for instructions 1.9 times an issue, now 0.8.
 //
 // Roles, in groups of four warps: forming P (tensor memory to tensor memory, a row per
 // thread), keeping the state and writing its parts for the next chunk, summing the

@@ -406,7 +406,8 @@ def gdn_linattn_fwd(q, k, v, log_decay, scale=1.0, state_in=None, o=None, state_
     head.  Per head S = e^g S + v k^T, o = scale S q.  States are fp32
     [N,H,d_v,d_k], or pools addressed by ``slots``, as in ``gdn_conv_fwd``.
     ``segment`` is the length in tokens of the pieces that long sequences are
-    cut into (0: chosen by the library); ``workspace`` a uint8 CUDA tensor of
+    cut into (0: chosen by the library, which takes the longest sequence of a
+    pack to be twice the mean); ``workspace`` a uint8 CUDA tensor of
     ``gdn_linattn_fwd_workspace_size(...)`` bytes, allocated here if None.
     """
     shape, dtype, index = _values(v, 4, "[B,T,H,d_v]")
